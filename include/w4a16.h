@@ -68,6 +68,7 @@ extern "C" {
 #define W4_ERR_WORKSPACE  6  /* workspace missing or smaller than required */
 #define W4_ERR_DEVICE     7  /* current device is not sm_103 or lacks a needed driver entry point */
 #define W4_ERR_TIMEOUT    8  /* a device-side bounded wait expired (reported by w4a16_device_status) */
+#define W4_ERR_INDEX      9  /* a kernel met a page, length or offset out of range (reported by w4a16_device_status) */
 
 /*
  * Launch flag of the *_ex calls.  W4A16_OVERLAP_PREVIOUS lets the call's
@@ -323,13 +324,153 @@ W4A16_API int f16_gemm(const uint16_t *x16, const uint16_t *w16, uint16_t *y,
 W4A16_API int f16_gemm_ex(const uint16_t *x16, const uint16_t *w16, uint16_t *y, int M, int N,
                           int K, unsigned flags, void *stream);
 
+/*
+ * Attention with a paged key/value cache: what a decoder layer does between
+ * its q/k/v projections and its o projection.  The three calls share the
+ * conventions above (binary16 tensors, fp32 arithmetic, host checks, one
+ * stream).  Activations are [tokens][heads][head_dim] with strides in
+ * elements: `*_token` from token to token, `*_head` from head to head, both
+ * multiples of 8 (16 bytes), the head_dim elements of a head contiguous.
+ * Index arrays (int32) need their natural alignment only.
+ *
+ * Sequences.  A call works on the tokens of `batch` sequences, whose new
+ * tokens lie one after the other: sequence b has the tokens q_offsets[b] <= t
+ * < q_offsets[b + 1], and kv_lens[b] tokens in the cache, these new ones
+ * among them (they are its last).  Its token t therefore stands at position
+ *     p = kv_lens[b] - (q_offsets[b + 1] - q_offsets[b]) + (t - q_offsets[b]).
+ * Position p of sequence b is kept in token p % page_size of page
+ * block_table[b][p / page_size].  Table entries that no visible position
+ * needs may hold anything.  A sequence may bring no token, and may have
+ * kv_lens[b] = 0 (a padded slot of a batch).  Lengths, offsets and pages are
+ * read on the device, so that a captured graph can be replayed with others;
+ * those out of range are clamped or skipped, never followed, and reported by
+ * w4a16_device_status as W4_ERR_INDEX.
+ */
+typedef struct {
+    const int32_t *block_table; /* [batch][table_stride], the first max_pages of a row are used */
+    const int32_t *q_offsets;   /* [batch + 1], ascending */
+    const int32_t *kv_lens;     /* [batch], at most max_pages * page_size */
+    int32_t batch;              /* >= 1 */
+    int32_t max_pages;          /* >= 1 */
+    int32_t table_stride;       /* >= max_pages */
+    int32_t total_q;            /* tokens of the q, k, v tensors (rows past q_offsets[batch] are left alone) */
+    int32_t max_q_len;          /* the most new tokens of one sequence: a kernel is chosen by it (results hold for any) */
+} f16_kv_batch;
+
+/*
+ * A paged cache: binary16 k and v, num_pages pages of page_size tokens of
+ * `heads` key/value heads, with strides in elements (multiples of 8), in any
+ * order of page, token and head.  Filled in by f16_kv_cache_init, which also
+ * encodes the tensor maps of its copies; plain data, copied and dropped freely.
+ */
+typedef struct {
+    uint16_t *k, *v;
+    int64_t k_page, k_token, k_head;
+    int64_t v_page, v_token, v_head;
+    int32_t num_pages, page_size, heads, head_dim;
+    int32_t box_rows, reserved;
+    uint64_t k_map[16], v_map[16];
+} f16_kv_cache;
+
+/*
+ * f16_kv_cache_init - describe a cache (host only, nothing is enqueued).
+ *   strides   {page, token, head} in elements
+ *   num_pages >= 1;  page_size a multiple of 8;  heads >= 1;
+ *   head_dim  a multiple of 8, 8..256
+ * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_DEVICE.
+ */
+W4A16_API int f16_kv_cache_init(f16_kv_cache *cache, uint16_t *k, uint16_t *v, const int64_t k_strides[3],
+                                const int64_t v_strides[3], int num_pages, int page_size, int heads, int head_dim);
+
+/*
+ * A rotation of positions.  Pair i < rot / 2 of a head is turned by
+ * p * turns[i] / 2^64 of a full turn at position p, and scaled by factor:
+ *     (a, b) -> factor * (a cos - b sin, a sin + b cos).
+ * turns[i] = round(2^64 * theta_i / (2 pi)) for an angle of theta_i per
+ * position; p * turns[i] wraps modulo 2^64, which is the reduction of the
+ * angle to one turn, exact at every position.  Negative positions turn back.
+ * Pairs are (2i, 2i + 1) when interleaved, else (i, i + rot / 2); the
+ * elements from rot on are copied.
+ */
+typedef struct {
+    const uint64_t *turns; /* [rot / 2], device memory */
+    int32_t rot;           /* a multiple of 8, 8..head_dim */
+    int32_t interleaved;   /* 0 or 1 */
+    float factor;          /* 1, or the scale of a stretched context */
+} f16_rotation;
+
+/*
+ * f16_rope - rotate the heads of a tensor: y[t][h] = R(positions[t]) x[t][h].
+ *   positions  int32 [tokens], any value; NULL: token t is at position t
+ *   x, y       strided as above; y may be x (in place), else they must not overlap
+ *   tokens >= 0;  heads >= 1;  head_dim a multiple of 8, 8..256
+ * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_DEVICE, W4_ERR_LAUNCH.
+ */
+W4A16_API int f16_rope(const uint16_t *x, int64_t x_token, int64_t x_head, uint16_t *y, int64_t y_token,
+                       int64_t y_head, const int32_t *positions, const f16_rotation *rotation, int tokens, int heads,
+                       int head_dim, void *stream);
+
+/*
+ * f16_kv_append - write the new tokens' keys and values into the cache, the
+ * keys rotated on the way, and rotate the queries in the same launch.
+ *   k, v       [total_q][cache heads][head_dim], strided
+ *   rotation   NULL: nothing is rotated
+ *   positions  int32 [total_q], the rotation's positions where they are not
+ *              the cache's (NULL: they are)
+ *   q, y       [total_q][q_heads][head_dim], strided: y = R q (y may be q).
+ *              q NULL: keys and values only
+ * Cache slots of other positions keep their contents.  A token whose position
+ * is negative (a padded slot) is not written to the cache.
+ * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_DEVICE, W4_ERR_LAUNCH.
+ */
+W4A16_API int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head, const uint16_t *v, int64_t v_token,
+                            int64_t v_head, const f16_kv_cache *cache, const f16_kv_batch *batch,
+                            const f16_rotation *rotation, const int32_t *positions, const uint16_t *q,
+                            int64_t q_token, int64_t q_head, uint16_t *y, int64_t y_token, int64_t y_head,
+                            int q_heads, void *stream);
+
+/*
+ * f16_attention - attention of the new tokens over the cache:
+ *     y[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j,
+ * over the positions j of t's sequence that it sees: j < kv_lens[b], with
+ * causal != 0 also j <= p, with window > 0 also j > p - window (p is t's
+ * position, above).  Query head h reads key/value head h / (q_heads / heads).
+ *   q, y    [total_q][q_heads][head_dim], strided (y may be q)
+ *   lse     float [total_q][q_heads]: log of the sum of exp(scale q . k_j), or NULL
+ *   scale   > 0, finite;  causal 0 or 1;  window >= 0 (0: none)
+ *   q_heads a multiple of the cache's heads, at most 1024 for each
+ *   workspace  device buffer of at least f16_attention_workspace_bytes bytes,
+ *              16-byte aligned; contents on entry are ignored.  Calls ordered
+ *              on one stream may share it.
+ * Products are binary16 with fp32 sums; the softmax's statistics and the
+ * output's sum are fp32, the probabilities are rounded to binary16 for the
+ * product with v, and y is rounded once.  A token that sees no position gets
+ * y = 0 and lse = -infinity.  What the cache holds at positions that no token
+ * of the call sees, and past a sequence's end, does not matter, NaN and
+ * infinities included; keys and values that some token of a sequence sees are
+ * taken to be finite (a value that is not may show in the sequence's earlier
+ * tokens too).  Results are deterministic, and do not depend on what else the
+ * workspace held.
+ * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_WORKSPACE,
+ * W4_ERR_DEVICE, W4_ERR_LAUNCH.
+ */
+W4A16_API int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head, uint16_t *y, int64_t y_token,
+                            int64_t y_head, float *lse, int q_heads, float scale, int causal, int window,
+                            const f16_kv_cache *cache, const f16_kv_batch *batch, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Workspace bytes for f16_attention (0 if the sizes are invalid).  Depends
+ * only on its arguments, and does not grow with the batch or the context. */
+W4A16_API size_t f16_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q_len);
+
 /* Human-readable name of a status code (static string). */
 W4A16_API const char *w4a16_status_string(int status);
 
 /*
  * Synchronises the current device and reports whether any kernel of this
  * library gave up a bounded device-side wait since the last call
- * (W4_ERR_TIMEOUT), then clears the record.  W4A16_OK otherwise.
+ * (W4_ERR_TIMEOUT) or met an index out of range (W4_ERR_INDEX), then clears
+ * the record.  W4A16_OK otherwise.
  */
 W4A16_API int w4a16_device_status(void);
 

@@ -10,6 +10,9 @@ Weight format: ``qweight`` int32/uint32 [N][K/8] (8 four-bit codes per word,
 lowest nibble = lowest k), ``scales`` and ``biases`` float16 [N][K/group]
 (group 64 unless given); w[n][k] = scale * q + bias, or, with
 ``biases=None``, symmetric codes w[n][k] = scale * (q - 8).
+
+Between a layer's projections: rotary positions, a paged key/value cache and
+attention over it (``attention.py``).
 """
 from __future__ import annotations
 
@@ -20,13 +23,16 @@ import torch
 
 __all__ = ["OVERLAP_PREVIOUS", "w4_gemv", "w4_gemv_seq", "GemvList", "seq_workspace", "seq_workspace_bytes", "GemvOp",
            "lm_head_argmax_topk", "lm_head_workspace_bytes", "w4_dequant_f16", "f16_gemm", "w4_gemm",
-           "w4_gemm_workspace", "w4_gemm_workspace_bytes", "device_status", "W4A16Error", "LIB_PATH", "lib"]
+           "w4_gemm_workspace", "w4_gemm_workspace_bytes", "device_status", "W4A16Error", "LIB_PATH", "lib",
+           "KVBatch", "KVCache", "Rope", "attention_workspace", "attention_workspace_bytes", "f16_attention",
+           "f16_kv_append", "f16_rope", "rope_turns"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4a16.so")
 
 STATUS = {0: "W4A16_OK", 1: "W4_ERR_NULL", 2: "W4_ERR_SHAPE", 3: "W4_ERR_ALIGN", 4: "W4_ERR_GROUP",
-          5: "W4_ERR_LAUNCH", 6: "W4_ERR_WORKSPACE", 7: "W4_ERR_DEVICE", 8: "W4_ERR_TIMEOUT"}
+          5: "W4_ERR_LAUNCH", 6: "W4_ERR_WORKSPACE", 7: "W4_ERR_DEVICE", 8: "W4_ERR_TIMEOUT",
+          9: "W4_ERR_INDEX"}
 
 
 class W4A16Error(RuntimeError):
@@ -303,5 +309,10 @@ def f16_gemm(x16: torch.Tensor, w16: torch.Tensor, y: torch.Tensor | None = None
 
 
 def device_status() -> int:
-    """Synchronise and return the library's device-side status (0 = ok, 8 = a bounded wait expired)."""
+    """Synchronise and return the library's device-side status (0 = ok, 8 = a bounded wait expired,
+    9 = a page, length or offset was out of range)."""
     return int(lib.w4a16_device_status())
+
+
+from .attention import (KVBatch, KVCache, Rope, attention_workspace, attention_workspace_bytes,  # noqa: E402
+                        f16_attention, f16_kv_append, f16_rope, rope_turns)

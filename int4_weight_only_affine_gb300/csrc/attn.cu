@@ -1,0 +1,522 @@
+// f16_attention for few query rows (decode steps, drafted tokens, short
+// chunks), the join of split items, and the call's entry points.
+//
+// y = sum_j softmax_j(scale q k_j) v_j in one pass over the positions: with
+// the scores in powers of two, s_j = scale log2(e) q k_j, a running maximum m
+// and running sums l = sum 2^(s_j - m), o = sum 2^(s_j - m) v_j are corrected
+// by 2^(m_old - m_new) whenever m grows; partial (m, l, o) of disjoint
+// positions combine the same way.
+//
+// With few rows per key the pass is bound by reading K and V once: 4
+// head_dim bytes a position.  One persistent CTA per SM works through its
+// range of units (attn.cuh).  A producer warp copies the tiles, K and V of
+// KEYS positions each, page by page, with tensor copies into a ring of up to
+// 192 KB.  The other warps each own 16 positions of every tile, and keep
+// their own (m, l, o) of 16 rows in registers for the whole item: no warp
+// waits for another inside the loop.  16 x 16 scores and their product with V
+// are m16n8k16 tensor-core products, far below their rate here; the warps'
+// sums are merged through shared memory at the end of the item.
+#include <math.h>
+#include <string.h>
+
+#include "attn.cuh"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kMaxGrid = 256;  // CTAs of a launch, >= the SMs of the GPU
+constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
+
+template <int DP, int MT>
+struct RowCfg {
+    static constexpr int ROWS = 16 * MT;
+    static constexpr int KEYS = DP <= 128 ? 128 : 64;
+    static constexpr int WARPS = KEYS / 16;             // consumers
+    static constexpr int THREADS = 32 * (WARPS + 1);
+    static constexpr int HALF = KEYS * 128;             // bytes of 64 columns of a tile
+    static constexpr int TILE = HALF * (DP / 64);       // K or V
+    static constexpr int STAGES = 192 * 1024 / (2 * TILE);
+    static constexpr int MERGE_COLS = 32;               // columns merged at a time
+    static constexpr int MERGE_LD = MERGE_COLS + 4;     // floats per row of the merge buffer
+    static constexpr int MERGE = WARPS * ROWS * MERGE_LD * 4;
+    static constexpr int ML = WARPS * ROWS * 8;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * 2 * TILE + MERGE + ML + 16 * STAGES + 16;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 2^(a - b) for maxima of which either may be -infinity (nothing seen yet).
+__device__ __forceinline__ float corr(float a, float b) { return a == -INFINITY ? 0.f : exp2_approx(a - b); }
+
+template <int DP, int MT>
+__global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
+    attn_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ AttnArgs a) {
+    using C = RowCfg<DP, MT>;
+    constexpr int ROWS = C::ROWS, KEYS = C::KEYS, NT = 32 * C::WARPS;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PlanShared plan_sh;
+    const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw);
+    float *merge = reinterpret_cast<float *>(gbase + C::STAGES * 2 * C::TILE);
+    float2 *ml_sh = reinterpret_cast<float2 *>(gbase + C::STAGES * 2 * C::TILE + C::MERGE);
+    const uint32_t bar0 = base + C::STAGES * 2 * C::TILE + C::MERGE + C::ML;
+    volatile int *abort = reinterpret_cast<volatile int *>(gbase + (bar0 - base) + 16 * C::STAGES);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), C::WARPS);
+        }
+        *abort = 0;
+        a.joins[blockIdx.x].parts = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    make_plan<ROWS, KEYS, C::THREADS, 2>(a, plan_sh);  // (its barriers also publish the above)
+    const Plan plan = plan_sh.plan;
+    Pieces<ROWS, KEYS> pc(a, plan);
+
+    if (warp == C::WARPS) {
+        // ---------------- producer ----------------
+        constexpr int HALVES = DP / 64;
+        const int boxes = KEYS / a.box_rows * HALVES * 2;
+        int it = 0;
+        bool ok = true;
+        while (ok && pc.next()) {
+            for (int i = 0; i < pc.n; ++i, ++it) {
+                const int st = it % C::STAGES;
+                ok = mbar_wait(empty_bar(st), ((it / C::STAGES) & 1) ^ 1, abort);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_expect_tx(full_bar(st), 2 * C::TILE);
+                __syncwarp();
+                const int p0 = (pc.it.t0 + pc.tile0 + i) * KEYS;
+                const uint32_t kdst = base + st * 2 * C::TILE;
+                for (int x = lane; x < boxes; x += 32) {
+                    const int half = (x >> 1) % HALVES, row = (x >> 1) / HALVES * a.box_rows;
+                    const int p = p0 + row;
+                    const int page = page_of(a, pc.b, p, pc.it.lo, pc.it.hi);
+                    const uint32_t dst = kdst + (x & 1) * C::TILE + half * C::HALF + row * 128;
+                    tma_load_4d(dst, x & 1 ? &map_v : &map_k, 64 * half, p % a.page_size, pc.head, page, full_bar(st));
+                }
+            }
+        }
+        // Every copy has landed before the CTA may exit.
+        __syncwarp();
+        if (lane == 0)
+            for (int k = max(0, it - C::STAGES); k < it; ++k) mbar_wait(full_bar(k % C::STAGES), (k / C::STAGES) & 1);
+        return;
+    }
+
+    // ---------------- consumers ----------------
+    const int g = lane >> 2, t4 = lane & 3;
+    int it = 0;
+    while (pc.next()) {
+        const int row0 = pc.row0(), rows = pc.rows();
+        // Query fragments, and the positions each of this lane's rows sees.
+        uint32_t qf[MT][DP / 16][4];
+        int lb[MT][2], ub[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int r = row0 + 16 * mt + 8 * hf + g;
+                const bool in = r < row0 + rows;
+                const int tok = r / a.group, p = pc.s.kv - pc.s.qn + tok;
+                ub[mt][hf] = in ? (a.causal ? min(p + 1, pc.s.kv) : pc.s.kv) : 0;
+                lb[mt][hf] = a.window > 0 ? p - a.window + 1 : 0;
+                const uint16_t *qr = a.q + (pc.s.q0 + tok) * a.q_token +
+                                     (pc.head * a.group + r % a.group) * a.q_head;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const int c = 16 * k + 2 * t4;
+                    qf[mt][k][hf] = in && c < a.head_dim ? *reinterpret_cast<const uint32_t *>(qr + c) : 0u;
+                    qf[mt][k][2 + hf] =
+                        in && c + 8 < a.head_dim ? *reinterpret_cast<const uint32_t *>(qr + c + 8) : 0u;
+                }
+            }
+        // Tiles inside these bounds need no mask for any row of the item.
+        const int pf = pc.s.kv - pc.s.qn + row0 / a.group, pl = pc.s.kv - pc.s.qn + (row0 + rows - 1) / a.group;
+        const int all_ub = a.causal ? min(pf + 1, pc.s.kv) : pc.s.kv;
+        const int all_lb = a.window > 0 ? pl - a.window + 1 : 0;
+
+        float o[MT][DP / 8][4], m[MT][2], l[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            m[mt][0] = m[mt][1] = -INFINITY;
+            l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+        }
+
+        for (int i = 0; i < pc.n; ++i, ++it) {
+            const int st = it % C::STAGES;
+            const int j0 = (pc.it.t0 + pc.tile0 + i) * KEYS + 16 * warp;  // this warp's first position
+            const uint32_t kb = base + st * 2 * C::TILE, vb = kb + C::TILE;
+            mbar_wait(full_bar(st), (it / C::STAGES) & 1, abort);
+            const bool outside = j0 < pc.it.lo || j0 + 16 > pc.it.hi;
+            if (outside) {
+                // Rows of V that the item does not see hold anything; 0 x NaN must not reach the sums.
+                for (int x = lane; x < 16 * (DP / 8); x += 32) {
+                    const int row = x / (DP / 8), ch = x % (DP / 8);
+                    if (j0 + row < pc.it.lo || j0 + row >= pc.it.hi) {
+                        const uint32_t at = vb + (ch / 8) * C::HALF + (16 * warp + row) * 128 + (((ch ^ row) & 7) << 4);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                    }
+                }
+                __syncwarp();
+            }
+            if (j0 < pc.it.hi && j0 + 16 > pc.it.lo) {
+                float s[MT][2][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+                // Lane l addresses row (l & 7) + 8 (l >> 4) of the 16 positions, 8-column chunk (l >> 3) & 1:
+                // registers 0, 1 are the two chunks of positions 0-7, registers 2, 3 of positions 8-15.
+                const int krow = (lane & 7) + 8 * (lane >> 4), kch = (lane >> 3) & 1;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    uint32_t kf[4];
+                    const int ch = 2 * k + kch;
+                    ldsm4(kf, kb + (ch / 8) * C::HALF + (16 * warp + krow) * 128 + (((ch ^ krow) & 7) << 4));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma_16816(s[mt][0], qf[mt][k][0], qf[mt][k][1], qf[mt][k][2], qf[mt][k][3], kf[0], kf[1]);
+                        mma_16816(s[mt][1], qf[mt][k][0], qf[mt][k][1], qf[mt][k][2], qf[mt][k][3], kf[2], kf[3]);
+                    }
+                }
+                const bool masked = j0 + 16 > all_ub || j0 < all_lb;
+                uint32_t pf4[MT][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = j0 + 8 * n + 2 * t4 + (e & 1), hf = e >> 1;
+                            s[mt][n][e] *= a.scale;
+                            if (masked && (j >= ub[mt][hf] || j < lb[mt][hf])) s[mt][n][e] = -INFINITY;
+                        }
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float mx = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
+                                         fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+                        mx = fmaxf(mx, m[mt][hf]);
+                        const float c = corr(m[mt][hf], mx);
+                        const float ref = mx == -INFINITY ? 0.f : mx;
+                        if (__any_sync(~0u, mx != m[mt][hf])) {
+#pragma unroll
+                            for (int n = 0; n < DP / 8; ++n) {
+                                o[mt][n][2 * hf] *= c;
+                                o[mt][n][2 * hf + 1] *= c;
+                            }
+                        }
+                        m[mt][hf] = mx;
+                        float p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[e] = exp2_approx(s[mt][e >> 1][2 * hf + (e & 1)] - ref);
+                        l[mt][hf] = l[mt][hf] * c + ((p[0] + p[1]) + (p[2] + p[3]));
+                        // Probabilities, at most 1, to binary16 for the product with V (the sum l keeps fp32).
+                        pf4[mt][hf] = pack2(p[0], p[1]);
+                        pf4[mt][2 + hf] = pack2(p[2], p[3]);
+                    }
+                }
+                // Lane l addresses position l & 15 of the 16, 8-column chunk l >> 4.
+                const int vrow = lane & 15, vch = lane >> 4;
+#pragma unroll
+                for (int n = 0; n < DP / 16; ++n) {
+                    uint32_t vf[4];
+                    const int ch = 2 * n + vch;
+                    ldsm4t(vf, vb + (ch / 8) * C::HALF + (16 * warp + vrow) * 128 + (((ch ^ vrow) & 7) << 4));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma_16816(o[mt][2 * n], pf4[mt][0], pf4[mt][1], pf4[mt][2], pf4[mt][3], vf[0], vf[1]);
+                        mma_16816(o[mt][2 * n + 1], pf4[mt][0], pf4[mt][1], pf4[mt][2], pf4[mt][3], vf[2], vf[3]);
+                    }
+                }
+            }
+            if (outside) fence_proxy_async_smem();  // the zeros above, before the next copy into the slot
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_bar(st));
+        }
+
+        // ---------------- merge the warps' sums ----------------
+        auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float v = l[mt][hf];
+                v += __shfl_xor_sync(~0u, v, 1);
+                v += __shfl_xor_sync(~0u, v, 2);
+                if (t4 == 0) ml_sh[warp * ROWS + 16 * mt + 8 * hf + g] = make_float2(m[mt][hf], v);
+            }
+        sync();
+        // Maximum and sum of row r over the warps.
+        auto row_ml = [&](int r) {
+            float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < C::WARPS; ++w) mx = fmaxf(mx, ml_sh[w * ROWS + r].x);
+#pragma unroll
+            for (int w = 0; w < C::WARPS; ++w) sum += ml_sh[w * ROWS + r].y * corr(ml_sh[w * ROWS + r].x, mx);
+            return make_float2(mx, sum);
+        };
+        const bool whole = pc.begins && pc.ends;
+        if ((int)threadIdx.x < rows) {
+            const int r = threadIdx.x;
+            const float2 ml = row_ml(r);
+            if (whole) {
+                const int gr = row0 + r;
+                if (a.lse)
+                    a.lse[(long long)(pc.s.q0 + gr / a.group) * (a.kv_heads * a.group) + pc.head * a.group +
+                          gr % a.group] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+            } else {
+                reinterpret_cast<float2 *>(a.part_ml)[(long long)pc.slot() * ROWS + r] = ml;
+            }
+        }
+        if (threadIdx.x == 0 && pc.begins && !pc.ends)
+            a.joins[blockIdx.x] = JoinItem{pc.parts(plan), pc.s.q0, pc.head, row0, rows};
+        float f[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) f[mt][hf] = corr(m[mt][hf], row_ml(16 * mt + 8 * hf + g).x);
+#pragma unroll
+        for (int cb = 0; cb < DP / C::MERGE_COLS; ++cb) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < C::MERGE_COLS / 8; ++n)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+                        *reinterpret_cast<float2 *>(
+                            &merge[(warp * ROWS + 16 * mt + 8 * hf + g) * C::MERGE_LD + 8 * n + 2 * t4]) =
+                            make_float2(o[mt][C::MERGE_COLS / 8 * cb + n][2 * hf] * f[mt][hf],
+                                        o[mt][C::MERGE_COLS / 8 * cb + n][2 * hf + 1] * f[mt][hf]);
+            sync();
+            for (int x = threadIdx.x; x < ROWS * (C::MERGE_COLS / 4); x += NT) {
+                const int r = x / (C::MERGE_COLS / 4), c = 4 * (x % (C::MERGE_COLS / 4)), col = C::MERGE_COLS * cb + c;
+                if (r >= rows || col >= a.head_dim) continue;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < C::WARPS; ++w) {
+                    const float4 u = *reinterpret_cast<const float4 *>(&merge[(w * ROWS + r) * C::MERGE_LD + c]);
+                    v.x += u.x;
+                    v.y += u.y;
+                    v.z += u.z;
+                    v.w += u.w;
+                }
+                if (whole) {
+                    const float sum = row_ml(r).y, inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+                    const int gr = row0 + r;
+                    uint16_t *dst = a.y + (pc.s.q0 + gr / a.group) * a.y_token +
+                                    (pc.head * a.group + gr % a.group) * a.y_head + col;
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+                } else {
+                    *reinterpret_cast<float4 *>(a.part_o + ((long long)pc.slot() * ROWS + r) * a.head_dim + col) = v;
+                }
+            }
+            sync();
+        }
+    }
+}
+
+// Joins the parts of the item that starts in CTA blockIdx.x's range: one warp
+// per row, lane l the columns 4 l .. 4 l + 3 (and those 128 further on).
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnArgs a, int tile_rows) {
+    pdl_wait();
+    const JoinItem j = a.joins[blockIdx.x];
+    const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (j.parts == 0 || row >= j.rows) return;
+    // Part i is at slot first + 2 i - (i > 0): the beginning lies in the odd
+    // slot of its CTA, every later part in the even slot of the next ones.
+    const int first = 2 * blockIdx.x + 1;
+    auto part_row = [&](int i) { return (long long)(first + 2 * i - (i > 0 ? 1 : 0)) * tile_rows + row; };
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+    float mx = -INFINITY;
+    for (int i = lane; i < j.parts; i += 32) mx = fmaxf(mx, ml[part_row(i)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+    float sum = 0.f;
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int i0 = 0; i0 < j.parts; i0 += 8) {
+        float4 v[8][2];
+        float2 c[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k;
+            c[k] = make_float2(-INFINITY, 0.f);
+            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < j.parts) {
+                const long long r = part_row(i);
+                c[k] = ml[r];
+                const float *src = a.part_o + r * a.head_dim;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (128 * h + 4 * lane < a.head_dim)
+                        v[k][h] = *reinterpret_cast<const float4 *>(src + 128 * h + 4 * lane);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float f = corr(c[k].x, mx);
+            sum += c[k].y * f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                acc[h].x += v[k][h].x * f;
+                acc[h].y += v[k][h].y * f;
+                acc[h].z += v[k][h].z * f;
+                acc[h].w += v[k][h].w * f;
+            }
+        }
+    }
+    const int gr = j.row0 + row;
+    const long long tok = j.q0 + gr / a.group;
+    const int head = j.head * a.group + gr % a.group;
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (128 * h + 4 * lane < a.head_dim)
+            *reinterpret_cast<uint2 *>(a.y + tok * a.y_token + head * a.y_head + 128 * h + 4 * lane) =
+                make_uint2(pack2(acc[h].x * inv, acc[h].y * inv), pack2(acc[h].z * inv, acc[h].w * inv));
+    if (a.lse && lane == 0)
+        a.lse[tok * (a.kv_heads * a.group) + head] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+int launch_join(const AttnArgs &a, int grid, int tile_rows, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)((tile_rows + kJoinWarps - 1) / kJoinWarps), 1);
+    cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, attn_join_kernel, a, tile_rows) != cudaSuccess) {
+        cudaGetLastError();
+        return W4_ERR_LAUNCH;
+    }
+    return W4A16_OK;
+}
+
+template <int DP, int MT>
+int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
+    using C = RowCfg<DP, MT>;
+    static_assert(C::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
+    if (!set_smem_once(reinterpret_cast<const void *>(attn_rows_kernel<DP, MT>), (int)C::SMEM)) return W4_ERR_LAUNCH;
+    attn_rows_kernel<DP, MT><<<grid, C::THREADS, C::SMEM, stream>>>(mk, mv, a);
+    const int st = launch_status();
+    return st != W4A16_OK ? st : launch_join(a, grid, C::ROWS, stream);
+}
+
+// Workspace: the join records, then two partial tiles per CTA (statistics, outputs).
+constexpr size_t kJoinBytes = kMaxGrid * sizeof(JoinItem);
+size_t workspace_need(int rows, int head_dim) {
+    return (kJoinBytes + (size_t)2 * kMaxGrid * rows * (2 + head_dim) * 4 + 15) / 16 * 16;
+}
+
+}  // namespace
+
+// Reads and clears this translation unit's records: bit 0 an expired wait, bit 1 a bad index; -1 on error.
+int attn_status() {
+    int w = 0, b = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&w, g_wait_expired, sizeof(int)) != cudaSuccess ||
+        cudaMemcpyFromSymbol(&b, g_bad_index, sizeof(int)) != cudaSuccess)
+        return -1;
+    if (w) cudaMemcpyToSymbol(g_wait_expired, &zero, sizeof(int));
+    if (b) cudaMemcpyToSymbol(g_bad_index, &zero, sizeof(int));
+    return (w ? 1 : 0) | (b ? 2 : 0);
+}
+}  // namespace w4a16
+
+using namespace w4a16;
+
+extern "C" size_t f16_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q_len) {
+    if (kv_heads < 1 || kv_heads > kMaxHeads || q_heads < kv_heads || q_heads % kv_heads != 0 ||
+        q_heads / kv_heads > kMaxHeads || !head_dim_ok(head_dim) || max_q_len < 0)
+        return 0;
+    return workspace_need(16, head_dim);
+}
+
+extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head, uint16_t *y, int64_t y_token,
+                             int64_t y_head, float *lse, int q_heads, float scale, int causal, int window,
+                             const f16_kv_cache *cache, const f16_kv_batch *batch, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    int st = check_cache(cache);
+    if (st != W4A16_OK) return st;
+    AttnArgs a;
+    st = check_batch(batch, cache->page_size, a.b);
+    if (st != W4A16_OK) return st;
+    const int heads = cache->heads, d = cache->head_dim;
+    if (q_heads < heads || q_heads % heads != 0 || q_heads / heads > kMaxHeads || !(scale > 0.f) ||
+        !(scale < INFINITY) || (causal & ~1) != 0 || window < 0 ||
+        (long long)batch->total_q * (q_heads / heads) > 0x40000000ll)
+        return W4_ERR_SHAPE;
+    if (batch->total_q == 0) return W4A16_OK;
+    if (!q || !y) return W4_ERR_NULL;
+    if (!aligned16(q) || !aligned16(y) || !aligned16(workspace) || !stride_ok(q_token) || !stride_ok(q_head) ||
+        !stride_ok(y_token) || !stride_ok(y_head) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+        return W4_ERR_ALIGN;
+    if (!workspace || workspace_bytes < f16_attention_workspace_bytes(q_heads, heads, d, batch->max_q_len))
+        return W4_ERR_WORKSPACE;
+    if (device_cc() != 103) return W4_ERR_DEVICE;
+    const int rows = 16;
+    a.q = q;
+    a.y = y;
+    a.lse = lse;
+    a.q_token = q_token;
+    a.q_head = q_head;
+    a.y_token = y_token;
+    a.y_head = y_head;
+    a.group = q_heads / heads;
+    a.kv_heads = heads;
+    a.head_dim = d;
+    a.causal = causal;
+    a.window = window < 0x40000000 ? window : 0x40000000;
+    a.num_pages = cache->num_pages;
+    a.page_size = cache->page_size;
+    a.box_rows = cache->box_rows;
+    a.few_tiles = (long long)batch->max_q_len * a.group <= 4 * rows;
+    a.scale = scale * kLog2e;
+    uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
+    a.joins = reinterpret_cast<JoinItem *>(ws);
+    a.part_ml = reinterpret_cast<float *>(ws + kJoinBytes);
+    a.part_o = a.part_ml + (size_t)2 * kMaxGrid * rows * 2;
+    alignas(64) CUtensorMap mk, mv;
+    memcpy(&mk, cache->k_map, sizeof(mk));
+    memcpy(&mv, cache->v_map, sizeof(mv));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+    if (d <= 64) return launch_rows<64, 1>(mk, mv, a, grid, s);
+    if (d <= 128) return launch_rows<128, 1>(mk, mv, a, grid, s);
+    if (d <= 192) return launch_rows<192, 1>(mk, mv, a, grid, s);
+    return launch_rows<256, 1>(mk, mv, a, grid, s);
+}

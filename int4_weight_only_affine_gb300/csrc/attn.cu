@@ -22,6 +22,12 @@
 #include "attn.cuh"
 
 namespace w4a16 {
+
+// attn_tc.cu
+int attn_tc_launch(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream);
+int attn_tc_rows();
+int attn_tc_status();
+
 namespace {
 
 constexpr int kMaxGrid = 256;  // CTAs of a launch, >= the SMs of the GPU
@@ -436,6 +442,10 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
     return st != W4A16_OK ? st : launch_join(a, grid, C::ROWS, stream);
 }
 
+// Whether a call takes the tcgen05 kernel: more rows per sequence and
+// key/value head than one tile of the row kernel, heads of at most 128.
+bool takes_tc(int group, int head_dim, int max_q_len) { return (long long)group * max_q_len > 16 && head_dim <= 128; }
+
 // Workspace: the join records, then two partial tiles per CTA (statistics, outputs).
 constexpr size_t kJoinBytes = kMaxGrid * sizeof(JoinItem);
 size_t workspace_need(int rows, int head_dim) {
@@ -451,9 +461,11 @@ int attn_status() {
     if (cudaMemcpyFromSymbol(&w, g_wait_expired, sizeof(int)) != cudaSuccess ||
         cudaMemcpyFromSymbol(&b, g_bad_index, sizeof(int)) != cudaSuccess)
         return -1;
+    const int tc = attn_tc_status();
+    if (tc < 0) return -1;
     if (w) cudaMemcpyToSymbol(g_wait_expired, &zero, sizeof(int));
     if (b) cudaMemcpyToSymbol(g_bad_index, &zero, sizeof(int));
-    return (w ? 1 : 0) | (b ? 2 : 0);
+    return (w ? 1 : 0) | (b ? 2 : 0) | tc;
 }
 }  // namespace w4a16
 
@@ -463,7 +475,7 @@ extern "C" size_t f16_attention_workspace_bytes(int q_heads, int kv_heads, int h
     if (kv_heads < 1 || kv_heads > kMaxHeads || q_heads < kv_heads || q_heads % kv_heads != 0 ||
         q_heads / kv_heads > kMaxHeads || !head_dim_ok(head_dim) || max_q_len < 0)
         return 0;
-    return workspace_need(16, head_dim);
+    return workspace_need(takes_tc(q_heads / kv_heads, head_dim, max_q_len) ? attn_tc_rows() : 16, head_dim);
 }
 
 extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head, uint16_t *y, int64_t y_token,
@@ -488,7 +500,8 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     if (!workspace || workspace_bytes < f16_attention_workspace_bytes(q_heads, heads, d, batch->max_q_len))
         return W4_ERR_WORKSPACE;
     if (device_cc() != 103) return W4_ERR_DEVICE;
-    const int rows = 16;
+    const bool tc = takes_tc(q_heads / heads, d, batch->max_q_len);
+    const int rows = tc ? attn_tc_rows() : 16;
     a.q = q;
     a.y = y;
     a.lse = lse;
@@ -515,6 +528,10 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     memcpy(&mv, cache->v_map, sizeof(mv));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+    if (tc) {
+        st = attn_tc_launch(mk, mv, a, grid, s);
+        return st != W4A16_OK ? st : launch_join(a, grid, rows, s);
+    }
     if (d <= 64) return launch_rows<64, 1>(mk, mv, a, grid, s);
     if (d <= 128) return launch_rows<128, 1>(mk, mv, a, grid, s);
     if (d <= 192) return launch_rows<192, 1>(mk, mv, a, grid, s);

@@ -31,7 +31,7 @@ int attn_tc_status();
 namespace {
 
 constexpr int kMaxGrid = 256;  // CTAs of a launch, >= the SMs of the GPU
-constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 template <int DP, int MT>
 struct RowCfg {
@@ -57,14 +57,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// 2^(a - b) for maxima of which either may be -infinity (nothing seen yet).
-__device__ __forceinline__ float corr(float a, float b) { return a == -INFINITY ? 0.f : exp2_approx(a - b); }
-
 template <int DP, int MT>
 __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -92,6 +84,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
         }
         *abort = 0;
         a.joins[blockIdx.x].parts = 0;
+        prefetch_maps(&map_k, &map_v);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     make_plan<ROWS, KEYS, C::THREADS, 2>(a, plan_sh);  // (its barriers also publish the above)
@@ -150,7 +143,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
                 ub[mt][hf] = in ? (a.causal ? min(p + 1, pc.s.kv) : pc.s.kv) : 0;
                 lb[mt][hf] = a.window > 0 ? p - a.window + 1 : 0;
                 const uint16_t *qr = a.q + (pc.s.q0 + tok) * a.q_token +
-                                     (pc.head * a.group + r % a.group) * a.q_head;
+                                     (pc.head * (int)a.group.d + r % a.group) * a.q_head;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     const int c = 16 * k + 2 * t4;
@@ -299,8 +292,8 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
             if (whole) {
                 const int gr = row0 + r;
                 if (a.lse)
-                    a.lse[(long long)(pc.s.q0 + gr / a.group) * (a.kv_heads * a.group) + pc.head * a.group +
-                          gr % a.group] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+                    a.lse[(long long)(pc.s.q0 + gr / a.group) * (a.kv_heads * (int)a.group.d) + pc.head * (int)a.group.d +
+                          gr % a.group] = log_sum(ml.x, ml.y);
             } else {
                 reinterpret_cast<float2 *>(a.part_ml)[(long long)pc.slot() * ROWS + r] = ml;
             }
@@ -338,10 +331,10 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
                     v.w += u.w;
                 }
                 if (whole) {
-                    const float sum = row_ml(r).y, inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+                    const float inv = inverse(row_ml(r).y);
                     const int gr = row0 + r;
                     uint16_t *dst = a.y + (pc.s.q0 + gr / a.group) * a.y_token +
-                                    (pc.head * a.group + gr % a.group) * a.y_head + col;
+                                    (pc.head * (int)a.group.d + gr % a.group) * a.y_head + col;
                     *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
                 } else {
                     *reinterpret_cast<float4 *>(a.part_o + ((long long)pc.slot() * ROWS + r) * a.head_dim + col) = v;
@@ -352,84 +345,80 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
     }
 }
 
-// Joins the parts of the item that starts in CTA blockIdx.x's range: one warp
-// per row, lane l the columns 4 l .. 4 l + 3 (and those 128 further on).
+// Join of the items that the row kernel cut: block (c, r) joins row r of the
+// item that starts in the range of CTA c.  Its warps take the parts in turn,
+// lane l of each the columns 4 l .. 4 l + 3 (and those 128 further on), and
+// merge through shared memory.  A part's rows lie one after the other.
 constexpr int kJoinWarps = 8;
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnArgs a, int tile_rows) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int ROWS = 16;
+    __shared__ float4 sh_o[kJoinWarps][2][32];
+    __shared__ float2 sh_ml[kJoinWarps];
     pdl_wait();
     const JoinItem j = a.joins[blockIdx.x];
-    const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (j.parts == 0 || row >= j.rows) return;
-    // Part i is at slot first + 2 i - (i > 0): the beginning lies in the odd
-    // slot of its CTA, every later part in the even slot of the next ones.
-    const int first = 2 * blockIdx.x + 1;
-    auto part_row = [&](int i) { return (long long)(first + 2 * i - (i > 0 ? 1 : 0)) * tile_rows + row; };
+    const int row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (row >= j.rows || j.parts == 0) return;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-    float mx = -INFINITY;
-    for (int i = lane; i < j.parts; i += 32) mx = fmaxf(mx, ml[part_row(i)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-    float sum = 0.f;
+    float mx = -INFINITY, sum = 0.f;
     float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int i0 = 0; i0 < j.parts; i0 += 8) {
-        float4 v[8][2];
-        float2 c[8];
+    for (int i0 = warp; i0 < j.parts; i0 += 4 * kJoinWarps) {  // four parts' loads in flight
+        float4 v[4][2];
+        float2 c[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int i = i0 + k;
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * kJoinWarps;
             c[k] = make_float2(-INFINITY, 0.f);
             v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i < j.parts) {
-                const long long r = part_row(i);
+                const long long r = part_slot(blockIdx.x, i) * ROWS + row;
                 c[k] = ml[r];
-                const float *src = a.part_o + r * a.head_dim;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (128 * h + 4 * lane < a.head_dim)
-                        v[k][h] = *reinterpret_cast<const float4 *>(src + 128 * h + 4 * lane);
+                        v[k][h] = *reinterpret_cast<const float4 *>(a.part_o + r * a.head_dim + 128 * h + 4 * lane);
             }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float f = corr(c[k].x, mx);
-            sum += c[k].y * f;
+        for (int k = 0; k < 4; ++k) {
+            const float top = fmaxf(mx, c[k].x), f0 = corr(mx, top), f1 = corr(c[k].x, top);
+            mx = top;
+            sum = sum * f0 + c[k].y * f1;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                acc[h].x += v[k][h].x * f;
-                acc[h].y += v[k][h].y * f;
-                acc[h].z += v[k][h].z * f;
-                acc[h].w += v[k][h].w * f;
+                acc[h].x = acc[h].x * f0 + v[k][h].x * f1;
+                acc[h].y = acc[h].y * f0 + v[k][h].y * f1;
+                acc[h].z = acc[h].z * f0 + v[k][h].z * f1;
+                acc[h].w = acc[h].w * f0 + v[k][h].w * f1;
             }
         }
     }
-    const int gr = j.row0 + row;
-    const long long tok = j.q0 + gr / a.group;
-    const int head = j.head * a.group + gr % a.group;
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    sh_o[warp][0][lane] = acc[0];
+    sh_o[warp][1][lane] = acc[1];
+    if (lane == 0) sh_ml[warp] = make_float2(mx, sum);
+    __syncthreads();
+    if (warp >= 2 || 128 * warp + 4 * lane >= a.head_dim) return;
+    const int h = warp;
+    mx = -INFINITY;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (128 * h + 4 * lane < a.head_dim)
-            *reinterpret_cast<uint2 *>(a.y + tok * a.y_token + head * a.y_head + 128 * h + 4 * lane) =
-                make_uint2(pack2(acc[h].x * inv, acc[h].y * inv), pack2(acc[h].z * inv, acc[h].w * inv));
-    if (a.lse && lane == 0)
-        a.lse[tok * (a.kv_heads * a.group) + head] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
-}
-
-int launch_join(const AttnArgs &a, int grid, int tile_rows, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)((tile_rows + kJoinWarps - 1) / kJoinWarps), 1);
-    cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_join_kernel, a, tile_rows) != cudaSuccess) {
-        cudaGetLastError();
-        return W4_ERR_LAUNCH;
+    for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, sh_ml[w].x);
+    sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = corr(sh_ml[w].x, mx);
+        sum += sh_ml[w].y * f;
+        const float4 v = sh_o[w][h][lane];
+        o.x += v.x * f;
+        o.y += v.y * f;
+        o.z += v.z * f;
+        o.w += v.w * f;
     }
-    return W4A16_OK;
+    const int gr = j.row0 + row, head = j.head * (int)a.group.d + gr % a.group;
+    const long long tok = j.q0 + gr / a.group;
+    const float inv = inverse(sum);
+    *reinterpret_cast<uint2 *>(a.y + tok * a.y_token + head * a.y_head + 128 * h + 4 * lane) =
+        make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+    if (a.lse && threadIdx.x == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
 }
 
 template <int DP, int MT>
@@ -439,7 +428,7 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
     if (!set_smem_once(reinterpret_cast<const void *>(attn_rows_kernel<DP, MT>), (int)C::SMEM)) return W4_ERR_LAUNCH;
     attn_rows_kernel<DP, MT><<<grid, C::THREADS, C::SMEM, stream>>>(mk, mv, a);
     const int st = launch_status();
-    return st != W4A16_OK ? st : launch_join(a, grid, C::ROWS, stream);
+    return st != W4A16_OK ? st : launch_dependent(join_rows_kernel, dim3(grid, 16), 32 * kJoinWarps, a, stream);
 }
 
 // Whether a call takes the tcgen05 kernel: more rows per sequence and
@@ -509,15 +498,15 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     a.q_head = q_head;
     a.y_token = y_token;
     a.y_head = y_head;
-    a.group = q_heads / heads;
+    a.group = fast_div(q_heads / heads);
     a.kv_heads = heads;
     a.head_dim = d;
     a.causal = causal;
     a.window = window < 0x40000000 ? window : 0x40000000;
     a.num_pages = cache->num_pages;
-    a.page_size = cache->page_size;
+    a.page_size = fast_div(cache->page_size);
     a.box_rows = cache->box_rows;
-    a.few_tiles = (long long)batch->max_q_len * a.group <= 4 * rows;
+    a.few_tiles = (long long)batch->max_q_len * (q_heads / heads) <= 4 * rows;
     a.scale = scale * kLog2e;
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     a.joins = reinterpret_cast<JoinItem *>(ws);
@@ -528,10 +517,7 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     memcpy(&mv, cache->v_map, sizeof(mv));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
-    if (tc) {
-        st = attn_tc_launch(mk, mv, a, grid, s);
-        return st != W4A16_OK ? st : launch_join(a, grid, rows, s);
-    }
+    if (tc) return attn_tc_launch(mk, mv, a, grid, s);
     if (d <= 64) return launch_rows<64, 1>(mk, mv, a, grid, s);
     if (d <= 128) return launch_rows<128, 1>(mk, mv, a, grid, s);
     if (d <= 192) return launch_rows<192, 1>(mk, mv, a, grid, s);

@@ -14,6 +14,8 @@
 // lengths, and the split depends on nothing but the batch, so results repeat.
 #pragma once
 
+#include <math.h>
+
 #include "kv.cuh"
 
 namespace w4a16 {
@@ -24,12 +26,13 @@ struct AttnArgs {
     uint16_t *y;
     float *lse;
     long long q_token, q_head, y_token, y_head;
-    int group, kv_heads, head_dim;
+    FastDiv group, page_size;
+    int kv_heads, head_dim;
     int causal, window;
-    int num_pages, page_size, box_rows;
+    int num_pages, box_rows;
     int few_tiles;  // a sequence is expected to have few row tiles (chooses how the plan is summed)
     float scale;    // times log2(e): the softmax is taken in powers of two
-    float *part_o;  // [2 * grid][rows][head_dim]
+    float *part_o;  // [2 * grid][rows x head_dim], in the order of the kernel that writes it
     float *part_ml; // [2 * grid][rows][2]: running maximum (base-2 scaled scores) and sum
     struct JoinItem *joins;  // [grid]
 };
@@ -52,7 +55,7 @@ struct Item {
 template <int ROWS, int KEYS>
 __device__ __forceinline__ Item item_of(const AttnArgs &a, const Seq &s, int rt) {
     Item it;
-    const int rows = s.qn * a.group;
+    const int rows = s.qn * (int)a.group.d;
     it.nrt = (rows + ROWS - 1) / ROWS;
     const int r0 = rt * ROWS, r1 = min(r0 + ROWS, rows) - 1;
     const int p0 = s.kv - s.qn + r0 / a.group, p1 = s.kv - s.qn + r1 / a.group;
@@ -65,34 +68,41 @@ __device__ __forceinline__ Item item_of(const AttnArgs &a, const Seq &s, int rt)
 
 // Units of one key/value head of sequence s, summed by one thread or (WARP) by a warp.
 template <int ROWS, int KEYS, bool WARP>
-__device__ __forceinline__ long long head_units(const AttnArgs &a, const Seq &s) {
-    const int nrt = (s.qn * a.group + ROWS - 1) / ROWS;
-    long long n = 0;
+__device__ __forceinline__ uint32_t head_units(const AttnArgs &a, const Seq &s) {
+    const int nrt = (s.qn * (int)a.group.d + ROWS - 1) / ROWS;
+    uint32_t n = 0;
     for (int rt = WARP ? (int)(threadIdx.x & 31) : 0; rt < nrt; rt += WARP ? 32 : 1) n += item_of<ROWS, KEYS>(a, s, rt).nt;
-    if (WARP) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(~0u, n, o);
-    }
-    return n;
+    return WARP ? __reduce_add_sync(~0u, n) : n;
 }
 
-// Where a CTA's range begins, and how many units it has.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Where a CTA's range begins, and how many units it has.  The first `extra`
+// CTAs have per + 1 units, the others per.  (Calls of 2^31 units and more are
+// refused on the host.)
 struct Plan {
-    long long total;  // units of the whole call
-    long long first, count;
+    uint32_t total, per, extra;
+    uint32_t first, count;
     int b, head, rt, tile;  // first unit: sequence, head, row tile, key tile within the item
-    int ctas;               // CTAs that have units
 };
+
+// The CTA whose range holds a unit.
+__device__ __forceinline__ uint32_t unit_owner(const Plan &p, uint32_t unit) {
+    const uint32_t cut = p.extra * (p.per + 1);
+    return unit < cut ? unit / (p.per + 1) : p.extra + (unit - cut) / p.per;
+}
 
 struct PlanShared {
-    long long sums[32];
+    uint32_t sums[32];
     Plan plan;
 };
-
-__device__ __forceinline__ long long range_start(long long total, int c, int ctas) { return total * c / ctas; }
-__device__ __forceinline__ int range_owner(long long total, long long unit, int ctas) {
-    return (int)(((unit + 1) * ctas - 1) / total);
-}
 
 // Called by all THREADS threads of the CTA.  Workers (threads, or warps where
 // sequences have many row tiles) sum contiguous runs of sequences; a scan
@@ -100,92 +110,83 @@ __device__ __forceinline__ int range_owner(long long total, long long unit, int 
 // worker walks down to the sequence, head, row tile and key tile.
 template <int ROWS, int KEYS, int THREADS, int MIN_UNITS, bool WARP>
 __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) {
-    constexpr int W = THREADS / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int worker = WARP ? warp : (int)threadIdx.x, workers = WARP ? W : THREADS;
-    const int per = (a.b.batch + workers - 1) / workers;
-    const int b0 = min(worker * per, a.b.batch), b1 = min(b0 + per, a.b.batch);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += head_units<ROWS, KEYS, WARP>(a, load_seq(a.b, b)) * a.kv_heads;
-    long long before = 0;  // units of the workers before this one in its warp
-    long long warp_sum = mine;
+    constexpr uint32_t W = THREADS / 32;
+    const int lane = threadIdx.x & 31;
+    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t worker = WARP ? warp : threadIdx.x, workers = WARP ? W : THREADS;
+    const uint32_t batch = (uint32_t)a.b.batch, per = (batch + workers - 1) / workers;
+    const uint32_t b0 = min(worker * per, batch), b1 = min(b0 + per, batch);
+    uint32_t mine = 0, units = 0;  // units: of a head of the worker's last sequence
+    Seq s = {0, 0, 0};
+    for (uint32_t b = b0; b < b1; ++b) {
+        s = load_seq(a.b, (int)b);
+        units = head_units<ROWS, KEYS, WARP>(a, s);
+        mine += units * a.kv_heads;
+    }
+    uint32_t before = 0, warp_sum = mine;  // units of earlier workers
     if (!WARP) {
-        long long inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(~0u, inc, o);
-            if (lane >= o) inc += v;
-        }
+        const uint32_t inc = warp_scan(mine, lane);
         before = inc - mine;
         warp_sum = __shfl_sync(~0u, inc, 31);
     }
     if (lane == 0) sh.sums[warp] = warp_sum;
     __syncthreads();
-    long long total = 0;
+    uint32_t total = 0;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const long long v = sh.sums[i];
+    for (uint32_t i = 0; i < W; ++i) {
+        const uint32_t v = sh.sums[i];
         if (i < warp) before += v;
         total += v;
     }
-    int ctas = (int)gridDim.x;
-    if (total < (long long)ctas * MIN_UNITS) ctas = max((int)((total + MIN_UNITS - 1) / MIN_UNITS), 1);
-    const int c = (int)blockIdx.x;
-    const long long first = c < ctas ? range_start(total, c, ctas) : total;
-    const long long last = c < ctas ? range_start(total, c + 1, ctas) : total;
-    if (first < last && first >= before && first < before + mine) {
-        long long res = first - before;
-        int b = b0;
-        for (;; ++b) {
-            const Seq s = load_seq(a.b, b);
-            const long long n = head_units<ROWS, KEYS, WARP>(a, s);
-            if (res < n * a.kv_heads) {
-                const int head = (int)(res / n);
-                res -= head * n;
-                int rt = 0;
-                if (WARP) {  // 32 row tiles at a time
-                    const int nrt = (s.qn * a.group + ROWS - 1) / ROWS;
-                    for (;; rt += 32) {
-                        const int v = rt + lane < nrt ? item_of<ROWS, KEYS>(a, s, rt + lane).nt : 0;
-                        long long inc = v;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const long long x = __shfl_up_sync(~0u, inc, o);
-                            if (lane >= o) inc += x;
-                        }
-                        const unsigned m = __ballot_sync(~0u, inc > res);
-                        if (m) {
-                            const int k = __ffs(m) - 1;
-                            res -= __shfl_sync(~0u, inc - v, k);
-                            rt += k;
-                            break;
-                        }
-                        res -= __shfl_sync(~0u, inc, 31);
-                    }
-                } else {
-                    for (;; ++rt) {
-                        const int v = item_of<ROWS, KEYS>(a, s, rt).nt;
-                        if (res < v) break;
-                        res -= v;
-                    }
-                }
-                if (!WARP || lane == 0) {
-                    sh.plan.b = b;
-                    sh.plan.head = head;
-                    sh.plan.rt = rt;
-                    sh.plan.tile = (int)res;
-                }
-                break;
+    uint32_t ctas = gridDim.x;
+    const uint32_t c = blockIdx.x;
+    if (total < ctas * MIN_UNITS) ctas = max((total + MIN_UNITS - 1) / MIN_UNITS, 1u);
+    Plan p;
+    p.total = total;
+    p.per = total / ctas;
+    p.extra = total - p.per * ctas;
+    p.first = p.per * c + min(c, p.extra);
+    p.count = c < ctas ? p.per + (c < p.extra ? 1 : 0) : 0;
+    if (p.count > 0 && p.first >= before && p.first - before < mine) {
+        uint32_t res = p.first - before;
+        uint32_t b = b0;
+        if (b1 - b0 > 1)
+            for (;; ++b) {
+                s = load_seq(a.b, (int)b);
+                units = head_units<ROWS, KEYS, WARP>(a, s);
+                if (res < units * a.kv_heads) break;
+                res -= units * a.kv_heads;
             }
-            res -= n * a.kv_heads;
+        p.b = (int)b;
+        p.head = (int)(res / units);
+        res -= p.head * units;
+        int rt = 0;
+        if (WARP) {  // 32 row tiles at a time
+            const int nrt = (s.qn * (int)a.group.d + ROWS - 1) / ROWS;
+            for (;; rt += 32) {
+                const uint32_t v = rt + lane < nrt ? item_of<ROWS, KEYS>(a, s, rt + lane).nt : 0;
+                const uint32_t inc = warp_scan(v, lane);
+                const unsigned m = __ballot_sync(~0u, inc > res);
+                if (m) {
+                    const int k = __ffs(m) - 1;
+                    res -= __shfl_sync(~0u, inc - v, k);
+                    rt += k;
+                    break;
+                }
+                res -= __shfl_sync(~0u, inc, 31);
+            }
+        } else {
+            for (;; ++rt) {
+                const uint32_t v = item_of<ROWS, KEYS>(a, s, rt).nt;
+                if (res < v) break;
+                res -= v;
+            }
         }
+        p.rt = rt;
+        p.tile = (int)res;
+        if (!WARP || lane == 0) sh.plan = p;
     }
-    if (threadIdx.x == 0) {
-        sh.plan.total = total;
-        sh.plan.first = first;
-        sh.plan.count = last - first;
-        sh.plan.ctas = ctas;
-    }
+    if (p.count == 0 && threadIdx.x == 0) sh.plan = p;
     __syncthreads();
 }
 
@@ -201,8 +202,8 @@ __device__ __forceinline__ void make_plan(const AttnArgs &a, PlanShared &sh) {
 template <int ROWS, int KEYS>
 struct Pieces {
     const AttnArgs &a;
-    long long left;  // units not yet handed out
-    long long at;    // index of the next unit
+    uint32_t left;  // units not yet handed out
+    uint32_t at;    // index of the next unit
     int b, head, rt, tile;
     Seq s;
     // the piece
@@ -217,8 +218,8 @@ struct Pieces {
     }
 
     __device__ __forceinline__ bool next() {
-        if (left <= 0) return false;
-        while (rt * ROWS >= s.qn * a.group) {  // past the sequence's row tiles
+        if (left == 0) return false;
+        while (rt * ROWS >= s.qn * (int)a.group.d) {  // past the sequence's row tiles
             rt = 0;
             if (s.qn == 0 || ++head == a.kv_heads) {
                 head = 0;
@@ -227,7 +228,7 @@ struct Pieces {
         }
         it = item_of<ROWS, KEYS>(a, s, rt);
         tile0 = tile;
-        n = (int)min((long long)(it.nt - tile), left);
+        n = (int)min((uint32_t)(it.nt - tile), left);
         begins = tile == 0;
         ends = tile + n == it.nt;
         left -= n;
@@ -237,14 +238,20 @@ struct Pieces {
         return true;
     }
     __device__ __forceinline__ int row0() const { return (rt - 1) * ROWS; }
-    __device__ __forceinline__ int rows() const { return min(ROWS, s.qn * a.group - row0()); }
+    __device__ __forceinline__ int rows() const { return min(ROWS, s.qn * (int)a.group.d - row0()); }
     // Partial-result slot of a piece that is not a whole item.
     __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (begins ? 1 : 0); }
     // CTAs that share the item of a piece that begins but does not end it.
     __device__ __forceinline__ int parts(const Plan &p) const {
-        return range_owner(p.total, at - n + it.nt - 1, p.ctas) - (int)blockIdx.x + 1;
+        return (int)(unit_owner(p, at - n + it.nt - 1) - blockIdx.x + 1);
     }
 };
+
+// The tensor maps' descriptors, fetched ahead of their first copies.
+__device__ __forceinline__ void prefetch_maps(const CUtensorMap *k, const CUtensorMap *v) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(v) : "memory");
+}
 
 // Tensor-map coordinates of the copy of positions p .. p + box_rows - 1 (one
 // page holds them): the page, or num_pages, from which copies read zeros,
@@ -271,6 +278,45 @@ __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 2^(a - b) for maxima of which either may be -infinity (nothing seen yet).
+__device__ __forceinline__ float corr(float a, float b) { return a == -INFINITY ? 0.f : exp2_approx(a - b); }
+
+// 1 / sum, 0 for a row that saw nothing; not finite if the sum is not.
+__device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); }
+
+// Natural logarithm of sum * 2^mx.
+__device__ __forceinline__ float log_sum(float mx, float sum) {
+    return sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+}
+
+// Slot of part i of the item that starts in the range of CTA c: the beginning
+// lies in the odd slot of c, every later part in the even slot of the next ones.
+__device__ __forceinline__ long long part_slot(int c, int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); }
+
+// Launch as a programmatic dependent of the kernel before it on the stream.
+template <class K>
+int launch_dependent(K kernel, dim3 grid, int threads, const AttnArgs &a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return W4_ERR_LAUNCH;
+    }
+    return W4A16_OK;
 }
 
 }  // namespace w4a16

@@ -14,7 +14,9 @@
 //  * Warp 9: one thread issues S_t = Q_t K^T (both operands in shared memory)
 //    and O_t += P_t V (P_t from tensor memory).
 //  * Warps 0-3 and 4-7: softmax of tile 0 and 1, one thread to a row, so row
-//    maxima and sums need no exchange.  O_t is rescaled in tensor memory only
+//    maxima and sums need no exchange.  Each half of P_t is handed over as it
+//    is written, so its product with V starts while the other half's
+//    exponentials are taken.  O_t is rescaled in tensor memory only
 //    when a row's maximum has grown by more than 2^8 since the last time:
 //    until then probabilities are taken against the older maximum, which
 //    makes them at most 256 and changes nothing else (the quotient o / l does
@@ -31,17 +33,20 @@ namespace w4a16 {
 namespace {
 
 constexpr int QROWS = 256, KEYS = 128;
-constexpr int TC_THREADS = 320;
+constexpr int TC_THREADS = 384;
+// Registers a thread: 168 at launch (64512 in all); the softmax's two warp
+// groups take what the third (copies, MMA issue, two idle warps) gives up.
+constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 200, REGS_OTHER = 104;
+static_assert(2 * REGS_SOFTMAX + REGS_OTHER == 3 * REGS_LAUNCH, "register split");
 constexpr int HALF = KEYS * 128;  // bytes of 64 columns of 128 rows
 constexpr float kGrow = 8.f;      // growth of the maximum (base 2) that rescales
-constexpr float kLn2 = 0.69314718055994531f;
 
 template <int DP>
 struct TcCfg {
     static constexpr int HALVES = DP / 64;
     static constexpr int TILE = HALVES * HALF;                    // 128 rows of Q, K or V
     static constexpr int SLOTS = DP == 64 ? 8 : 5;                // ring of K and V tiles
-    static constexpr int BARS = 2 * SLOTS + 2 * 4 + 1;
+    static constexpr int BARS = 2 * SLOTS + 2 * 5 + 1;
     static constexpr size_t SMEM = 1024 + (size_t)(2 + SLOTS) * TILE + 8 * BARS + 16;
     // Tensor-memory columns.  A head of 64 leaves room for P beside S; with
     // 128, P_t lies in the columns of S_t, whose next product therefore waits
@@ -80,6 +85,19 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// mbar_wait without a call: the register split leaves no room for one.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t spin = 0; spin < kMaxSpins; ++spin) {
+        if (mbar_try(bar, parity)) return true;
+        if ((spin & 63) == 63 && ((abort && *abort) || global_ns() - t0 > kWaitNs)) break;
+    }
+    if (!abort || !*abort) atomicExch(&g_wait_expired, 1);
+    if (abort) *abort = 1;
+    return false;
+}
+
 #define R8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
 #define O8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
@@ -103,11 +121,54 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[32
                  I8(r, 24), "r"(addr)
                  : "memory");
 }
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::I8(r, 0),
+        I8(r, 8), "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
+// Two fp32 in one 64-bit register pair, and operations on both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(uint32_t a, uint32_t b) {
+    f32x2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+    return v;
+}
+__device__ __forceinline__ f32x2 pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float2 both(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return d;
+}
+
+// Scores of positions 32 C .. 32 C + 31 of a unit: those outside [lo, hi) to
+// -infinity, maxima of the others into m4.
+template <int C>
+__device__ __forceinline__ void mask_and_max(uint32_t (&s)[32], float (&m4)[4], bool masked, int lo, int hi) {
+    if (masked) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (32 * C + i < lo || 32 * C + i >= hi) s[i] = 0xFF800000u;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) m4[i / 2 % 4] = max3(m4[i / 2 % 4], s[i], s[i + 1]);
 }
 
 template <int DP>
@@ -128,9 +189,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     auto kv_empty = [&](int s) { return bar0 + 8u * (C::SLOTS + s); };
     auto q_full = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + t); };      // Q_t written
     auto s_full = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 2 + t); };  // S_t computed
-    auto p_full = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 4 + t); };  // P_t written (and S_t read, O_t rescaled)
-    auto o_done = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 6 + t); };  // O_t += P_t V done
-    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 8);
+    auto o_done = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 4 + t); };  // O_t += P_t V done
+    // A half (64 positions) of P_t written (and S_t read, O_t rescaled).
+    auto p_full = [&](int t, int h) { return bar0 + 8u * (2 * C::SLOTS + 6 + 2 * t + h); };
+    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 10);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
@@ -142,12 +204,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_full(t), 128);
             mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), 128);
+            mbar_init(p_full(t, 0), 128);
+            mbar_init(p_full(t, 1), 128);
             mbar_init(o_done(t), 1);
         }
         mbar_init(end_bar, 1);
         *abort = 0;
         a.joins[blockIdx.x].parts = 0;
+        prefetch_maps(&map_k, &map_v);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 9) {
@@ -162,106 +226,116 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const Plan plan = plan_sh.plan;
     Pieces<QROWS, KEYS> pc(a, plan);
 
-    if (warp == 8) {
-        // ---------------- copies: K and V of every unit, in turn ----------------
-        const int boxes = KEYS / a.box_rows * C::HALVES;
-        int it = 0;
-        bool ok = true;
-        while (ok && pc.next()) {
-            for (int i = 0; ok && i < 2 * pc.n; ++i) {
-                const int st = it % C::SLOTS;
-                ok = __all_sync(~0u, mbar_wait(kv_empty(st), ((it / C::SLOTS) & 1) ^ 1, abort));
-                if (!ok) break;
-                if (lane == 0) mbar_expect_tx(kv_full(st), C::TILE);
-                __syncwarp();
-                const int p0 = (pc.it.t0 + pc.tile0 + (i >> 1)) * KEYS;
-                for (int x = lane; x < boxes; x += 32) {
-                    const int half = x % C::HALVES, row = x / C::HALVES * a.box_rows, p = p0 + row;
-                    const int page = page_of(a, pc.b, p, pc.it.lo, pc.it.hi);
-                    tma_load_4d(ring + st * C::TILE + half * HALF + row * 128, i & 1 ? &map_v : &map_k, 64 * half,
-                                p % a.page_size, pc.head, page, kv_full(st));
-                }
-                ++it;
-            }
-        }
-        // Every copy has landed before the CTA may exit.
-        __syncwarp();
-        if (lane == 0)
-            for (int k = max(0, it - C::SLOTS); k < it; ++k) mbar_wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1);
-    } else if (warp == 9) {
-        // ---------------- MMA issue ----------------
-        if (lane == 0) {
-            constexpr uint32_t id_s = instr_desc(KEYS, 0), id_o = instr_desc(DP, 1);
-            int it = 0;             // ring position
-            uint32_t nq = 0;        // pieces begun
-            uint32_t steps[2] = {0, 0};  // P_t V products issued so far
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        if (warp == 8) {
+            // ---------------- copies: K and V of every unit, in turn ----------------
+            const int boxes = KEYS / a.box_rows * C::HALVES;
+            int it = 0;
             bool ok = true;
-            auto wait_slot = [&](int k) {
-                ok = ok && mbar_wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1, abort);
-                fence_after();
-            };
-            auto score = [&](int t, int k) {  // S_t = Q_t K^T
-                const uint32_t q = base + t * C::TILE, kt = ring + k % C::SLOTS * C::TILE;
-#pragma unroll
-                for (int s = 0; s < DP / 16; ++s) {
-                    const uint32_t off = (s / 4) * HALF + (s % 4) * 32;
-                    mma_ss(tmem + C::S0 + 128 * t, operand_desc(q + off, 16, 1024), operand_desc(kt + off, 16, 1024),
-                           id_s, s != 0);
-                }
-                commit(s_full(t));
-            };
-            uint32_t begun[2] = {0, 0};  // pieces of tile t
             while (ok && pc.next()) {
-                const int nt = pc.rows() > 128 ? 2 : 1;
-                ++nq;
-                for (int t = 0; t < nt; ++t) {
-                    ok = ok && mbar_wait(q_full(t), begun[t] & 1, abort);
-                    ++begun[t];
-                    // the columns of S_t, if P_t lies there: the last product of the piece before has read it
-                    if (C::P_IN_S && steps[t] > 0) ok = ok && mbar_wait(o_done(t), (steps[t] - 1) & 1, abort);
-                    if (t == 0) wait_slot(it);
+                for (int i = 0; ok && i < 2 * pc.n; ++i) {
+                    const int st = it % C::SLOTS;
+                    ok = __all_sync(~0u, wait(kv_empty(st), ((it / C::SLOTS) & 1) ^ 1, abort));
                     if (!ok) break;
-                    fence_after();
-                    score(t, it);
+                    if (lane == 0) mbar_expect_tx(kv_full(st), C::TILE);
+                    __syncwarp();
+                    const int p0 = (pc.it.t0 + pc.tile0 + (i >> 1)) * KEYS;
+                    for (int x = lane; x < boxes; x += 32) {
+                        const int half = x % C::HALVES, row = x / C::HALVES * a.box_rows, p = p0 + row;
+                        const int page = page_of(a, pc.b, p, pc.it.lo, pc.it.hi);
+                        tma_load_4d(ring + st * C::TILE + half * HALF + row * 128, i & 1 ? &map_v : &map_k, 64 * half,
+                                    p % a.page_size, pc.head, page, kv_full(st));
+                    }
+                    ++it;
                 }
-                if (!ok) break;
-                commit(kv_empty(it % C::SLOTS));
-                for (int j = 0; ok && j < pc.n; ++j) {
-                    const int kv = it + 1, kn = it + 2;
-                    const bool more = j + 1 < pc.n;
+            }
+            // Every copy has landed before the CTA may exit.
+            __syncwarp();
+            if (lane == 0)
+                for (int k = max(0, it - C::SLOTS); k < it; ++k) wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1, nullptr);
+        } else if (warp == 9) {
+            // ---------------- MMA issue ----------------
+            if (lane == 0) {
+                constexpr uint32_t id_s = instr_desc(KEYS, 0), id_o = instr_desc(DP, 1);
+                int it = 0;             // ring position
+                uint32_t steps[2] = {0, 0};  // P_t V products issued so far
+                bool ok = true;
+                auto wait_slot = [&](int k) {
+                    ok = ok && wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1, abort);
+                    fence_after();
+                };
+                auto score = [&](int t, int k) {  // S_t = Q_t K^T
+                    const uint32_t q = base + t * C::TILE, kt = ring + k % C::SLOTS * C::TILE;
+#pragma unroll
+                    for (int s = 0; s < DP / 16; ++s) {
+                        const uint32_t off = (s / 4) * HALF + (s % 4) * 32;
+                        mma_ss(tmem + C::S0 + 128 * t, operand_desc(q + off, 16, 1024), operand_desc(kt + off, 16, 1024),
+                               id_s, s != 0);
+                    }
+                    commit(s_full(t));
+                };
+                uint32_t begun[2] = {0, 0};  // pieces of tile t
+                while (ok && pc.next()) {
+                    const int nt = pc.rows() > 128 ? 2 : 1;
                     for (int t = 0; t < nt; ++t) {
-                        if (t == 0) wait_slot(kv);
-                        ok = ok && mbar_wait(p_full(t), steps[t] & 1, abort);
+                        ok = ok && wait(q_full(t), begun[t] & 1, abort);
+                        ++begun[t];
+                        // the columns of S_t, if P_t lies there: the last product of the piece before has read it
+                        if (C::P_IN_S && steps[t] > 0) ok = ok && wait(o_done(t), (steps[t] - 1) & 1, abort);
+                        if (t == 0) wait_slot(it);
                         if (!ok) break;
                         fence_after();
-                        const uint32_t vt = ring + kv % C::SLOTS * C::TILE;
-#pragma unroll
-                        for (int s = 0; s < KEYS / 16; ++s)
-                            mma_ts(tmem + C::O0 + DP * t, tmem + C::P0 + C::P_STEP * t + 8 * s,
-                                   operand_desc(vt + s * 2048, HALF, 1024), id_o, (j | s) != 0);
-                        commit(o_done(t));
-                        if (t == nt - 1) commit(kv_empty(kv % C::SLOTS));
-                        ++steps[t];
-                        if (more) {
-                            if (t == 0) wait_slot(kn);
-                            if (C::P_IN_S) ok = ok && mbar_wait(o_done(t), (steps[t] - 1) & 1, abort);
-                            if (!ok) break;
-                            score(t, kn);
-                            if (t == nt - 1) commit(kv_empty(kn % C::SLOTS));
-                        }
+                        score(t, it);
                     }
-                    it += 2;
+                    if (!ok) break;
+                    commit(kv_empty(it % C::SLOTS));
+                    for (int j = 0; ok && j < pc.n; ++j) {
+                        const int kv = it + 1, kn = it + 2;
+                        const bool more = j + 1 < pc.n;
+                        for (int t = 0; t < nt; ++t) {
+                            if (t == 0) wait_slot(kv);
+                            const uint32_t vt = ring + kv % C::SLOTS * C::TILE;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                ok = ok && wait(p_full(t, h), steps[t] & 1, abort);
+                                if (!ok) break;
+                                fence_after();
+#pragma unroll
+                                for (int s = 4 * h; s < 4 * h + 4; ++s)
+                                    mma_ts(tmem + C::O0 + DP * t, tmem + C::P0 + C::P_STEP * t + 8 * s,
+                                           operand_desc(vt + s * 2048, HALF, 1024), id_o, (j | s) != 0);
+                            }
+                            if (!ok) break;
+                            commit(o_done(t));
+                            if (t == nt - 1) commit(kv_empty(kv % C::SLOTS));
+                            ++steps[t];
+                            if (more) {
+                                if (t == 0) wait_slot(kn);
+                                if (C::P_IN_S) ok = ok && wait(o_done(t), (steps[t] - 1) & 1, abort);
+                                if (!ok) break;
+                                score(t, kn);
+                                if (t == nt - 1) commit(kv_empty(kn % C::SLOTS));
+                            }
+                        }
+                        it += 2;
+                    }
                 }
+                commit(end_bar);  // every product is done before the CTA may exit
+                wait(end_bar, 0, nullptr);
             }
-            commit(end_bar);  // every product is done before the CTA may exit
-            mbar_wait(end_bar, 0);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         // ---------------- softmax: warps 4 t .. 4 t + 3 for tile t, one thread to a row ----------------
         const int t = warp >> 2, quad = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t s_at = lanes + C::S0 + 128 * t, p_at = lanes + C::P0 + C::P_STEP * t, o_at = lanes + C::O0 + DP * t;
+        // Row rl of this warp's 32 rows of Q_t, 16-byte chunk ch (also the way out of y's rows).
+        const uint32_t my_rows = base + t * C::TILE + 32 * quad * 128;
+        auto stage_at = [&](int rl, int ch) { return my_rows + (ch / 8) * HALF + rl * 128 + (((ch ^ rl) & 7) << 4); };
+        const f32x2 scale2 = pair(a.scale, a.scale);
         uint32_t steps = 0;
         int it = 0;
         while (pc.next()) {
@@ -269,23 +343,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             it += 2 * pc.n;
             const int rows = pc.rows(), row0 = pc.row0();
             if (128 * t >= rows) continue;
-            // Q_t: the warp's 32 rows, 16 bytes a lane, swizzled.
-            for (int x = lane; x < 32 * (DP / 8); x += 32) {
-                const int rl = 32 * quad + x / (DP / 8), ch = x % (DP / 8), r = 128 * t + rl, gr = row0 + r;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows && 8 * ch < a.head_dim)
-                    v = *reinterpret_cast<const uint4 *>(a.q + (pc.s.q0 + gr / a.group) * a.q_token +
-                                                         (pc.head * a.group + gr % a.group) * a.q_head + 8 * ch);
-                const uint32_t at = base + t * C::TILE + (ch / 8) * HALF + rl * 128 + (((ch ^ rl) & 7) << 4);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                             : "memory");
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(q_full(t));
-
             const int r = 128 * t + 32 * quad + lane;  // this thread's row of the item
             const bool in = r < rows;
             const int gr = row0 + r;
+            const long long tok = pc.s.q0 + gr / a.group;
+            const int head = pc.head * (int)a.group.d + gr % a.group;
+            // Q_t: the warp's 32 rows, 16 bytes a lane, swizzled, all in flight together.
+            const long long q_row = in ? tok * a.q_token + head * a.q_head : -1;
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) {
+                const int x = 32 * i + lane, rl = x / (DP / 8), ch = x % (DP / 8);
+                const long long at = __shfl_sync(~0u, q_row, rl);
+                const bool has = at >= 0 && 8 * ch < a.head_dim;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(stage_at(rl, ch)),
+                             "l"(has ? a.q + at + 8 * ch : a.q), "r"(has ? 16 : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            mbar_arrive(q_full(t));
+
             const int p = pc.s.kv - pc.s.qn + gr / a.group;
             const int ub = in ? (a.causal ? min(p + 1, pc.s.kv) : pc.s.kv) : 0;
             const int lb = a.window > 0 ? p - a.window + 1 : 0;
@@ -298,34 +375,33 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             float ref = -INFINITY, sum = 0.f;  // reference maximum (base-2 scaled scores) and sum
             for (int j = 0; j < pc.n; ++j, ++steps) {
                 const int j0 = (pc.it.t0 + pc.tile0 + j) * KEYS;
-                mbar_wait(s_full(t), steps & 1, abort);
+                wait(s_full(t), steps & 1, abort);
                 fence_after();
                 uint32_t sr[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_load(s_at + 32 * c, sr[c]);
+                tmem_load(s_at, sr[0]);
+                tmem_load(s_at + 32, sr[1]);
                 tmem_load_wait();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_loaded(sr[c]);
-                if (j0 + KEYS > all_ub || j0 < all_lb) {
-                    const int lo = lb - j0, hi = ub - j0;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * c + i < lo || 32 * c + i >= hi) sr[c][i] = 0xFF800000u;  // -infinity
-                }
+                tmem_load(s_at + 64, sr[2]);
+                tmem_load(s_at + 96, sr[3]);
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(sr[c][i]));
+                const bool masked = j0 + KEYS > all_ub || j0 < all_lb;
+                const int lo = lb - j0, hi = ub - j0;
+                tmem_loaded(sr[0]);
+                tmem_loaded(sr[1]);
+                mask_and_max<0>(sr[0], m4, masked, lo, hi);
+                mask_and_max<1>(sr[1], m4, masked, lo, hi);
+                tmem_load_wait();
+                tmem_loaded(sr[2]);
+                tmem_loaded(sr[3]);
+                mask_and_max<2>(sr[2], m4, masked, lo, hi);
+                mask_and_max<3>(sr[3], m4, masked, lo, hi);
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale;
                 const bool grow = mx > ref + kGrow || (ref == -INFINITY && mx > ref);
                 if (__any_sync(~0u, grow)) {
                     const float nr = grow ? mx : ref;
                     const float c = ref == -INFINITY ? 0.f : exp2_approx(ref - nr);
                     if (j > 0) {
-                        mbar_wait(o_done(t), (steps - 1) & 1, abort);
+                        wait(o_done(t), (steps - 1) & 1, abort);
                         fence_after();
 #pragma unroll 1
                         for (int cb = 0; cb < DP / 32; ++cb) {
@@ -345,25 +421,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         ref = nr;
                     }
                 }
-                const float base2 = ref == -INFINITY ? 0.f : ref;
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pr[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float e0 = exp2_approx(fmaf(__uint_as_float(sr[2 * h + i / 16][2 * i % 32]), a.scale, -base2));
-                        const float e1 = exp2_approx(fmaf(__uint_as_float(sr[2 * h + i / 16][2 * i % 32 + 1]), a.scale, -base2));
-                        s4[i & 3] += e0 + e1;
-                        pr[i] = pack2(e0, e1);
-                    }
-                    tmem_store(p_at + 32 * h, pr);
-                }
-                sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 if (t == 0 && (j0 < pc.it.lo || j0 + KEYS > pc.it.hi)) {
                     // Rows of V that the item does not see: one to a thread.
                     const int k = first_slot + 2 * j + 1, row = 32 * quad + lane;
-                    mbar_wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1, abort);
+                    wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1, abort);
                     if (j0 + row < pc.it.lo || j0 + row >= pc.it.hi) {
 #pragma unroll
                         for (int x = 0; x < DP / 8; ++x)
@@ -374,52 +435,81 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                tmem_store_wait();
-                fence_before();
-                mbar_arrive(p_full(t));
+                const float minus = ref == -INFINITY ? 0.f : -ref;
+                const f32x2 minus2 = pair(minus, minus);
+                f32x2 s2[2] = {0, 0};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pr[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float2 e = both(fma2(pair(sr[c][2 * i], sr[c][2 * i + 1]), scale2, minus2));
+                        e.x = exp2_approx(e.x);
+                        e.y = exp2_approx(e.y);
+                        s2[i & 1] = add2(s2[i & 1], pair(e.x, e.y));
+                        pr[i] = pack2(e.x, e.y);
+                    }
+                    tmem_store16(p_at + 16 * c, pr);
+                    if (c & 1) {
+                        tmem_store_wait();
+                        fence_before();
+                        mbar_arrive(p_full(t, c >> 1));
+                    }
+                }
+                const float2 s4 = both(add2(s2[0], s2[1]));
+                sum += s4.x + s4.y;
             }
 
             // ---------------- the piece's rows ----------------
-            mbar_wait(o_done(t), (steps - 1) & 1, abort);
+            wait(o_done(t), (steps - 1) & 1, abort);
             fence_after();
             const bool whole = pc.begins && pc.ends;
-            const long long tok = pc.s.q0 + gr / a.group;
-            const int head = pc.head * a.group + gr % a.group;
-            const long long prow = (long long)pc.slot() * QROWS + r;
-            const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
             if (in) {
                 if (!whole)
-                    reinterpret_cast<float2 *>(a.part_ml)[prow] = make_float2(ref, sum);
+                    reinterpret_cast<float2 *>(a.part_ml)[(long long)pc.slot() * QROWS + r] = make_float2(ref, sum);
                 else if (a.lse)
-                    a.lse[tok * (a.kv_heads * a.group) + head] = sum > 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+                    a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(ref, sum);
             }
             if (threadIdx.x == 0 && pc.begins && !pc.ends)
                 a.joins[blockIdx.x] = JoinItem{pc.parts(plan), pc.s.q0, pc.head, row0, rows};
+            const float inv = inverse(sum);
+            float4 *part = reinterpret_cast<float4 *>(a.part_o) + (long long)pc.slot() * QROWS * (a.head_dim / 4) + r;
 #pragma unroll 1
             for (int cb = 0; cb < DP / 32; ++cb) {
                 uint32_t o[32];
                 tmem_load(o_at + 32 * cb, o);
                 tmem_load_wait();
                 tmem_loaded(o);
-                if (!in) continue;
-                if (whole) {
-                    uint16_t *dst = a.y + tok * a.y_token + head * a.y_head + 32 * cb;
+                if (whole) {  // through this warp's rows of Q_t (its products are done)
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        if (32 * cb + i < a.head_dim) {
-                            uint32_t h[4];
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t h[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                h[e] = pack2(__uint_as_float(o[i + 2 * e]) * inv, __uint_as_float(o[i + 2 * e + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(h[0], h[1], h[2], h[3]);
-                        }
-                } else {
-                    float *dst = a.part_o + prow * a.head_dim + 32 * cb;
+                        for (int e = 0; e < 4; ++e)
+                            h[e] = pack2(__uint_as_float(o[i + 2 * e]) * inv, __uint_as_float(o[i + 2 * e + 1]) * inv);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage_at(lane, 4 * cb + i / 8)),
+                                     "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                                     : "memory");
+                    }
+                } else if (in) {  // 4 columns of all rows lie together
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         if (32 * cb + i < a.head_dim)
-                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            part[(8 * cb + i / 4) * QROWS] =
+                                make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                            __uint_as_float(o[i + 3]));
                 }
+            }
+            if (whole) {
+                __syncwarp();
+                const long long y_row = in ? tok * a.y_token + head * a.y_head : -1;
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) {
+                    const int x = 32 * i + lane, rl = x / (DP / 8), ch = x % (DP / 8);
+                    const long long at = __shfl_sync(~0u, y_row, rl);
+                    if (at >= 0 && 8 * ch < a.head_dim) *reinterpret_cast<uint4 *>(a.y + at + 8 * ch) = lds128(stage_at(rl, ch));
+                }
+                __syncwarp();
             }
             fence_before();  // the reads above, before the next piece's first product writes O_t
         }
@@ -433,12 +523,100 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     }
 }
 
+// Join of the items that attn_tc_kernel cut: block (c, n) joins rows 32 n ..
+// 32 n + 31 of the item that starts in the range of CTA c, a lane to a row, a
+// warp to every 8th group of 4 columns.
+constexpr int JOIN_WARPS = 8;
+__global__ void __launch_bounds__(32 * JOIN_WARPS) join_tc_kernel(const __grid_constant__ AttnArgs a) {
+    __shared__ __align__(16) uint16_t out[32][128 + 8];
+    pdl_wait();
+    const JoinItem j = a.joins[blockIdx.x];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = 32 * blockIdx.y + lane;
+    if (32 * (int)blockIdx.y >= j.rows || j.parts == 0) return;
+    const int groups = a.head_dim / 4;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + r;
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o) + r;
+    float mx = -INFINITY, sum = 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < j.rows) {
+        for (int i0 = 0; i0 < j.parts; i0 += 4) {  // four parts' loads in flight
+            float4 v[4][4];
+            float2 c[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                c[k] = make_float2(-INFINITY, 0.f);
+                if (i0 + k < j.parts) {
+                    const long long slot = part_slot(blockIdx.x, i0 + k);
+                    c[k] = ml[slot * QROWS];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        if (warp + JOIN_WARPS * g < groups) v[k][g] = po[(slot * groups + warp + JOIN_WARPS * g) * QROWS];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (i0 + k >= j.parts) break;
+                const float top = fmaxf(mx, c[k].x), f0 = corr(mx, top), f1 = corr(c[k].x, top);
+                mx = top;
+                sum = sum * f0 + c[k].y * f1;
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    if (warp + JOIN_WARPS * g < groups) {
+                        acc[g].x = acc[g].x * f0 + v[k][g].x * f1;
+                        acc[g].y = acc[g].y * f0 + v[k][g].y * f1;
+                        acc[g].z = acc[g].z * f0 + v[k][g].z * f1;
+                        acc[g].w = acc[g].w * f0 + v[k][g].w * f1;
+                    }
+            }
+        }
+        const float inv = inverse(sum);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            if (warp + JOIN_WARPS * g < groups)
+                *reinterpret_cast<uint2 *>(&out[lane][4 * (warp + JOIN_WARPS * g)]) =
+                    make_uint2(pack2(acc[g].x * inv, acc[g].y * inv), pack2(acc[g].z * inv, acc[g].w * inv));
+        if (a.lse && warp == 0) {
+            const int gr = j.row0 + r;
+            a.lse[(long long)(j.q0 + gr / a.group) * (a.kv_heads * (int)a.group.d) + j.head * (int)a.group.d +
+                  gr % a.group] = log_sum(mx, sum);
+        }
+    }
+    __syncthreads();
+    const int chunks = a.head_dim / 8;
+    for (int x = threadIdx.x; x < 32 * chunks; x += 32 * JOIN_WARPS) {
+        const int rl = x / chunks, ch = x % chunks, gr = j.row0 + 32 * blockIdx.y + rl;
+        if (32 * (int)blockIdx.y + rl < j.rows)
+            *reinterpret_cast<uint4 *>(a.y + (j.q0 + gr / a.group) * a.y_token +
+                                       (j.head * (int)a.group.d + gr % a.group) * a.y_head + 8 * ch) =
+                *reinterpret_cast<const uint4 *>(&out[rl][8 * ch]);
+    }
+}
+
+// The register split needs what the compiler gave each thread at launch: a
+// kernel launched with fewer would wait for registers that never come.
+template <int DP>
+bool regs_ok() {
+    static const bool ok = [] {
+        cudaFuncAttributes f;
+        if (cudaFuncGetAttributes(&f, attn_tc_kernel<DP>) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        return f.numRegs == REGS_LAUNCH;
+    }();
+    return ok;
+}
+
 template <int DP>
 int launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
     static_assert(TcCfg<DP>::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
+    if (!regs_ok<DP>()) return W4_ERR_DEVICE;
     if (!set_smem_once(reinterpret_cast<const void *>(attn_tc_kernel<DP>), (int)TcCfg<DP>::SMEM)) return W4_ERR_LAUNCH;
     attn_tc_kernel<DP><<<grid, TC_THREADS, TcCfg<DP>::SMEM, stream>>>(mk, mv, a);
-    return launch_status();
+    const int st = launch_status();
+    return st != W4A16_OK ? st : launch_dependent(join_tc_kernel, dim3(grid, QROWS / 32), 32 * JOIN_WARPS, a, stream);
 }
 
 }  // namespace

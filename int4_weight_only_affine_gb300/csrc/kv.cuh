@@ -13,6 +13,22 @@ static __device__ int g_bad_index = 0;
 
 constexpr int kMaxHeads = 1024;
 
+// Division of 0 <= n < 2^31 by a d fixed on the host: with l = ceil(log2 d)
+// and m = ceil(2^(31 + l) / d) < 2^32, floor(n m / 2^(31 + l)) is floor(n / d),
+// since m exceeds 2^(31 + l) / d by less than 1 <= 2^l / d and n < 2^31.
+struct FastDiv {
+    uint32_t d, m, shift;
+};
+inline FastDiv fast_div(int d) {
+    uint32_t l = 0;
+    while ((1ull << l) < (uint64_t)d) ++l;
+    return FastDiv{(uint32_t)d, (uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+__device__ __forceinline__ int operator/(int n, const FastDiv &f) {
+    return (int)(((uint64_t)(uint32_t)n * f.m) >> f.shift);
+}
+__device__ __forceinline__ int operator%(int n, const FastDiv &f) { return n - n / f * (int)f.d; }
+
 struct KvBatch {
     const int32_t *table, *q_offsets, *kv_lens;
     int batch, max_pages, table_stride, total_q;

@@ -369,7 +369,8 @@ typedef struct {
     int64_t v_page, v_token, v_head;
     int32_t num_pages, page_size, heads, head_dim;
     int32_t box_rows, reserved;
-    uint64_t k_map[16], v_map[16];
+    uint64_t k_map[16], v_map[16];   /* copies of box_rows tokens x 64 elements */
+    uint64_t k_wide[16], v_wide[16]; /* of whole heads (head_dim a multiple of 64 above 64) */
 } f16_kv_cache;
 
 /*

@@ -36,11 +36,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 template <int DP, int MT>
 struct RowCfg {
     static constexpr int ROWS = 16 * MT;
-    static constexpr int KEYS = DP <= 128 ? 128 : 64;
+    static constexpr int KEYS = kv_tile(DP);
     static constexpr int WARPS = KEYS / 16;             // consumers
     static constexpr int THREADS = 32 * (WARPS + 1);
-    static constexpr int HALF = KEYS * 128;             // bytes of 64 columns of a tile
-    static constexpr int TILE = HALF * (DP / 64);       // K or V
+    static constexpr int TILE = KEYS * 128 * (DP / 64); // bytes of K or V
     static constexpr int STAGES = 192 * 1024 / (2 * TILE);
     static constexpr int MERGE_COLS = 32;               // columns merged at a time
     static constexpr int MERGE_LD = MERGE_COLS + 4;     // floats per row of the merge buffer
@@ -57,7 +56,8 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
-template <int DP, int MT>
+// WIDE: the tensor maps copy whole heads.
+template <int DP, int MT, bool WIDE>
 __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const __grid_constant__ AttnArgs a) {
@@ -94,38 +94,56 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
     if (warp == C::WARPS) {
         // ---------------- producer ----------------
         constexpr int HALVES = DP / 64;
-        const int boxes = KEYS / a.box_rows * HALVES * 2;
+        const int boxes = KEYS / a.box_rows;  // at most 16
         int it = 0;
         bool ok = true;
-        while (ok && pc.next()) {
-            for (int i = 0; i < pc.n; ++i, ++it) {
+        while (ok && uniform(pc.next())) {
+            const int n = uniform(pc.n), head = uniform(pc.head);
+            int p0 = uniform(pc.it.t0 + pc.tile0) * KEYS;
+            for (int i = 0; i < n; ++i, ++it, p0 += KEYS) {
                 const int st = it % C::STAGES;
-                ok = mbar_wait(empty_bar(st), ((it / C::STAGES) & 1) ^ 1, abort);
-                if (!__all_sync(~0u, ok)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_expect_tx(full_bar(st), 2 * C::TILE);
-                __syncwarp();
-                const int p0 = (pc.it.t0 + pc.tile0 + i) * KEYS;
-                const uint32_t kdst = base + st * 2 * C::TILE;
-                for (int x = lane; x < boxes; x += 32) {
-                    const int half = (x >> 1) % HALVES, row = (x >> 1) / HALVES * a.box_rows;
-                    const int p = p0 + row;
-                    const int page = page_of(a, pc.b, p, pc.it.lo, pc.it.hi);
-                    const uint32_t dst = kdst + (x & 1) * C::TILE + half * C::HALF + row * 128;
-                    tma_load_4d(dst, x & 1 ? &map_v : &map_k, 64 * half, p % a.page_size, pc.head, page, full_bar(st));
+                const int page = lane < boxes ? page_of(a, pc.b, p0 + lane * a.box_rows, pc.it.lo, pc.it.hi) : 0;
+                ok = __all_sync(~0u, mbar_wait(empty_bar(st), ((it / C::STAGES) & 1) ^ 1, abort));
+                if (!ok) break;
+                const uint32_t kdst = base + st * 2 * C::TILE, vdst = kdst + C::TILE, bar = full_bar(st);
+                if (elect_one()) mbar_expect_tx(bar, 2 * C::TILE);
+                for (int x = 0; x < boxes; ++x) {
+                    const int pg = __shfl_sync(~0u, page, x), row = x * a.box_rows, at = (p0 + row) % a.page_size;
+                    if (!elect_one()) continue;
+                    if (WIDE) {
+                        tma_load_5d(kdst + row * HALVES * 128, &map_k, 0, at, 0, head, pg, bar);
+                        tma_load_5d(vdst + row * HALVES * 128, &map_v, 0, at, 0, head, pg, bar);
+                    } else {
+#pragma unroll
+                        for (int half = 0; half < HALVES; ++half) {
+                            const uint32_t off = row * HALVES * 128 + half * a.box_rows * 128;
+                            tma_load_4d(kdst + off, &map_k, 64 * half, at, head, pg, bar);
+                            tma_load_4d(vdst + off, &map_v, 64 * half, at, head, pg, bar);
+                        }
+                    }
                 }
             }
         }
         // Every copy has landed before the CTA may exit.
-        __syncwarp();
-        if (lane == 0)
-            for (int k = max(0, it - C::STAGES); k < it; ++k) mbar_wait(full_bar(k % C::STAGES), (k / C::STAGES) & 1);
+        for (int k = max(0, it - C::STAGES); k < it; ++k) mbar_wait(full_bar(k % C::STAGES), (k / C::STAGES) & 1);
         return;
     }
 
     // ---------------- consumers ----------------
+    // A tile lies copy by copy, each as columns of 64 of its box_rows rows.
+    // 8-row groups start on 1024 bytes, so a row's swizzle is that of row % 8.
+    const uint32_t half_bytes = a.box_rows * 128;
+    auto row_at = [&](int row) {
+        const int box = row & ~(a.box_rows - 1);
+        return (uint32_t)(box * (DP / 64) * 128 + (row - box) * 128);
+    };
+    // Lane l addresses row (l & 7) + 8 (l >> 4) of its warp's 16 positions of K, 8-column chunk (l >> 3) & 1: registers
+    // 0, 1 of a load are the two chunks of positions 0-7, registers 2, 3 of positions 8-15.
+    const int krow = (lane & 7) + 8 * (lane >> 4), kch = (lane >> 3) & 1;
+    const uint32_t k_off = row_at(16 * warp + krow);
+    // And position l & 15, 8-column chunk l >> 4 of V.
+    const int vrow = lane & 15, vch = lane >> 4;
+    const uint32_t v_off = row_at(16 * warp + vrow);
     const int g = lane >> 2, t4 = lane & 3;
     int it = 0;
     while (pc.next()) {
@@ -179,7 +197,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
                 for (int x = lane; x < 16 * (DP / 8); x += 32) {
                     const int row = x / (DP / 8), ch = x % (DP / 8);
                     if (j0 + row < pc.it.lo || j0 + row >= pc.it.hi) {
-                        const uint32_t at = vb + (ch / 8) * C::HALF + (16 * warp + row) * 128 + (((ch ^ row) & 7) << 4);
+                        const uint32_t at = vb + row_at(16 * warp + row) + (ch / 8) * half_bytes + (((ch ^ row) & 7) << 4);
                         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
                     }
                 }
@@ -193,14 +211,11 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
-                // Lane l addresses row (l & 7) + 8 (l >> 4) of the 16 positions, 8-column chunk (l >> 3) & 1:
-                // registers 0, 1 are the two chunks of positions 0-7, registers 2, 3 of positions 8-15.
-                const int krow = (lane & 7) + 8 * (lane >> 4), kch = (lane >> 3) & 1;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     uint32_t kf[4];
                     const int ch = 2 * k + kch;
-                    ldsm4(kf, kb + (ch / 8) * C::HALF + (16 * warp + krow) * 128 + (((ch ^ krow) & 7) << 4));
+                    ldsm4(kf, kb + k_off + (ch / 8) * half_bytes + (((ch ^ krow) & 7) << 4));
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         mma_16816(s[mt][0], qf[mt][k][0], qf[mt][k][1], qf[mt][k][2], qf[mt][k][3], kf[0], kf[1]);
@@ -245,13 +260,11 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
                         pf4[mt][2 + hf] = pack2(p[2], p[3]);
                     }
                 }
-                // Lane l addresses position l & 15 of the 16, 8-column chunk l >> 4.
-                const int vrow = lane & 15, vch = lane >> 4;
 #pragma unroll
                 for (int n = 0; n < DP / 16; ++n) {
                     uint32_t vf[4];
                     const int ch = 2 * n + vch;
-                    ldsm4t(vf, vb + (ch / 8) * C::HALF + (16 * warp + vrow) * 128 + (((ch ^ vrow) & 7) << 4));
+                    ldsm4t(vf, vb + v_off + (ch / 8) * half_bytes + (((ch ^ vrow) & 7) << 4));
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         mma_16816(o[mt][2 * n], pf4[mt][0], pf4[mt][1], pf4[mt][2], pf4[mt][3], vf[0], vf[1]);
@@ -421,12 +434,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
     if (a.lse && threadIdx.x == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
 }
 
-template <int DP, int MT>
+template <int DP, int MT, bool WIDE>
 int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
     using C = RowCfg<DP, MT>;
     static_assert(C::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
-    if (!set_smem_once(reinterpret_cast<const void *>(attn_rows_kernel<DP, MT>), (int)C::SMEM)) return W4_ERR_LAUNCH;
-    attn_rows_kernel<DP, MT><<<grid, C::THREADS, C::SMEM, stream>>>(mk, mv, a);
+    if (!set_smem_once(reinterpret_cast<const void *>(attn_rows_kernel<DP, MT, WIDE>), (int)C::SMEM)) return W4_ERR_LAUNCH;
+    attn_rows_kernel<DP, MT, WIDE><<<grid, C::THREADS, C::SMEM, stream>>>(mk, mv, a);
     const int st = launch_status();
     return st != W4A16_OK ? st : launch_dependent(join_rows_kernel, dim3(grid, 16), 32 * kJoinWarps, a, stream);
 }
@@ -512,14 +525,18 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     a.joins = reinterpret_cast<JoinItem *>(ws);
     a.part_ml = reinterpret_cast<float *>(ws + kJoinBytes);
     a.part_o = a.part_ml + (size_t)2 * kMaxGrid * rows * 2;
+    const bool wide = !tc && d % 64 == 0 && d > 64;
     alignas(64) CUtensorMap mk, mv;
-    memcpy(&mk, cache->k_map, sizeof(mk));
-    memcpy(&mv, cache->v_map, sizeof(mv));
+    memcpy(&mk, wide ? cache->k_wide : cache->k_map, sizeof(mk));
+    memcpy(&mv, wide ? cache->v_wide : cache->v_map, sizeof(mv));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
     if (tc) return attn_tc_launch(mk, mv, a, grid, s);
-    if (d <= 64) return launch_rows<64, 1>(mk, mv, a, grid, s);
-    if (d <= 128) return launch_rows<128, 1>(mk, mv, a, grid, s);
-    if (d <= 192) return launch_rows<192, 1>(mk, mv, a, grid, s);
-    return launch_rows<256, 1>(mk, mv, a, grid, s);
+    if (d <= 64) return launch_rows<64, 1, false>(mk, mv, a, grid, s);
+    if (d == 128) return launch_rows<128, 1, true>(mk, mv, a, grid, s);
+    if (d < 128) return launch_rows<128, 1, false>(mk, mv, a, grid, s);
+    if (d == 192) return launch_rows<192, 1, true>(mk, mv, a, grid, s);
+    if (d < 192) return launch_rows<192, 1, false>(mk, mv, a, grid, s);
+    if (d == 256) return launch_rows<256, 1, true>(mk, mv, a, grid, s);
+    return launch_rows<256, 1, false>(mk, mv, a, grid, s);
 }

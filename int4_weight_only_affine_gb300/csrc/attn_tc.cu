@@ -10,9 +10,10 @@
 //    probabilities P_t (binary16) and output sums O_t (fp32) live in tensor
 //    memory, one row to a lane.  While the softmax of one tile runs, the
 //    tensor cores work on the other.
-//  * Warp 8: copies K and V tiles page by page (tensor copies) into a ring.
-//  * Warp 9: one thread issues S_t = Q_t K^T (both operands in shared memory)
-//    and O_t += P_t V (P_t from tensor memory).
+//  * Warps 8 and 11: copy K and V tiles page by page (tensor copies) into a ring.
+//  * Warps 9 and 10: one thread for each tile issues S_t = Q_t K^T (both
+//    operands in shared memory) and O_t += P_t V (P_t from tensor memory).
+//    (One thread for both tiles was itself the bound: 3850 cycles a unit.)
 //  * Warps 0-3 and 4-7: softmax of tile 0 and 1, one thread to a row, so row
 //    maxima and sums need no exchange.  Each half of P_t is handed over as it
 //    is written, so its product with V starts while the other half's
@@ -35,8 +36,8 @@ namespace {
 constexpr int QROWS = 256, KEYS = 128;
 constexpr int TC_THREADS = 384;
 // Registers a thread: 168 at launch (64512 in all); the softmax's two warp
-// groups take what the third (copies, MMA issue, two idle warps) gives up.
-constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 200, REGS_OTHER = 104;
+// groups take what the third (copies, MMA issue) gives up.
+constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 208, REGS_OTHER = 88;
 static_assert(2 * REGS_SOFTMAX + REGS_OTHER == 3 * REGS_LAUNCH, "register split");
 constexpr int HALF = KEYS * 128;  // bytes of 64 columns of 128 rows
 constexpr float kGrow = 8.f;      // growth of the maximum (base 2) that rescales
@@ -46,7 +47,7 @@ struct TcCfg {
     static constexpr int HALVES = DP / 64;
     static constexpr int TILE = HALVES * HALF;                    // 128 rows of Q, K or V
     static constexpr int SLOTS = DP == 64 ? 8 : 5;                // ring of K and V tiles
-    static constexpr int BARS = 2 * SLOTS + 2 * 5 + 1;
+    static constexpr int BARS = 2 * SLOTS + 2 * 6 + 1;
     static constexpr size_t SMEM = 1024 + (size_t)(2 + SLOTS) * TILE + 8 * BARS + 16;
     // Tensor-memory columns.  A head of 64 leaves room for P beside S; with
     // 128, P_t lies in the columns of S_t, whose next product therefore waits
@@ -87,13 +88,17 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 // mbar_wait without a call: the register split leaves no room for one.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    if (mbar_try(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
+    uint64_t t0 = 0;  // the clock is read only once a wait has become long
     for (uint32_t spin = 0; spin < kMaxSpins; ++spin) {
         if (mbar_try(bar, parity)) return true;
-        if ((spin & 63) == 63 && ((abort && *abort) || global_ns() - t0 > kWaitNs)) break;
+        if ((spin & 63) == 63) {
+            if (abort && *abort) return false;
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitNs) break;
+        }
     }
-    if (!abort || !*abort) atomicExch(&g_wait_expired, 1);
+    atomicExch(&g_wait_expired, 1);
     if (abort) *abort = 1;
     return false;
 }
@@ -192,23 +197,25 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     auto o_done = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 4 + t); };  // O_t += P_t V done
     // A half (64 positions) of P_t written (and S_t read, O_t rescaled).
     auto p_full = [&](int t, int h) { return bar0 + 8u * (2 * C::SLOTS + 6 + 2 * t + h); };
-    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 10);
+    auto turn = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 10 + t); };  // tile t may issue its products
+    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 12);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(kv_full(s), 1);
-            mbar_init(kv_empty(s), 1);
+            mbar_init(kv_empty(s), 2);  // both tiles' products
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(q_full(t), 128);
+            mbar_init(q_full(t), 4);  // one arrival a softmax warp
             mbar_init(s_full(t), 1);
-            mbar_init(p_full(t, 0), 128);
-            mbar_init(p_full(t, 1), 128);
+            mbar_init(p_full(t, 0), 4);
+            mbar_init(p_full(t, 1), 4);
             mbar_init(o_done(t), 1);
+            mbar_init(turn(t), 1);
         }
-        mbar_init(end_bar, 1);
+        mbar_init(end_bar, 2);
         *abort = 0;
         a.joins[blockIdx.x].parts = 0;
         prefetch_maps(&map_k, &map_v);
@@ -228,104 +235,129 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-        if (warp == 8) {
-            // ---------------- copies: K and V of every unit, in turn ----------------
-            const int boxes = KEYS / a.box_rows * C::HALVES;
-            int it = 0;
+        if (warp == 8 || warp == 11) {
+            // ---------------- copies: warp 8 the K tile, warp 11 the V tile of every unit, in turn ----------------
+            const bool is_v = uniform(warp) == 11;
+            const CUtensorMap *map = is_v ? &map_v : &map_k;
+            const int boxes = KEYS / a.box_rows;  // at most 16
+            int it = is_v ? 1 : 0;
             bool ok = true;
-            while (ok && pc.next()) {
-                for (int i = 0; ok && i < 2 * pc.n; ++i) {
+            while (ok && uniform(pc.next())) {
+                const int n = uniform(pc.n), head = uniform(pc.head);
+                int p0 = uniform(pc.it.t0 + pc.tile0) * KEYS;
+                for (int i = 0; i < n; ++i, it += 2, p0 += KEYS) {
                     const int st = it % C::SLOTS;
+                    const int page = lane < boxes ? page_of(a, pc.b, p0 + lane * a.box_rows, pc.it.lo, pc.it.hi) : 0;
                     ok = __all_sync(~0u, wait(kv_empty(st), ((it / C::SLOTS) & 1) ^ 1, abort));
                     if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(kv_full(st), C::TILE);
-                    __syncwarp();
-                    const int p0 = (pc.it.t0 + pc.tile0 + (i >> 1)) * KEYS;
-                    for (int x = lane; x < boxes; x += 32) {
-                        const int half = x % C::HALVES, row = x / C::HALVES * a.box_rows, p = p0 + row;
-                        const int page = page_of(a, pc.b, p, pc.it.lo, pc.it.hi);
-                        tma_load_4d(ring + st * C::TILE + half * HALF + row * 128, i & 1 ? &map_v : &map_k, 64 * half,
-                                    p % a.page_size, pc.head, page, kv_full(st));
+                    const uint32_t dst = ring + st * C::TILE, bar = kv_full(st);
+                    if (elect_one()) mbar_expect_tx(bar, C::TILE);
+                    for (int x = 0; x < boxes; ++x) {
+                        const int pg = __shfl_sync(~0u, page, x), row = x * a.box_rows;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int half = 0; half < C::HALVES; ++half)
+                                tma_load_4d(dst + half * HALF + row * 128, map, 64 * half, (p0 + row) % a.page_size, head, pg,
+                                            bar);
+                        }
                     }
-                    ++it;
                 }
             }
-            // Every copy has landed before the CTA may exit.
-            __syncwarp();
-            if (lane == 0)
-                for (int k = max(0, it - C::SLOTS); k < it; ++k) wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1, nullptr);
-        } else if (warp == 9) {
-            // ---------------- MMA issue ----------------
-            if (lane == 0) {
-                constexpr uint32_t id_s = instr_desc(KEYS, 0), id_o = instr_desc(DP, 1);
-                int it = 0;             // ring position
-                uint32_t steps[2] = {0, 0};  // P_t V products issued so far
-                bool ok = true;
-                auto wait_slot = [&](int k) {
-                    ok = ok && wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1, abort);
-                    fence_after();
-                };
-                auto score = [&](int t, int k) {  // S_t = Q_t K^T
-                    const uint32_t q = base + t * C::TILE, kt = ring + k % C::SLOTS * C::TILE;
+            // Every copy has landed before the CTA may exit (those whose slot was taken again, by a tile up to one after
+            // this warp's last, have).
+            for (int k = it - 2; k >= 0 && k > it - 1 - C::SLOTS; k -= 2)
+                wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1, nullptr);
+        } else if (warp < 11) {
+            // ---------------- MMA issue, tile t ----------------
+            // The whole warp walks the units, on values the compiler sees to
+            // be the warp's and keeps in uniform registers, where the MMAs
+            // take them from; one elected thread issues.
+            constexpr uint32_t id_s = instr_desc(KEYS, 0), id_o = instr_desc(DP, 1);
+            const int t = uniform(warp) - 9;
+            const uint32_t tm = uniform(tmem);
+            const uint32_t s_at = tm + C::S0 + 128 * t, p_at = tm + C::P0 + C::P_STEP * t, o_at = tm + C::O0 + DP * t;
+            const uint64_t q = operand_desc(base + t * C::TILE, 16, 1024);
+            int slot = 0;                          // next slot of the ring, and its phase
+            uint32_t phase = 0, begun = 0, steps = 0;  // pieces begun and P V products issued
+            uint32_t turns = 0;                        // steps of pieces with both tiles
+            bool ok = true;
+            auto advance = [&] {
+                if (++slot == C::SLOTS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
+            auto await = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(~0u, ok && wait(bar, parity, abort)); };
+            auto score = [&] {  // S = Q K^T, K in the next slot
+                const uint64_t kt = operand_desc(ring + slot * C::TILE, 16, 1024);
+                if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < DP / 16; ++s) {
-                        const uint32_t off = (s / 4) * HALF + (s % 4) * 32;
-                        mma_ss(tmem + C::S0 + 128 * t, operand_desc(q + off, 16, 1024), operand_desc(kt + off, 16, 1024),
-                               id_s, s != 0);
+                    for (int s = 0; s < DP / 16; ++s) {  // 16 columns: 32 bytes on, or the next 64 columns
+                        const uint32_t off = ((s / 4) * HALF + (s % 4) * 32) >> 4;
+                        mma_ss(s_at, q + off, kt + off, id_s, s != 0);
                     }
                     commit(s_full(t));
-                };
-                uint32_t begun[2] = {0, 0};  // pieces of tile t
-                while (ok && pc.next()) {
-                    const int nt = pc.rows() > 128 ? 2 : 1;
-                    for (int t = 0; t < nt; ++t) {
-                        ok = ok && wait(q_full(t), begun[t] & 1, abort);
-                        ++begun[t];
-                        // the columns of S_t, if P_t lies there: the last product of the piece before has read it
-                        if (C::P_IN_S && steps[t] > 0) ok = ok && wait(o_done(t), (steps[t] - 1) & 1, abort);
-                        if (t == 0) wait_slot(it);
-                        if (!ok) break;
-                        fence_after();
-                        score(t, it);
-                    }
-                    if (!ok) break;
-                    commit(kv_empty(it % C::SLOTS));
-                    for (int j = 0; ok && j < pc.n; ++j) {
-                        const int kv = it + 1, kn = it + 2;
-                        const bool more = j + 1 < pc.n;
-                        for (int t = 0; t < nt; ++t) {
-                            if (t == 0) wait_slot(kv);
-                            const uint32_t vt = ring + kv % C::SLOTS * C::TILE;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                ok = ok && wait(p_full(t, h), steps[t] & 1, abort);
-                                if (!ok) break;
-                                fence_after();
-#pragma unroll
-                                for (int s = 4 * h; s < 4 * h + 4; ++s)
-                                    mma_ts(tmem + C::O0 + DP * t, tmem + C::P0 + C::P_STEP * t + 8 * s,
-                                           operand_desc(vt + s * 2048, HALF, 1024), id_o, (j | s) != 0);
-                            }
-                            if (!ok) break;
-                            commit(o_done(t));
-                            if (t == nt - 1) commit(kv_empty(kv % C::SLOTS));
-                            ++steps[t];
-                            if (more) {
-                                if (t == 0) wait_slot(kn);
-                                if (C::P_IN_S) ok = ok && wait(o_done(t), (steps[t] - 1) & 1, abort);
-                                if (!ok) break;
-                                score(t, kn);
-                                if (t == nt - 1) commit(kv_empty(kn % C::SLOTS));
-                            }
-                        }
-                        it += 2;
-                    }
+                    commit(kv_empty(slot));
                 }
-                commit(end_bar);  // every product is done before the CTA may exit
-                wait(end_bar, 0, nullptr);
+                advance();
+            };
+            while (ok && uniform(pc.next())) {
+                const int n = uniform(pc.n), rows = uniform(pc.rows());
+                if (128 * t >= rows) {  // no such tile: only hand the slots on
+                    for (int i = 0; ok && i < 2 * n; ++i) {
+                        await(kv_full(slot), phase);
+                        if (ok && elect_one()) mbar_arrive(kv_empty(slot));
+                        advance();
+                    }
+                    continue;
+                }
+                await(q_full(t), begun++ & 1);
+                await(kv_full(slot), phase);
+                // the columns of S, if P lies there: the last product of the piece before has read it
+                if (C::P_IN_S && steps > 0) await(o_done(t), (steps - 1) & 1);
+                if (!ok) break;
+                fence_after();
+                score();
+                const bool both_tiles = rows > 128;
+                for (int j = 0; j < n; ++j) {
+                    const int v_slot = slot;
+                    const bool more = j + 1 < n;
+                    // K of the next unit too, ahead of the probabilities
+                    await(kv_full(slot), phase);
+                    advance();
+                    if (more) await(kv_full(slot), phase);
+                    const uint64_t vt = operand_desc(ring + v_slot * C::TILE, HALF, 1024);
+                    if (both_tiles) await(turn(t), (turns++ & 1) ^ (t == 0 ? 1 : 0));
+                    await(p_full(t, 0), steps & 1);
+                    if (!ok) break;
+                    fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) mma_ts(o_at, p_at + 8 * s, vt + s * (2048 >> 4), id_o, (j | s) != 0);
+                    }
+                    await(p_full(t, 1), steps & 1);
+                    if (!ok) break;
+                    fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = 4; s < 8; ++s) mma_ts(o_at, p_at + 8 * s, vt + s * (2048 >> 4), id_o, 1);
+                        commit(o_done(t));
+                        commit(kv_empty(v_slot));
+                    }
+                    if (more) {
+                        if (C::P_IN_S) await(o_done(t), steps & 1);
+                        if (!ok) break;
+                    }
+                    // The other tile's products may queue up behind this one's last.
+                    if (both_tiles && elect_one()) mbar_arrive(turn(t ^ 1));
+                    if (more) score();
+                    ++steps;
+                }
             }
-            __syncwarp();
+            if (elect_one()) commit(end_bar);  // every product is done before the CTA may exit
+            wait(end_bar, 0, nullptr);
         }
+        __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         // ---------------- softmax: warps 4 t .. 4 t + 3 for tile t, one thread to a row ----------------
@@ -361,7 +393,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
-            mbar_arrive(q_full(t));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full(t));
 
             const int p = pc.s.kv - pc.s.qn + gr / a.group;
             const int ub = in ? (a.causal ? min(p + 1, pc.s.kv) : pc.s.kv) : 0;
@@ -421,8 +454,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         ref = nr;
                     }
                 }
-                if (t == 0 && (j0 < pc.it.lo || j0 + KEYS > pc.it.hi)) {
-                    // Rows of V that the item does not see: one to a thread.
+                if (j0 < pc.it.lo || j0 + KEYS > pc.it.hi) {
+                    // Rows of V that the item does not see: one to a thread (both tiles write the same zeros, each
+                    // before its own product).
                     const int k = first_slot + 2 * j + 1, row = 32 * quad + lane;
                     wait(kv_full(k % C::SLOTS), (k / C::SLOTS) & 1, abort);
                     if (j0 + row < pc.it.lo || j0 + row >= pc.it.hi) {
@@ -453,7 +487,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     if (c & 1) {
                         tmem_store_wait();
                         fence_before();
-                        mbar_arrive(p_full(t, c >> 1));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_full(t, c >> 1));
                     }
                 }
                 const float2 s4 = both(add2(s2[0], s2[1]));

@@ -75,18 +75,21 @@ inline int check_batch(const f16_kv_batch *b, int page_size, KvBatch &out) {
 
 inline bool head_dim_ok(int d) { return d >= 8 && d <= 256 && d % 8 == 0; }
 
+// Positions of a key tile of the kernels for this head_dim (at most).
+__host__ __device__ constexpr int kv_tile(int head_dim) { return head_dim <= 128 ? 128 : 64; }
+
 // Rows of one copy from the cache: the largest power of two that divides the
-// page, up to 64 (8 rows are one swizzle atom, so every copy starts on one).
-inline int kv_box_rows(int page_size) {
+// page, up to a tile (8 rows are one swizzle atom, so every copy starts on one).
+inline int kv_box_rows(int page_size, int head_dim) {
     int r = 8;
-    while (r < 64 && page_size % (2 * r) == 0) r *= 2;
+    while (r < kv_tile(head_dim) && page_size % (2 * r) == 0) r *= 2;
     return r;
 }
 
 inline int check_cache(const f16_kv_cache *c) {
     if (!c || !c->k || !c->v) return W4_ERR_NULL;
     if (c->num_pages < 1 || c->page_size < 8 || c->page_size % 8 != 0 || c->heads < 1 || c->heads > kMaxHeads ||
-        !head_dim_ok(c->head_dim) || c->box_rows != kv_box_rows(c->page_size))
+        !head_dim_ok(c->head_dim) || c->box_rows != kv_box_rows(c->page_size, c->head_dim))
         return W4_ERR_SHAPE;
     return W4A16_OK;
 }

@@ -241,6 +241,28 @@ int launch(K kernel, long long warps, void *stream, A... args) {
     return launch_status();
 }
 
+// Encodes a binary16 tensor map with 128-byte swizzle; false for a stride it
+// cannot take (2^40 bytes and more).
+bool f16_map(uint64_t (&out)[16], void *x, int rank, const uint64_t *dims, const uint64_t *strides,
+             const uint32_t *box) {
+    static_assert(sizeof(CUtensorMap) == sizeof(out), "tensor map size");
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i > 0) s[i - 1] = strides[i - 1];
+    }
+    alignas(64) CUtensorMap m;
+    if (encode_fn()(&m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank, x, d, s, b, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    memcpy(out, &m, sizeof(m));
+    return true;
+}
+
 }  // namespace
 
 // Reads and clears this translation unit's record of bad indexes.
@@ -330,6 +352,7 @@ extern "C" int f16_kv_cache_init(f16_kv_cache *c, uint16_t *k, uint16_t *v, cons
     if (!aligned16(k) || !aligned16(v)) return W4_ERR_ALIGN;
     for (int i = 0; i < 3; ++i)
         if (!stride_ok(ks[i]) || !stride_ok(vs[i])) return W4_ERR_ALIGN;
+    if (!encode_fn()) return W4_ERR_DEVICE;
     c->k = k;
     c->v = v;
     c->k_page = ks[0];
@@ -342,26 +365,24 @@ extern "C" int f16_kv_cache_init(f16_kv_cache *c, uint16_t *k, uint16_t *v, cons
     c->page_size = page_size;
     c->heads = heads;
     c->head_dim = head_dim;
-    c->box_rows = kv_box_rows(page_size);
+    c->box_rows = kv_box_rows(page_size, head_dim);
     c->reserved = 0;
-    // Copies of box_rows tokens x 64 elements of one head of one page, 128-byte
-    // swizzle.  Elements past head_dim read as zero (heads are padded to 64).
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return W4_ERR_DEVICE;
+    // Copies of box_rows tokens of one head of one page, 128-byte swizzle: 64
+    // elements of each (elements past head_dim read as zero: heads are padded
+    // to 64), or all head_dim elements as columns of 64, one after the other.
     for (int i = 0; i < 2; ++i) {
         const int64_t *s = i ? vs : ks;
-        const cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)page_size, (cuuint64_t)heads,
-                                    (cuuint64_t)num_pages};
-        const cuuint64_t strides[3] = {(cuuint64_t)s[1] * 2, (cuuint64_t)s[2] * 2, (cuuint64_t)s[0] * 2};
-        const cuuint32_t box[4] = {64, (cuuint32_t)c->box_rows, 1, 1};
-        const cuuint32_t one[4] = {1, 1, 1, 1};
-        alignas(64) CUtensorMap m;
-        if (fn(&m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, i ? v : k, dims, strides, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return W4_ERR_SHAPE;  // a stride the copies cannot take (2^40 bytes and more)
-        static_assert(sizeof(m) == sizeof(c->k_map), "tensor map size");
-        memcpy(i ? c->v_map : c->k_map, &m, sizeof(m));
+        uint16_t *x = i ? v : k;
+        const uint64_t st[5] = {2, (uint64_t)s[1] * 2, 128, (uint64_t)s[2] * 2, (uint64_t)s[0] * 2};
+        const uint64_t dims[4] = {(uint64_t)head_dim, (uint64_t)page_size, (uint64_t)heads, (uint64_t)num_pages};
+        const uint64_t strides[3] = {st[1], st[3], st[4]};
+        const uint32_t box[4] = {64, (uint32_t)c->box_rows, 1, 1};
+        if (!f16_map(i ? c->v_map : c->k_map, x, 4, dims, strides, box)) return W4_ERR_SHAPE;
+        if (head_dim % 64 != 0 || head_dim == 64) continue;
+        const uint64_t wide_dims[5] = {64, (uint64_t)page_size, (uint64_t)head_dim / 64, (uint64_t)heads,
+                                       (uint64_t)num_pages};
+        const uint32_t wide_box[5] = {64, (uint32_t)c->box_rows, (uint32_t)head_dim / 64, 1, 1};
+        if (!f16_map(i ? c->v_wide : c->k_wide, x, 5, wide_dims, st + 1, wide_box)) return W4_ERR_SHAPE;
     }
     return W4A16_OK;
 }

@@ -20,7 +20,7 @@ class Cache(ctypes.Structure):
     _fields_ = [("k", P), ("v", P), ("k_strides", L * 3), ("v_strides", L * 3), ("num_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("box_rows", ctypes.c_int32), ("reserved", ctypes.c_int32), ("k_map", ctypes.c_uint64 * 16),
-                ("v_map", ctypes.c_uint64 * 16)]
+                ("v_map", ctypes.c_uint64 * 16), ("k_wide", ctypes.c_uint64 * 16), ("v_wide", ctypes.c_uint64 * 16)]
 
 
 class Rotation(ctypes.Structure):

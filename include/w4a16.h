@@ -439,10 +439,17 @@ W4A16_API int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head, 
  *   q, y    [total_q][q_heads][head_dim], strided (y may be q)
  *   lse     float [total_q][q_heads]: log of the sum of exp(scale q . k_j), or NULL
  *   scale   > 0, finite;  causal 0 or 1;  window >= 0 (0: none)
+ *   total_q x q_heads x max_pages x page_size up to about 2^42 (W4_ERR_SHAPE)
  *   q_heads a multiple of the cache's heads, at most 1024 for each
  *   workspace  device buffer of at least f16_attention_workspace_bytes bytes,
- *              16-byte aligned; contents on entry are ignored.  Calls ordered
- *              on one stream may share it.
+ *              16-byte aligned, ZERO-FILLED before its first use and then
+ *              passed unchanged to later calls (its counters are left ready for
+ *              the next one).  Calls ordered on one stream may share it; calls
+ *              that may run concurrently need separate ones.
+ * The launch is cooperative (every block resident): blocks that share a
+ * sequence wait for each other's partial results (bounded: on expiry the rows
+ * concerned stay unwritten, w4a16_device_status reports W4_ERR_TIMEOUT and the
+ * workspace has to be zeroed again).
  * Products are binary16 with fp32 sums; the softmax's statistics and the
  * output's sum are fp32, the probabilities are rounded to binary16 for the
  * product with v, and y is rounded once.  A token that sees no position gets
@@ -450,8 +457,7 @@ W4A16_API int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head, 
  * of the call sees, and past a sequence's end, does not matter, NaN and
  * infinities included; keys and values that some token of a sequence sees are
  * taken to be finite (a value that is not may show in the sequence's earlier
- * tokens too).  Results are deterministic, and do not depend on what else the
- * workspace held.
+ * tokens too).  Results are deterministic.
  * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_WORKSPACE,
  * W4_ERR_DEVICE, W4_ERR_LAUNCH.
  */

@@ -250,11 +250,11 @@ def attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, max_q_
 
 
 def attention_workspace(cache: KVCache, q_heads: int, max_q_len: int) -> torch.Tensor:
-    """A workspace for f16_attention on this cache with up to max_q_len new
-    tokens of a sequence (contents do not matter; reusable by every later call
-    that needs no more)."""
+    """A zero-filled workspace for f16_attention on this cache with up to
+    max_q_len new tokens of a sequence (reusable by every later call that needs
+    no more)."""
     need = attention_workspace_bytes(q_heads, cache.heads, cache.head_dim, max_q_len)
-    return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.k.device)
+    return torch.zeros(max(need, 16), dtype=torch.uint8, device=cache.k.device)
 
 
 def f16_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, y: torch.Tensor | None = None,
@@ -264,7 +264,8 @@ def f16_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, y: torch.Tens
     sequence in the cache up to its own (all of them with causal False; the
     last `window` of them where that is not 0).  scale: 1 / sqrt(dim) when
     None.  lse: float32 [total_q][heads], receives log sum exp of the scaled
-    scores.  workspace: from attention_workspace; a fresh one is made when None."""
+    scores.  workspace: from attention_workspace (zero-filled once, then
+    reused); a fresh one is made when None."""
     pq, qt, qh = _heads(q, "q")
     n, h, d = q.shape
     if y is None:

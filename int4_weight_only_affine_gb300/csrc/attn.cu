@@ -19,6 +19,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "attn.cuh"
 
 namespace w4a16 {
@@ -37,14 +39,13 @@ template <int DP, int MT>
 struct RowCfg {
     static constexpr int ROWS = 16 * MT;
     static constexpr int KEYS = kv_tile(DP);
+    using Work = Cut<ROWS, KEYS, 2, 3, ROWS>;
     static constexpr int WARPS = KEYS / 16;             // consumers
     static constexpr int THREADS = 32 * (WARPS + 1);
     static constexpr int TILE = KEYS * 128 * (DP / 64); // bytes of K or V
     static constexpr int STAGES = 192 * 1024 / (2 * TILE);
-    static constexpr int MERGE_COLS = 32;               // columns merged at a time
-    static constexpr int MERGE_LD = MERGE_COLS + 4;     // floats per row of the merge buffer
-    static constexpr int MERGE = WARPS * ROWS * MERGE_LD * 4;
-    static constexpr int ML = WARPS * ROWS * 8;
+    static constexpr int MERGE = WARPS * ROWS * 36 * 4; // 32 columns of every warp's rows, or 64 of 8 rows, and padding
+    static constexpr int ML = (WARPS + 1) * ROWS * 8;
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * 2 * TILE + MERGE + ML + 16 * STAGES + 16;
 };
 
@@ -56,6 +57,78 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
+// Row r of a shared item, by WARPS warps: they take the parts in turn, lane l
+// of each the columns 4 l .. 4 l + 3 (and those 128 further on), and merge
+// through sh.  A part's rows lie one after the other.
+template <int WARPS, int ROWS, class Sync>
+__device__ __forceinline__ void join_row(const AttnArgs &a, const Part &part, int r, float *sh, Sync sync) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float4 *sh_o = reinterpret_cast<float4 *>(sh);                         // [WARPS][2][32]
+    float2 *sh_ml = reinterpret_cast<float2 *>(sh + WARPS * 2 * 32 * 4);  // [WARPS]
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+    float mx = -INFINITY, sum = 0.f;
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int i0 = warp; i0 < part.parts; i0 += 4 * WARPS) {  // four parts' loads in flight
+        float4 v[4][2];
+        float2 c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * WARPS;
+            c[k] = make_float2(-INFINITY, 0.f);
+            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < part.parts) {
+                const long long row = part_slot(part.first, i) * ROWS + r;
+                c[k] = __ldcg(ml + row);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (128 * h + 4 * lane < a.head_dim)
+                        v[k][h] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + row * a.head_dim + 128 * h + 4 * lane));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float top = fmaxf(mx, c[k].x), f0 = corr(mx, top), f1 = corr(c[k].x, top);
+            mx = top;
+            sum = sum * f0 + c[k].y * f1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                acc[h].x = acc[h].x * f0 + v[k][h].x * f1;
+                acc[h].y = acc[h].y * f0 + v[k][h].y * f1;
+                acc[h].z = acc[h].z * f0 + v[k][h].z * f1;
+                acc[h].w = acc[h].w * f0 + v[k][h].w * f1;
+            }
+        }
+    }
+    sh_o[(warp * 2) * 32 + lane] = acc[0];
+    sh_o[(warp * 2 + 1) * 32 + lane] = acc[1];
+    if (lane == 0) sh_ml[warp] = make_float2(mx, sum);
+    sync();
+    if (warp < 2 && 128 * warp + 4 * lane < a.head_dim) {
+        mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sh_ml[w].x);
+        sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float f = corr(sh_ml[w].x, mx);
+            sum += sh_ml[w].y * f;
+            const float4 v = sh_o[(w * 2 + warp) * 32 + lane];
+            o.x += v.x * f;
+            o.y += v.y * f;
+            o.z += v.z * f;
+            o.w += v.w * f;
+        }
+        const int gr = part.row0 + r, head = part.head * (int)a.group.d + gr % a.group;
+        const long long tok = part.q0 + gr / a.group;
+        const float inv = inverse(sum);
+        *reinterpret_cast<uint2 *>(a.y + tok * a.y_token + head * a.y_head + 128 * warp + 4 * lane) =
+            make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+        if (a.lse && threadIdx.x == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
+    }
+    sync();
+}
+
 // WIDE: the tensor maps copy whole heads.
 template <int DP, int MT, bool WIDE>
 __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
@@ -70,26 +143,25 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
     uint8_t *gbase = smem_raw + (base - raw);
     float *merge = reinterpret_cast<float *>(gbase + C::STAGES * 2 * C::TILE);
     float2 *ml_sh = reinterpret_cast<float2 *>(gbase + C::STAGES * 2 * C::TILE + C::MERGE);
+    float2 *row_sh = ml_sh + C::WARPS * ROWS;
     const uint32_t bar0 = base + C::STAGES * 2 * C::TILE + C::MERGE + C::ML;
     volatile int *abort = reinterpret_cast<volatile int *>(gbase + (bar0 - base) + 16 * C::STAGES);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), C::WARPS);
         }
         *abort = 0;
-        a.joins[blockIdx.x].parts = 0;
         prefetch_maps(&map_k, &map_v);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    make_plan<ROWS, KEYS, C::THREADS, 2>(a, plan_sh);  // (its barriers also publish the above)
+    make_plan<typename C::Work, C::THREADS>(a, plan_sh);  // (its barriers also publish the above)
     const Plan plan = plan_sh.plan;
-    Pieces<ROWS, KEYS> pc(a, plan);
+    Pieces<typename C::Work> pc(a, plan);
 
     if (warp == C::WARPS) {
         // ---------------- producer ----------------
@@ -145,6 +217,9 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
     const int vrow = lane & 15, vch = lane >> 4;
     const uint32_t v_off = row_at(16 * warp + vrow);
     const int g = lane >> 2, t4 = lane & 3;
+    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
+    Part shared0, shared1;  // items that this CTA shares with earlier and later ones
+    int shares = 0;
     int it = 0;
     while (pc.next()) {
         const int row0 = pc.row0(), rows = pc.rows();
@@ -204,13 +279,14 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
                 __syncwarp();
             }
             if (j0 < pc.it.hi && j0 + 16 > pc.it.lo) {
-                float s[MT][2][4];
+                // Two sums of half the columns each: shorter chains of dependent products.
+                float s[MT][2][4], s2[MT][2][4];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+                        for (int e = 0; e < 4; ++e) s[mt][n][e] = s2[mt][n][e] = 0.f;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     uint32_t kf[4];
@@ -218,12 +294,15 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
                     ldsm4(kf, kb + k_off + (ch / 8) * half_bytes + (((ch ^ krow) & 7) << 4));
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        mma_16816(s[mt][0], qf[mt][k][0], qf[mt][k][1], qf[mt][k][2], qf[mt][k][3], kf[0], kf[1]);
-                        mma_16816(s[mt][1], qf[mt][k][0], qf[mt][k][1], qf[mt][k][2], qf[mt][k][3], kf[2], kf[3]);
+                        auto &d = k & 1 ? s2[mt] : s[mt];
+                        mma_16816(d[0], qf[mt][k][0], qf[mt][k][1], qf[mt][k][2], qf[mt][k][3], kf[0], kf[1]);
+                        mma_16816(d[1], qf[mt][k][0], qf[mt][k][1], qf[mt][k][2], qf[mt][k][3], kf[2], kf[3]);
                     }
                 }
                 const bool masked = j0 + 16 > all_ub || j0 < all_lb;
                 uint32_t pf4[MT][4];
+                float mx[MT][2];
+                bool grown = false;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -231,35 +310,52 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int j = j0 + 8 * n + 2 * t4 + (e & 1), hf = e >> 1;
-                            s[mt][n][e] *= a.scale;
+                            s[mt][n][e] = (s[mt][n][e] + s2[mt][n][e]) * a.scale;
                             if (masked && (j >= ub[mt][hf] || j < lb[mt][hf])) s[mt][n][e] = -INFINITY;
                         }
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        float mx = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
-                                         fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                        mx = fmaxf(mx, m[mt][hf]);
-                        const float c = corr(m[mt][hf], mx);
-                        const float ref = mx == -INFINITY ? 0.f : mx;
-                        if (__any_sync(~0u, mx != m[mt][hf])) {
+                    for (int hf = 0; hf < 2; ++hf)
+                        mx[mt][hf] = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
+                                           fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+                }
+#pragma unroll
+                for (int step = 1; step <= 2; step <<= 1)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) mx[mt][hf] = fmaxf(mx[mt][hf], __shfl_xor_sync(~0u, mx[mt][hf], step));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) grown |= mx[mt][hf] > m[mt][hf];
+                if (__any_sync(~0u, grown)) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const float top = fmaxf(mx[mt][hf], m[mt][hf]), c = corr(m[mt][hf], top);
+                            m[mt][hf] = top;
+                            l[mt][hf] *= c;
 #pragma unroll
                             for (int n = 0; n < DP / 8; ++n) {
                                 o[mt][n][2 * hf] *= c;
                                 o[mt][n][2 * hf + 1] *= c;
                             }
                         }
-                        m[mt][hf] = mx;
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float ref = m[mt][hf] == -INFINITY ? 0.f : m[mt][hf];
                         float p[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) p[e] = exp2_approx(s[mt][e >> 1][2 * hf + (e & 1)] - ref);
-                        l[mt][hf] = l[mt][hf] * c + ((p[0] + p[1]) + (p[2] + p[3]));
+                        l[mt][hf] += (p[0] + p[1]) + (p[2] + p[3]);
                         // Probabilities, at most 1, to binary16 for the product with V (the sum l keeps fp32).
                         pf4[mt][hf] = pack2(p[0], p[1]);
                         pf4[mt][2 + hf] = pack2(p[2], p[3]);
                     }
-                }
 #pragma unroll
                 for (int n = 0; n < DP / 16; ++n) {
                     uint32_t vf[4];
@@ -278,7 +374,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
         }
 
         // ---------------- merge the warps' sums ----------------
-        auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
+        const bool whole = pc.begins && pc.ends;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -289,149 +385,100 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
                 if (t4 == 0) ml_sh[warp * ROWS + 16 * mt + 8 * hf + g] = make_float2(m[mt][hf], v);
             }
         sync();
-        // Maximum and sum of row r over the warps.
-        auto row_ml = [&](int r) {
+        if ((int)threadIdx.x < rows) {  // a row's maximum and sum over the warps; what its outputs are scaled by
+            const int r = threadIdx.x;
+            float2 w[C::WARPS];
             float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < C::WARPS; ++w) mx = fmaxf(mx, ml_sh[w * ROWS + r].x);
+            for (int i = 0; i < C::WARPS; ++i) {
+                w[i] = ml_sh[i * ROWS + r];
+                mx = fmaxf(mx, w[i].x);
+            }
 #pragma unroll
-            for (int w = 0; w < C::WARPS; ++w) sum += ml_sh[w * ROWS + r].y * corr(ml_sh[w * ROWS + r].x, mx);
-            return make_float2(mx, sum);
-        };
-        const bool whole = pc.begins && pc.ends;
-        if ((int)threadIdx.x < rows) {
-            const int r = threadIdx.x;
-            const float2 ml = row_ml(r);
-            if (whole) {
+            for (int i = 0; i < C::WARPS; ++i) sum += w[i].y * corr(w[i].x, mx);
+            row_sh[r] = make_float2(mx, whole ? inverse(sum) : 1.f);
+            if (!whole) {
+                reinterpret_cast<float2 *>(a.part_ml)[(long long)pc.slot() * ROWS + r] = make_float2(mx, sum);
+            } else if (a.lse) {
                 const int gr = row0 + r;
-                if (a.lse)
-                    a.lse[(long long)(pc.s.q0 + gr / a.group) * (a.kv_heads * (int)a.group.d) + pc.head * (int)a.group.d +
-                          gr % a.group] = log_sum(ml.x, ml.y);
-            } else {
-                reinterpret_cast<float2 *>(a.part_ml)[(long long)pc.slot() * ROWS + r] = ml;
+                a.lse[(long long)(pc.s.q0 + gr / a.group) * (a.kv_heads * (int)a.group.d) + pc.head * (int)a.group.d +
+                      gr % a.group] = log_sum(mx, sum);
             }
         }
-        if (threadIdx.x == 0 && pc.begins && !pc.ends)
-            a.joins[blockIdx.x] = JoinItem{pc.parts(plan), pc.s.q0, pc.head, row0, rows};
+        sync();
         float f[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) f[mt][hf] = corr(m[mt][hf], row_ml(16 * mt + 8 * hf + g).x);
-#pragma unroll
-        for (int cb = 0; cb < DP / C::MERGE_COLS; ++cb) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < C::MERGE_COLS / 8; ++n)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-                        *reinterpret_cast<float2 *>(
-                            &merge[(warp * ROWS + 16 * mt + 8 * hf + g) * C::MERGE_LD + 8 * n + 2 * t4]) =
-                            make_float2(o[mt][C::MERGE_COLS / 8 * cb + n][2 * hf] * f[mt][hf],
-                                        o[mt][C::MERGE_COLS / 8 * cb + n][2 * hf + 1] * f[mt][hf]);
-            sync();
-            for (int x = threadIdx.x; x < ROWS * (C::MERGE_COLS / 4); x += NT) {
-                const int r = x / (C::MERGE_COLS / 4), c = 4 * (x % (C::MERGE_COLS / 4)), col = C::MERGE_COLS * cb + c;
-                if (r >= rows || col >= a.head_dim) continue;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < C::WARPS; ++w) {
-                    const float4 u = *reinterpret_cast<const float4 *>(&merge[(w * ROWS + r) * C::MERGE_LD + c]);
-                    v.x += u.x;
-                    v.y += u.y;
-                    v.z += u.z;
-                    v.w += u.w;
-                }
-                if (whole) {
-                    const float inv = inverse(row_ml(r).y);
-                    const int gr = row0 + r;
-                    uint16_t *dst = a.y + (pc.s.q0 + gr / a.group) * a.y_token +
-                                    (pc.head * (int)a.group.d + gr % a.group) * a.y_head + col;
-                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
-                } else {
-                    *reinterpret_cast<float4 *>(a.part_o + ((long long)pc.slot() * ROWS + r) * a.head_dim + col) = v;
-                }
+            for (int hf = 0; hf < 2; ++hf) {
+                const float2 w = row_sh[16 * mt + 8 * hf + g];
+                f[mt][hf] = corr(m[mt][hf], w.x) * w.y;
             }
-            sync();
+        // Outputs, COLS columns of HALVES x 8 rows at a time.
+        auto merge_rows = [&](auto halves) {
+            constexpr int HALVES = decltype(halves)::value, COLS = HALVES == 1 ? 64 : 32, LD = COLS + 8 / HALVES;
+#pragma unroll
+            for (int cb = 0; cb < DP / COLS; ++cb) {
+#pragma unroll
+                for (int n = 0; n < COLS / 8; ++n)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) {
+                        const int mt = h >> 1, hf = h & 1;
+                        *reinterpret_cast<float2 *>(&merge[(warp * 8 * HALVES + 8 * h + g) * LD + 8 * n + 2 * t4]) =
+                            make_float2(o[mt][COLS / 8 * cb + n][2 * hf] * f[mt][hf],
+                                        o[mt][COLS / 8 * cb + n][2 * hf + 1] * f[mt][hf]);
+                    }
+                sync();
+                for (int x = threadIdx.x; x < 8 * HALVES * (COLS / 4); x += NT) {
+                    const int r = x / (COLS / 4), c = 4 * (x % (COLS / 4)), col = COLS * cb + c;
+                    if (r >= rows || col >= a.head_dim) continue;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < C::WARPS; ++w) {
+                        const float4 u = *reinterpret_cast<const float4 *>(&merge[(w * 8 * HALVES + r) * LD + c]);
+                        v.x += u.x;
+                        v.y += u.y;
+                        v.z += u.z;
+                        v.w += u.w;
+                    }
+                    if (whole) {
+                        const int gr = row0 + r;
+                        uint16_t *dst = a.y + (pc.s.q0 + gr / a.group) * a.y_token +
+                                        (pc.head * (int)a.group.d + gr % a.group) * a.y_head + col;
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+                    } else {
+                        *reinterpret_cast<float4 *>(a.part_o + ((long long)pc.slot() * ROWS + r) * a.head_dim + col) = v;
+                    }
+                }
+                sync();
+            }
+        };
+        if (rows <= 8)
+            merge_rows(std::integral_constant<int, 1>());
+        else
+            merge_rows(std::integral_constant<int, 2 * MT>());
+        if (!whole) {
+            const Part part = pc.part(plan);
+            if (threadIdx.x == 0) part_written(a, part);
+            if (shares++ == 0)
+                shared0 = part;
+            else
+                shared1 = part;
         }
     }
-}
 
-// Join of the items that the row kernel cut: block (c, r) joins row r of the
-// item that starts in the range of CTA c.  Its warps take the parts in turn,
-// lane l of each the columns 4 l .. 4 l + 3 (and those 128 further on), and
-// merge through shared memory.  A part's rows lie one after the other.
-constexpr int kJoinWarps = 8;
-__global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int ROWS = 16;
-    __shared__ float4 sh_o[kJoinWarps][2][32];
-    __shared__ float2 sh_ml[kJoinWarps];
-    pdl_wait();
-    const JoinItem j = a.joins[blockIdx.x];
-    const int row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (row >= j.rows || j.parts == 0) return;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-    float mx = -INFINITY, sum = 0.f;
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int i0 = warp; i0 < j.parts; i0 += 4 * kJoinWarps) {  // four parts' loads in flight
-        float4 v[4][2];
-        float2 c[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int i = i0 + k * kJoinWarps;
-            c[k] = make_float2(-INFINITY, 0.f);
-            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < j.parts) {
-                const long long r = part_slot(blockIdx.x, i) * ROWS + row;
-                c[k] = ml[r];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (128 * h + 4 * lane < a.head_dim)
-                        v[k][h] = *reinterpret_cast<const float4 *>(a.part_o + r * a.head_dim + 128 * h + 4 * lane);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float top = fmaxf(mx, c[k].x), f0 = corr(mx, top), f1 = corr(c[k].x, top);
-            mx = top;
-            sum = sum * f0 + c[k].y * f1;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                acc[h].x = acc[h].x * f0 + v[k][h].x * f1;
-                acc[h].y = acc[h].y * f0 + v[k][h].y * f1;
-                acc[h].z = acc[h].z * f0 + v[k][h].z * f1;
-                acc[h].w = acc[h].w * f0 + v[k][h].w * f1;
-            }
-        }
+    // ---------------- join this CTA's rows of the items it shares ----------------
+    for (int i = 0; i < shares; ++i) {
+        const Part part = i == 0 ? shared0 : shared1;
+        const int joiners = min(part.parts, part.rows);
+        if (part.index >= joiners) continue;
+        if (threadIdx.x == 0) *abort = parts_written(a, part, part.parts) ? 0 : 1;
+        sync();
+        const bool ok = *abort == 0;
+        for (int r = part.index; ok && r < part.rows; r += joiners) join_row<C::WARPS, ROWS>(a, part, r, merge, sync);
+        sync();
+        if (threadIdx.x == 0 && ok) part_joined(a, part, joiners);
     }
-    sh_o[warp][0][lane] = acc[0];
-    sh_o[warp][1][lane] = acc[1];
-    if (lane == 0) sh_ml[warp] = make_float2(mx, sum);
-    __syncthreads();
-    if (warp >= 2 || 128 * warp + 4 * lane >= a.head_dim) return;
-    const int h = warp;
-    mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, sh_ml[w].x);
-    sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        const float f = corr(sh_ml[w].x, mx);
-        sum += sh_ml[w].y * f;
-        const float4 v = sh_o[w][h][lane];
-        o.x += v.x * f;
-        o.y += v.y * f;
-        o.z += v.z * f;
-        o.w += v.w * f;
-    }
-    const int gr = j.row0 + row, head = j.head * (int)a.group.d + gr % a.group;
-    const long long tok = j.q0 + gr / a.group;
-    const float inv = inverse(sum);
-    *reinterpret_cast<uint2 *>(a.y + tok * a.y_token + head * a.y_head + 128 * h + 4 * lane) =
-        make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
-    if (a.lse && threadIdx.x == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
 }
 
 template <int DP, int MT, bool WIDE>
@@ -439,19 +486,17 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
     using C = RowCfg<DP, MT>;
     static_assert(C::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
     if (!set_smem_once(reinterpret_cast<const void *>(attn_rows_kernel<DP, MT, WIDE>), (int)C::SMEM)) return W4_ERR_LAUNCH;
-    attn_rows_kernel<DP, MT, WIDE><<<grid, C::THREADS, C::SMEM, stream>>>(mk, mv, a);
-    const int st = launch_status();
-    return st != W4A16_OK ? st : launch_dependent(join_rows_kernel, dim3(grid, 16), 32 * kJoinWarps, a, stream);
+    return launch_resident(attn_rows_kernel<DP, MT, WIDE>, grid, C::THREADS, C::SMEM, stream, mk, mv, a);
 }
 
 // Whether a call takes the tcgen05 kernel: more rows per sequence and
 // key/value head than one tile of the row kernel, heads of at most 128.
 bool takes_tc(int group, int head_dim, int max_q_len) { return (long long)group * max_q_len > 16 && head_dim <= 128; }
 
-// Workspace: the join records, then two partial tiles per CTA (statistics, outputs).
-constexpr size_t kJoinBytes = kMaxGrid * sizeof(JoinItem);
+// Workspace: the counters, then two partial tiles per CTA (statistics, outputs).
+constexpr size_t kCounterBytes = 2 * kMaxGrid * sizeof(unsigned);
 size_t workspace_need(int rows, int head_dim) {
-    return (kJoinBytes + (size_t)2 * kMaxGrid * rows * (2 + head_dim) * 4 + 15) / 16 * 16;
+    return (kCounterBytes + (size_t)2 * kMaxGrid * rows * (2 + head_dim) * 4 + 15) / 16 * 16;
 }
 
 }  // namespace
@@ -522,15 +567,22 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     a.few_tiles = (long long)batch->max_q_len * (q_heads / heads) <= 4 * rows;
     a.scale = scale * kLog2e;
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
-    a.joins = reinterpret_cast<JoinItem *>(ws);
-    a.part_ml = reinterpret_cast<float *>(ws + kJoinBytes);
+    a.arrived = reinterpret_cast<unsigned *>(ws);
+    a.left = a.arrived + kMaxGrid;
+    a.part_ml = reinterpret_cast<float *>(ws + kCounterBytes);
     a.part_o = a.part_ml + (size_t)2 * kMaxGrid * rows * 2;
     const bool wide = !tc && d % 64 == 0 && d > 64;
     alignas(64) CUtensorMap mk, mv;
     memcpy(&mk, wide ? cache->k_wide : cache->k_map, sizeof(mk));
     memcpy(&mv, wide ? cache->v_wide : cache->v_map, sizeof(mv));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+    // No more CTAs than there can be units (lengths are known on the device only).
+    const int keys = kv_tile(d);
+    const long long tiles = ((long long)batch->total_q * (q_heads / heads) + rows - 1) / rows + batch->batch;
+    const long long units = tiles * heads * ((a.b.max_kv + keys - 1) / keys + 8);  // (and their items' extra cost)
+    if (units >= 0x7FFFFFFFll) return W4_ERR_SHAPE;
+    int grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
+    if (units < grid) grid = (int)units;
     if (tc) return attn_tc_launch(mk, mv, a, grid, s);
     if (d <= 64) return launch_rows<64, 1, false>(mk, mv, a, grid, s);
     if (d == 128) return launch_rows<128, 1, true>(mk, mv, a, grid, s);

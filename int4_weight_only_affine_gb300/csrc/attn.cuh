@@ -5,13 +5,17 @@
 // r % G of the group (G = q_heads / kv_heads).  An item is a tile of `rows`
 // such rows (of one sequence, one key/value head) with the range of
 // positions [lo, hi) that any of its rows sees; a unit is one tile of `keys`
-// positions of that range.  All items' units, in the order (sequence, head,
+// positions of that range.  An item costs its units and, for its queries and
+// outputs, EXTRA units more.  All items' costs, in the order (sequence, head,
 // row tile, key tile), are cut into one contiguous range per CTA, equal to
 // within a unit, whatever the lengths.  An item cut by a range boundary is
 // computed in parts: each part's CTA leaves its unnormalised output, running
-// maximum and sum in the workspace, and a second kernel joins them.  Every
-// CTA works its range out from the lengths by itself: the host needs no
-// lengths, and the split depends on nothing but the batch, so results repeat.
+// maximum and sum in the workspace and counts itself in; when a CTA is done
+// with its own range it waits for the parts of the items it shares (all CTAs
+// are resident: a cooperative launch) and joins its share of their rows, in
+// the parts' order.  Every CTA works its range out from the lengths by itself:
+// the host needs no lengths, and the split depends on nothing but the batch,
+// so results repeat.
 #pragma once
 
 #include <math.h>
@@ -34,30 +38,37 @@ struct AttnArgs {
     float scale;    // times log2(e): the softmax is taken in powers of two
     float *part_o;  // [2 * grid][rows x head_dim], in the order of the kernel that writes it
     float *part_ml; // [2 * grid][rows][2]: running maximum (base-2 scaled scores) and sum
-    struct JoinItem *joins;  // [grid]
+    unsigned *arrived, *left;  // [grid]: of the item that starts in a CTA's range; zero between calls
 };
 
-// An item that starts in the range of CTA c and is finished by later CTAs:
-// parts at slots 2c + 1, 2(c + 1), 2(c + 2), ...
-struct JoinItem {
-    int parts;  // 0: none
-    int q0;     // first token of the sequence
-    int head;   // key/value head
-    int row0, rows;
+// A CTA's part of an item that several CTAs share.
+struct Part {
+    int first, parts, index;  // CTA whose range the item starts in, CTAs that share it, this one's place among them
+    int q0, head, row0, rows;  // the sequence's first token, key/value head, rows of the item
+};
+
+// How a kernel's work is cut: rows and positions of a unit, an item's extra
+// cost, the least cost worth a CTA of its own.  The two key tiles next to an
+// end of an item of more than SNAP_ROWS rows are not cut off: joining so many
+// rows takes as long.
+template <int ROWS_, int KEYS_, int EXTRA_, int LEAST_, int SNAP_ROWS_>
+struct Cut {
+    static constexpr int ROWS = ROWS_, KEYS = KEYS_, EXTRA = EXTRA_, LEAST = LEAST_, SNAP_ROWS = SNAP_ROWS_;
 };
 
 struct Item {
-    int nrt;     // row tiles of the sequence
+    int rows;    // of the tile
     int lo, hi;  // positions [lo, hi) seen by any row of the tile
     int t0, nt;  // key tiles t0 .. t0 + nt - 1 (nt >= 1: an item that sees nothing still writes its zeros)
 };
 
-template <int ROWS, int KEYS>
+template <class C>
 __device__ __forceinline__ Item item_of(const AttnArgs &a, const Seq &s, int rt) {
+    constexpr int ROWS = C::ROWS, KEYS = C::KEYS;
     Item it;
     const int rows = s.qn * (int)a.group.d;
-    it.nrt = (rows + ROWS - 1) / ROWS;
     const int r0 = rt * ROWS, r1 = min(r0 + ROWS, rows) - 1;
+    it.rows = r1 - r0 + 1;
     const int p0 = s.kv - s.qn + r0 / a.group, p1 = s.kv - s.qn + r1 / a.group;
     it.hi = a.causal ? min(max(p1 + 1, 0), s.kv) : s.kv;
     it.lo = a.window > 0 ? min(max(p0 - a.window + 1, 0), it.hi) : 0;
@@ -66,12 +77,13 @@ __device__ __forceinline__ Item item_of(const AttnArgs &a, const Seq &s, int rt)
     return it;
 }
 
-// Units of one key/value head of sequence s, summed by one thread or (WARP) by a warp.
-template <int ROWS, int KEYS, bool WARP>
-__device__ __forceinline__ uint32_t head_units(const AttnArgs &a, const Seq &s) {
-    const int nrt = (s.qn * (int)a.group.d + ROWS - 1) / ROWS;
+// Cost of one key/value head of sequence s, summed by one thread or (WARP) by a warp.
+template <class C, bool WARP>
+__device__ __forceinline__ uint32_t head_cost(const AttnArgs &a, const Seq &s) {
+    const int nrt = (s.qn * (int)a.group.d + C::ROWS - 1) / C::ROWS;
     uint32_t n = 0;
-    for (int rt = WARP ? (int)(threadIdx.x & 31) : 0; rt < nrt; rt += WARP ? 32 : 1) n += item_of<ROWS, KEYS>(a, s, rt).nt;
+    for (int rt = WARP ? (int)(threadIdx.x & 31) : 0; rt < nrt; rt += WARP ? 32 : 1)
+        n += item_of<C>(a, s, rt).nt + C::EXTRA;
     return WARP ? __reduce_add_sync(~0u, n) : n;
 }
 
@@ -84,19 +96,19 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {  // inclus
     return v;
 }
 
-// Where a CTA's range begins, and how many units it has.  The first `extra`
-// CTAs have per + 1 units, the others per.  (Calls of 2^31 units and more are
+// Where a CTA's range begins, and its length.  The first `more` CTAs' ranges
+// are per + 1 long, the others' per.  (Calls whose cost may reach 2^31 are
 // refused on the host.)
 struct Plan {
-    uint32_t total, per, extra;
+    uint32_t per, more;
     uint32_t first, count;
-    int b, head, rt, tile;  // first unit: sequence, head, row tile, key tile within the item
+    int b, head, rt, off;  // its first item: sequence, head, row tile; how far into the item's cost it begins
 };
 
-// The CTA whose range holds a unit.
-__device__ __forceinline__ uint32_t unit_owner(const Plan &p, uint32_t unit) {
-    const uint32_t cut = p.extra * (p.per + 1);
-    return unit < cut ? unit / (p.per + 1) : p.extra + (unit - cut) / p.per;
+// The CTA whose range holds a unit of cost.
+__device__ __forceinline__ uint32_t owner(const Plan &p, uint32_t at) {
+    const uint32_t cut = p.more * (p.per + 1);
+    return at < cut ? at / (p.per + 1) : p.more + (at - cut) / p.per;
 }
 
 struct PlanShared {
@@ -106,9 +118,9 @@ struct PlanShared {
 
 // Called by all THREADS threads of the CTA.  Workers (threads, or warps where
 // sequences have many row tiles) sum contiguous runs of sequences; a scan
-// over the workers finds the run that holds the CTA's first unit, and its
-// worker walks down to the sequence, head, row tile and key tile.
-template <int ROWS, int KEYS, int THREADS, int MIN_UNITS, bool WARP>
+// over the workers finds the run that holds the beginning of the CTA's range,
+// and its worker walks down to the sequence, head and row tile.
+template <class C, int THREADS, bool WARP>
 __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) {
     constexpr uint32_t W = THREADS / 32;
     const int lane = threadIdx.x & 31;
@@ -116,14 +128,14 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
     const uint32_t worker = WARP ? warp : threadIdx.x, workers = WARP ? W : THREADS;
     const uint32_t batch = (uint32_t)a.b.batch, per = (batch + workers - 1) / workers;
     const uint32_t b0 = min(worker * per, batch), b1 = min(b0 + per, batch);
-    uint32_t mine = 0, units = 0;  // units: of a head of the worker's last sequence
+    uint32_t mine = 0, cost = 0;  // cost: of a head of the worker's last sequence
     Seq s = {0, 0, 0};
     for (uint32_t b = b0; b < b1; ++b) {
         s = load_seq(a.b, (int)b);
-        units = head_units<ROWS, KEYS, WARP>(a, s);
-        mine += units * a.kv_heads;
+        cost = head_cost<C, WARP>(a, s);
+        mine += cost * a.kv_heads;
     }
-    uint32_t before = 0, warp_sum = mine;  // units of earlier workers
+    uint32_t before = 0, warp_sum = mine;  // cost of earlier workers
     if (!WARP) {
         const uint32_t inc = warp_scan(mine, lane);
         before = inc - mine;
@@ -140,31 +152,30 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
     }
     uint32_t ctas = gridDim.x;
     const uint32_t c = blockIdx.x;
-    if (total < ctas * MIN_UNITS) ctas = max((total + MIN_UNITS - 1) / MIN_UNITS, 1u);
+    if (total < ctas * C::LEAST) ctas = max((total + C::LEAST - 1) / C::LEAST, 1u);
     Plan p;
-    p.total = total;
     p.per = total / ctas;
-    p.extra = total - p.per * ctas;
-    p.first = p.per * c + min(c, p.extra);
-    p.count = c < ctas ? p.per + (c < p.extra ? 1 : 0) : 0;
+    p.more = total - p.per * ctas;
+    p.first = p.per * c + min(c, p.more);
+    p.count = c < ctas ? p.per + (c < p.more ? 1 : 0) : 0;
     if (p.count > 0 && p.first >= before && p.first - before < mine) {
         uint32_t res = p.first - before;
         uint32_t b = b0;
         if (b1 - b0 > 1)
             for (;; ++b) {
                 s = load_seq(a.b, (int)b);
-                units = head_units<ROWS, KEYS, WARP>(a, s);
-                if (res < units * a.kv_heads) break;
-                res -= units * a.kv_heads;
+                cost = head_cost<C, WARP>(a, s);
+                if (res < cost * a.kv_heads) break;
+                res -= cost * a.kv_heads;
             }
         p.b = (int)b;
-        p.head = (int)(res / units);
-        res -= p.head * units;
+        p.head = (int)(res / cost);
+        res -= p.head * cost;
         int rt = 0;
         if (WARP) {  // 32 row tiles at a time
-            const int nrt = (s.qn * (int)a.group.d + ROWS - 1) / ROWS;
+            const int nrt = (s.qn * (int)a.group.d + C::ROWS - 1) / C::ROWS;
             for (;; rt += 32) {
-                const uint32_t v = rt + lane < nrt ? item_of<ROWS, KEYS>(a, s, rt + lane).nt : 0;
+                const uint32_t v = rt + lane < nrt ? item_of<C>(a, s, rt + lane).nt + C::EXTRA : 0;
                 const uint32_t inc = warp_scan(v, lane);
                 const unsigned m = __ballot_sync(~0u, inc > res);
                 if (m) {
@@ -177,73 +188,88 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
             }
         } else {
             for (;; ++rt) {
-                const uint32_t v = item_of<ROWS, KEYS>(a, s, rt).nt;
+                const uint32_t v = item_of<C>(a, s, rt).nt + C::EXTRA;
                 if (res < v) break;
                 res -= v;
             }
         }
         p.rt = rt;
-        p.tile = (int)res;
+        p.off = (int)res;
         if (!WARP || lane == 0) sh.plan = p;
     }
     if (p.count == 0 && threadIdx.x == 0) sh.plan = p;
     __syncthreads();
 }
 
-template <int ROWS, int KEYS, int THREADS, int MIN_UNITS>
+template <class C, int THREADS>
 __device__ __forceinline__ void make_plan(const AttnArgs &a, PlanShared &sh) {
     if (a.few_tiles)
-        make_plan_by<ROWS, KEYS, THREADS, MIN_UNITS, false>(a, sh);
+        make_plan_by<C, THREADS, false>(a, sh);
     else
-        make_plan_by<ROWS, KEYS, THREADS, MIN_UNITS, true>(a, sh);
+        make_plan_by<C, THREADS, true>(a, sh);
 }
 
-// Walks a CTA's range piece by piece (a piece: its units of one item).
-template <int ROWS, int KEYS>
+// Walks a CTA's range piece by piece (a piece: its key tiles of one item).
+template <class C>
 struct Pieces {
+    static constexpr int ROWS = C::ROWS;
     const AttnArgs &a;
-    uint32_t left;  // units not yet handed out
-    uint32_t at;    // index of the next unit
-    int b, head, rt, tile;
+    uint32_t left;  // of the range's cost
+    uint32_t at;    // cost before the next item
+    int b, head, rt, off;
     Seq s;
     // the piece
     Item it;
-    int n;              // key tiles it.t0 + tile0 .. of the piece
+    int n;              // key tiles it.t0 + tile0 .. of the piece, one at least
     int tile0;          // first of them, within the item
     bool begins, ends;  // it holds the item's first and last tile
 
     __device__ __forceinline__ Pieces(const AttnArgs &args, const Plan &p)
-        : a(args), left(p.count), at(p.first), b(p.b), head(p.head), rt(p.rt), tile(p.tile) {
+        : a(args), left(p.count), at(p.first - p.off), b(p.b), head(p.head), rt(p.rt), off(p.off) {
         if (left > 0) s = load_seq(a.b, b);
     }
 
+    // Cuts at key tile uncut_lo() or before are moved to the item's beginning,
+    // at uncut_hi() or after to its end.
+    __device__ __forceinline__ int snap() const { return it.rows > C::SNAP_ROWS ? 2 : 0; }
+    __device__ __forceinline__ int uncut_lo() const { return min(snap(), it.nt / 2); }
+    __device__ __forceinline__ int uncut_hi() const { return max(it.nt - snap(), it.nt / 2 + 1); }
+    __device__ __forceinline__ int snapped(int cut) const {
+        return cut <= uncut_lo() ? 0 : (cut >= uncut_hi() ? it.nt : cut);
+    }
+
     __device__ __forceinline__ bool next() {
-        if (left == 0) return false;
-        while (rt * ROWS >= s.qn * (int)a.group.d) {  // past the sequence's row tiles
-            rt = 0;
-            if (s.qn == 0 || ++head == a.kv_heads) {
-                head = 0;
-                s = load_seq(a.b, ++b);
+        while (left > 0) {
+            while (rt * ROWS >= s.qn * (int)a.group.d) {  // past the sequence's row tiles
+                rt = 0;
+                if (s.qn == 0 || ++head == a.kv_heads) {
+                    head = 0;
+                    s = load_seq(a.b, ++b);
+                }
             }
+            it = item_of<C>(a, s, rt);
+            const int cost = it.nt + C::EXTRA, end = (int)min((uint32_t)cost, left + off);
+            tile0 = snapped(off - C::EXTRA);
+            n = snapped(end - C::EXTRA) - tile0;
+            begins = tile0 == 0;
+            ends = tile0 + n == it.nt;
+            left -= end - off;
+            at += cost;
+            off = 0;
+            ++rt;
+            if (n > 0) return true;  // else another CTA has all that this one might have of the item
         }
-        it = item_of<ROWS, KEYS>(a, s, rt);
-        tile0 = tile;
-        n = (int)min((uint32_t)(it.nt - tile), left);
-        begins = tile == 0;
-        ends = tile + n == it.nt;
-        left -= n;
-        at += n;
-        tile = 0;
-        ++rt;
-        return true;
+        return false;
     }
     __device__ __forceinline__ int row0() const { return (rt - 1) * ROWS; }
-    __device__ __forceinline__ int rows() const { return min(ROWS, s.qn * (int)a.group.d - row0()); }
+    __device__ __forceinline__ int rows() const { return it.rows; }
     // Partial-result slot of a piece that is not a whole item.
     __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (begins ? 1 : 0); }
-    // CTAs that share the item of a piece that begins but does not end it.
-    __device__ __forceinline__ int parts(const Plan &p) const {
-        return (int)(unit_owner(p, at - n + it.nt - 1) - blockIdx.x + 1);
+    // Of a piece that is not a whole item.
+    __device__ __forceinline__ Part part(const Plan &p) const {
+        const int first = begins ? (int)blockIdx.x : (int)owner(p, at - it.nt + uncut_lo());
+        const int last = ends ? (int)blockIdx.x : (int)owner(p, at - it.nt + uncut_hi() - 1);
+        return Part{first, last - first + 1, (int)blockIdx.x - first, s.q0, head, row0(), rows()};
     }
 };
 
@@ -324,19 +350,55 @@ __device__ __forceinline__ float log_sum(float mx, float sum) {
 // lies in the odd slot of c, every later part in the even slot of the next ones.
 __device__ __forceinline__ long long part_slot(int c, int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); }
 
-// Launch as a programmatic dependent of the kernel before it on the stream.
+// Counts a part in: its partial results were written by threads that the
+// calling thread has synchronised with.
+__device__ __forceinline__ void part_written(const AttnArgs &a, const Part &p) {
+    __threadfence();
+    asm volatile("fence.proxy.async;" ::: "memory");  // (where copies read it)
+    atomicAdd(a.arrived + p.first, 1u);
+}
+
+// Until `count` arrivals for the item (bounded; on expiry its rows stay
+// unwritten, w4a16_device_status says so and the workspace has to be zeroed).
+__device__ __forceinline__ bool parts_written(const AttnArgs &a, const Part &p, unsigned count) {
+    uint64_t t0 = 0;
+    for (uint32_t spin = 0;; ++spin) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.arrived + p.first) : "memory");
+        if (v == count) return true;
+        if ((spin & 63) == 63) {
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitNs) break;
+        }
+    }
+    atomicExch(&g_wait_expired, 1);
+    return false;
+}
+
+// The last of the `joiners` CTAs to be done with an item resets its counters.
+__device__ __forceinline__ void part_joined(const AttnArgs &a, const Part &p, unsigned joiners) {
+    if (atomicAdd(a.left + p.first, 1u) == joiners - 1) {
+        a.arrived[p.first] = 0;
+        a.left[p.first] = 0;
+    }
+}
+
+// Launch with every CTA resident (they wait for one another's parts).
 template <class K>
-int launch_dependent(K kernel, dim3 grid, int threads, const AttnArgs &a, cudaStream_t stream) {
+int launch_resident(K kernel, int grid, int threads, size_t smem, cudaStream_t stream, const CUtensorMap &mk,
+                    const CUtensorMap &mv, const AttnArgs &a) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    attr.id = cudaLaunchAttributeCooperative;
+    attr.val.cooperative = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, mk, mv, a) != cudaSuccess) {
         cudaGetLastError();
         return W4_ERR_LAUNCH;
     }

@@ -34,6 +34,8 @@ namespace w4a16 {
 namespace {
 
 constexpr int QROWS = 256, KEYS = 128;
+using Work = Cut<QROWS, KEYS, 3, 4, 128>;
+constexpr int FEW_PARTS = 4;
 constexpr int TC_THREADS = 384;
 // Registers a thread: 168 at launch (64512 in all); the softmax's two warp
 // groups take what the third (copies, MMA issue) gives up.
@@ -47,7 +49,7 @@ struct TcCfg {
     static constexpr int HALVES = DP / 64;
     static constexpr int TILE = HALVES * HALF;                    // 128 rows of Q, K or V
     static constexpr int SLOTS = DP == 64 ? 8 : 5;                // ring of K and V tiles
-    static constexpr int BARS = 2 * SLOTS + 2 * 6 + 1;
+    static constexpr int BARS = 2 * SLOTS + 2 * 6 + 2;
     static constexpr size_t SMEM = 1024 + (size_t)(2 + SLOTS) * TILE + 8 * BARS + 16;
     // Tensor-memory columns.  A head of 64 leaves room for P beside S; with
     // 128, P_t lies in the columns of S_t, whose next product therefore waits
@@ -163,17 +165,149 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
     return d;
 }
 
-// Scores of positions 32 C .. 32 C + 31 of a unit: those outside [lo, hi) to
-// -infinity, maxima of the others into m4.
+// Scores of positions 32 C .. 32 C + 31 of a unit: those outside [lo, hi) to -infinity.
 template <int C>
-__device__ __forceinline__ void mask_and_max(uint32_t (&s)[32], float (&m4)[4], bool masked, int lo, int hi) {
-    if (masked) {
+__device__ __forceinline__ void mask(uint32_t (&s)[32], int lo, int hi) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (32 * C + i < lo || 32 * C + i >= hi) s[i] = 0xFF800000u;
+    for (int i = 0; i < 32; ++i)
+        if (32 * C + i < lo || 32 * C + i >= hi) s[i] = 0xFF800000u;
+}
+
+// Probabilities 2^(s scale + minus) of 32 scores, rounded to binary16 in p
+// and summed (unrounded) into s2; with MAX the maxima of s and u into m4.
+template <bool MAX>
+__device__ __forceinline__ void exps(const uint32_t (&s)[32], const uint32_t (&u)[32], uint32_t (&p)[16], f32x2 scale2,
+                                     float minus, f32x2 (&s2)[2], float (&m4)[4]) {
+    const f32x2 minus2 = pair(minus, minus);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float2 e = both(fma2(pair(s[2 * i], s[2 * i + 1]), scale2, minus2));
+        e.x = exp2_approx(e.x);
+        e.y = exp2_approx(e.y);
+        if (MAX) {
+            m4[i & 1] = max3(m4[i & 1], s[2 * i], s[2 * i + 1]);
+            m4[2 + (i & 1)] = max3(m4[2 + (i & 1)], u[2 * i], u[2 * i + 1]);
+        }
+        s2[i & 1] = add2(s2[i & 1], pair(e.x, e.y));
+        p[i] = pack2(e.x, e.y);
     }
+}
+
+// Rows that a shared item's parts are stored with (4 columns of all rows
+// together, [head_dim / 4][part_rows][4], so that a range of columns is one
+// contiguous copy).
+__device__ __forceinline__ int part_rows(int rows) { return (rows + 31) & ~31; }
+
+// This CTA's columns of a shared item, groups of 4 from g0 to g1, by the 256
+// softmax threads, a thread to a row: the parts' columns are copied into the
+// ring (and their statistics over Q), as many parts at a time as fit, and
+// summed in the parts' order.
+template <int DP, class Sync>
+__device__ __forceinline__ void join_columns(const AttnArgs &a, const Part &part, int g0, int g1, uint32_t ring,
+                                             uint32_t ml_sh, uint32_t bar, uint32_t &phase, Sync sync) {
+    constexpr int MOST = DP / 8;  // groups of 4 columns of one of at least two CTAs
+    const int rows = part_rows(part.rows), r = threadIdx.x, ng = g1 - g0;
+    const uint32_t bytes = (uint32_t)(ng * rows * 16), ml_bytes = (uint32_t)(rows * 8);
+    const int most = min(TcCfg<DP>::SLOTS * TcCfg<DP>::TILE / (int)bytes, 2 * TcCfg<DP>::TILE / (QROWS * 8));
+    float mx = -INFINITY, sum = 0.f;
+    float4 acc[MOST];
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) m4[i / 2 % 4] = max3(m4[i / 2 % 4], s[i], s[i + 1]);
+    for (int g = 0; g < MOST; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < part.parts; p0 += most) {
+        const int n = min(most, part.parts - p0);
+        if (threadIdx.x == 0) {
+            mbar_expect_tx(bar, n * (bytes + ml_bytes));
+            for (int k = 0; k < n; ++k) {
+                const long long slot = part_slot(part.first, p0 + k);
+                bulk_load(ml_sh + k * ml_bytes, a.part_ml + slot * QROWS * 2, ml_bytes, bar);
+                bulk_load(ring + k * bytes, a.part_o + slot * QROWS * a.head_dim + (long long)g0 * rows * 4, bytes, bar);
+            }
+        }
+        wait(bar, phase, nullptr);
+        phase ^= 1;
+        if (r < part.rows) {
+            for (int k = 0; k < n; ++k) {
+                float2 ml;
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ml.x), "=f"(ml.y) : "r"(ml_sh + k * ml_bytes + 8 * r));
+                const float top = fmaxf(mx, ml.x), f0 = corr(mx, top), f1 = corr(ml.x, top);
+                mx = top;
+                sum = sum * f0 + ml.y * f1;
+#pragma unroll
+                for (int g = 0; g < MOST; ++g) {
+                    if (g >= ng) break;
+                    const uint4 v = lds128(ring + k * bytes + (g * rows + r) * 16);
+                    acc[g].x = acc[g].x * f0 + __uint_as_float(v.x) * f1;
+                    acc[g].y = acc[g].y * f0 + __uint_as_float(v.y) * f1;
+                    acc[g].z = acc[g].z * f0 + __uint_as_float(v.z) * f1;
+                    acc[g].w = acc[g].w * f0 + __uint_as_float(v.w) * f1;
+                }
+            }
+        }
+        fence_proxy_async_smem();  // the reads above, before the next copies
+        sync();
+    }
+    if (r >= part.rows) return;
+    const int gr = part.row0 + r, head = part.head * (int)a.group.d + gr % a.group;
+    const long long tok = part.q0 + gr / a.group;
+    const float inv = inverse(sum);
+    uint16_t *y = a.y + tok * a.y_token + head * a.y_head + 4 * g0;
+#pragma unroll
+    for (int g = 0; g < MOST; ++g) {
+        if (g >= ng) break;
+        *reinterpret_cast<uint2 *>(y + 4 * g) =
+            make_uint2(pack2(acc[g].x * inv, acc[g].y * inv), pack2(acc[g].z * inv, acc[g].w * inv));
+    }
+    if (a.lse && g0 == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
+}
+
+// Block x of a shared item of many parts: 32 rows x 32 columns, a lane to a
+// row, a warp to 4 columns, 16 parts' loads in flight.
+__device__ __forceinline__ void join_block(const AttnArgs &a, const Part &part, int x) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col_blocks = (a.head_dim + 31) / 32, groups = a.head_dim / 4, rows = part_rows(part.rows);
+    const int rb = x / col_blocks, r = 32 * rb + lane, g = 8 * (x - rb * col_blocks) + warp;
+    if (r >= part.rows || g >= groups) return;
+    float mx = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < part.parts; i0 += 16) {
+        float4 v[16];
+        float2 c[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            c[k] = make_float2(-INFINITY, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + k < part.parts) {
+                const long long slot = part_slot(part.first, i0 + k);
+                c[k] = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + slot * QROWS + r);
+                v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + slot * groups * QROWS + g * rows + r);
+            }
+        }
+        float top = mx;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) top = fmaxf(top, c[k].x);
+        const float f0 = corr(mx, top);
+        mx = top;
+        sum *= f0;
+        acc.x *= f0;
+        acc.y *= f0;
+        acc.z *= f0;
+        acc.w *= f0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float f = corr(c[k].x, top);
+            sum += c[k].y * f;
+            acc.x += v[k].x * f;
+            acc.y += v[k].y * f;
+            acc.z += v[k].z * f;
+            acc.w += v[k].w * f;
+        }
+    }
+    const int gr = part.row0 + r, head = part.head * (int)a.group.d + gr % a.group;
+    const long long tok = part.q0 + gr / a.group;
+    const float inv = inverse(sum);
+    *reinterpret_cast<uint2 *>(a.y + tok * a.y_token + head * a.y_head + 4 * g) =
+        make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
+    if (a.lse && g == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
 }
 
 template <int DP>
@@ -189,7 +323,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const uint32_t bar0 = ring + C::SLOTS * C::TILE;
     uint8_t *tail = smem_raw + (bar0 - raw) + 8 * C::BARS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail);
-    volatile int *abort = reinterpret_cast<volatile int *>(tail + 4);
+    volatile int *abort = reinterpret_cast<volatile int *>(tail + 4), *join_ok = abort + 1;
     auto kv_full = [&](int s) { return bar0 + 8u * s; };
     auto kv_empty = [&](int s) { return bar0 + 8u * (C::SLOTS + s); };
     auto q_full = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + t); };      // Q_t written
@@ -198,10 +332,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     // A half (64 positions) of P_t written (and S_t read, O_t rescaled).
     auto p_full = [&](int t, int h) { return bar0 + 8u * (2 * C::SLOTS + 6 + 2 * t + h); };
     auto turn = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 10 + t); };  // tile t may issue its products
-    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 12);
+    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 12), join_bar = end_bar + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(kv_full(s), 1);
@@ -216,8 +349,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             mbar_init(turn(t), 1);
         }
         mbar_init(end_bar, 2);
+        mbar_init(join_bar, 1);
         *abort = 0;
-        a.joins[blockIdx.x].parts = 0;
         prefetch_maps(&map_k, &map_v);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -227,11 +360,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     fence_before();
-    make_plan<QROWS, KEYS, TC_THREADS, 1>(a, plan_sh);  // (its barriers also publish the above)
+    make_plan<Work, TC_THREADS>(a, plan_sh);  // (its barriers also publish the above)
     fence_after();
     const uint32_t tmem = *tmem_slot;
     const Plan plan = plan_sh.plan;
-    Pieces<QROWS, KEYS> pc(a, plan);
+    Pieces<Work> pc(a, plan);
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
@@ -368,33 +501,60 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const uint32_t my_rows = base + t * C::TILE + 32 * quad * 128;
         auto stage_at = [&](int rl, int ch) { return my_rows + (ch / 8) * HALF + rl * 128 + (((ch ^ rl) & 7) << 4); };
         const f32x2 scale2 = pair(a.scale, a.scale);
+        Part shared0, shared1;  // items that this CTA shares with earlier and later ones
+        int shares = 0;
+        bool unsignalled = false;  // this thread has a part to count in
         uint32_t steps = 0;
         int it = 0;
         while (pc.next()) {
             const int first_slot = it;
             it += 2 * pc.n;
             const int rows = pc.rows(), row0 = pc.row0();
-            if (128 * t >= rows) continue;
+            const bool whole = pc.begins && pc.ends;
+            auto note_part = [&] {
+                if (whole) return;
+                if (shares++ == 0)
+                    shared0 = pc.part(plan);
+                else
+                    shared1 = pc.part(plan);
+            };
+            auto signal_part = [&] {  // (of the first shared item: a later one is this CTA's last)
+                if (unsignalled) part_written(a, shared0);
+                unsignalled = false;
+            };
+            if (128 * t >= rows) {
+                signal_part();
+                note_part();
+                continue;
+            }
             const int r = 128 * t + 32 * quad + lane;  // this thread's row of the item
             const bool in = r < rows;
             const int gr = row0 + r;
             const long long tok = pc.s.q0 + gr / a.group;
             const int head = pc.head * (int)a.group.d + gr % a.group;
             // Q_t: the warp's 32 rows, 16 bytes a lane, swizzled, all in flight together.
+            // Four lanes take 64 bytes of a row, 8 rows at a time: a row's address is needed once.
             const long long q_row = in ? tok * a.q_token + head * a.q_head : -1;
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i) {
-                const int x = 32 * i + lane, rl = x / (DP / 8), ch = x % (DP / 8);
+            for (int rb = 0; rb < 32; rb += 8) {
+                const int rl = rb + (lane >> 2);
                 const long long at = __shfl_sync(~0u, q_row, rl);
-                const bool has = at >= 0 && 8 * ch < a.head_dim;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(stage_at(rl, ch)),
-                             "l"(has ? a.q + at + 8 * ch : a.q), "r"(has ? 16 : 0)
-                             : "memory");
+                const uint16_t *src = a.q + (at >= 0 ? at : 0) + 8 * (lane & 3);
+#pragma unroll
+                for (int c4 = 0; c4 < DP / 8; c4 += 4) {
+                    const int ch = c4 + (lane & 3);
+                    const bool has = at >= 0 && 8 * ch < a.head_dim;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(stage_at(rl, ch)),
+                                 "l"(has ? src + 8 * c4 : a.q), "r"(has ? 16 : 0)
+                                 : "memory");
+                }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full(t));
+            signal_part();  // now that there is time, until S_t is there
+            note_part();
 
             const int p = pc.s.kv - pc.s.qn + gr / a.group;
             const int ub = in ? (a.causal ? min(p + 1, pc.s.kv) : pc.s.kv) : 0;
@@ -411,28 +571,31 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 wait(s_full(t), steps & 1, abort);
                 fence_after();
                 uint32_t sr[4][32];
-                tmem_load(s_at, sr[0]);
-                tmem_load(s_at + 32, sr[1]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_load(s_at + 32 * c, sr[c]);
                 tmem_load_wait();
-                tmem_load(s_at + 64, sr[2]);
-                tmem_load(s_at + 96, sr[3]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_loaded(sr[c]);
+                if (j0 + KEYS > all_ub || j0 < all_lb) {
+                    const int lo = lb - j0, hi = ub - j0;
+                    mask<0>(sr[0], lo, hi);
+                    mask<1>(sr[1], lo, hi);
+                    mask<2>(sr[2], lo, hi);
+                    mask<3>(sr[3], lo, hi);
+                }
+                // The first half's exponentials against the reference so far, while the unit's maximum is found: the
+                // reference mostly holds.
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                const bool masked = j0 + KEYS > all_ub || j0 < all_lb;
-                const int lo = lb - j0, hi = ub - j0;
-                tmem_loaded(sr[0]);
-                tmem_loaded(sr[1]);
-                mask_and_max<0>(sr[0], m4, masked, lo, hi);
-                mask_and_max<1>(sr[1], m4, masked, lo, hi);
-                tmem_load_wait();
-                tmem_loaded(sr[2]);
-                tmem_loaded(sr[3]);
-                mask_and_max<2>(sr[2], m4, masked, lo, hi);
-                mask_and_max<3>(sr[3], m4, masked, lo, hi);
+                uint32_t pr[2][16];
+                f32x2 s2[2] = {0, 0};
+                float minus = ref == -INFINITY ? 0.f : -ref;
+                exps<true>(sr[0], sr[2], pr[0], scale2, minus, s2, m4);
+                exps<true>(sr[1], sr[3], pr[1], scale2, minus, s2, m4);
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale;
                 const bool grow = mx > ref + kGrow || (ref == -INFINITY && mx > ref);
                 if (__any_sync(~0u, grow)) {
                     const float nr = grow ? mx : ref;
-                    const float c = ref == -INFINITY ? 0.f : exp2_approx(ref - nr);
+                    const float c = grow ? corr(ref, nr) : 1.f;
                     if (j > 0) {
                         wait(o_done(t), (steps - 1) & 1, abort);
                         fence_after();
@@ -442,17 +605,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                             tmem_load(o_at + 32 * cb, o);
                             tmem_load_wait();
                             tmem_loaded(o);
-                            const float f = grow ? c : 1.f;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
                             tmem_store(o_at + 32 * cb, o);
                         }
                         tmem_store_wait();
                     }
-                    if (grow) {
-                        sum *= c;
-                        ref = nr;
-                    }
+                    sum *= c;
+                    ref = nr;
+                    minus = ref == -INFINITY ? 0.f : -ref;
+                    s2[0] = s2[1] = 0;
+                    exps<false>(sr[0], sr[2], pr[0], scale2, minus, s2, m4);
+                    exps<false>(sr[1], sr[3], pr[1], scale2, minus, s2, m4);
                 }
                 if (j0 < pc.it.lo || j0 + KEYS > pc.it.hi) {
                     // Rows of V that the item does not see: one to a thread (both tiles write the same zeros, each
@@ -469,27 +633,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                const float minus = ref == -INFINITY ? 0.f : -ref;
-                const f32x2 minus2 = pair(minus, minus);
-                f32x2 s2[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pr[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 e = both(fma2(pair(sr[c][2 * i], sr[c][2 * i + 1]), scale2, minus2));
-                        e.x = exp2_approx(e.x);
-                        e.y = exp2_approx(e.y);
-                        s2[i & 1] = add2(s2[i & 1], pair(e.x, e.y));
-                        pr[i] = pack2(e.x, e.y);
+                for (int h = 0; h < 2; ++h) {
+                    if (h) {
+                        exps<false>(sr[2], sr[2], pr[0], scale2, minus, s2, m4);
+                        exps<false>(sr[3], sr[3], pr[1], scale2, minus, s2, m4);
                     }
-                    tmem_store16(p_at + 16 * c, pr);
-                    if (c & 1) {
-                        tmem_store_wait();
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(p_full(t, c >> 1));
-                    }
+                    tmem_store16(p_at + 32 * h, pr[0]);
+                    tmem_store16(p_at + 32 * h + 16, pr[1]);
+                    tmem_store_wait();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(t, h));
                 }
                 const float2 s4 = both(add2(s2[0], s2[1]));
                 sum += s4.x + s4.y;
@@ -498,17 +653,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             // ---------------- the piece's rows ----------------
             wait(o_done(t), (steps - 1) & 1, abort);
             fence_after();
-            const bool whole = pc.begins && pc.ends;
             if (in) {
                 if (!whole)
                     reinterpret_cast<float2 *>(a.part_ml)[(long long)pc.slot() * QROWS + r] = make_float2(ref, sum);
                 else if (a.lse)
                     a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(ref, sum);
             }
-            if (threadIdx.x == 0 && pc.begins && !pc.ends)
-                a.joins[blockIdx.x] = JoinItem{pc.parts(plan), pc.s.q0, pc.head, row0, rows};
             const float inv = inverse(sum);
             float4 *part = reinterpret_cast<float4 *>(a.part_o) + (long long)pc.slot() * QROWS * (a.head_dim / 4) + r;
+            const int p_rows = part_rows(rows);
 #pragma unroll 1
             for (int cb = 0; cb < DP / 32; ++cb) {
                 uint32_t o[32];
@@ -530,7 +683,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         if (32 * cb + i < a.head_dim)
-                            part[(8 * cb + i / 4) * QROWS] =
+                            part[(8 * cb + i / 4) * p_rows] =
                                 make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
                                             __uint_as_float(o[i + 3]));
                 }
@@ -539,14 +692,56 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 __syncwarp();
                 const long long y_row = in ? tok * a.y_token + head * a.y_head : -1;
 #pragma unroll
-                for (int i = 0; i < DP / 8; ++i) {
-                    const int x = 32 * i + lane, rl = x / (DP / 8), ch = x % (DP / 8);
+                for (int rb = 0; rb < 32; rb += 8) {
+                    const int rl = rb + (lane >> 2);
                     const long long at = __shfl_sync(~0u, y_row, rl);
-                    if (at >= 0 && 8 * ch < a.head_dim) *reinterpret_cast<uint4 *>(a.y + at + 8 * ch) = lds128(stage_at(rl, ch));
+                    uint4 v[DP / 32];
+#pragma unroll
+                    for (int k = 0; k < DP / 32; ++k) v[k] = lds128(stage_at(rl, 4 * k + (lane & 3)));
+#pragma unroll
+                    for (int k = 0; k < DP / 32; ++k) {
+                        const int ch = 4 * k + (lane & 3);
+                        if (at >= 0 && 8 * ch < a.head_dim) *reinterpret_cast<uint4 *>(a.y + at + 8 * ch) = v[k];
+                    }
                 }
                 __syncwarp();
             }
             fence_before();  // the reads above, before the next piece's first product writes O_t
+            if (!whole) {
+                if (t == 0)  // this tile's warps
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                else
+                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                unsignalled = (threadIdx.x & 127) == 0;
+            }
+        }
+        // ---------------- join this CTA's share of the items it shares, all eight warps ----------------
+        // (Both tiles' warps meet before the first copy into the ring: every product is done.)
+        if (unsignalled) part_written(a, shares == 1 ? shared0 : shared1);
+        uint32_t join_phase = 0;
+        for (int i = 0; i < shares; ++i) {
+            const Part part = i == 0 ? shared0 : shared1;
+            auto sync = [] { asm volatile("bar.sync 3, 256;" ::: "memory"); };
+            // Few parts: ranges of columns, by copies (LDGs of 128 KB and more ran at 17 bytes a cycle here, against
+            // some 60).  Many: blocks of rows and columns.
+            const bool few = part.parts <= FEW_PARTS;
+            const int groups = a.head_dim / 4, blocks = (part.rows + 31) / 32 * ((a.head_dim + 31) / 32);
+            const int joiners = min(part.parts, few ? groups : blocks);
+            if (part.index >= joiners) continue;
+            if (threadIdx.x == 0) {
+                *join_ok = parts_written(a, part, part.parts * (part.rows > 128 ? 2 : 1)) ? 1 : 0;
+                asm volatile("fence.proxy.async;" ::: "memory");  // the parts were stored by threads, and are read by copies
+            }
+            fence_proxy_async_smem();  // (and shared memory that threads used is written by copies)
+            sync();
+            const bool ok = *join_ok != 0;
+            if (ok && !few)
+                for (int x = part.index; x < blocks; x += joiners) join_block(a, part, x);
+            if (ok && few)
+                join_columns<DP>(a, part, part.index * groups / joiners, (part.index + 1) * groups / joiners, ring, base,
+                                 join_bar, join_phase, sync);
+            sync();
+            if (threadIdx.x == 0 && ok) part_joined(a, part, joiners);
         }
     }
 
@@ -555,77 +750,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if (warp == 9) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-    }
-}
-
-// Join of the items that attn_tc_kernel cut: block (c, n) joins rows 32 n ..
-// 32 n + 31 of the item that starts in the range of CTA c, a lane to a row, a
-// warp to every 8th group of 4 columns.
-constexpr int JOIN_WARPS = 8;
-__global__ void __launch_bounds__(32 * JOIN_WARPS) join_tc_kernel(const __grid_constant__ AttnArgs a) {
-    __shared__ __align__(16) uint16_t out[32][128 + 8];
-    pdl_wait();
-    const JoinItem j = a.joins[blockIdx.x];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = 32 * blockIdx.y + lane;
-    if (32 * (int)blockIdx.y >= j.rows || j.parts == 0) return;
-    const int groups = a.head_dim / 4;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + r;
-    const float4 *po = reinterpret_cast<const float4 *>(a.part_o) + r;
-    float mx = -INFINITY, sum = 0.f;
-    float4 acc[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < j.rows) {
-        for (int i0 = 0; i0 < j.parts; i0 += 4) {  // four parts' loads in flight
-            float4 v[4][4];
-            float2 c[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                c[k] = make_float2(-INFINITY, 0.f);
-                if (i0 + k < j.parts) {
-                    const long long slot = part_slot(blockIdx.x, i0 + k);
-                    c[k] = ml[slot * QROWS];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        if (warp + JOIN_WARPS * g < groups) v[k][g] = po[(slot * groups + warp + JOIN_WARPS * g) * QROWS];
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (i0 + k >= j.parts) break;
-                const float top = fmaxf(mx, c[k].x), f0 = corr(mx, top), f1 = corr(c[k].x, top);
-                mx = top;
-                sum = sum * f0 + c[k].y * f1;
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    if (warp + JOIN_WARPS * g < groups) {
-                        acc[g].x = acc[g].x * f0 + v[k][g].x * f1;
-                        acc[g].y = acc[g].y * f0 + v[k][g].y * f1;
-                        acc[g].z = acc[g].z * f0 + v[k][g].z * f1;
-                        acc[g].w = acc[g].w * f0 + v[k][g].w * f1;
-                    }
-            }
-        }
-        const float inv = inverse(sum);
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-            if (warp + JOIN_WARPS * g < groups)
-                *reinterpret_cast<uint2 *>(&out[lane][4 * (warp + JOIN_WARPS * g)]) =
-                    make_uint2(pack2(acc[g].x * inv, acc[g].y * inv), pack2(acc[g].z * inv, acc[g].w * inv));
-        if (a.lse && warp == 0) {
-            const int gr = j.row0 + r;
-            a.lse[(long long)(j.q0 + gr / a.group) * (a.kv_heads * (int)a.group.d) + j.head * (int)a.group.d +
-                  gr % a.group] = log_sum(mx, sum);
-        }
-    }
-    __syncthreads();
-    const int chunks = a.head_dim / 8;
-    for (int x = threadIdx.x; x < 32 * chunks; x += 32 * JOIN_WARPS) {
-        const int rl = x / chunks, ch = x % chunks, gr = j.row0 + 32 * blockIdx.y + rl;
-        if (32 * (int)blockIdx.y + rl < j.rows)
-            *reinterpret_cast<uint4 *>(a.y + (j.q0 + gr / a.group) * a.y_token +
-                                       (j.head * (int)a.group.d + gr % a.group) * a.y_head + 8 * ch) =
-                *reinterpret_cast<const uint4 *>(&out[rl][8 * ch]);
     }
 }
 
@@ -649,9 +773,7 @@ int launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, i
     static_assert(TcCfg<DP>::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
     if (!regs_ok<DP>()) return W4_ERR_DEVICE;
     if (!set_smem_once(reinterpret_cast<const void *>(attn_tc_kernel<DP>), (int)TcCfg<DP>::SMEM)) return W4_ERR_LAUNCH;
-    attn_tc_kernel<DP><<<grid, TC_THREADS, TcCfg<DP>::SMEM, stream>>>(mk, mv, a);
-    const int st = launch_status();
-    return st != W4A16_OK ? st : launch_dependent(join_tc_kernel, dim3(grid, QROWS / 32), 32 * JOIN_WARPS, a, stream);
+    return launch_resident(attn_tc_kernel<DP>, grid, TC_THREADS, TcCfg<DP>::SMEM, stream, mk, mv, a);
 }
 
 }  // namespace

@@ -39,7 +39,7 @@ template <int DP, int MT>
 struct RowCfg {
     static constexpr int ROWS = 16 * MT;
     static constexpr int KEYS = kv_tile(DP);
-    using Work = Cut<ROWS, KEYS, 2, 3, ROWS>;
+    using Work = Cut<ROWS, KEYS, 2, 1, ROWS>;
     static constexpr int WARPS = KEYS / 16;             // consumers
     static constexpr int THREADS = 32 * (WARPS + 1);
     static constexpr int TILE = KEYS * 128 * (DP / 64); // bytes of K or V
@@ -60,42 +60,56 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
 // Row r of a shared item, by WARPS warps: they take the parts in turn, lane l
 // of each the columns 4 l .. 4 l + 3 (and those 128 further on), and merge
 // through sh.  A part's rows lie one after the other.
-template <int WARPS, int ROWS, class Sync>
+template <int DP, int WARPS, int ROWS, class Sync>
 __device__ __forceinline__ void join_row(const AttnArgs &a, const Part &part, int r, float *sh, Sync sync) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float4 *sh_o = reinterpret_cast<float4 *>(sh);                         // [WARPS][2][32]
     float2 *sh_ml = reinterpret_cast<float2 *>(sh + WARPS * 2 * 32 * 4);  // [WARPS]
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
     float mx = -INFINITY, sum = 0.f;
+    constexpr int H = DP > 128 ? 2 : 1, FLIGHT = 10 / H;  // parts of a warp whose loads are in flight
     float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int i0 = warp; i0 < part.parts; i0 += 4 * WARPS) {  // four parts' loads in flight
-        float4 v[4][2];
-        float2 c[4];
+    for (int i0 = warp; i0 < part.parts; i0 += FLIGHT * WARPS) {
+        float4 v[FLIGHT][H];
+        float2 c[FLIGHT];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < FLIGHT; ++k) {
             const int i = i0 + k * WARPS;
             c[k] = make_float2(-INFINITY, 0.f);
-            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int h = 0; h < H; ++h) v[k][h] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i < part.parts) {
                 const long long row = part_slot(part.first, i) * ROWS + r;
                 c[k] = __ldcg(ml + row);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < H; ++h)
                     if (128 * h + 4 * lane < a.head_dim)
                         v[k][h] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + row * a.head_dim + 128 * h + 4 * lane));
             }
         }
+        float top = mx;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float top = fmaxf(mx, c[k].x), f0 = corr(mx, top), f1 = corr(c[k].x, top);
-            mx = top;
-            sum = sum * f0 + c[k].y * f1;
+        for (int k = 0; k < FLIGHT; ++k) top = fmaxf(top, c[k].x);
+        const float f0 = corr(mx, top);
+        mx = top;
+        sum *= f0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                acc[h].x = acc[h].x * f0 + v[k][h].x * f1;
-                acc[h].y = acc[h].y * f0 + v[k][h].y * f1;
-                acc[h].z = acc[h].z * f0 + v[k][h].z * f1;
-                acc[h].w = acc[h].w * f0 + v[k][h].w * f1;
+        for (int h = 0; h < H; ++h) {
+            acc[h].x *= f0;
+            acc[h].y *= f0;
+            acc[h].z *= f0;
+            acc[h].w *= f0;
+        }
+#pragma unroll
+        for (int k = 0; k < FLIGHT; ++k) {
+            const float f = corr(c[k].x, top);
+            sum += c[k].y * f;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                acc[h].x += v[k][h].x * f;
+                acc[h].y += v[k][h].y * f;
+                acc[h].z += v[k][h].z * f;
+                acc[h].w += v[k][h].w * f;
             }
         }
     }
@@ -475,7 +489,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
         if (threadIdx.x == 0) *abort = parts_written(a, part, part.parts) ? 0 : 1;
         sync();
         const bool ok = *abort == 0;
-        for (int r = part.index; ok && r < part.rows; r += joiners) join_row<C::WARPS, ROWS>(a, part, r, merge, sync);
+        for (int r = part.index; ok && r < part.rows; r += joiners) join_row<DP, C::WARPS, ROWS>(a, part, r, merge, sync);
         sync();
         if (threadIdx.x == 0 && ok) part_joined(a, part, joiners);
     }

@@ -15,14 +15,16 @@
 //    operands in shared memory) and O_t += P_t V (P_t from tensor memory).
 //    (One thread for both tiles was itself the bound: 3850 cycles a unit.)
 //  * Warps 0-3 and 4-7: softmax of tile 0 and 1, one thread to a row, so row
-//    maxima and sums need no exchange.  Each half of P_t is handed over as it
-//    is written, so its product with V starts while the other half's
-//    exponentials are taken.  O_t is rescaled in tensor memory only
-//    when a row's maximum has grown by more than 2^8 since the last time:
-//    until then probabilities are taken against the older maximum, which
-//    makes them at most 256 and changes nothing else (the quotient o / l does
-//    not depend on the reference; binary16 holds 256 with the same relative
-//    precision as 1).
+//    sums need no exchange.  Each half of P_t is handed over as it is written,
+//    so its product with V starts while the other half's exponentials are
+//    taken.  (Two threads to a row, with 16 warps: no faster; tensor memory's
+//    loads and stores and the agreement of the two took what was won.)
+//  * Probabilities are taken against a reference that mostly stays: the
+//    maximum of the row's first 64 positions.  Any reference gives the same
+//    quotient o / l, and binary16 holds 2^15 with the same relative precision
+//    as 1; so no unit's maximum is looked for.  Only where the sum of 64
+//    probabilities passes 2^15 (none can have, up to there) is the reference
+//    raised to the maximum and O_t rescaled in tensor memory.
 //  * Positions outside a row's range get probability 0; rows of V that no row
 //    of the item sees are zeroed in shared memory, as they may hold anything.
 #include <math.h>
@@ -42,14 +44,14 @@ constexpr int TC_THREADS = 384;
 constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 208, REGS_OTHER = 88;
 static_assert(2 * REGS_SOFTMAX + REGS_OTHER == 3 * REGS_LAUNCH, "register split");
 constexpr int HALF = KEYS * 128;  // bytes of 64 columns of 128 rows
-constexpr float kGrow = 8.f;      // growth of the maximum (base 2) that rescales
+constexpr float kMostSum = 32768.f;  // of 64 probabilities: 2^15, half of what binary16 holds
 
 template <int DP>
 struct TcCfg {
     static constexpr int HALVES = DP / 64;
     static constexpr int TILE = HALVES * HALF;                    // 128 rows of Q, K or V
     static constexpr int SLOTS = DP == 64 ? 8 : 5;                // ring of K and V tiles
-    static constexpr int BARS = 2 * SLOTS + 2 * 6 + 2;
+    static constexpr int BARS = 2 * SLOTS + 2 * 7 + 2;
     static constexpr size_t SMEM = 1024 + (size_t)(2 + SLOTS) * TILE + 8 * BARS + 16;
     // Tensor-memory columns.  A head of 64 leaves room for P beside S; with
     // 128, P_t lies in the columns of S_t, whose next product therefore waits
@@ -174,20 +176,15 @@ __device__ __forceinline__ void mask(uint32_t (&s)[32], int lo, int hi) {
 }
 
 // Probabilities 2^(s scale + minus) of 32 scores, rounded to binary16 in p
-// and summed (unrounded) into s2; with MAX the maxima of s and u into m4.
-template <bool MAX>
-__device__ __forceinline__ void exps(const uint32_t (&s)[32], const uint32_t (&u)[32], uint32_t (&p)[16], f32x2 scale2,
-                                     float minus, f32x2 (&s2)[2], float (&m4)[4]) {
+// and summed (unrounded) into s2.
+__device__ __forceinline__ void exps(const uint32_t (&s)[32], uint32_t (&p)[16], f32x2 scale2, float minus,
+                                     f32x2 (&s2)[2]) {
     const f32x2 minus2 = pair(minus, minus);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         float2 e = both(fma2(pair(s[2 * i], s[2 * i + 1]), scale2, minus2));
         e.x = exp2_approx(e.x);
         e.y = exp2_approx(e.y);
-        if (MAX) {
-            m4[i & 1] = max3(m4[i & 1], s[2 * i], s[2 * i + 1]);
-            m4[2 + (i & 1)] = max3(m4[2 + (i & 1)], u[2 * i], u[2 * i + 1]);
-        }
         s2[i & 1] = add2(s2[i & 1], pair(e.x, e.y));
         p[i] = pack2(e.x, e.y);
     }
@@ -332,7 +329,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     // A half (64 positions) of P_t written (and S_t read, O_t rescaled).
     auto p_full = [&](int t, int h) { return bar0 + 8u * (2 * C::SLOTS + 6 + 2 * t + h); };
     auto turn = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 10 + t); };  // tile t may issue its products
-    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 12), join_bar = end_bar + 8;
+    auto o_half = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 12 + t); };  // the first half of P_t V done
+    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 14), join_bar = end_bar + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -347,6 +345,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             mbar_init(p_full(t, 1), 4);
             mbar_init(o_done(t), 1);
             mbar_init(turn(t), 1);
+            mbar_init(o_half(t), 1);
         }
         mbar_init(end_bar, 2);
         mbar_init(join_bar, 1);
@@ -467,6 +466,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int s = 0; s < 4; ++s) mma_ts(o_at, p_at + 8 * s, vt + s * (2048 >> 4), id_o, (j | s) != 0);
+                        commit(o_half(t));
                     }
                     await(p_full(t, 1), steps & 1);
                     if (!ok) break;
@@ -565,7 +565,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const int all_ub = a.causal ? min(pf + 1, pc.s.kv) : pc.s.kv;
             const int all_lb = a.window > 0 ? pl - a.window + 1 : 0;
 
-            float ref = -INFINITY, sum = 0.f;  // reference maximum (base-2 scaled scores) and sum
+            // Reference (of scores in base 2) and sum.  (Rows past the item's end see nothing and need no reference.)
+            float ref = in ? -INFINITY : 0.f, sum = 0.f;
             for (int j = 0; j < pc.n; ++j, ++steps) {
                 const int j0 = (pc.it.t0 + pc.tile0 + j) * KEYS;
                 wait(s_full(t), steps & 1, abort);
@@ -582,41 +583,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     mask<1>(sr[1], lo, hi);
                     mask<2>(sr[2], lo, hi);
                     mask<3>(sr[3], lo, hi);
-                }
-                // The first half's exponentials against the reference so far, while the unit's maximum is found: the
-                // reference mostly holds.
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                uint32_t pr[2][16];
-                f32x2 s2[2] = {0, 0};
-                float minus = ref == -INFINITY ? 0.f : -ref;
-                exps<true>(sr[0], sr[2], pr[0], scale2, minus, s2, m4);
-                exps<true>(sr[1], sr[3], pr[1], scale2, minus, s2, m4);
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale;
-                const bool grow = mx > ref + kGrow || (ref == -INFINITY && mx > ref);
-                if (__any_sync(~0u, grow)) {
-                    const float nr = grow ? mx : ref;
-                    const float c = grow ? corr(ref, nr) : 1.f;
-                    if (j > 0) {
-                        wait(o_done(t), (steps - 1) & 1, abort);
-                        fence_after();
-#pragma unroll 1
-                        for (int cb = 0; cb < DP / 32; ++cb) {
-                            uint32_t o[32];
-                            tmem_load(o_at + 32 * cb, o);
-                            tmem_load_wait();
-                            tmem_loaded(o);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
-                            tmem_store(o_at + 32 * cb, o);
-                        }
-                        tmem_store_wait();
-                    }
-                    sum *= c;
-                    ref = nr;
-                    minus = ref == -INFINITY ? 0.f : -ref;
-                    s2[0] = s2[1] = 0;
-                    exps<false>(sr[0], sr[2], pr[0], scale2, minus, s2, m4);
-                    exps<false>(sr[1], sr[3], pr[1], scale2, minus, s2, m4);
                 }
                 if (j0 < pc.it.lo || j0 + KEYS > pc.it.hi) {
                     // Rows of V that the item does not see: one to a thread (both tiles write the same zeros, each
@@ -635,10 +601,42 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (h) {
-                        exps<false>(sr[2], sr[2], pr[0], scale2, minus, s2, m4);
-                        exps<false>(sr[3], sr[3], pr[1], scale2, minus, s2, m4);
+                    uint32_t pr[2][16];
+                    float part_sum;
+#pragma unroll 1
+                    for (bool again = false;; again = true) {
+                        f32x2 s2[2] = {0, 0};
+                        const float minus = ref == -INFINITY ? 0.f : -ref;
+                        exps(sr[2 * h], pr[0], scale2, minus, s2);
+                        exps(sr[2 * h + 1], pr[1], scale2, minus, s2);
+                        const float2 e = both(add2(s2[0], s2[1]));
+                        part_sum = e.x + e.y;
+                        const bool raise = !(part_sum <= kMostSum) || ref == -INFINITY;
+                        if (again || !__any_sync(~0u, raise)) break;
+                        float m = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) m = max3(m, sr[2 * h][i], sr[2 * h + 1][i]);
+                        const float nr = raise ? fmaxf(ref, m * a.scale) : ref;
+                        const float c = nr != ref ? corr(ref, nr) : 1.f;
+                        if (j + h > 0) {  // O_t holds something
+                            wait(h ? o_half(t) : o_done(t), (h ? steps : steps - 1) & 1, abort);
+                            fence_after();
+#pragma unroll 1
+                            for (int cb = 0; cb < DP / 32; ++cb) {
+                                uint32_t o[32];
+                                tmem_load(o_at + 32 * cb, o);
+                                tmem_load_wait();
+                                tmem_loaded(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+                                tmem_store(o_at + 32 * cb, o);
+                            }
+                            tmem_store_wait();
+                        }
+                        sum *= c;
+                        ref = nr;
                     }
+                    sum += part_sum;
                     tmem_store16(p_at + 32 * h, pr[0]);
                     tmem_store16(p_at + 32 * h + 16, pr[1]);
                     tmem_store_wait();
@@ -646,8 +644,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(p_full(t, h));
                 }
-                const float2 s4 = both(add2(s2[0], s2[1]));
-                sum += s4.x + s4.y;
             }
 
             // ---------------- the piece's rows ----------------

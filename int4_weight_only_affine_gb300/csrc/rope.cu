@@ -10,8 +10,7 @@
 // Both calls move every element once in and once out and are bound by that.
 // A lane owns one unit of a head: 8 elements, 16 bytes, which are 4 rotated
 // pairs (of adjacent elements, or 4 elements of each half) or 8 elements to
-// copy.  A warp takes one token and up to kHeadsPerLane * (256 / head_dim)
-// of its heads, so a lane turns the same pairs of each of its heads and
+// copy.  A warp takes one token and up to HPL * (256 / head_dim) of its heads, so a lane turns the same pairs of each of its heads and
 // computes their sines once; all its loads are issued before the sines and
 // the index look-ups that do not depend on them.
 #include <string.h>
@@ -21,8 +20,14 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kHeadsPerLane = 4;
+// Heads of a lane (HPL below).  Eight where there are warps enough for the
+// GPU: the look-ups and sines of a warp serve more of its bytes (append,
+// 16384 tokens of 16 + 2 x 8 heads of 128: 46.2 us, against 55.8 with four and
+// 81 with two; sixteen: 53).  Four where there are not: a shorter path from
+// load to store (append, 16 tokens: 3.0 us in a graph, against 3.7).
+constexpr int kManyHeads = 8, kFewHeads = 4;
 constexpr int kWarps = 4;
+constexpr int kBlocks = 8;  // resident on an SM
 
 struct Rot {
     const uint64_t *turns;
@@ -111,7 +116,8 @@ __device__ __forceinline__ Unit turned(const Unit &u, const Turn &t, int interle
 
 // Warp w of the grid takes heads [g * per, (g + 1) * per) of token w / groups,
 // g = w % groups; lane l the unit l % units of every (32 / units)-th of them.
-__global__ void __launch_bounds__(32 * kWarps)
+template <int HPL>
+__global__ void __launch_bounds__(32 * kWarps, kBlocks)
     rope_kernel(Heads x, Heads y, const int32_t *__restrict__ positions, Rot r, int tokens, int heads, int units,
                 int groups) {
     const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -119,18 +125,18 @@ __global__ void __launch_bounds__(32 * kWarps)
     const long long t = w / (unsigned)groups;
     const int side = 32 / units, sub = lane / units, u = lane % units;
     if (t >= tokens || sub >= side) return;
-    const int h0 = (int)(w % (unsigned)groups) * side * kHeadsPerLane + sub;
+    const int h0 = (int)(w % (unsigned)groups) * side * HPL + sub;
     const int2 at = unit_parts(u, r);
-    Unit v[kHeadsPerLane];
+    Unit v[HPL];
 #pragma unroll
-    for (int j = 0; j < kHeadsPerLane; ++j)
+    for (int j = 0; j < HPL; ++j)
         if (h0 + j * side < heads) v[j] = load_unit(x.x + t * x.token + (h0 + j * side) * x.head, at);
     uint16_t *dst = const_cast<uint16_t *>(y.x) + t * y.token;
     const bool rotated = 8 * u < r.rot;
     Turn turn;
     if (rotated) turn = turn_of(r, u, positions ? __ldg(positions + t) : (int)t);
 #pragma unroll
-    for (int j = 0; j < kHeadsPerLane; ++j)
+    for (int j = 0; j < HPL; ++j)
         if (h0 + j * side < heads)
             store_unit(dst + (h0 + j * side) * y.head, at, rotated ? turned(v[j], turn, r.interleaved) : v[j]);
 }
@@ -165,18 +171,19 @@ struct AppendArgs {
 
 // As rope_kernel, over the heads of q, then k, then v of one token; the
 // token's sequence, and the page of its position, are found by the warp.
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_constant__ AppendArgs a) {
+template <int HPL>
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const __grid_constant__ AppendArgs a) {
     const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const int t = (int)(w / (unsigned)a.groups);
     if (t >= a.b.total_q) return;
     const int side = 32 / a.units, sub = lane / a.units, u = lane % a.units;
     const int heads = a.q_heads + 2 * a.kv_heads;
-    const int h0 = (int)(w % (unsigned)a.groups) * side * kHeadsPerLane + sub;
+    const int h0 = (int)(w % (unsigned)a.groups) * side * HPL + sub;
     const int2 at = unit_parts(u, a.r);
-    Unit v[kHeadsPerLane];
+    Unit v[HPL];
 #pragma unroll
-    for (int j = 0; j < kHeadsPerLane; ++j) {
+    for (int j = 0; j < HPL; ++j) {
         const int h = h0 + j * side;
         if (sub < side && h < heads) {
             const int hk = h - a.q_heads, hv = hk - a.kv_heads;
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
     Turn turn;
     if (rotated) turn = turn_of(a.r, u, a.positions ? __ldg(a.positions + t) : p);
 #pragma unroll
-    for (int j = 0; j < kHeadsPerLane; ++j) {
+    for (int j = 0; j < HPL; ++j) {
         const int h = h0 + j * side;
         if (h >= heads) break;
         const int hk = h - a.q_heads, hv = hk - a.kv_heads;
@@ -228,11 +235,12 @@ int check_rotation(const f16_rotation *r, int head_dim, Rot &out) {
     return W4A16_OK;
 }
 
-// Warps per token for `heads` heads of `units` 16-byte units.
-int head_groups(int heads, int units) {
-    const int per = 32 / units * kHeadsPerLane;
+// Warps per token for `heads` heads of `units` 16-byte units, hpl to a lane.
+int head_groups(int heads, int units, int hpl) {
+    const int per = 32 / units * hpl;
     return (heads + per - 1) / per;
 }
+bool many_warps(long long warps) { return warps > (long long)sm_count() * kBlocks * kWarps; }
 
 template <class K, class... A>
 int launch(K kernel, long long warps, void *stream, A... args) {
@@ -293,9 +301,11 @@ extern "C" int f16_rope(const uint16_t *x, int64_t x_token, int64_t x_head, uint
         !stride_ok(y_head) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
         return W4_ERR_ALIGN;
     if (device_cc() != 103) return W4_ERR_DEVICE;
-    const int units = head_dim / 8, groups = head_groups(heads, units);
-    return launch(rope_kernel, (long long)tokens * groups, stream, Heads{x, x_token, x_head},
-                  Heads{y, y_token, y_head}, positions, r, tokens, heads, units, groups);
+    const int units = head_dim / 8, few = head_groups(heads, units, kFewHeads), many = head_groups(heads, units, kManyHeads);
+    const bool big = many_warps((long long)tokens * many);
+    return launch(big ? rope_kernel<kManyHeads> : rope_kernel<kFewHeads>, (long long)tokens * (big ? many : few), stream,
+                  Heads{x, x_token, x_head}, Heads{y, y_token, y_head}, positions, r, tokens, heads, units,
+                  big ? many : few);
 }
 
 extern "C" int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head, const uint16_t *v, int64_t v_token,
@@ -339,8 +349,12 @@ extern "C" int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head,
     a.q_heads = q ? q_heads : 0;
     a.kv_heads = cache->heads;
     a.units = cache->head_dim / 8;
-    a.groups = head_groups(a.q_heads + 2 * a.kv_heads, a.units);
-    return launch(append_kernel, (long long)batch->total_q * a.groups, stream, a);
+    const int heads = a.q_heads + 2 * a.kv_heads;
+    a.groups = head_groups(heads, a.units, kManyHeads);
+    const bool big = many_warps((long long)batch->total_q * a.groups);
+    if (!big) a.groups = head_groups(heads, a.units, kFewHeads);
+    return launch(big ? append_kernel<kManyHeads> : append_kernel<kFewHeads>, (long long)batch->total_q * a.groups, stream,
+                  a);
 }
 
 extern "C" int f16_kv_cache_init(f16_kv_cache *c, uint16_t *k, uint16_t *v, const int64_t ks[3], const int64_t vs[3],

@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
         prefetch_maps(&map_k, &map_v);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    pdl_wait();
     make_plan<typename C::Work, C::THREADS>(a, plan_sh);  // (its barriers also publish the above)
     const Plan plan = plan_sh.plan;
     Pieces<typename C::Work> pc(a, plan);
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
             merge_rows(std::integral_constant<int, 2 * MT>());
         if (!whole) {
             const Part part = pc.part(plan);
-            if (threadIdx.x == 0) part_written(a, part);
+            if (threadIdx.x == 0) part_written<false>(a, part);
             if (shares++ == 0)
                 shared0 = part;
             else

@@ -351,10 +351,11 @@ __device__ __forceinline__ float log_sum(float mx, float sum) {
 __device__ __forceinline__ long long part_slot(int c, int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); }
 
 // Counts a part in: its partial results were written by threads that the
-// calling thread has synchronised with.
+// calling thread has synchronised with.  COPIED: they are read by copies.
+template <bool COPIED>
 __device__ __forceinline__ void part_written(const AttnArgs &a, const Part &p) {
     __threadfence();
-    asm volatile("fence.proxy.async;" ::: "memory");  // (where copies read it)
+    if (COPIED) asm volatile("fence.proxy.async.global;" ::: "memory");
     atomicAdd(a.arrived + p.first, 1u);
 }
 
@@ -393,11 +394,13 @@ int launch_resident(K kernel, int grid, int threads, size_t smem, cudaStream_t s
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeCooperative;
-    attr.val.cooperative = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (the kernels wait for the one before first)
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kernel, mk, mv, a) != cudaSuccess) {
         cudaGetLastError();
         return W4_ERR_LAUNCH;

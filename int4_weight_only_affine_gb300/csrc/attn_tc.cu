@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             (uint32_t)__cvta_generic_to_shared(tmem_slot)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    pdl_wait();
     fence_before();
     make_plan<Work, TC_THREADS>(a, plan_sh);  // (its barriers also publish the above)
     fence_after();
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     shared1 = pc.part(plan);
             };
             auto signal_part = [&] {  // (of the first shared item: a later one is this CTA's last)
-                if (unsignalled) part_written(a, shared0);
+                if (unsignalled) part_written<true>(a, shared0);
                 unsignalled = false;
             };
             if (128 * t >= rows) {
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         // ---------------- join this CTA's share of the items it shares, all eight warps ----------------
         // (Both tiles' warps meet before the first copy into the ring: every product is done.)
-        if (unsignalled) part_written(a, shares == 1 ? shared0 : shared1);
+        if (unsignalled) part_written<true>(a, shares == 1 ? shared0 : shared1);
         uint32_t join_phase = 0;
         for (int i = 0; i < shares; ++i) {
             const Part part = i == 0 ? shared0 : shared1;
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             if (part.index >= joiners) continue;
             if (threadIdx.x == 0) {
                 *join_ok = parts_written(a, part, part.parts * (part.rows > 128 ? 2 : 1)) ? 1 : 0;
-                asm volatile("fence.proxy.async;" ::: "memory");  // the parts were stored by threads, and are read by copies
+                asm volatile("fence.proxy.async.global;" ::: "memory");  // the parts were stored by threads, and are read by copies
             }
             fence_proxy_async_smem();  // (and shared memory that threads used is written by copies)
             sync();

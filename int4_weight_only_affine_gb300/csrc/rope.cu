@@ -120,6 +120,7 @@ template <int HPL>
 __global__ void __launch_bounds__(32 * kWarps, kBlocks)
     rope_kernel(Heads x, Heads y, const int32_t *__restrict__ positions, Rot r, int tokens, int heads, int units,
                 int groups) {
+    pdl_wait();
     const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const long long t = w / (unsigned)groups;
@@ -173,6 +174,7 @@ struct AppendArgs {
 // token's sequence, and the page of its position, are found by the warp.
 template <int HPL>
 __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const __grid_constant__ AppendArgs a) {
+    pdl_wait();
     const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const int t = (int)(w / (unsigned)a.groups);
@@ -242,11 +244,25 @@ int head_groups(int heads, int units, int hpl) {
 }
 bool many_warps(long long warps) { return warps > (long long)sm_count() * kBlocks * kWarps; }
 
+// Launch as a programmatic dependent (the kernels wait for the one before
+// first: it only takes the launch itself off the path).
 template <class K, class... A>
 int launch(K kernel, long long warps, void *stream, A... args) {
     if (warps > 0x7FFFFFFFll) return W4_ERR_SHAPE;
-    kernel<<<(unsigned)((warps + kWarps - 1) / kWarps), 32 * kWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(args...);
-    return launch_status();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((warps + kWarps - 1) / kWarps), 1, 1);
+    cfg.blockDim = dim3(32 * kWarps, 1, 1);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return W4_ERR_LAUNCH;
+    }
+    return W4A16_OK;
 }
 
 // Encodes a binary16 tensor map with 128-byte swizzle; false for a stride it

@@ -594,7 +594,7 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     // No more CTAs than there can be units (lengths are known on the device only).
     const int keys = kv_tile(d);
     const long long tiles = ((long long)batch->total_q * (q_heads / heads) + rows - 1) / rows + batch->batch;
-    const long long units = tiles * heads * ((a.b.max_kv + keys - 1) / keys + 8);  // (and their items' extra cost)
+    const long long units = tiles * heads * (2ll * ((a.b.max_kv + keys - 1) / keys) + 8);  // (at their cost)
     if (units >= 0x7FFFFFFFll) return W4_ERR_SHAPE;
     int grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
     if (units < grid) grid = (int)units;

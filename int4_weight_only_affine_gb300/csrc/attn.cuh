@@ -5,8 +5,8 @@
 // r % G of the group (G = q_heads / kv_heads).  An item is a tile of `rows`
 // such rows (of one sequence, one key/value head) with the range of
 // positions [lo, hi) that any of its rows sees; a unit is one tile of `keys`
-// positions of that range.  An item costs its units and, for its queries and
-// outputs, EXTRA units more.  All items' costs, in the order (sequence, head,
+// positions of that range.  An item costs its units (twice, if it has many
+// rows) and, for its queries and outputs, EXTRA more.  All items' costs, in the order (sequence, head,
 // row tile, key tile), are cut into one contiguous range per CTA, equal to
 // within a unit, whatever the lengths.  An item cut by a range boundary is
 // computed in parts: each part's CTA leaves its unnormalised output, running
@@ -48,18 +48,19 @@ struct Part {
 };
 
 // How a kernel's work is cut: rows and positions of a unit, an item's extra
-// cost, the least cost worth a CTA of its own.  The two key tiles next to an
-// end of an item of more than SNAP_ROWS rows are not cut off: joining so many
-// rows takes as long.
-template <int ROWS_, int KEYS_, int EXTRA_, int LEAST_, int SNAP_ROWS_>
+// cost, the least cost worth a CTA of its own.  A unit of an item of more than
+// FEW_ROWS rows costs 2, and the two key tiles next to an end of such an item
+// are not cut off: joining so many rows takes as long.
+template <int ROWS_, int KEYS_, int EXTRA_, int LEAST_, int FEW_ROWS_>
 struct Cut {
-    static constexpr int ROWS = ROWS_, KEYS = KEYS_, EXTRA = EXTRA_, LEAST = LEAST_, SNAP_ROWS = SNAP_ROWS_;
+    static constexpr int ROWS = ROWS_, KEYS = KEYS_, EXTRA = EXTRA_, LEAST = LEAST_, FEW_ROWS = FEW_ROWS_;
 };
 
 struct Item {
     int rows;    // of the tile
     int lo, hi;  // positions [lo, hi) seen by any row of the tile
     int t0, nt;  // key tiles t0 .. t0 + nt - 1 (nt >= 1: an item that sees nothing still writes its zeros)
+    int weight;  // of a unit
 };
 
 template <class C>
@@ -74,16 +75,21 @@ __device__ __forceinline__ Item item_of(const AttnArgs &a, const Seq &s, int rt)
     it.lo = a.window > 0 ? min(max(p0 - a.window + 1, 0), it.hi) : 0;
     it.t0 = it.lo / KEYS;
     it.nt = max((it.hi + KEYS - 1) / KEYS - it.t0, 1);
+    it.weight = it.rows > C::FEW_ROWS ? 2 : 1;
     return it;
 }
 
 // Cost of one key/value head of sequence s, summed by one thread or (WARP) by a warp.
+template <class C>
+__device__ __forceinline__ int cost_of(const Item &it) {
+    return it.nt * it.weight + C::EXTRA;
+}
 template <class C, bool WARP>
 __device__ __forceinline__ uint32_t head_cost(const AttnArgs &a, const Seq &s) {
     const int nrt = (s.qn * (int)a.group.d + C::ROWS - 1) / C::ROWS;
     uint32_t n = 0;
     for (int rt = WARP ? (int)(threadIdx.x & 31) : 0; rt < nrt; rt += WARP ? 32 : 1)
-        n += item_of<C>(a, s, rt).nt + C::EXTRA;
+        n += cost_of<C>(item_of<C>(a, s, rt));
     return WARP ? __reduce_add_sync(~0u, n) : n;
 }
 
@@ -175,7 +181,7 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
         if (WARP) {  // 32 row tiles at a time
             const int nrt = (s.qn * (int)a.group.d + C::ROWS - 1) / C::ROWS;
             for (;; rt += 32) {
-                const uint32_t v = rt + lane < nrt ? item_of<C>(a, s, rt + lane).nt + C::EXTRA : 0;
+                const uint32_t v = rt + lane < nrt ? cost_of<C>(item_of<C>(a, s, rt + lane)) : 0;
                 const uint32_t inc = warp_scan(v, lane);
                 const unsigned m = __ballot_sync(~0u, inc > res);
                 if (m) {
@@ -188,7 +194,7 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
             }
         } else {
             for (;; ++rt) {
-                const uint32_t v = item_of<C>(a, s, rt).nt + C::EXTRA;
+                const uint32_t v = cost_of<C>(item_of<C>(a, s, rt));
                 if (res < v) break;
                 res -= v;
             }
@@ -231,10 +237,12 @@ struct Pieces {
 
     // Cuts at key tile uncut_lo() or before are moved to the item's beginning,
     // at uncut_hi() or after to its end.
-    __device__ __forceinline__ int snap() const { return it.rows > C::SNAP_ROWS ? 2 : 0; }
+    __device__ __forceinline__ int snap() const { return it.weight > 1 ? 2 : 0; }
     __device__ __forceinline__ int uncut_lo() const { return min(snap(), it.nt / 2); }
     __device__ __forceinline__ int uncut_hi() const { return max(it.nt - snap(), it.nt / 2 + 1); }
-    __device__ __forceinline__ int snapped(int cut) const {
+    // The key tile that a cut at cost x of the item comes before.
+    __device__ __forceinline__ int cut_tile(int x) const {
+        const int cut = x <= C::EXTRA ? 0 : (it.weight > 1 ? (x - C::EXTRA) >> 1 : x - C::EXTRA);
         return cut <= uncut_lo() ? 0 : (cut >= uncut_hi() ? it.nt : cut);
     }
 
@@ -248,9 +256,9 @@ struct Pieces {
                 }
             }
             it = item_of<C>(a, s, rt);
-            const int cost = it.nt + C::EXTRA, end = (int)min((uint32_t)cost, left + off);
-            tile0 = snapped(off - C::EXTRA);
-            n = snapped(end - C::EXTRA) - tile0;
+            const int cost = cost_of<C>(it), end = (int)min((uint32_t)cost, left + off);
+            tile0 = cut_tile(off);
+            n = cut_tile(end) - tile0;
             begins = tile0 == 0;
             ends = tile0 + n == it.nt;
             left -= end - off;
@@ -267,8 +275,9 @@ struct Pieces {
     __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (begins ? 1 : 0); }
     // Of a piece that is not a whole item.
     __device__ __forceinline__ Part part(const Plan &p) const {
-        const int first = begins ? (int)blockIdx.x : (int)owner(p, at - it.nt + uncut_lo());
-        const int last = ends ? (int)blockIdx.x : (int)owner(p, at - it.nt + uncut_hi() - 1);
+        const uint32_t tiles0 = at - it.nt * it.weight;  // cost before the item's first tile
+        const int first = begins ? (int)blockIdx.x : (int)owner(p, tiles0 + (uncut_lo() + 1) * it.weight - 1);
+        const int last = ends ? (int)blockIdx.x : (int)owner(p, tiles0 + uncut_hi() * it.weight - 1);
         return Part{first, last - first + 1, (int)blockIdx.x - first, s.q0, head, row0(), rows()};
     }
 };

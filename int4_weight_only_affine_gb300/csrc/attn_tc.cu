@@ -25,6 +25,8 @@
 //    as 1; so no unit's maximum is looked for.  Only where the sum of 64
 //    probabilities passes 2^15 (none can have, up to there) is the reference
 //    raised to the maximum and O_t rescaled in tensor memory.
+//  * An item of at most 128 rows has both tiles work on the same rows, one on
+//    the even units, one on the odd ones; their sums are merged at its end.
 //  * Positions outside a row's range get probability 0; rows of V that no row
 //    of the item sees are zeroed in shared memory, as they may hold anything.
 #include <math.h>
@@ -36,13 +38,9 @@ namespace w4a16 {
 namespace {
 
 constexpr int QROWS = 256, KEYS = 128;
-using Work = Cut<QROWS, KEYS, 3, 4, 128>;
+using Work = Cut<QROWS, KEYS, 6, 6, 128>;
 constexpr int FEW_PARTS = 4;
 constexpr int TC_THREADS = 384;
-// Registers a thread: 168 at launch (64512 in all); the softmax's two warp
-// groups take what the third (copies, MMA issue) gives up.
-constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 208, REGS_OTHER = 88;
-static_assert(2 * REGS_SOFTMAX + REGS_OTHER == 3 * REGS_LAUNCH, "register split");
 constexpr int HALF = KEYS * 128;  // bytes of 64 columns of 128 rows
 constexpr float kMostSum = 32768.f;  // of 64 probabilities: 2^15, half of what binary16 holds
 
@@ -90,7 +88,7 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// mbar_wait without a call: the register split leaves no room for one.
+// mbar_wait without a call (which would spill what the warps hold).
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     uint64_t t0 = 0;  // the clock is read only once a wait has become long
     for (uint32_t spin = 0; spin < kMaxSpins; ++spin) {
@@ -165,14 +163,6 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
     return d;
-}
-
-// Scores of positions 32 C .. 32 C + 31 of a unit: those outside [lo, hi) to -infinity.
-template <int C>
-__device__ __forceinline__ void mask(uint32_t (&s)[32], int lo, int hi) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (32 * C + i < lo || 32 * C + i >= hi) s[i] = 0xFF800000u;
 }
 
 // Probabilities 2^(s scale + minus) of 32 scores, rounded to binary16 in p
@@ -307,6 +297,9 @@ __device__ __forceinline__ void join_block(const AttnArgs &a, const Part &part, 
     if (a.lse && g == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
 }
 
+// Whether both tiles take the same rows, and alternate units.
+__device__ __forceinline__ bool split_units(int rows, int n) { return rows <= 128 && n >= 2; }
+
 template <int DP>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -367,7 +360,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     Pieces<Work> pc(a, plan);
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
         if (warp == 8 || warp == 11) {
             // ---------------- copies: warp 8 the K tile, warp 11 the V tile of every unit, in turn ----------------
             const bool is_v = uniform(warp) == 11;
@@ -436,14 +428,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             };
             while (ok && uniform(pc.next())) {
                 const int n = uniform(pc.n), rows = uniform(pc.rows());
-                if (128 * t >= rows) {  // no such tile: only hand the slots on
-                    for (int i = 0; ok && i < 2 * n; ++i) {
+                const bool split = split_units(rows, n), both_tiles = rows > 128;
+                auto hand_on = [&](int slots) {  // slots that this tile does not use
+                    for (int i = 0; ok && i < slots; ++i) {
                         await(kv_full(slot), phase);
                         if (ok && elect_one()) mbar_arrive(kv_empty(slot));
                         advance();
                     }
+                };
+                if (128 * t >= rows && !split) {
+                    hand_on(2 * n);
                     continue;
                 }
+                const int stride = split ? 2 : 1;
+                if (split && t) hand_on(2);
                 await(q_full(t), begun++ & 1);
                 await(kv_full(slot), phase);
                 // the columns of S, if P lies there: the last product of the piece before has read it
@@ -451,14 +449,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if (!ok) break;
                 fence_after();
                 score();
-                const bool both_tiles = rows > 128;
-                for (int j = 0; j < n; ++j) {
+                bool first = true;
+                for (int j = split ? t : 0; j < n; j += stride) {
                     const int v_slot = slot;
-                    const bool more = j + 1 < n;
+                    const bool more = j + stride < n;
                     // K of the next unit too, ahead of the probabilities
                     await(kv_full(slot), phase);
                     advance();
-                    if (more) await(kv_full(slot), phase);
+                    if (more && !split) await(kv_full(slot), phase);
                     const uint64_t vt = operand_desc(ring + v_slot * C::TILE, HALF, 1024);
                     if (both_tiles) await(turn(t), (turns++ & 1) ^ (t == 0 ? 1 : 0));
                     await(p_full(t, 0), steps & 1);
@@ -466,9 +464,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) mma_ts(o_at, p_at + 8 * s, vt + s * (2048 >> 4), id_o, (j | s) != 0);
+                        for (int s = 0; s < 4; ++s) mma_ts(o_at, p_at + 8 * s, vt + s * (2048 >> 4), id_o, !first || s != 0);
                         commit(o_half(t));
                     }
+                    first = false;
                     await(p_full(t, 1), steps & 1);
                     if (!ok) break;
                     fence_after();
@@ -478,7 +477,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         commit(o_done(t));
                         commit(kv_empty(v_slot));
                     }
+                    if (split && j + 1 < n) hand_on(2);
                     if (more) {
+                        if (split) await(kv_full(slot), phase);
                         if (C::P_IN_S) await(o_done(t), steps & 1);
                         if (!ok) break;
                     }
@@ -493,7 +494,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         // ---------------- softmax: warps 4 t .. 4 t + 3 for tile t, one thread to a row ----------------
         const int t = warp >> 2, quad = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -523,12 +523,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if (unsignalled) part_written<true>(a, shared0);
                 unsignalled = false;
             };
-            if (128 * t >= rows) {
+            const bool split = split_units(rows, pc.n);
+            const int tile_row = split ? 0 : 128 * t;
+            if (tile_row >= rows) {
                 signal_part();
                 note_part();
                 continue;
             }
-            const int r = 128 * t + 32 * quad + lane;  // this thread's row of the item
+            const int r = tile_row + 32 * quad + lane;  // this thread's row of the item
             const bool in = r < rows;
             const int gr = row0 + r;
             const long long tok = pc.s.q0 + gr / a.group;
@@ -561,29 +563,32 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const int ub = in ? (a.causal ? min(p + 1, pc.s.kv) : pc.s.kv) : 0;
             const int lb = a.window > 0 ? p - a.window + 1 : 0;
             // Units inside these bounds need no mask for any row of the tile.
-            const int pf = pc.s.kv - pc.s.qn + (row0 + 128 * t) / a.group;
-            const int pl = pc.s.kv - pc.s.qn + (row0 + min(rows, 128 * t + 128) - 1) / a.group;
+            const int pf = pc.s.kv - pc.s.qn + (row0 + tile_row) / a.group;
+            const int pl = pc.s.kv - pc.s.qn + (row0 + min(rows, tile_row + 128) - 1) / a.group;
             const int all_ub = a.causal ? min(pf + 1, pc.s.kv) : pc.s.kv;
             const int all_lb = a.window > 0 ? pl - a.window + 1 : 0;
 
             // Reference (of scores in base 2) and sum.  (Rows past the item's end see nothing and need no reference.)
             float ref = in ? -INFINITY : 0.f, sum = 0.f;
-            for (int j = 0; j < pc.n; ++j, ++steps) {
+            const int j_first = split ? t : 0;
+            for (int j = j_first; j < pc.n; j += split ? 2 : 1, ++steps) {
                 const int j0 = (pc.it.t0 + pc.tile0 + j) * KEYS;
                 wait(s_full(t), steps & 1, abort);
                 fence_after();
-                uint32_t sr[4][32];
+                if (j0 + KEYS > all_ub || j0 < all_lb) {  // positions that not every row sees: scores to -infinity
+#pragma unroll 1
+                    for (int c = 0; c < KEYS; c += 32) {
+                        const int lo = lb - j0 - c, hi = ub - j0 - c;
+                        uint32_t v[32];
+                        tmem_load(s_at + c, v);
+                        tmem_load_wait();
+                        tmem_loaded(v);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_load(s_at + 32 * c, sr[c]);
-                tmem_load_wait();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_loaded(sr[c]);
-                if (j0 + KEYS > all_ub || j0 < all_lb) {
-                    const int lo = lb - j0, hi = ub - j0;
-                    mask<0>(sr[0], lo, hi);
-                    mask<1>(sr[1], lo, hi);
-                    mask<2>(sr[2], lo, hi);
-                    mask<3>(sr[3], lo, hi);
+                        for (int i = 0; i < 32; ++i)
+                            if (i < lo || i >= hi) v[i] = 0xFF800000u;
+                        tmem_store(s_at + c, v);
+                    }
+                    tmem_store_wait();
                 }
                 if (j0 < pc.it.lo || j0 + KEYS > pc.it.hi) {
                     // Rows of V that the item does not see: one to a thread (both tiles write the same zeros, each
@@ -600,26 +605,32 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     }
                     fence_proxy_async_smem();
                 }
-#pragma unroll
+                // (Loops kept short where they can be: the warps' code is fetched anew every time round.)
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t pr[2][16];
+                    uint32_t sr[2][32], pr[2][16];
+                    tmem_load(s_at + 64 * h, sr[0]);
+                    tmem_load(s_at + 64 * h + 32, sr[1]);
+                    tmem_load_wait();
+                    tmem_loaded(sr[0]);
+                    tmem_loaded(sr[1]);
                     float part_sum;
 #pragma unroll 1
                     for (bool again = false;; again = true) {
                         f32x2 s2[2] = {0, 0};
                         const float minus = ref == -INFINITY ? 0.f : -ref;
-                        exps(sr[2 * h], pr[0], scale2, minus, s2);
-                        exps(sr[2 * h + 1], pr[1], scale2, minus, s2);
+                        exps(sr[0], pr[0], scale2, minus, s2);
+                        exps(sr[1], pr[1], scale2, minus, s2);
                         const float2 e = both(add2(s2[0], s2[1]));
                         part_sum = e.x + e.y;
                         const bool raise = !(part_sum <= kMostSum) || ref == -INFINITY;
                         if (again || !__any_sync(~0u, raise)) break;
                         float m = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) m = max3(m, sr[2 * h][i], sr[2 * h + 1][i]);
+                        for (int i = 0; i < 32; ++i) m = max3(m, sr[0][i], sr[1][i]);
                         const float nr = raise ? fmaxf(ref, m * a.scale) : ref;
                         const float c = nr != ref ? corr(ref, nr) : 1.f;
-                        if (j + h > 0) {  // O_t holds something
+                        if (j > j_first || h > 0) {  // O_t holds something
                             wait(h ? o_half(t) : o_done(t), (h ? steps : steps - 1) & 1, abort);
                             fence_after();
 #pragma unroll 1
@@ -650,7 +661,25 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             // ---------------- the piece's rows ----------------
             wait(o_done(t), (steps - 1) & 1, abort);
             fence_after();
-            if (in) {
+            const uint32_t other = base + C::TILE;  // over Q_1
+            float f0 = 1.f, f1 = 0.f;
+            auto both_sync = [] { asm volatile("bar.sync 4, 256;" ::: "memory"); };
+            if (split) {  // tile 0 gets tile 1's reference and sum, then its outputs 32 columns at a time
+                const uint32_t at = other + 8 * (32 * quad + lane);
+                if (t) asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(ref), "f"(sum) : "memory");
+                both_sync();
+                if (!t) {
+                    float2 v;
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+                    const float top = fmaxf(ref, v.x);
+                    f0 = corr(ref, top);
+                    f1 = corr(v.x, top);
+                    ref = top;
+                    sum = sum * f0 + v.y * f1;
+                }
+                both_sync();
+            }
+            if (in && !(split && t)) {
                 if (!whole)
                     reinterpret_cast<float2 *>(a.part_ml)[(long long)pc.slot() * QROWS + r] = make_float2(ref, sum);
                 else if (a.lse)
@@ -665,6 +694,24 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 tmem_load(o_at + 32 * cb, o);
                 tmem_load_wait();
                 tmem_loaded(o);
+                if (split) {
+                    const uint32_t at = other + 4 * (32 * quad + lane);
+                    if (t) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 512 * i), "r"(o[i]) : "memory");
+                    }
+                    both_sync();
+                    if (!t) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            float v;
+                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at + 512 * i));
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + v * f1);
+                        }
+                    }
+                    both_sync();
+                    if (t) continue;
+                }
                 if (whole) {  // through this warp's rows of Q_t (its products are done)
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
@@ -685,7 +732,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                             __uint_as_float(o[i + 3]));
                 }
             }
-            if (whole) {
+            if (whole && !(split && t)) {
                 __syncwarp();
                 const long long y_row = in ? tok * a.y_token + head * a.y_head : -1;
 #pragma unroll
@@ -704,7 +751,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 __syncwarp();
             }
             fence_before();  // the reads above, before the next piece's first product writes O_t
-            if (!whole) {
+            if (!whole && !(split && t)) {
                 if (t == 0)  // this tile's warps
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 else
@@ -750,25 +797,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     }
 }
 
-// The register split needs what the compiler gave each thread at launch: a
-// kernel launched with fewer would wait for registers that never come.
-template <int DP>
-bool regs_ok() {
-    static const bool ok = [] {
-        cudaFuncAttributes f;
-        if (cudaFuncGetAttributes(&f, attn_tc_kernel<DP>) != cudaSuccess) {
-            cudaGetLastError();
-            return false;
-        }
-        return f.numRegs == REGS_LAUNCH;
-    }();
-    return ok;
-}
-
 template <int DP>
 int launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
     static_assert(TcCfg<DP>::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
-    if (!regs_ok<DP>()) return W4_ERR_DEVICE;
     if (!set_smem_once(reinterpret_cast<const void *>(attn_tc_kernel<DP>), (int)TcCfg<DP>::SMEM)) return W4_ERR_LAUNCH;
     return launch_resident(attn_tc_kernel<DP>, grid, TC_THREADS, TcCfg<DP>::SMEM, stream, mk, mv, a);
 }

@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 }
             };
             auto await = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(~0u, ok && wait(bar, parity, abort)); };
-            auto score = [&] {  // S = Q K^T, K in the next slot
-                const uint64_t kt = operand_desc(ring + slot * C::TILE, 16, 1024);
+            auto score = [&](int at) {  // S = Q K^T, K in slot `at`
+                const uint64_t kt = operand_desc(ring + at * C::TILE, 16, 1024);
                 if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < DP / 16; ++s) {  // 16 columns: 32 bytes on, or the next 64 columns
@@ -422,9 +422,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         mma_ss(s_at, q + off, kt + off, id_s, s != 0);
                     }
                     commit(s_full(t));
-                    commit(kv_empty(slot));
+                    commit(kv_empty(at));
                 }
-                advance();
             };
             while (ok && uniform(pc.next())) {
                 const int n = uniform(pc.n), rows = uniform(pc.rows());
@@ -448,7 +447,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if (C::P_IN_S && steps > 0) await(o_done(t), (steps - 1) & 1);
                 if (!ok) break;
                 fence_after();
-                score();
+                score(slot);
+                advance();
                 bool first = true;
                 for (int j = split ? t : 0; j < n; j += stride) {
                     const int v_slot = slot;
@@ -477,15 +477,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         commit(o_done(t));
                         commit(kv_empty(v_slot));
                     }
-                    if (split && j + 1 < n) hand_on(2);
+                    // The next K, past the other tile's unit in between.
+                    const int skip = split ? 2 : 0;
+                    const bool wraps = slot + skip >= C::SLOTS;
+                    const int k_slot = wraps ? slot + skip - C::SLOTS : slot + skip;
                     if (more) {
-                        if (split) await(kv_full(slot), phase);
+                        if (split) await(kv_full(k_slot), phase ^ (wraps ? 1 : 0));
                         if (C::P_IN_S) await(o_done(t), steps & 1);
                         if (!ok) break;
                     }
                     // The other tile's products may queue up behind this one's last.
                     if (both_tiles && elect_one()) mbar_arrive(turn(t ^ 1));
-                    if (more) score();
+                    if (more) score(k_slot);
+                    if (split && j + 1 < n) hand_on(2);
+                    if (more) advance();
                     ++steps;
                 }
             }

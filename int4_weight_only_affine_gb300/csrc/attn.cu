@@ -35,9 +35,9 @@ namespace {
 constexpr int kMaxGrid = 256;  // CTAs of a launch, >= the SMs of the GPU
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int DP, int MT>
+template <int DP>
 struct RowCfg {
-    static constexpr int ROWS = 16 * MT;
+    static constexpr int ROWS = 16;
     static constexpr int KEYS = kv_tile(DP);
     using Work = Cut<ROWS, KEYS, 2, 1, ROWS>;
     static constexpr int WARPS = KEYS / 16;             // consumers
@@ -144,11 +144,11 @@ __device__ __forceinline__ void join_row(const AttnArgs &a, const Part &part, in
 }
 
 // WIDE: the tensor maps copy whole heads.
-template <int DP, int MT, bool WIDE>
-__global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
+template <int DP, bool WIDE>
+__global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const __grid_constant__ AttnArgs a) {
-    using C = RowCfg<DP, MT>;
+    using C = RowCfg<DP>;
     constexpr int ROWS = C::ROWS, KEYS = C::KEYS, NT = 32 * C::WARPS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PlanShared plan_sh;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
             for (int i = 0; i < n; ++i, ++it, p0 += KEYS) {
                 const int st = it % C::STAGES;
                 const int page = lane < boxes ? page_of(a, pc.b, p0 + lane * a.box_rows, pc.it.lo, pc.it.hi) : 0;
-                ok = __all_sync(~0u, mbar_wait(empty_bar(st), ((it / C::STAGES) & 1) ^ 1, abort));
+                ok = __all_sync(~0u, wait(empty_bar(st), ((it / C::STAGES) & 1) ^ 1, abort));
                 if (!ok) break;
                 const uint32_t kdst = base + st * 2 * C::TILE, vdst = kdst + C::TILE, bar = full_bar(st);
                 if (elect_one()) mbar_expect_tx(bar, 2 * C::TILE);
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
             }
         }
         // Every copy has landed before the CTA may exit.
-        for (int k = max(0, it - C::STAGES); k < it; ++k) mbar_wait(full_bar(k % C::STAGES), (k / C::STAGES) & 1);
+        for (int k = max(0, it - C::STAGES); k < it; ++k) wait(full_bar(k % C::STAGES), (k / C::STAGES) & 1, nullptr);
         return;
     }
 
@@ -239,48 +239,43 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
     while (pc.next()) {
         const int row0 = pc.row0(), rows = pc.rows();
         // Query fragments, and the positions each of this lane's rows sees.
-        uint32_t qf[MT][DP / 16][4];
-        int lb[MT][2], ub[MT][2];
+        uint32_t qf[DP / 16][4];
+        int lb[2], ub[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int hf = 0; hf < 2; ++hf) {
+            const int r = row0 + 8 * hf + g;
+            const bool in = r < row0 + rows;
+            const int tok = r / a.group, p = pc.s.kv - pc.s.qn + tok;
+            ub[hf] = in ? (a.causal ? min(p + 1, pc.s.kv) : pc.s.kv) : 0;
+            lb[hf] = a.window > 0 ? p - a.window + 1 : 0;
+            const uint16_t *qr = a.q + (pc.s.q0 + tok) * a.q_token +
+                                 (pc.head * (int)a.group.d + r % a.group) * a.q_head;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int r = row0 + 16 * mt + 8 * hf + g;
-                const bool in = r < row0 + rows;
-                const int tok = r / a.group, p = pc.s.kv - pc.s.qn + tok;
-                ub[mt][hf] = in ? (a.causal ? min(p + 1, pc.s.kv) : pc.s.kv) : 0;
-                lb[mt][hf] = a.window > 0 ? p - a.window + 1 : 0;
-                const uint16_t *qr = a.q + (pc.s.q0 + tok) * a.q_token +
-                                     (pc.head * (int)a.group.d + r % a.group) * a.q_head;
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    const int c = 16 * k + 2 * t4;
-                    qf[mt][k][hf] = in && c < a.head_dim ? *reinterpret_cast<const uint32_t *>(qr + c) : 0u;
-                    qf[mt][k][2 + hf] =
-                        in && c + 8 < a.head_dim ? *reinterpret_cast<const uint32_t *>(qr + c + 8) : 0u;
-                }
+            for (int k = 0; k < DP / 16; ++k) {
+                const int c = 16 * k + 2 * t4;
+                qf[k][hf] = in && c < a.head_dim ? *reinterpret_cast<const uint32_t *>(qr + c) : 0u;
+                qf[k][2 + hf] =
+                    in && c + 8 < a.head_dim ? *reinterpret_cast<const uint32_t *>(qr + c + 8) : 0u;
             }
+        }
         // Tiles inside these bounds need no mask for any row of the item.
         const int pf = pc.s.kv - pc.s.qn + row0 / a.group, pl = pc.s.kv - pc.s.qn + (row0 + rows - 1) / a.group;
         const int all_ub = a.causal ? min(pf + 1, pc.s.kv) : pc.s.kv;
         const int all_lb = a.window > 0 ? pl - a.window + 1 : 0;
 
-        float o[MT][DP / 8][4], m[MT][2], l[MT][2];
+        float o[DP / 8][4], m[2], l[2];
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            m[mt][0] = m[mt][1] = -INFINITY;
-            l[mt][0] = l[mt][1] = 0.f;
+        for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
-            for (int n = 0; n < DP / 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
-        }
+            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
 
         for (int i = 0; i < pc.n; ++i, ++it) {
             const int st = it % C::STAGES;
             const int j0 = (pc.it.t0 + pc.tile0 + i) * KEYS + 16 * warp;  // this warp's first position
             const uint32_t kb = base + st * 2 * C::TILE, vb = kb + C::TILE;
-            mbar_wait(full_bar(st), (it / C::STAGES) & 1, abort);
+            wait(full_bar(st), (it / C::STAGES) & 1, abort);
             const bool outside = j0 < pc.it.lo || j0 + 16 > pc.it.hi;
             if (outside) {
                 // Rows of V that the item does not see hold anything; 0 x NaN must not reach the sums.
@@ -295,92 +290,73 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
             }
             if (j0 < pc.it.hi && j0 + 16 > pc.it.lo) {
                 // Two sums of half the columns each: shorter chains of dependent products.
-                float s[MT][2][4], s2[MT][2][4];
+                float s[2][4], s2[2][4];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[mt][n][e] = s2[mt][n][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     uint32_t kf[4];
                     const int ch = 2 * k + kch;
                     ldsm4(kf, kb + k_off + (ch / 8) * half_bytes + (((ch ^ krow) & 7) << 4));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        auto &d = k & 1 ? s2[mt] : s[mt];
-                        mma_16816(d[0], qf[mt][k][0], qf[mt][k][1], qf[mt][k][2], qf[mt][k][3], kf[0], kf[1]);
-                        mma_16816(d[1], qf[mt][k][0], qf[mt][k][1], qf[mt][k][2], qf[mt][k][3], kf[2], kf[3]);
-                    }
+                    auto &d = k & 1 ? s2 : s;
+                    mma_16816(d[0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], kf[0], kf[1]);
+                    mma_16816(d[1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], kf[2], kf[3]);
                 }
                 const bool masked = j0 + 16 > all_ub || j0 < all_lb;
-                uint32_t pf4[MT][4];
-                float mx[MT][2];
+                uint32_t pf4[4];
+                float mx[2];
                 bool grown = false;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = j0 + 8 * n + 2 * t4 + (e & 1), hf = e >> 1;
-                            s[mt][n][e] = (s[mt][n][e] + s2[mt][n][e]) * a.scale;
-                            if (masked && (j >= ub[mt][hf] || j < lb[mt][hf])) s[mt][n][e] = -INFINITY;
-                        }
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-                        mx[mt][hf] = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
-                                           fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+                    for (int e = 0; e < 4; ++e) {
+                    const int j = j0 + 8 * n + 2 * t4 + (e & 1), hf = e >> 1;
+                    s[n][e] = (s[n][e] + s2[n][e]) * a.scale;
+                    if (masked && (j >= ub[hf] || j < lb[hf])) s[n][e] = -INFINITY;
                 }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                    mx[hf] = fmaxf(fmaxf(s[0][2 * hf], s[0][2 * hf + 1]),
+                                       fmaxf(s[1][2 * hf], s[1][2 * hf + 1]));
 #pragma unroll
                 for (int step = 1; step <= 2; step <<= 1)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int hf = 0; hf < 2; ++hf) mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(~0u, mx[hf], step));
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) mx[mt][hf] = fmaxf(mx[mt][hf], __shfl_xor_sync(~0u, mx[mt][hf], step));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) grown |= mx[mt][hf] > m[mt][hf];
+                for (int hf = 0; hf < 2; ++hf) grown |= mx[hf] > m[hf];
                 if (__any_sync(~0u, grown)) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float top = fmaxf(mx[hf], m[hf]), c = corr(m[hf], top);
+                        m[hf] = top;
+                        l[hf] *= c;
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const float top = fmaxf(mx[mt][hf], m[mt][hf]), c = corr(m[mt][hf], top);
-                            m[mt][hf] = top;
-                            l[mt][hf] *= c;
-#pragma unroll
-                            for (int n = 0; n < DP / 8; ++n) {
-                                o[mt][n][2 * hf] *= c;
-                                o[mt][n][2 * hf + 1] *= c;
-                            }
+                        for (int n = 0; n < DP / 8; ++n) {
+                            o[n][2 * hf] *= c;
+                            o[n][2 * hf + 1] *= c;
                         }
+                    }
                 }
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float ref = m[hf] == -INFINITY ? 0.f : m[hf];
+                    float p[4];
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const float ref = m[mt][hf] == -INFINITY ? 0.f : m[mt][hf];
-                        float p[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) p[e] = exp2_approx(s[mt][e >> 1][2 * hf + (e & 1)] - ref);
-                        l[mt][hf] += (p[0] + p[1]) + (p[2] + p[3]);
-                        // Probabilities, at most 1, to binary16 for the product with V (the sum l keeps fp32).
-                        pf4[mt][hf] = pack2(p[0], p[1]);
-                        pf4[mt][2 + hf] = pack2(p[2], p[3]);
-                    }
+                    for (int e = 0; e < 4; ++e) p[e] = exp2_approx(s[e >> 1][2 * hf + (e & 1)] - ref);
+                    l[hf] += (p[0] + p[1]) + (p[2] + p[3]);
+                    // Probabilities, at most 1, to binary16 for the product with V (the sum l keeps fp32).
+                    pf4[hf] = pack2(p[0], p[1]);
+                    pf4[2 + hf] = pack2(p[2], p[3]);
+                }
 #pragma unroll
                 for (int n = 0; n < DP / 16; ++n) {
                     uint32_t vf[4];
                     const int ch = 2 * n + vch;
                     ldsm4t(vf, vb + v_off + (ch / 8) * half_bytes + (((ch ^ vrow) & 7) << 4));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma_16816(o[mt][2 * n], pf4[mt][0], pf4[mt][1], pf4[mt][2], pf4[mt][3], vf[0], vf[1]);
-                        mma_16816(o[mt][2 * n + 1], pf4[mt][0], pf4[mt][1], pf4[mt][2], pf4[mt][3], vf[2], vf[3]);
-                    }
+                    mma_16816(o[2 * n], pf4[0], pf4[1], pf4[2], pf4[3], vf[0], vf[1]);
+                    mma_16816(o[2 * n + 1], pf4[0], pf4[1], pf4[2], pf4[3], vf[2], vf[3]);
                 }
             }
             if (outside) fence_proxy_async_smem();  // the zeros above, before the next copy into the slot
@@ -391,14 +367,12 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
         // ---------------- merge the warps' sums ----------------
         const bool whole = pc.begins && pc.ends;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float v = l[mt][hf];
-                v += __shfl_xor_sync(~0u, v, 1);
-                v += __shfl_xor_sync(~0u, v, 2);
-                if (t4 == 0) ml_sh[warp * ROWS + 16 * mt + 8 * hf + g] = make_float2(m[mt][hf], v);
-            }
+        for (int hf = 0; hf < 2; ++hf) {
+            float v = l[hf];
+            v += __shfl_xor_sync(~0u, v, 1);
+            v += __shfl_xor_sync(~0u, v, 2);
+            if (t4 == 0) ml_sh[warp * ROWS + 8 * hf + g] = make_float2(m[hf], v);
+        }
         sync();
         if ((int)threadIdx.x < rows) {  // a row's maximum and sum over the warps; what its outputs are scaled by
             const int r = threadIdx.x;
@@ -421,14 +395,12 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
             }
         }
         sync();
-        float f[MT][2];
+        float f[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const float2 w = row_sh[16 * mt + 8 * hf + g];
-                f[mt][hf] = corr(m[mt][hf], w.x) * w.y;
-            }
+        for (int hf = 0; hf < 2; ++hf) {
+            const float2 w = row_sh[8 * hf + g];
+            f[hf] = corr(m[hf], w.x) * w.y;
+        }
         // Outputs, COLS columns of HALVES x 8 rows at a time.
         auto merge_rows = [&](auto halves) {
             constexpr int HALVES = decltype(halves)::value, COLS = HALVES == 1 ? 64 : 32, LD = COLS + 8 / HALVES;
@@ -437,12 +409,9 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
 #pragma unroll
                 for (int n = 0; n < COLS / 8; ++n)
 #pragma unroll
-                    for (int h = 0; h < HALVES; ++h) {
-                        const int mt = h >> 1, hf = h & 1;
-                        *reinterpret_cast<float2 *>(&merge[(warp * 8 * HALVES + 8 * h + g) * LD + 8 * n + 2 * t4]) =
-                            make_float2(o[mt][COLS / 8 * cb + n][2 * hf] * f[mt][hf],
-                                        o[mt][COLS / 8 * cb + n][2 * hf + 1] * f[mt][hf]);
-                    }
+                    for (int h = 0; h < HALVES; ++h)
+                    *reinterpret_cast<float2 *>(&merge[(warp * 8 * HALVES + 8 * h + g) * LD + 8 * n + 2 * t4]) =
+                        make_float2(o[COLS / 8 * cb + n][2 * h] * f[h], o[COLS / 8 * cb + n][2 * h + 1] * f[h]);
                 sync();
                 for (int x = threadIdx.x; x < 8 * HALVES * (COLS / 4); x += NT) {
                     const int r = x / (COLS / 4), c = 4 * (x % (COLS / 4)), col = COLS * cb + c;
@@ -471,7 +440,7 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
         if (rows <= 8)
             merge_rows(std::integral_constant<int, 1>());
         else
-            merge_rows(std::integral_constant<int, 2 * MT>());
+            merge_rows(std::integral_constant<int, 2>());
         if (!whole) {
             const Part part = pc.part(plan);
             if (threadIdx.x == 0) part_written<false>(a, part);
@@ -496,12 +465,12 @@ __global__ void __launch_bounds__(RowCfg<DP, MT>::THREADS, 1)
     }
 }
 
-template <int DP, int MT, bool WIDE>
+template <int DP, bool WIDE>
 int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
-    using C = RowCfg<DP, MT>;
+    using C = RowCfg<DP>;
     static_assert(C::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
-    if (!set_smem_once(reinterpret_cast<const void *>(attn_rows_kernel<DP, MT, WIDE>), (int)C::SMEM)) return W4_ERR_LAUNCH;
-    return launch_resident(attn_rows_kernel<DP, MT, WIDE>, grid, C::THREADS, C::SMEM, stream, mk, mv, a);
+    if (!set_smem_once(reinterpret_cast<const void *>(attn_rows_kernel<DP, WIDE>), (int)C::SMEM)) return W4_ERR_LAUNCH;
+    return launch_resident(attn_rows_kernel<DP, WIDE>, grid, C::THREADS, C::SMEM, stream, mk, mv, a);
 }
 
 // Whether a call takes the tcgen05 kernel: more rows per sequence and
@@ -599,11 +568,11 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     int grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
     if (units < grid) grid = (int)units;
     if (tc) return attn_tc_launch(mk, mv, a, grid, s);
-    if (d <= 64) return launch_rows<64, 1, false>(mk, mv, a, grid, s);
-    if (d == 128) return launch_rows<128, 1, true>(mk, mv, a, grid, s);
-    if (d < 128) return launch_rows<128, 1, false>(mk, mv, a, grid, s);
-    if (d == 192) return launch_rows<192, 1, true>(mk, mv, a, grid, s);
-    if (d < 192) return launch_rows<192, 1, false>(mk, mv, a, grid, s);
-    if (d == 256) return launch_rows<256, 1, true>(mk, mv, a, grid, s);
-    return launch_rows<256, 1, false>(mk, mv, a, grid, s);
+    if (d <= 64) return launch_rows<64, false>(mk, mv, a, grid, s);
+    if (d == 128) return launch_rows<128, true>(mk, mv, a, grid, s);
+    if (d < 128) return launch_rows<128, false>(mk, mv, a, grid, s);
+    if (d == 192) return launch_rows<192, true>(mk, mv, a, grid, s);
+    if (d < 192) return launch_rows<192, false>(mk, mv, a, grid, s);
+    if (d == 256) return launch_rows<256, true>(mk, mv, a, grid, s);
+    return launch_rows<256, false>(mk, mv, a, grid, s);
 }

@@ -201,7 +201,14 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
         }
         p.rt = rt;
         p.off = (int)res;
-        if (!WARP || lane == 0) sh.plan = p;
+        if (!WARP || lane == 0) {
+            sh.plan = p;
+            // The pages of the first tile will be wanted next.
+            const Item it = item_of<C>(a, s, rt);
+            const int at = (it.t0 + max(p.off - C::EXTRA, 0) / it.weight) * C::KEYS;
+            if (at < it.hi)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(a.b.table + (long long)p.b * a.b.table_stride + at / a.page_size));
+        }
     }
     if (p.count == 0 && threadIdx.x == 0) sh.plan = p;
     __syncthreads();
@@ -281,6 +288,24 @@ struct Pieces {
         return Part{first, last - first + 1, (int)blockIdx.x - first, s.q0, head, row0(), rows()};
     }
 };
+
+// mbar_wait without a call, and without a look at the clock (which takes as
+// long as most waits here) until the wait has become long.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    uint64_t t0 = 0;
+    for (uint32_t spin = 0; spin < kMaxSpins; ++spin) {
+        if (mbar_try(bar, parity)) return true;
+        if ((spin & 63) == 63) {
+            if (abort && *abort) return false;
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitNs) break;
+        }
+    }
+    atomicExch(&g_wait_expired, 1);
+    if (abort) *abort = 1;
+    return false;
+}
 
 // The tensor maps' descriptors, fetched ahead of their first copies.
 __device__ __forceinline__ void prefetch_maps(const CUtensorMap *k, const CUtensorMap *v) {

@@ -88,23 +88,6 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// mbar_wait without a call (which would spill what the warps hold).
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    uint64_t t0 = 0;  // the clock is read only once a wait has become long
-    for (uint32_t spin = 0; spin < kMaxSpins; ++spin) {
-        if (mbar_try(bar, parity)) return true;
-        if ((spin & 63) == 63) {
-            if (abort && *abort) return false;
-            const uint64_t now = global_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitNs) break;
-        }
-    }
-    atomicExch(&g_wait_expired, 1);
-    if (abort) *abort = 1;
-    return false;
-}
-
 #define R8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
 #define O8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])

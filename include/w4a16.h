@@ -446,10 +446,11 @@ W4A16_API int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head, 
  *              passed unchanged to later calls (its counters are left ready for
  *              the next one).  Calls ordered on one stream may share it; calls
  *              that may run concurrently need separate ones.
- * The launch is cooperative (every block resident): blocks that share a
- * sequence wait for each other's partial results (bounded: on expiry the rows
- * concerned stay unwritten, w4a16_device_status reports W4_ERR_TIMEOUT and the
- * workspace has to be zeroed again).
+ * Blocks that share a sequence wait for each other's partial results, once
+ * every block of the call has begun (bounded: on expiry, which a workspace
+ * that was not zeroed brings about, the rows concerned stay unwritten,
+ * w4a16_device_status reports W4_ERR_TIMEOUT and the workspace has to be
+ * zeroed again).
  * Products are binary16 with fp32 sums; the softmax's statistics and the
  * output's sum are fp32, the probabilities are rounded to binary16 for the
  * product with v, and y is rounded once.  A token that sees no position gets

@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_wait();
+    if (threadIdx.x == 0) cta_begins(a);
     make_plan<typename C::Work, C::THREADS>(a, plan_sh);  // (its barriers also publish the above)
     const Plan plan = plan_sh.plan;
     Pieces<typename C::Work> pc(a, plan);
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
     const int g = lane >> 2, t4 = lane & 3;
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
     Part shared0, shared1;  // items that this CTA shares with earlier and later ones
+    unsigned seen0 = 0, seen1 = 0;  // (thread 0) their counts with this CTA's part
     int shares = 0;
     int it = 0;
     while (pc.next()) {
@@ -443,11 +445,14 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
             merge_rows(std::integral_constant<int, 2>());
         if (!whole) {
             const Part part = pc.part(plan);
-            if (threadIdx.x == 0) part_written<false>(a, part);
-            if (shares++ == 0)
+            const unsigned count = threadIdx.x == 0 ? count_part<false>(a, part) : 0;
+            if (shares++ == 0) {
                 shared0 = part;
-            else
+                seen0 = count;
+            } else {
                 shared1 = part;
+                seen1 = count;
+            }
         }
     }
 
@@ -455,14 +460,20 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
     for (int i = 0; i < shares; ++i) {
         const Part part = i == 0 ? shared0 : shared1;
         const int joiners = min(part.parts, part.rows);
-        if (part.index >= joiners) continue;
-        if (threadIdx.x == 0) *abort = parts_written(a, part, part.parts) ? 0 : 1;
+        if (threadIdx.x == 0) {
+            const unsigned seen = i == 0 ? seen0 : seen1;
+            // (A CTA with no share of the rows need not wait, unless it is the last and the others do not.)
+            *abort = await_parts(a, part, seen, part.index < joiners && seen < kWontWait, part.parts);
+        }
         sync();
-        const bool ok = *abort == 0;
-        for (int r = part.index; ok && r < part.rows; r += joiners) join_row<DP, C::WARPS, ROWS>(a, part, r, merge, sync);
+        const int mode = *abort;
+        if (mode == kJoinShare)
+            for (int r = part.index; r < part.rows; r += joiners) join_row<DP, C::WARPS, ROWS>(a, part, r, merge, sync);
+        if (mode == kJoinAll)
+            for (int r = 0; r < part.rows; ++r) join_row<DP, C::WARPS, ROWS>(a, part, r, merge, sync);
         sync();
-        if (threadIdx.x == 0 && ok) part_joined(a, part, joiners);
     }
+    if (threadIdx.x == 0) cta_finishes(a);
 }
 
 template <int DP, bool WIDE>
@@ -470,7 +481,7 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
     using C = RowCfg<DP>;
     static_assert(C::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
     if (!set_smem_once(reinterpret_cast<const void *>(attn_rows_kernel<DP, WIDE>), (int)C::SMEM)) return W4_ERR_LAUNCH;
-    return launch_resident(attn_rows_kernel<DP, WIDE>, grid, C::THREADS, C::SMEM, stream, mk, mv, a);
+    return launch_dependent(attn_rows_kernel<DP, WIDE>, grid, C::THREADS, C::SMEM, stream, mk, mv, a);
 }
 
 // Whether a call takes the tcgen05 kernel: more rows per sequence and
@@ -478,7 +489,8 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
 bool takes_tc(int group, int head_dim, int max_q_len) { return (long long)group * max_q_len > 16 && head_dim <= 128; }
 
 // Workspace: the counters, then two partial tiles per CTA (statistics, outputs).
-constexpr size_t kCounterBytes = 2 * kMaxGrid * sizeof(unsigned);
+constexpr size_t kCounterBytes = 2048;
+static_assert((kMaxGrid + 2) * sizeof(unsigned) <= kCounterBytes, "counters");
 size_t workspace_need(int rows, int head_dim) {
     return (kCounterBytes + (size_t)2 * kMaxGrid * rows * (2 + head_dim) * 4 + 15) / 16 * 16;
 }
@@ -552,7 +564,8 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     a.scale = scale * kLog2e;
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     a.arrived = reinterpret_cast<unsigned *>(ws);
-    a.left = a.arrived + kMaxGrid;
+    a.begun = a.arrived + kMaxGrid;
+    a.finished = a.begun + 1;
     a.part_ml = reinterpret_cast<float *>(ws + kCounterBytes);
     a.part_o = a.part_ml + (size_t)2 * kMaxGrid * rows * 2;
     const bool wide = !tc && d % 64 == 0 && d > 64;

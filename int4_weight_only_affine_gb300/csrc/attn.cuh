@@ -11,9 +11,13 @@
 // within a unit, whatever the lengths.  An item cut by a range boundary is
 // computed in parts: each part's CTA leaves its unnormalised output, running
 // maximum and sum in the workspace and counts itself in; when a CTA is done
-// with its own range it waits for the parts of the items it shares (all CTAs
-// are resident: a cooperative launch) and joins its share of their rows, in
-// the parts' order.  Every CTA works its range out from the lengths by itself:
+// with its own range it waits for the parts of the items it shares and joins
+// its share of their rows, in the parts' order.  A CTA waits only if every CTA
+// of the launch had begun when it counted its part in (so each will finish,
+// whatever else the GPU runs); otherwise it says so as it counts, and the last
+// to count a part of the item in joins all of it.  (A cooperative launch would
+// promise the same, but is not overlapped with the end of the kernel before:
+// 2.6 us a call.)  Every CTA works its range out from the lengths by itself:
 // the host needs no lengths, and the split depends on nothing but the batch,
 // so results repeat.
 #pragma once
@@ -38,7 +42,10 @@ struct AttnArgs {
     float scale;    // times log2(e): the softmax is taken in powers of two
     float *part_o;  // [2 * grid][rows x head_dim], in the order of the kernel that writes it
     float *part_ml; // [2 * grid][rows][2]: running maximum (base-2 scaled scores) and sum
-    unsigned *arrived, *left;  // [grid]: of the item that starts in a CTA's range; zero between calls
+    // Zero between calls: parts counted in of the item that starts in a CTA's
+    // range [grid] (and above bit 16 those that will not wait), CTAs begun and
+    // finished.
+    unsigned *arrived, *begun, *finished;
 };
 
 // A CTA's part of an item that several CTAs share.
@@ -384,57 +391,80 @@ __device__ __forceinline__ float log_sum(float mx, float sum) {
 // lies in the odd slot of c, every later part in the even slot of the next ones.
 __device__ __forceinline__ long long part_slot(int c, int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); }
 
-// Counts a part in: its partial results were written by threads that the
-// calling thread has synchronised with.  COPIED: they are read by copies.
+// A CTA begins: called by one thread, after the kernel before is done.
+__device__ __forceinline__ void cta_begins(const AttnArgs &a) { atomicAdd(a.begun, 1u); }
+
+// A CTA is done with everything: called by one thread.  The last one leaves the counters as they were found.
+__device__ __forceinline__ void cta_finishes(const AttnArgs &a) {
+    if (atomicAdd(a.finished, 1u) != gridDim.x - 1) return;
+    for (unsigned i = 0; i < gridDim.x; ++i) a.arrived[i] = 0;
+    *a.begun = 0;
+    *a.finished = 0;
+}
+
+constexpr unsigned kCountMask = 0xFFFFu, kWontWait = 0x10000u;
+
+// Counts a part in, by a thread that its writers have synchronised with;
+// returns the item's count with it.  COPIED: the parts are read by copies.
 template <bool COPIED>
-__device__ __forceinline__ void part_written(const AttnArgs &a, const Part &p) {
+__device__ __forceinline__ unsigned count_part(const AttnArgs &a, const Part &p) {
     __threadfence();
     if (COPIED) asm volatile("fence.proxy.async.global;" ::: "memory");
-    atomicAdd(a.arrived + p.first, 1u);
+    unsigned begun;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(begun) : "l"(a.begun) : "memory");
+    const unsigned mine = 1u + (begun == gridDim.x ? 0u : kWontWait);
+    return atomicAdd(a.arrived + p.first, mine) + mine;
 }
 
-// Until `count` arrivals for the item (bounded; on expiry its rows stay
-// unwritten, w4a16_device_status says so and the workspace has to be zeroed).
-__device__ __forceinline__ bool parts_written(const AttnArgs &a, const Part &p, unsigned count) {
-    uint64_t t0 = 0;
-    for (uint32_t spin = 0;; ++spin) {
-        unsigned v;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.arrived + p.first) : "memory");
-        if (v == count) return true;
-        if ((spin & 63) == 63) {
-            const uint64_t now = global_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitNs) break;
+// What a CTA joins of an item it shares.
+enum : int { kJoinNothing = 0, kJoinShare = 1, kJoinAll = 2 };
+
+// Asked by one thread with the count as it saw it; waits until all `parts`
+// arrivals are in, unless it counted itself as not waiting.  A wait is bounded:
+// when it runs out, and where there are more arrivals than parts (a workspace
+// that was not zeroed), w4a16_device_status says so.
+__device__ __forceinline__ int await_parts(const AttnArgs &a, const Part &p, unsigned seen, bool waits, unsigned parts) {
+    const bool last = (seen & kCountMask) == parts;
+    if ((seen & kCountMask) > parts || (seen >> 16) > parts) {
+        atomicExch(&g_wait_expired, 1);
+        return kJoinNothing;
+    }
+    if (!last) {
+        if (!waits) return kJoinNothing;
+        uint64_t t0 = 0;
+        for (uint32_t spin = 0;; ++spin) {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(a.arrived + p.first) : "memory");
+            if ((seen & kCountMask) == parts) break;
+            if ((spin & 63) == 63) {
+                const uint64_t now = global_ns();
+                if (t0 == 0) t0 = now;
+                if (now - t0 > kWaitNs) {
+                    atomicExch(&g_wait_expired, 1);
+                    return kJoinNothing;
+                }
+            }
         }
     }
-    atomicExch(&g_wait_expired, 1);
-    return false;
+    __threadfence();
+    if (seen < kWontWait) return kJoinShare;
+    return last ? kJoinAll : kJoinNothing;
 }
 
-// The last of the `joiners` CTAs to be done with an item resets its counters.
-__device__ __forceinline__ void part_joined(const AttnArgs &a, const Part &p, unsigned joiners) {
-    if (atomicAdd(a.left + p.first, 1u) == joiners - 1) {
-        a.arrived[p.first] = 0;
-        a.left[p.first] = 0;
-    }
-}
-
-// Launch with every CTA resident (they wait for one another's parts).
+// Launch as a programmatic dependent (the kernels wait for the one before
+// first: it only takes the launch itself off the path).
 template <class K>
-int launch_resident(K kernel, int grid, int threads, size_t smem, cudaStream_t stream, const CUtensorMap &mk,
-                    const CUtensorMap &mv, const AttnArgs &a) {
+int launch_dependent(K kernel, int grid, int threads, size_t smem, cudaStream_t stream, const CUtensorMap &mk,
+                     const CUtensorMap &mv, const AttnArgs &a) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (the kernels wait for the one before first)
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, mk, mv, a) != cudaSuccess) {
         cudaGetLastError();
         return W4_ERR_LAUNCH;

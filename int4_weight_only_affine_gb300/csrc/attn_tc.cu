@@ -50,7 +50,7 @@ struct TcCfg {
     static constexpr int TILE = HALVES * HALF;                    // 128 rows of Q, K or V
     static constexpr int SLOTS = DP == 64 ? 8 : 5;                // ring of K and V tiles
     static constexpr int BARS = 2 * SLOTS + 2 * 7 + 2;
-    static constexpr size_t SMEM = 1024 + (size_t)(2 + SLOTS) * TILE + 8 * BARS + 16;
+    static constexpr size_t SMEM = 1024 + (size_t)(2 + SLOTS) * TILE + 8 * BARS + 32;
     // Tensor-memory columns.  A head of 64 leaves room for P beside S; with
     // 128, P_t lies in the columns of S_t, whose next product therefore waits
     // for O_t += P_t V to finish.
@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const uint32_t bar0 = ring + C::SLOTS * C::TILE;
     uint8_t *tail = smem_raw + (bar0 - raw) + 8 * C::BARS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail);
-    volatile int *abort = reinterpret_cast<volatile int *>(tail + 4), *join_ok = abort + 1;
+    volatile int *abort = reinterpret_cast<volatile int *>(tail + 4), *join_mode = abort + 1;
+    volatile unsigned *seen_sh = reinterpret_cast<volatile unsigned *>(tail + 12);  // [shared item][tile]
     auto kv_full = [&](int s) { return bar0 + 8u * s; };
     auto kv_empty = [&](int s) { return bar0 + 8u * (C::SLOTS + s); };
     auto q_full = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + t); };      // Q_t written
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     pdl_wait();
+    if (threadIdx.x == 0) cta_begins(a);
     fence_before();
     make_plan<Work, TC_THREADS>(a, plan_sh);  // (its barriers also publish the above)
     fence_after();
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const f32x2 scale2 = pair(a.scale, a.scale);
         Part shared0, shared1;  // items that this CTA shares with earlier and later ones
         int shares = 0;
-        bool unsignalled = false;  // this thread has a part to count in
+        bool uncounted = false;  // this thread has a part to count in
         uint32_t steps = 0;
         int it = 0;
         while (pc.next()) {
@@ -507,14 +509,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 else
                     shared1 = pc.part(plan);
             };
-            auto signal_part = [&] {  // (of the first shared item: a later one is this CTA's last)
-                if (unsignalled) part_written<true>(a, shared0);
-                unsignalled = false;
+            auto count_first = [&] {  // (of the first shared item: a later one is this CTA's last)
+                if (uncounted) seen_sh[t] = count_part<true>(a, shared0);
+                uncounted = false;
             };
             const bool split = split_units(rows, pc.n);
             const int tile_row = split ? 0 : 128 * t;
             if (tile_row >= rows) {
-                signal_part();
+                count_first();
                 note_part();
                 continue;
             }
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full(t));
-            signal_part();  // now that there is time, until S_t is there
+            count_first();  // now that there is time, until S_t is there
             note_part();
 
             const int p = pc.s.kv - pc.s.qn + gr / a.group;
@@ -744,12 +746,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 else
                     asm volatile("bar.sync 2, 128;" ::: "memory");
-                unsignalled = (threadIdx.x & 127) == 0;
+                uncounted = (threadIdx.x & 127) == 0;
             }
         }
         // ---------------- join this CTA's share of the items it shares, all eight warps ----------------
         // (Both tiles' warps meet before the first copy into the ring: every product is done.)
-        if (unsignalled) part_written<true>(a, shares == 1 ? shared0 : shared1);
+        if (uncounted) seen_sh[2 * (shares - 1) + t] = count_part<true>(a, shares == 1 ? shared0 : shared1);
         uint32_t join_phase = 0;
         for (int i = 0; i < shares; ++i) {
             const Part part = i == 0 ? shared0 : shared1;
@@ -759,26 +761,34 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const bool few = part.parts <= FEW_PARTS;
             const int groups = a.head_dim / 4, blocks = (part.rows + 31) / 32 * ((a.head_dim + 31) / 32);
             const int joiners = min(part.parts, few ? groups : blocks);
-            if (part.index >= joiners) continue;
+            fence_proxy_async_smem();  // (shared memory that threads used is written by copies)
+            sync();
             if (threadIdx.x == 0) {
-                *join_ok = parts_written(a, part, part.parts * (part.rows > 128 ? 2 : 1)) ? 1 : 0;
+                // The later of the counts that the tiles' threads saw; not waiting, if one said so or has no share.
+                const unsigned tiles = part.rows > 128 ? 2 : 1, all = part.parts * tiles;
+                const unsigned s0 = seen_sh[2 * i], s1 = tiles == 2 ? seen_sh[2 * i + 1] : 0;
+                const unsigned seen = (s1 & kCountMask) > (s0 & kCountMask) ? s1 : s0;
+                *join_mode = await_parts(a, part, seen, part.index < joiners && seen < kWontWait, all);
                 asm volatile("fence.proxy.async.global;" ::: "memory");  // the parts were stored by threads, and are read by copies
             }
-            fence_proxy_async_smem();  // (and shared memory that threads used is written by copies)
             sync();
-            const bool ok = *join_ok != 0;
-            if (ok && !few)
-                for (int x = part.index; x < blocks; x += joiners) join_block(a, part, x);
-            if (ok && few)
-                join_columns<DP>(a, part, part.index * groups / joiners, (part.index + 1) * groups / joiners, ring, base,
-                                 join_bar, join_phase, sync);
-            sync();
-            if (threadIdx.x == 0 && ok) part_joined(a, part, joiners);
+            const int mode = *join_mode;
+            // Columns are one range to a joiner, blocks are dealt out in turn.
+            const int pieces = few ? joiners : blocks;
+            const int step = mode == kJoinAll ? 1 : joiners;
+            for (int x = mode == kJoinAll ? 0 : part.index; mode != kJoinNothing && x < pieces; x += step) {
+                if (few)
+                    join_columns<DP>(a, part, x * groups / joiners, (x + 1) * groups / joiners, ring, base, join_bar,
+                                     join_phase, sync);
+                else
+                    join_block(a, part, x);
+            }
         }
     }
 
     fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) cta_finishes(a);
     if (warp == 9) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -789,7 +799,7 @@ template <int DP>
 int launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
     static_assert(TcCfg<DP>::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
     if (!set_smem_once(reinterpret_cast<const void *>(attn_tc_kernel<DP>), (int)TcCfg<DP>::SMEM)) return W4_ERR_LAUNCH;
-    return launch_resident(attn_tc_kernel<DP>, grid, TC_THREADS, TcCfg<DP>::SMEM, stream, mk, mv, a);
+    return launch_dependent(attn_tc_kernel<DP>, grid, TC_THREADS, TcCfg<DP>::SMEM, stream, mk, mv, a);
 }
 
 }  // namespace

@@ -256,6 +256,44 @@ def test_other_stream_and_captured_graph(w4):
     assert w4.device_status() == 0
 
 
+def test_calls_on_two_streams_at_once(w4):
+    """Calls that share the GPU, each with a workspace of its own: blocks of a call that cannot all run at once."""
+    import torch
+    hq, hkv, d = 16, 2, 128
+    cases = []
+    for k, (ql, kl) in enumerate((([1, 1], [30000, 100]), ([200, 1], [9000, 3000]), ([3], [20000]), ([700], [2500]))):
+        batch = Batch(ql, kl, 16, seed=k)
+        q, kc, vc = data(batch, hq, hkv, d, k)
+        cache, kb = w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch)
+        want = w4.f16_attention(to_dev(q), cache, kb)
+        cases.append((to_dev(q), cache, kb, want, w4.attention_workspace(cache, hq, 700), torch.cuda.Stream(),
+                      [torch.empty_like(want) for _ in range(20)]))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for q, cache, kb, want, ws, stream, ys in cases:
+            w4.f16_attention(q, cache, kb, y=ys[i], workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    assert w4.device_status() == 0
+    for q, cache, kb, want, ws, stream, ys in cases:
+        assert all(bool((y == want).all()) for y in ys)
+        assert not bool(ws[:2048].any())
+
+
+def test_workspace_that_was_not_zeroed(w4):
+    """Waits for parts that cannot all come in run out, are reported, and the call works again on a zeroed workspace."""
+    batch = Batch([1], [9000], 16, seed=5)
+    q, kc, vc = data(batch, 16, 2, 128, 5)
+    cache, kb = w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch)
+    ws = w4.attention_workspace(cache, 16, 1)
+    ws[:1024] = 1   # counts of parts far past any item's
+    w4.f16_attention(to_dev(q), cache, kb, workspace=ws)
+    assert w4.device_status() == 8 and w4.device_status() == 0
+    ws.zero_()
+    wy, _, ty, _ = attention(q, kc, vc, batch, 128**-0.5)
+    check(w4.f16_attention(to_dev(q), cache, kb, workspace=ws), wy, ty, "y")
+    assert w4.device_status() == 0
+
+
 def test_offsets_past_32_bits(w4):
     """Pages that lie beyond 2**32 elements of the cache."""
     import torch

@@ -174,7 +174,6 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_wait();
-    if (threadIdx.x == 0) cta_begins(a);
     make_plan<typename C::Work, C::THREADS>(a, plan_sh);  // (its barriers also publish the above)
     const Plan plan = plan_sh.plan;
     Pieces<typename C::Work> pc(a, plan);
@@ -233,9 +232,15 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
     const int vrow = lane & 15, vch = lane >> 4;
     const uint32_t v_off = row_at(16 * warp + vrow);
     const int g = lane >> 2, t4 = lane & 3;
+    if (threadIdx.x == NT - 32) {  // (off the way: the first positions are being copied)
+        const Begin begin = cta_begins(a);
+        plan_sh.begun_before = begin.before;
+        cta_has_begun(a, begin);
+    }
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
     Part shared0, shared1;  // items that this CTA shares with earlier and later ones
     unsigned seen0 = 0, seen1 = 0;  // (thread 0) their counts with this CTA's part
+    bool waits = true;              // and whether it may wait for the others'
     int shares = 0;
     int it = 0;
     while (pc.next()) {
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
             merge_rows(std::integral_constant<int, 2>());
         if (!whole) {
             const Part part = pc.part(plan);
-            const unsigned count = threadIdx.x == 0 ? count_part<false>(a, part) : 0;
+            const unsigned count = threadIdx.x == 0 ? count_part<false>(a, part, plan_sh.begun_before, waits) : 0;
             if (shares++ == 0) {
                 shared0 = part;
                 seen0 = count;
@@ -462,8 +467,8 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
         const int joiners = min(part.parts, part.rows);
         if (threadIdx.x == 0) {
             const unsigned seen = i == 0 ? seen0 : seen1;
-            // (A CTA with no share of the rows need not wait, unless it is the last and the others do not.)
-            *abort = await_parts(a, part, seen, part.index < joiners && seen < kWontWait, part.parts);
+            // (A CTA with no share of the rows need not wait.  One that said it would not may be the last to count.)
+            *abort = await_parts(a, part, seen, part.index < joiners && waits, part.parts);
         }
         sync();
         const int mode = *abort;
@@ -472,8 +477,8 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
         if (mode == kJoinAll)
             for (int r = 0; r < part.rows; ++r) join_row<DP, C::WARPS, ROWS>(a, part, r, merge, sync);
         sync();
+        if (threadIdx.x == 0) part_done(a, part);
     }
-    if (threadIdx.x == 0) cta_finishes(a);
 }
 
 template <int DP, bool WIDE>
@@ -489,8 +494,7 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
 bool takes_tc(int group, int head_dim, int max_q_len) { return (long long)group * max_q_len > 16 && head_dim <= 128; }
 
 // Workspace: the counters, then two partial tiles per CTA (statistics, outputs).
-constexpr size_t kCounterBytes = 2048;
-static_assert((kMaxGrid + 2) * sizeof(unsigned) <= kCounterBytes, "counters");
+constexpr size_t kCounterBytes = (2 * kMaxGrid + 4) * sizeof(unsigned);
 size_t workspace_need(int rows, int head_dim) {
     return (kCounterBytes + (size_t)2 * kMaxGrid * rows * (2 + head_dim) * 4 + 15) / 16 * 16;
 }
@@ -564,8 +568,9 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     a.scale = scale * kLog2e;
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     a.arrived = reinterpret_cast<unsigned *>(ws);
-    a.begun = a.arrived + kMaxGrid;
-    a.finished = a.begun + 1;
+    a.left = a.arrived + kMaxGrid;
+    a.begun = a.left + kMaxGrid;
+    a.begun_before = a.begun + 1;
     a.part_ml = reinterpret_cast<float *>(ws + kCounterBytes);
     a.part_o = a.part_ml + (size_t)2 * kMaxGrid * rows * 2;
     const bool wide = !tc && d % 64 == 0 && d > 64;

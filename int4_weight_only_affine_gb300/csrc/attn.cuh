@@ -42,10 +42,11 @@ struct AttnArgs {
     float scale;    // times log2(e): the softmax is taken in powers of two
     float *part_o;  // [2 * grid][rows x head_dim], in the order of the kernel that writes it
     float *part_ml; // [2 * grid][rows][2]: running maximum (base-2 scaled scores) and sum
-    // Zero between calls: parts counted in of the item that starts in a CTA's
-    // range [grid] (and above bit 16 those that will not wait), CTAs begun and
-    // finished.
-    unsigned *arrived, *begun, *finished;
+    // Of the item that starts in a CTA's range, zero between calls: parts
+    // counted in (and above bit 16 those that will not wait), and CTAs done
+    // with it.
+    unsigned *arrived, *left;
+    unsigned *begun, *begun_before;  // CTAs begun in all calls, and in the calls before
 };
 
 // A CTA's part of an item that several CTAs share.
@@ -127,6 +128,7 @@ __device__ __forceinline__ uint32_t owner(const Plan &p, uint32_t at) {
 struct PlanShared {
     uint32_t sums[32];
     Plan plan;
+    unsigned begun_before;
 };
 
 // Called by all THREADS threads of the CTA.  Workers (threads, or warps where
@@ -391,63 +393,76 @@ __device__ __forceinline__ float log_sum(float mx, float sum) {
 // lies in the odd slot of c, every later part in the even slot of the next ones.
 __device__ __forceinline__ long long part_slot(int c, int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); }
 
-// A CTA begins: called by one thread, after the kernel before is done.
-__device__ __forceinline__ void cta_begins(const AttnArgs &a) { atomicAdd(a.begun, 1u); }
-
-// A CTA is done with everything: called by one thread.  The last one leaves the counters as they were found.
-__device__ __forceinline__ void cta_finishes(const AttnArgs &a) {
-    if (atomicAdd(a.finished, 1u) != gridDim.x - 1) return;
-    for (unsigned i = 0; i < gridDim.x; ++i) a.arrived[i] = 0;
-    *a.begun = 0;
-    *a.finished = 0;
+// A CTA begins: by one thread, after the kernel before is done.  begun counts
+// on from call to call; begun_before is moved up by the last CTA to begin,
+// when every other has read it.
+struct Begin {
+    unsigned before, mine;
+};
+__device__ __forceinline__ Begin cta_begins(const AttnArgs &a) {
+    Begin b;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(b.before) : "l"(a.begun_before) : "memory");
+    b.mine = atomicAdd(a.begun, 1u);
+    return b;
+}
+__device__ __forceinline__ void cta_has_begun(const AttnArgs &a, const Begin &b) {  // (when the count is back)
+    if (b.mine + 1 == b.before + gridDim.x) *a.begun_before = b.before + gridDim.x;
 }
 
 constexpr unsigned kCountMask = 0xFFFFu, kWontWait = 0x10000u;
 
 // Counts a part in, by a thread that its writers have synchronised with;
-// returns the item's count with it.  COPIED: the parts are read by copies.
+// returns the item's count with it, and clears `waits` where the CTA may not
+// wait for the others.  COPIED: the parts are read by copies.
 template <bool COPIED>
-__device__ __forceinline__ unsigned count_part(const AttnArgs &a, const Part &p) {
+__device__ __forceinline__ unsigned count_part(const AttnArgs &a, const Part &p, unsigned begun_before, bool &waits) {
+    unsigned begun;  // (on its way while the fence is)
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(begun) : "l"(a.begun) : "memory");
     __threadfence();
     if (COPIED) asm volatile("fence.proxy.async.global;" ::: "memory");
-    unsigned begun;
-    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(begun) : "l"(a.begun) : "memory");
-    const unsigned mine = 1u + (begun == gridDim.x ? 0u : kWontWait);
+    const bool all = begun == begun_before + gridDim.x;
+    waits = waits && all;
+    const unsigned mine = 1u + (all ? 0u : kWontWait);
     return atomicAdd(a.arrived + p.first, mine) + mine;
 }
 
 // What a CTA joins of an item it shares.
 enum : int { kJoinNothing = 0, kJoinShare = 1, kJoinAll = 2 };
 
-// Asked by one thread with the count as it saw it; waits until all `parts`
-// arrivals are in, unless it counted itself as not waiting.  A wait is bounded:
-// when it runs out, and where there are more arrivals than parts (a workspace
-// that was not zeroed), w4a16_device_status says so.
+// Asked by one thread with the count as it saw it; with `waits` it waits until
+// all `parts` arrivals are in.  A wait is bounded: when it runs out, and where
+// there are more arrivals than parts (a workspace that was not zeroed),
+// w4a16_device_status says so.
 __device__ __forceinline__ int await_parts(const AttnArgs &a, const Part &p, unsigned seen, bool waits, unsigned parts) {
-    const bool last = (seen & kCountMask) == parts;
-    if ((seen & kCountMask) > parts || (seen >> 16) > parts) {
+    unsigned now = seen;
+    if (waits) {
+        uint64_t t0 = 0;
+        for (uint32_t spin = 0;; ++spin) {  // (the first look does not need `seen`, which may still be on its way)
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(a.arrived + p.first) : "memory");
+            if ((now & kCountMask) >= parts) break;
+            if ((spin & 63) == 63) {
+                const uint64_t t = global_ns();
+                if (t0 == 0) t0 = t;
+                if (t - t0 > kWaitNs) break;
+            }
+        }
+        if ((now & kCountMask) == parts && now < kWontWait) return kJoinShare;
+    }
+    if ((now & kCountMask) > parts || (now >> 16) > parts || (waits && (now & kCountMask) < parts)) {
         atomicExch(&g_wait_expired, 1);
         return kJoinNothing;
     }
-    if (!last) {
-        if (!waits) return kJoinNothing;
-        uint64_t t0 = 0;
-        for (uint32_t spin = 0;; ++spin) {
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(a.arrived + p.first) : "memory");
-            if ((seen & kCountMask) == parts) break;
-            if ((spin & 63) == 63) {
-                const uint64_t now = global_ns();
-                if (t0 == 0) t0 = now;
-                if (now - t0 > kWaitNs) {
-                    atomicExch(&g_wait_expired, 1);
-                    return kJoinNothing;
-                }
-            }
-        }
-    }
+    if ((seen & kCountMask) != parts) return kJoinNothing;
     __threadfence();
-    if (seen < kWontWait) return kJoinShare;
-    return last ? kJoinAll : kJoinNothing;
+    return seen < kWontWait ? kJoinShare : kJoinAll;
+}
+
+// A CTA is done with an item: the last of them all leaves its counts at zero.
+__device__ __forceinline__ void part_done(const AttnArgs &a, const Part &p) {
+    if (atomicAdd(a.left + p.first, 1u) == (unsigned)p.parts - 1) {
+        a.arrived[p.first] = 0;
+        a.left[p.first] = 0;
+    }
 }
 
 // Launch as a programmatic dependent (the kernels wait for the one before

@@ -336,10 +336,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     pdl_wait();
-    if (threadIdx.x == 0) cta_begins(a);
+    constexpr int BEGINNER = 96;  // (of a warp without sequences of its own in small batches)
+    Begin begin = {0, 0};
+    if (threadIdx.x == BEGINNER) {
+        begin = cta_begins(a);
+        plan_sh.begun_before = begin.before;
+    }
     fence_before();
     make_plan<Work, TC_THREADS>(a, plan_sh);  // (its barriers also publish the above)
     fence_after();
+    if (threadIdx.x == BEGINNER) cta_has_begun(a, begin);
     const uint32_t tmem = *tmem_slot;
     const Plan plan = plan_sh.plan;
     Pieces<Work> pc(a, plan);
@@ -495,6 +501,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         Part shared0, shared1;  // items that this CTA shares with earlier and later ones
         int shares = 0;
         bool uncounted = false;  // this thread has a part to count in
+        bool waits = true;       // and whether it may wait for the others'
         uint32_t steps = 0;
         int it = 0;
         while (pc.next()) {
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     shared1 = pc.part(plan);
             };
             auto count_first = [&] {  // (of the first shared item: a later one is this CTA's last)
-                if (uncounted) seen_sh[t] = count_part<true>(a, shared0);
+                if (uncounted) seen_sh[t] = count_part<true>(a, shared0, plan_sh.begun_before, waits);
                 uncounted = false;
             };
             const bool split = split_units(rows, pc.n);
@@ -751,7 +758,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         // ---------------- join this CTA's share of the items it shares, all eight warps ----------------
         // (Both tiles' warps meet before the first copy into the ring: every product is done.)
-        if (uncounted) seen_sh[2 * (shares - 1) + t] = count_part<true>(a, shares == 1 ? shared0 : shared1);
+        if (uncounted) seen_sh[2 * (shares - 1) + t] = count_part<true>(a, shares == 1 ? shared0 : shared1, plan_sh.begun_before, waits);
         uint32_t join_phase = 0;
         for (int i = 0; i < shares; ++i) {
             const Part part = i == 0 ? shared0 : shared1;
@@ -764,11 +771,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             fence_proxy_async_smem();  // (shared memory that threads used is written by copies)
             sync();
             if (threadIdx.x == 0) {
-                // The later of the counts that the tiles' threads saw; not waiting, if one said so or has no share.
+                // The later of the counts that the tiles' threads saw.  (A CTA with no share need not wait.)
                 const unsigned tiles = part.rows > 128 ? 2 : 1, all = part.parts * tiles;
                 const unsigned s0 = seen_sh[2 * i], s1 = tiles == 2 ? seen_sh[2 * i + 1] : 0;
                 const unsigned seen = (s1 & kCountMask) > (s0 & kCountMask) ? s1 : s0;
-                *join_mode = await_parts(a, part, seen, part.index < joiners && seen < kWontWait, all);
+                *join_mode = await_parts(a, part, seen, part.index < joiners && waits, all);
                 asm volatile("fence.proxy.async.global;" ::: "memory");  // the parts were stored by threads, and are read by copies
             }
             sync();
@@ -783,12 +790,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 else
                     join_block(a, part, x);
             }
+            sync();
+            if (threadIdx.x == 0) part_done(a, part);
         }
     }
 
     fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) cta_finishes(a);
     if (warp == 9) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));

@@ -50,10 +50,10 @@ def run(w4, batch, hq, hkv, d, causal=True, window=0, scale=None, seed=0, max_q=
     lse = torch.full((batch.tokens, hq), 7.0, dtype=torch.float32, device="cuda")
     kb = device_batch(w4, batch, max_q)
     ws = w4.attention_workspace(cache, hq, kb.max_q_len)
-    ws[2048:] = 255   # NaN past the counters: what an earlier call left there may not matter
+    ws[2064:] = 255   # NaN past the counters: what an earlier call left there may not matter
     w4.f16_attention(to_dev(q), cache, kb, y=y, lse=lse, scale=scale, causal=causal, window=window, workspace=ws)
     assert w4.device_status() == 0
-    assert not bool(ws[:2048].any())   # the counters are ready for the next call
+    assert not bool(ws[:2048].any())   # the counts of parts are ready for the next call
     sc = d**-0.5 if scale is None else scale
     wy, wl, ty, tl = attention(q, kc, vc, batch, sc, causal, window)
     check(y, wy, ty, "y")

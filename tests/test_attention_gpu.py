@@ -279,6 +279,26 @@ def test_calls_on_two_streams_at_once(w4):
         assert not bool(ws[:2048].any())
 
 
+@pytest.mark.parametrize("ql,kl,hq,hkv,d", [([1, 1], [30000, 100], 16, 2, 128), ([200, 1], [9000, 3000], 16, 2, 128),
+                                            ([700], [2500], 16, 2, 128), ([90, 60], [3000, 2000], 14, 2, 64),
+                                            ([64], [9001], 16, 8, 128), ([2000], [2000], 8, 8, 64)])
+def test_blocks_that_may_not_wait(w4, ql, kl, hq, hkv, d):
+    """With a count of begun blocks that says some never began (as when another call holds part of the GPU), no
+    block waits for another's part, and the last to count a part in joins them: the same bits."""
+    import torch
+    batch = Batch(ql, kl, 16, seed=3)
+    q, kc, vc = data(batch, hq, hkv, d, 3)
+    cache, kb = w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch)
+    ws = w4.attention_workspace(cache, hq, max(ql))
+    lse, lse2 = (torch.empty(batch.tokens, hq, device="cuda") for _ in range(2))
+    y = w4.f16_attention(to_dev(q), cache, kb, lse=lse, workspace=ws)
+    ws.zero_()
+    ws.view(torch.int32)[513] = 1000   # blocks begun in earlier calls, which the count of all calls lacks
+    y2 = w4.f16_attention(to_dev(q), cache, kb, lse=lse2, workspace=ws)
+    assert w4.device_status() == 0 and not bool(ws[:2048].any())
+    assert bool((y == y2).all()) and bool((lse == lse2).all())
+
+
 def test_workspace_that_was_not_zeroed(w4):
     """Waits for parts that cannot all come in run out, are reported, and the call works again on a zeroed workspace."""
     batch = Batch([1], [9000], 16, seed=5)

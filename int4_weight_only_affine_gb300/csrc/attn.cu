@@ -39,7 +39,7 @@ template <int DP>
 struct RowCfg {
     static constexpr int ROWS = 16;
     static constexpr int KEYS = kv_tile(DP);
-    using Work = Cut<ROWS, KEYS, 2, 1, ROWS>;
+    using Work = Cut<ROWS, KEYS, 2, 1, ROWS, 4, 1>;
     static constexpr int WARPS = KEYS / 16;             // consumers
     static constexpr int THREADS = 32 * (WARPS + 1);
     static constexpr int TILE = KEYS * 128 * (DP / 64); // bytes of K or V
@@ -57,91 +57,125 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
-// Row r of a shared item, by WARPS warps: they take the parts in turn, lane l
-// of each the columns 4 l .. 4 l + 3 (and those 128 further on), and merge
-// through sh.  A part's rows lie one after the other.
-template <int DP, int WARPS, int ROWS, class Sync>
-__device__ __forceinline__ void join_row(const AttnArgs &a, const Part &part, int r, float *sh, Sync sync) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float4 *sh_o = reinterpret_cast<float4 *>(sh);                         // [WARPS][2][32]
-    float2 *sh_ml = reinterpret_cast<float2 *>(sh + WARPS * 2 * 32 * 4);  // [WARPS]
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-    float mx = -INFINITY, sum = 0.f;
-    constexpr int H = DP > 128 ? 2 : 1, FLIGHT = 10 / H;  // parts of a warp whose loads are in flight
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int i0 = warp; i0 < part.parts; i0 += FLIGHT * WARPS) {
-        float4 v[FLIGHT][H];
-        float2 c[FLIGHT];
+// Joins rows of a shared item, by WARPS warps.  A part's rows lie one after the
+// other; lane l takes the columns 4 l .. 4 l + 3, and those 128 further on.
+template <int DP, int WARPS, int ROWS>
+struct Join {
+    static constexpr int H = DP > 128 ? 2 : 1, FLIGHT = 10 / H;  // parts of a row whose loads are in flight
+    const AttnArgs &a;
+    const Part &part;
+
+    // Sums of row r over the parts i0, i0 + STEP, ...
+    template <int STEP>
+    __device__ __forceinline__ void sum_parts(int r, int i0, float &mx, float &sum, float4 (&acc)[2]) const {
+        const int lane = threadIdx.x & 31;
+        const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+        mx = -INFINITY;
+        sum = 0.f;
+        acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (; i0 < part.parts; i0 += FLIGHT * STEP) {
+            float4 v[FLIGHT][H];
+            float2 c[FLIGHT];
 #pragma unroll
-        for (int k = 0; k < FLIGHT; ++k) {
-            const int i = i0 + k * WARPS;
-            c[k] = make_float2(-INFINITY, 0.f);
+            for (int k = 0; k < FLIGHT; ++k) {
+                const int i = i0 + k * STEP;
+                c[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int h = 0; h < H; ++h) v[k][h] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < part.parts) {
-                const long long row = part_slot(part.first, i) * ROWS + r;
-                c[k] = __ldcg(ml + row);
+                for (int h = 0; h < H; ++h) v[k][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < part.parts) {
+                    const long long row = part_slot(part.first, i) * ROWS + r;
+                    c[k] = __ldcg(ml + row);
 #pragma unroll
-                for (int h = 0; h < H; ++h)
-                    if (128 * h + 4 * lane < a.head_dim)
-                        v[k][h] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + row * a.head_dim + 128 * h + 4 * lane));
+                    for (int h = 0; h < H; ++h)
+                        if (128 * h + 4 * lane < a.head_dim)
+                            v[k][h] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + row * a.head_dim + 128 * h + 4 * lane));
+                }
             }
-        }
-        float top = mx;
+            float top = mx;
 #pragma unroll
-        for (int k = 0; k < FLIGHT; ++k) top = fmaxf(top, c[k].x);
-        const float f0 = corr(mx, top);
-        mx = top;
-        sum *= f0;
+            for (int k = 0; k < FLIGHT; ++k) top = fmaxf(top, c[k].x);
+            const float f0 = corr(mx, top);
+            mx = top;
+            sum *= f0;
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            acc[h].x *= f0;
-            acc[h].y *= f0;
-            acc[h].z *= f0;
-            acc[h].w *= f0;
-        }
+            for (int h = 0; h < H; ++h) scale4(acc[h], f0);
 #pragma unroll
-        for (int k = 0; k < FLIGHT; ++k) {
-            const float f = corr(c[k].x, top);
-            sum += c[k].y * f;
+            for (int k = 0; k < FLIGHT; ++k) {
+                const float f = corr(c[k].x, top);
+                sum += c[k].y * f;
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                acc[h].x += v[k][h].x * f;
-                acc[h].y += v[k][h].y * f;
-                acc[h].z += v[k][h].z * f;
-                acc[h].w += v[k][h].w * f;
+                for (int h = 0; h < H; ++h) add4(acc[h], v[k][h], f);
             }
         }
     }
-    sh_o[(warp * 2) * 32 + lane] = acc[0];
-    sh_o[(warp * 2 + 1) * 32 + lane] = acc[1];
-    if (lane == 0) sh_ml[warp] = make_float2(mx, sum);
-    sync();
-    if (warp < 2 && 128 * warp + 4 * lane < a.head_dim) {
-        mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sh_ml[w].x);
-        sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            const float f = corr(sh_ml[w].x, mx);
-            sum += sh_ml[w].y * f;
-            const float4 v = sh_o[(w * 2 + warp) * 32 + lane];
-            o.x += v.x * f;
-            o.y += v.y * f;
-            o.z += v.z * f;
-            o.w += v.w * f;
-        }
+    __device__ __forceinline__ static void scale4(float4 &o, float f) {
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
+    }
+    __device__ __forceinline__ static void add4(float4 &o, const float4 &v, float f) {
+        o.x += v.x * f;
+        o.y += v.y * f;
+        o.z += v.z * f;
+        o.w += v.w * f;
+    }
+    // Columns 128 h + 4 lane .. of row r.
+    __device__ __forceinline__ void write(int r, int h, float mx, float sum, const float4 &o) const {
+        const int lane = threadIdx.x & 31, c = 128 * h + 4 * lane;
+        if (c >= a.head_dim) return;
         const int gr = part.row0 + r, head = part.head * (int)a.group.d + gr % a.group;
         const long long tok = part.q0 + gr / a.group;
         const float inv = inverse(sum);
-        *reinterpret_cast<uint2 *>(a.y + tok * a.y_token + head * a.y_head + 128 * warp + 4 * lane) =
+        *reinterpret_cast<uint2 *>(a.y + tok * a.y_token + head * a.y_head + c) =
             make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
-        if (a.lse && threadIdx.x == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
+        if (a.lse && c == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
     }
-    sync();
-}
+
+    // Rows r0, r0 + step, ..  Of few parts: a warp to a row, all its parts in
+    // flight at once.  Of many: all warps to a row, which take the parts in
+    // turn and merge through sh.
+    template <class Sync>
+    __device__ __forceinline__ void rows(int r0, int step, float *sh, Sync sync) const {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        float mx, sum;
+        float4 acc[2];
+        if (part.parts <= FLIGHT) {
+#pragma unroll 1
+            for (int r = r0 + warp * step; r < part.rows; r += WARPS * step) {
+                sum_parts<1>(r, 0, mx, sum, acc);
+#pragma unroll
+                for (int h = 0; h < H; ++h) write(r, h, mx, sum, acc[h]);
+            }
+            return;
+        }
+        float4 *sh_o = reinterpret_cast<float4 *>(sh);                        // [WARPS][2][32]
+        float2 *sh_ml = reinterpret_cast<float2 *>(sh + WARPS * 2 * 32 * 4);  // [WARPS]
+#pragma unroll 1
+        for (int r = r0; r < part.rows; r += step) {
+            sum_parts<WARPS>(r, warp, mx, sum, acc);
+#pragma unroll
+            for (int h = 0; h < H; ++h) sh_o[(warp * 2 + h) * 32 + lane] = acc[h];
+            if (lane == 0) sh_ml[warp] = make_float2(mx, sum);
+            sync();
+            if (warp < H) {
+                mx = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sh_ml[w].x);
+                sum = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) {
+                    const float f = corr(sh_ml[w].x, mx);
+                    sum += sh_ml[w].y * f;
+                    add4(o, sh_o[(w * 2 + warp) * 32 + lane], f);
+                }
+                write(r, warp, mx, sum, o);
+            }
+            sync();
+        }
+    }
+};
 
 // WIDE: the tensor maps copy whole heads.
 template <int DP, bool WIDE>
@@ -472,10 +506,10 @@ __global__ void __launch_bounds__(RowCfg<DP>::THREADS, 1)
         }
         sync();
         const int mode = *abort;
-        if (mode == kJoinShare)
-            for (int r = part.index; r < part.rows; r += joiners) join_row<DP, C::WARPS, ROWS>(a, part, r, merge, sync);
-        if (mode == kJoinAll)
-            for (int r = 0; r < part.rows; ++r) join_row<DP, C::WARPS, ROWS>(a, part, r, merge, sync);
+        const Join<DP, C::WARPS, ROWS> join{a, part};
+        const bool all = mode == kJoinAll;
+        if (all || (mode == kJoinShare && part.index < joiners))
+            join.rows(all ? 0 : part.index, all ? 1 : joiners, merge, sync);
         sync();
         if (threadIdx.x == 0) part_done(a, part);
     }

@@ -6,9 +6,11 @@
 // such rows (of one sequence, one key/value head) with the range of
 // positions [lo, hi) that any of its rows sees; a unit is one tile of `keys`
 // positions of that range.  An item costs its units (twice, if it has many
-// rows) and, for its queries and outputs, EXTRA more.  All items' costs, in the order (sequence, head,
-// row tile, key tile), are cut into one contiguous range per CTA, equal to
-// within a unit, whatever the lengths.  An item cut by a range boundary is
+// rows) and, for its queries and outputs, EXTRA more.  All items' costs, in
+// the order (sequence, head, row tile, key tile), are cut into one contiguous
+// range per CTA, equal to within a unit, whatever the lengths; cuts near an
+// item's end are moved to it, and where the items are few and alike each goes
+// whole to one CTA (Cut, make_plan_by).  An item cut by a range boundary is
 // computed in parts: each part's CTA leaves its unnormalised output, running
 // maximum and sum in the workspace and counts itself in; when a CTA is done
 // with its own range it waits for the parts of the items it shares and joins
@@ -57,11 +59,21 @@ struct Part {
 
 // How a kernel's work is cut: rows and positions of a unit, an item's extra
 // cost, the least cost worth a CTA of its own.  A unit of an item of more than
-// FEW_ROWS rows costs 2, and the two key tiles next to an end of such an item
-// are not cut off: joining so many rows takes as long.
-template <int ROWS_, int KEYS_, int EXTRA_, int LEAST_, int FEW_ROWS_>
+// FEW_ROWS rows costs 2.  Joining an item's parts takes as long as some units:
+//  * Where there are no more items than CTAs and none costs more than an even
+//    share and SLACK, each is left whole (single tokens of 16 sequences of 300
+//    positions, 8 heads of 128: 8.7 us, against 16.1 cut into even shares; of
+//    64 sequences of 2000, 2 heads: 29, against 38; items of 300 positions and
+//    32 rows: 13.4, against 22).
+//  * Else the two key tiles next to an end of an item that costs no more than
+//    that are not cut off (single tokens of 24 sequences of 300: 13, against
+//    18); of a costlier one, which is cut all the same, LONG (few rows) or two
+//    (many).  With an even share of 7, a 16001-position item of 128 rows
+//    takes 26 us with LONG = 0, 28 with 1; 600 positions of heads of 256 with
+//    4 rows 16.9 with 0, 14.2 with 1.
+template <int ROWS_, int KEYS_, int EXTRA_, int LEAST_, int FEW_ROWS_, int SLACK_, int LONG_>
 struct Cut {
-    static constexpr int ROWS = ROWS_, KEYS = KEYS_, EXTRA = EXTRA_, LEAST = LEAST_, FEW_ROWS = FEW_ROWS_;
+    static constexpr int ROWS = ROWS_, KEYS = KEYS_, EXTRA = EXTRA_, LEAST = LEAST_, FEW_ROWS = FEW_ROWS_, SLACK = SLACK_, LONG = LONG_;
 };
 
 struct Item {
@@ -92,12 +104,20 @@ template <class C>
 __device__ __forceinline__ int cost_of(const Item &it) {
     return it.nt * it.weight + C::EXTRA;
 }
+template <class C>
+__device__ __forceinline__ int row_tiles(const AttnArgs &a, const Seq &s) {
+    return (s.qn * (int)a.group.d + C::ROWS - 1) / C::ROWS;
+}
+// (And into most, if that is less, the cost of its costliest item.)
 template <class C, bool WARP>
-__device__ __forceinline__ uint32_t head_cost(const AttnArgs &a, const Seq &s) {
-    const int nrt = (s.qn * (int)a.group.d + C::ROWS - 1) / C::ROWS;
+__device__ __forceinline__ uint32_t head_cost(const AttnArgs &a, const Seq &s, uint32_t &most) {
+    const int nrt = row_tiles<C>(a, s);
     uint32_t n = 0;
-    for (int rt = WARP ? (int)(threadIdx.x & 31) : 0; rt < nrt; rt += WARP ? 32 : 1)
-        n += cost_of<C>(item_of<C>(a, s, rt));
+    for (int rt = WARP ? (int)(threadIdx.x & 31) : 0; rt < nrt; rt += WARP ? 32 : 1) {
+        const uint32_t cost = cost_of<C>(item_of<C>(a, s, rt));
+        n += cost;
+        most = max(most, cost);
+    }
     return WARP ? __reduce_add_sync(~0u, n) : n;
 }
 
@@ -125,8 +145,10 @@ __device__ __forceinline__ uint32_t owner(const Plan &p, uint32_t at) {
     return at < cut ? at / (p.per + 1) : p.more + (at - cut) / p.per;
 }
 
+constexpr uint32_t kDisorder = 0xFFFFFFFFu;  // in place of the greatest cost: offsets out of order
+
 struct PlanShared {
-    uint32_t sums[32];
+    uint32_t sums[32], items[32], most[32];
     Plan plan;
     unsigned begun_before;
 };
@@ -143,12 +165,14 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
     const uint32_t worker = WARP ? warp : threadIdx.x, workers = WARP ? W : THREADS;
     const uint32_t batch = (uint32_t)a.b.batch, per = (batch + workers - 1) / workers;
     const uint32_t b0 = min(worker * per, batch), b1 = min(b0 + per, batch);
-    uint32_t mine = 0, cost = 0;  // cost: of a head of the worker's last sequence
-    Seq s = {0, 0, 0};
+    uint32_t mine = 0, items = 0, most = 0, cost = 0;  // cost: of a head of the worker's last sequence
+    Seq s = {0, 0, 0, true};
     for (uint32_t b = b0; b < b1; ++b) {
         s = load_seq(a.b, (int)b);
-        cost = head_cost<C, WARP>(a, s);
+        cost = head_cost<C, WARP>(a, s, most);
         mine += cost * a.kv_heads;
+        items += row_tiles<C>(a, s) * a.kv_heads;
+        if (!s.ordered) most = kDisorder;
     }
     uint32_t before = 0, warp_sum = mine;  // cost of earlier workers
     if (!WARP) {
@@ -156,14 +180,24 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
         before = inc - mine;
         warp_sum = __shfl_sync(~0u, inc, 31);
     }
-    if (lane == 0) sh.sums[warp] = warp_sum;
+    const uint32_t warp_items = WARP ? items : __reduce_add_sync(~0u, items), warp_most = __reduce_max_sync(~0u, most);
+    if (lane == 0) {
+        sh.sums[warp] = warp_sum;
+        sh.items[warp] = warp_items;
+        sh.most[warp] = warp_most;
+    }
     __syncthreads();
-    uint32_t total = 0;
+    uint32_t total = 0, all_items = 0, all_most = 0, items_before = 0;
 #pragma unroll
     for (uint32_t i = 0; i < W; ++i) {
-        const uint32_t v = sh.sums[i];
-        if (i < warp) before += v;
+        const uint32_t v = sh.sums[i], n = sh.items[i];
+        if (i < warp) {
+            before += v;
+            items_before += n;
+        }
         total += v;
+        all_items += n;
+        all_most = max(all_most, sh.most[i]);
     }
     uint32_t ctas = gridDim.x;
     const uint32_t c = blockIdx.x;
@@ -173,13 +207,41 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
     p.more = total - p.per * ctas;
     p.first = p.per * c + min(c, p.more);
     p.count = c < ctas ? p.per + (c < p.more ? 1 : 0) : 0;
-    if (p.count > 0 && p.first >= before && p.first - before < mine) {
+    auto publish = [&] {
+        sh.plan = p;
+        // The pages of the first tile will be wanted next.
+        const Item it = item_of<C>(a, s, p.rt);
+        const int at = (it.t0 + max(p.off - C::EXTRA, 0) / it.weight) * C::KEYS;
+        if (at < it.hi)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(a.b.table + (long long)p.b * a.b.table_stride + at / a.page_size));
+    };
+    if (all_most == kDisorder) {  // (reported by load_seq) no sum above is to be relied on: nothing is computed
+        p.count = 0;
+    } else if (all_items <= gridDim.x && all_most <= p.per + C::SLACK) {  // an item to a CTA
+        p.count = c < all_items ? 1 : 0;
+        if (!WARP) items_before += warp_scan(items, lane) - items;
+        if (c >= items_before && c - items_before < items) {
+            uint32_t res = c - items_before, b = b0, nrt;
+            for (;; ++b) {
+                s = load_seq(a.b, (int)b);
+                nrt = row_tiles<C>(a, s);
+                if (res < nrt * a.kv_heads) break;
+                res -= nrt * a.kv_heads;
+            }
+            p.b = (int)b;
+            p.head = (int)(res / nrt);
+            p.rt = (int)(res - p.head * nrt);
+            p.off = 0;
+            p.count = cost_of<C>(item_of<C>(a, s, p.rt));
+            if (!WARP || lane == 0) publish();
+        }
+    } else if (p.count > 0 && p.first >= before && p.first - before < mine) {
         uint32_t res = p.first - before;
         uint32_t b = b0;
         if (b1 - b0 > 1)
             for (;; ++b) {
                 s = load_seq(a.b, (int)b);
-                cost = head_cost<C, WARP>(a, s);
+                cost = head_cost<C, WARP>(a, s, most);
                 if (res < cost * a.kv_heads) break;
                 res -= cost * a.kv_heads;
             }
@@ -188,7 +250,7 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
         res -= p.head * cost;
         int rt = 0;
         if (WARP) {  // 32 row tiles at a time
-            const int nrt = (s.qn * (int)a.group.d + C::ROWS - 1) / C::ROWS;
+            const int nrt = row_tiles<C>(a, s);
             for (;; rt += 32) {
                 const uint32_t v = rt + lane < nrt ? cost_of<C>(item_of<C>(a, s, rt + lane)) : 0;
                 const uint32_t inc = warp_scan(v, lane);
@@ -210,14 +272,7 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
         }
         p.rt = rt;
         p.off = (int)res;
-        if (!WARP || lane == 0) {
-            sh.plan = p;
-            // The pages of the first tile will be wanted next.
-            const Item it = item_of<C>(a, s, rt);
-            const int at = (it.t0 + max(p.off - C::EXTRA, 0) / it.weight) * C::KEYS;
-            if (at < it.hi)
-                asm volatile("prefetch.global.L1 [%0];" ::"l"(a.b.table + (long long)p.b * a.b.table_stride + at / a.page_size));
-        }
+        if (!WARP || lane == 0) publish();
     }
     if (p.count == 0 && threadIdx.x == 0) sh.plan = p;
     __syncthreads();
@@ -239,6 +294,7 @@ struct Pieces {
     uint32_t left;  // of the range's cost
     uint32_t at;    // cost before the next item
     int b, head, rt, off;
+    int per;
     Seq s;
     // the piece
     Item it;
@@ -247,13 +303,15 @@ struct Pieces {
     bool begins, ends;  // it holds the item's first and last tile
 
     __device__ __forceinline__ Pieces(const AttnArgs &args, const Plan &p)
-        : a(args), left(p.count), at(p.first - p.off), b(p.b), head(p.head), rt(p.rt), off(p.off) {
+        : a(args), left(p.count), at(p.first - p.off), b(p.b), head(p.head), rt(p.rt), off(p.off), per((int)p.per) {
         if (left > 0) s = load_seq(a.b, b);
     }
 
     // Cuts at key tile uncut_lo() or before are moved to the item's beginning,
     // at uncut_hi() or after to its end.
-    __device__ __forceinline__ int snap() const { return it.weight > 1 ? 2 : 0; }
+    __device__ __forceinline__ int snap() const {
+        return cost_of<C>(it) > per + C::SLACK ? min(it.weight > 1 ? 2 : C::LONG, per / 3) : 2;
+    }
     __device__ __forceinline__ int uncut_lo() const { return min(snap(), it.nt / 2); }
     __device__ __forceinline__ int uncut_hi() const { return max(it.nt - snap(), it.nt / 2 + 1); }
     // The key tile that a cut at cost x of the item comes before.

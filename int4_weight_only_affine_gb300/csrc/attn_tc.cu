@@ -38,7 +38,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int QROWS = 256, KEYS = 128;
-using Work = Cut<QROWS, KEYS, 6, 6, 128>;
+using Work = Cut<QROWS, KEYS, 6, 6, 128, 10, 0>;
 constexpr int FEW_PARTS = 4;
 constexpr int TC_THREADS = 384;
 constexpr int HALF = KEYS * 128;  // bytes of 64 columns of 128 rows

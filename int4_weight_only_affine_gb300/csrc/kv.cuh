@@ -39,6 +39,7 @@ struct KvBatch {
 // the cache, clamped to the tensors' sizes.
 struct Seq {
     int q0, qn, kv;
+    bool ordered;  // the offsets ascend, within the tensors
 };
 
 __device__ __forceinline__ Seq load_seq(const KvBatch &b, int i) {
@@ -47,7 +48,8 @@ __device__ __forceinline__ Seq load_seq(const KvBatch &b, int i) {
     s.q0 = min(max(o0, 0), b.total_q);
     s.qn = min(max(o1, s.q0), b.total_q) - s.q0;
     s.kv = min(max(kv, 0), b.max_kv);
-    if (s.q0 != o0 || s.q0 + s.qn != o1 || s.kv != kv) atomicExch(&g_bad_index, 1);
+    s.ordered = s.q0 == o0 && s.q0 + s.qn == o1;
+    if (!s.ordered || s.kv != kv) atomicExch(&g_bad_index, 1);
     return s;
 }
 

@@ -162,6 +162,19 @@ def test_many_sequences(w4, n):
     run(w4, Batch(ql, kl, 8, seed=n), 2, 1, 64, max_q=64)
 
 
+@pytest.mark.parametrize("q", [1, 8, 70])
+@pytest.mark.parametrize("n,kv", [(16, [300]), (24, [300]), (40, [600]), (16, [1200]), (16, [1200, 1000, 1100, 1190]),
+                                  (12, [2000, 70, 1, 900]), (64, [150, 700, 90])])
+def test_items_left_whole_or_cut(w4, q, n, kv):
+    """About as many items as the GPU has blocks, alike or not, with empty sequences among them."""
+    ql = [0 if i % 5 == 3 else q for i in range(n)]
+    kl = [max(kv[i % len(kv)], ql[i]) for i in range(n)]
+    run(w4, Batch(ql, kl, 16, seed=n + q), 16, 4, 128)
+    run(w4, Batch(ql, kl, 16, seed=n + q), 28, 4, 64)
+    if q < 70:
+        run(w4, Batch(ql, kl, 16, seed=n + q), 4, 2, 256)
+
+
 def test_max_q_len_is_a_hint(w4):
     """Results hold whatever max_q_len says."""
     for hint in (0, 1, 5, 10**6):
@@ -363,6 +376,23 @@ def test_indexes_out_of_range_are_reported(w4):
         kb = w4.KVBatch(to_dev(batch.table), to_dev(bad), to_dev(batch.kv_lens.astype(np.int32)), batch.tokens, max(ql))
         w4.f16_attention(to_dev(q), cache, kb)
         assert w4.device_status() == 9
+
+
+@pytest.mark.parametrize("q", [1, 60])
+def test_offsets_out_of_order_compute_nothing(w4, q):
+    """Offsets that fall are reported, and no row is written: no plan holds for them."""
+    import torch
+    batch = Batch([q] * 8, [100 + q] * 8, 16, seed=3)
+    x, kc, vc = data(batch, 16, 2, 128, 3)
+    bad = np.array([0, batch.tokens] * 4 + [0], np.int32)
+    kb = w4.KVBatch(to_dev(batch.table), to_dev(bad), to_dev(batch.kv_lens.astype(np.int32)), batch.tokens, q)
+    y = torch.full(x.shape, 7.0, dtype=torch.float16, device="cuda")
+    cache = w4.KVCache(to_dev(kc), to_dev(vc))
+    ws = w4.attention_workspace(cache, 16, q)
+    w4.f16_attention(to_dev(x), cache, kb, y=y, workspace=ws)
+    assert w4.device_status() == 9 and bool((y == 7.0).all())
+    wy, _, ty, _ = attention(x, kc, vc, batch, 128**-0.5)
+    check(w4.f16_attention(to_dev(x), cache, device_batch(w4, batch), workspace=ws), wy, ty, "in order again")
 
 
 def test_wrong_arguments_are_refused(w4):

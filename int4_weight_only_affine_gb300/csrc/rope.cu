@@ -10,9 +10,15 @@
 // Both calls move every element once in and once out and are bound by that.
 // A lane owns one unit of a head: 8 elements, 16 bytes, which are 4 rotated
 // pairs (of adjacent elements, or 4 elements of each half) or 8 elements to
-// copy.  A warp takes one token and up to HPL * (256 / head_dim) of its heads, so a lane turns the same pairs of each of its heads and
-// computes their sines once; all its loads are issued before the sines and
-// the index look-ups that do not depend on them.
+// copy.  A warp takes one token and up to HPL * (256 / head_dim) of its heads,
+// so a lane turns the same pairs of each of its heads and computes
+// their sines once; all its loads are issued before the sines and the index
+// look-ups that do not depend on them.
+//
+// Measured: rope of 16384 tokens x 16 heads of 128, 134 MB, 21.6 us, 6.2 TB/s;
+// append of 16384 tokens, 16 + 2 x 8 heads, 268 MB, 43.7 us, 6.1 TB/s, against
+// 6.69 TB/s of a plain copy.  Steps of a few tokens: 1.5 and 2.5 us in a graph,
+// the launch and one chain of dependent reads.
 #include <string.h>
 
 #include "kv.cuh"
@@ -20,12 +26,14 @@
 namespace w4a16 {
 namespace {
 
-// Heads of a lane (HPL below).  Eight where there are warps enough for the
-// GPU: the look-ups and sines of a warp serve more of its bytes (append,
-// 16384 tokens of 16 + 2 x 8 heads of 128: 46.2 us, against 55.8 with four and
-// 81 with two; sixteen: 53).  Four where there are not: a shorter path from
-// load to store (append, 16 tokens: 3.0 us in a graph, against 3.7).
-constexpr int kManyHeads = 8, kFewHeads = 4;
+// Heads of a lane (HPL below): the most whose warps fill half the GPU.  More
+// heads: the look-ups and sines of a warp serve more of its bytes (append,
+// 16384 tokens of 16 + 2 x 8 heads of 128: 43.7 us with 8, 53.6 with 4, 78.6
+// with 2, 79 with 16 (fewer loads fit the registers); 2000 tokens: 6.8 with 8,
+// 8.1 with 4).  Fewer: more warps, and a shorter path from load to store
+// (append in a graph, 16 tokens: 2.5 us with 1, 3.0 with 4; 1000 tokens: 4.8
+// with 4, 8.8 with 1).
+constexpr int kManyHeads = 8, kSomeHeads = 4;
 constexpr int kWarps = 4;
 constexpr int kBlocks = 8;  // resident on an SM
 
@@ -242,7 +250,12 @@ int head_groups(int heads, int units, int hpl) {
     const int per = 32 / units * hpl;
     return (heads + per - 1) / per;
 }
-bool many_warps(long long warps) { return warps > (long long)sm_count() * kBlocks * kWarps; }
+// Heads of a lane of a call (see kManyHeads).
+int heads_per_lane(long long tokens, int heads, int units) {
+    const long long slots = (long long)sm_count() * kBlocks * kWarps;  // warps that the GPU holds
+    if (tokens * head_groups(heads, units, kManyHeads) > slots / 2) return kManyHeads;
+    return tokens * head_groups(heads, units, 1) > slots / 2 ? kSomeHeads : 1;
+}
 
 // Launch as a programmatic dependent (the kernels wait for the one before
 // first: it only takes the launch itself off the path).
@@ -317,11 +330,12 @@ extern "C" int f16_rope(const uint16_t *x, int64_t x_token, int64_t x_head, uint
         !stride_ok(y_head) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
         return W4_ERR_ALIGN;
     if (device_cc() != 103) return W4_ERR_DEVICE;
-    const int units = head_dim / 8, few = head_groups(heads, units, kFewHeads), many = head_groups(heads, units, kManyHeads);
-    const bool big = many_warps((long long)tokens * many);
-    return launch(big ? rope_kernel<kManyHeads> : rope_kernel<kFewHeads>, (long long)tokens * (big ? many : few), stream,
-                  Heads{x, x_token, x_head}, Heads{y, y_token, y_head}, positions, r, tokens, heads, units,
-                  big ? many : few);
+    const int units = head_dim / 8, hpl = heads_per_lane(tokens, heads, units), groups = head_groups(heads, units, hpl);
+    return launch(hpl == kManyHeads   ? rope_kernel<kManyHeads>
+                  : hpl == kSomeHeads ? rope_kernel<kSomeHeads>
+                                      : rope_kernel<1>,
+                  (long long)tokens * groups, stream, Heads{x, x_token, x_head}, Heads{y, y_token, y_head}, positions, r,
+                  tokens, heads, units, groups);
 }
 
 extern "C" int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head, const uint16_t *v, int64_t v_token,
@@ -366,11 +380,12 @@ extern "C" int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head,
     a.kv_heads = cache->heads;
     a.units = cache->head_dim / 8;
     const int heads = a.q_heads + 2 * a.kv_heads;
-    a.groups = head_groups(heads, a.units, kManyHeads);
-    const bool big = many_warps((long long)batch->total_q * a.groups);
-    if (!big) a.groups = head_groups(heads, a.units, kFewHeads);
-    return launch(big ? append_kernel<kManyHeads> : append_kernel<kFewHeads>, (long long)batch->total_q * a.groups, stream,
-                  a);
+    const int hpl = heads_per_lane(batch->total_q, heads, a.units);
+    a.groups = head_groups(heads, a.units, hpl);
+    return launch(hpl == kManyHeads   ? append_kernel<kManyHeads>
+                  : hpl == kSomeHeads ? append_kernel<kSomeHeads>
+                                      : append_kernel<1>,
+                  (long long)batch->total_q * a.groups, stream, a);
 }
 
 extern "C" int f16_kv_cache_init(f16_kv_cache *c, uint16_t *k, uint16_t *v, const int64_t ks[3], const int64_t vs[3],

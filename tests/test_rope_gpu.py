@@ -39,6 +39,17 @@ def test_rope_layouts(w4, heads, d, rot, interleaved):
         assert np.array_equal(tail, x[..., rot:])
 
 
+@pytest.mark.parametrize("tokens,heads,d,rot", [(700, 16, 128, 128), (1501, 16, 128, 64), (2600, 9, 136, 136), (3001, 11, 80, 32),
+                                                (5000, 33, 72, 8), (6000, 1, 64, 64), (2500, 35, 256, 256)])
+def test_rope_many_tokens(w4, tokens, heads, d, rot):
+    """One, four and eight heads to a lane, and groups of heads that are not full."""
+    g = np.random.RandomState(tokens)
+    x = g.standard_normal((tokens, heads, d)).astype(np.float16)
+    pos = g.randint(0, 100000, tokens).astype(np.int32)
+    y = w4.f16_rope(to_dev(x), rope_of(w4, thetas(rot), 1.0), to_dev(pos))
+    close(y, rotate(x, pos, thetas(rot)), rotate_tol(x, pos, thetas(rot)))
+
+
 def test_rope_far_and_negative_positions(w4):
     """The angle's reduction is exact at every int32 position; a negative one turns back."""
     pos = np.array([0, 1, -1, 131071, 10**6, 2**24 + 1, 2**31 - 1, -2**31, -12345], np.int32)
@@ -161,6 +172,13 @@ def test_append_many_sequences(w4, n):
     g = np.random.RandomState(n)
     ql = g.randint(0, 3, n)
     append_case(w4, Batch(ql, np.maximum(ql, g.randint(0, 30, n)), 8, seed=n), 2, 1, 64, 64)
+
+
+@pytest.mark.parametrize("hq,hkv,d,rot", [(16, 8, 128, 128), (14, 2, 64, 64), (5, 3, 80, 32), (20, 1, 136, 0)])
+def test_append_many_tokens(w4, hq, hkv, d, rot):
+    """One, four and eight heads to a lane."""
+    for ql in ([60], [700, 3], [1500, 1, 900], [5000]):
+        append_case(w4, Batch(ql, [n + 7 for n in ql], 16, seed=d), hq, hkv, d, rot)
 
 
 def test_append_packed_projection(w4):

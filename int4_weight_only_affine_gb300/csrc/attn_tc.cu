@@ -226,18 +226,32 @@ __device__ __forceinline__ void join_columns(const AttnArgs &a, const Part &part
         fence_proxy_async_smem();  // the reads above, before the next copies
         sync();
     }
-    if (r >= part.rows) return;
-    const int gr = part.row0 + r, head = part.head * (int)a.group.d + gr % a.group;
-    const long long tok = part.q0 + gr / a.group;
-    const float inv = inverse(sum);
-    uint16_t *y = a.y + tok * a.y_token + head * a.y_head + 4 * g0;
+    // Out through the ring, so that lanes write neighbouring bytes of a row
+    // (an odd number of 8-byte words to a row: no bank conflicts).
+    const uint32_t pitch = 8 * (ng | 1);
+    if (r < part.rows) {
+        const float inv = inverse(sum);
 #pragma unroll
-    for (int g = 0; g < MOST; ++g) {
-        if (g >= ng) break;
-        *reinterpret_cast<uint2 *>(y + 4 * g) =
-            make_uint2(pack2(acc[g].x * inv, acc[g].y * inv), pack2(acc[g].z * inv, acc[g].w * inv));
+        for (int g = 0; g < MOST; ++g) {
+            if (g >= ng) break;
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(ring + r * pitch + 8 * g),
+                         "r"(pack2(acc[g].x * inv, acc[g].y * inv)), "r"(pack2(acc[g].z * inv, acc[g].w * inv))
+                         : "memory");
+        }
+        if (a.lse && g0 == 0) {
+            const int gr = part.row0 + r, head = part.head * (int)a.group.d + gr % a.group;
+            a.lse[(long long)(part.q0 + gr / a.group) * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
+        }
     }
-    if (a.lse && g0 == 0) a.lse[tok * (a.kv_heads * (int)a.group.d) + head] = log_sum(mx, sum);
+    sync();
+    for (int x = threadIdx.x; x < part.rows * ng; x += 256) {
+        const int row = x / ng, g = x - row * ng, gr = part.row0 + row;
+        const int head = part.head * (int)a.group.d + gr % a.group;
+        uint2 v;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(ring + row * pitch + 8 * g) : "memory");
+        *reinterpret_cast<uint2 *>(a.y + (part.q0 + gr / a.group) * a.y_token + head * a.y_head + 4 * (g0 + g)) = v;
+    }
+    sync();
 }
 
 // Block x of a shared item of many parts: 32 rows x 32 columns, a lane to a

@@ -48,7 +48,7 @@ template <int DP>
 struct RowCfg {
     static constexpr int ROWS = 16;
     static constexpr int KEYS = kv_tile(DP);
-    using Work = Cut<ROWS, KEYS, 2, 1, ROWS, 4, 1>;
+    using Work = Cut<ROWS, KEYS, 2, 1, ROWS, 4, 1, false>;
     static constexpr int WARPS = KEYS / 16;             // consumers
     static constexpr int THREADS = 32 * (WARPS + 1);
     static constexpr int TILE = KEYS * 128 * (DP / 64); // bytes of K or V
@@ -620,6 +620,8 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     a.left = a.arrived + kMaxGrid;
     a.begun = a.left + kMaxGrid;
     a.begun_before = a.begun + 1;
+    a.taken = a.begun + 2;
+    a.finished = a.begun + 3;
     a.part_ml = reinterpret_cast<float *>(ws + kCounterBytes);
     a.part_o = a.part_ml + (size_t)2 * kMaxGrid * rows * 2;
     const bool wide = !tc && d % 64 == 0 && d > 64;
@@ -634,6 +636,7 @@ extern "C" int f16_attention(const uint16_t *q, int64_t q_token, int64_t q_head,
     if (units >= 0x7FFFFFFFll) return W4_ERR_SHAPE;
     int grid = sm_count() < kMaxGrid ? sm_count() : kMaxGrid;
     if (units < grid) grid = (int)units;
+    a.may_queue = !a.few_tiles && tiles * heads > grid;
     if (tc) return attn_tc_launch(mk, mv, a, grid, s);
     if (d <= 64) return launch_rows<64, false>(mk, mv, a, grid, s);
     if (d == 128) return launch_rows<128, true>(mk, mv, a, grid, s);

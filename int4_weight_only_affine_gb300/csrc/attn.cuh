@@ -9,8 +9,9 @@
 // rows) and, for its queries and outputs, EXTRA more.  All items' costs, in
 // the order (sequence, head, row tile, key tile), are cut into one contiguous
 // range per CTA, equal to within a unit, whatever the lengths; cuts near an
-// item's end are moved to it, and where the items are few and alike each goes
-// whole to one CTA (Cut, make_plan_by).  An item cut by a range boundary is
+// item's end are moved to it; where the items are few and alike each goes
+// whole to one CTA, and where they are many and none costs more than an even
+// share they are taken whole from a queue (Cut, make_plan_by).  An item cut by a range boundary is
 // computed in parts: each part's CTA leaves its unnormalised output, running
 // maximum and sum in the workspace and counts itself in; when a CTA is done
 // with its own range it waits for the parts of the items it shares and joins
@@ -20,8 +21,8 @@
 // to count a part of the item in joins all of it.  (A cooperative launch would
 // promise the same, but is not overlapped with the end of the kernel before:
 // 2.6 us a call.)  Every CTA works its range out from the lengths by itself:
-// the host needs no lengths, and the split depends on nothing but the batch,
-// so results repeat.
+// the host needs no lengths, and no result depends on which CTA computes it, so
+// results repeat.
 #pragma once
 
 #include <math.h>
@@ -41,6 +42,7 @@ struct AttnArgs {
     int causal, window;
     int num_pages, box_rows;
     int few_tiles;  // a sequence is expected to have few row tiles (chooses how the plan is summed)
+    int may_queue;  // there may be more items than CTAs, of sequences with many row tiles
     float scale;    // times log2(e): the softmax is taken in powers of two
     float *part_o;  // [2 * grid][rows x head_dim], in the order of the kernel that writes it
     float *part_ml; // [2 * grid][rows][2]: running maximum (base-2 scaled scores) and sum
@@ -49,6 +51,7 @@ struct AttnArgs {
     // with it.
     unsigned *arrived, *left;
     unsigned *begun, *begun_before;  // CTAs begun in all calls, and in the calls before
+    unsigned *taken, *finished;      // of a queue of items: those taken, CTAs that found it empty (zero between calls)
 };
 
 // A CTA's part of an item that several CTAs share.
@@ -71,9 +74,14 @@ struct Part {
 //    (many).  With an even share of 7, a 16001-position item of 128 rows
 //    takes 26 us with LONG = 0, 28 with 1; 600 positions of heads of 256 with
 //    4 rows 16.9 with 0, 14.2 with 1.
-template <int ROWS_, int KEYS_, int EXTRA_, int LEAST_, int FEW_ROWS_, int SLACK_, int LONG_>
+// QUEUE: where there are more items than CTAs, none much above an even share,
+// no item need be cut (prompt of 8192 tokens, 16 heads of 128 on 8: 220 us,
+// against 229 in ranges; two of 1000, 32 heads on 8: 37, against 43; of 2048:
+// 53, against 57).
+template <int ROWS_, int KEYS_, int EXTRA_, int LEAST_, int FEW_ROWS_, int SLACK_, int LONG_, bool QUEUE_>
 struct Cut {
     static constexpr int ROWS = ROWS_, KEYS = KEYS_, EXTRA = EXTRA_, LEAST = LEAST_, FEW_ROWS = FEW_ROWS_, SLACK = SLACK_, LONG = LONG_;
+    static constexpr bool QUEUE = QUEUE_;
 };
 
 struct Item {
@@ -137,6 +145,7 @@ struct Plan {
     uint32_t per, more;
     uint32_t first, count;
     int b, head, rt, off;  // its first item: sequence, head, row tile; how far into the item's cost it begins
+    uint32_t queue;  // if not 0: no ranges, but a queue of so many places (Queue)
 };
 
 // The CTA whose range holds a unit of cost.
@@ -148,7 +157,7 @@ __device__ __forceinline__ uint32_t owner(const Plan &p, uint32_t at) {
 constexpr uint32_t kDisorder = 0xFFFFFFFFu;  // in place of the greatest cost: offsets out of order
 
 struct PlanShared {
-    uint32_t sums[32], items[32], most[32];
+    uint32_t sums[32], items[32], most[32], tiles[32];
     Plan plan;
     unsigned begun_before;
 };
@@ -165,13 +174,15 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
     const uint32_t worker = WARP ? warp : threadIdx.x, workers = WARP ? W : THREADS;
     const uint32_t batch = (uint32_t)a.b.batch, per = (batch + workers - 1) / workers;
     const uint32_t b0 = min(worker * per, batch), b1 = min(b0 + per, batch);
-    uint32_t mine = 0, items = 0, most = 0, cost = 0;  // cost: of a head of the worker's last sequence
+    uint32_t mine = 0, items = 0, most = 0, tiles = 0, cost = 0;  // cost: of a head of the worker's last sequence
     Seq s = {0, 0, 0, true};
     for (uint32_t b = b0; b < b1; ++b) {
         s = load_seq(a.b, (int)b);
         cost = head_cost<C, WARP>(a, s, most);
         mine += cost * a.kv_heads;
-        items += row_tiles<C>(a, s) * a.kv_heads;
+        const uint32_t n = row_tiles<C>(a, s);
+        items += n * a.kv_heads;
+        tiles = max(tiles, n);
         if (!s.ordered) most = kDisorder;
     }
     uint32_t before = 0, warp_sum = mine;  // cost of earlier workers
@@ -180,6 +191,10 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
         before = inc - mine;
         warp_sum = __shfl_sync(~0u, inc, 31);
     }
+    if (C::QUEUE && WARP) {
+        tiles = __reduce_max_sync(~0u, tiles);
+        if (lane == 0) sh.tiles[warp] = tiles;
+    }
     const uint32_t warp_items = WARP ? items : __reduce_add_sync(~0u, items), warp_most = __reduce_max_sync(~0u, most);
     if (lane == 0) {
         sh.sums[warp] = warp_sum;
@@ -187,7 +202,7 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
         sh.most[warp] = warp_most;
     }
     __syncthreads();
-    uint32_t total = 0, all_items = 0, all_most = 0, items_before = 0;
+    uint32_t total = 0, all_items = 0, all_most = 0, all_tiles = 0, items_before = 0;
 #pragma unroll
     for (uint32_t i = 0; i < W; ++i) {
         const uint32_t v = sh.sums[i], n = sh.items[i];
@@ -198,6 +213,7 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
         total += v;
         all_items += n;
         all_most = max(all_most, sh.most[i]);
+        if (C::QUEUE && WARP) all_tiles = max(all_tiles, sh.tiles[i]);
     }
     uint32_t ctas = gridDim.x;
     const uint32_t c = blockIdx.x;
@@ -207,6 +223,15 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
     p.more = total - p.per * ctas;
     p.first = p.per * c + min(c, p.more);
     p.count = c < ctas ? p.per + (c < p.more ? 1 : 0) : 0;
+    p.queue = 0;
+    if (C::QUEUE && WARP && all_items > gridDim.x && all_most <= p.per + C::SLACK) {
+        // Taken whole, costliest first, items of at most an even share and SLACK
+        // end at about the same time, if their costs differ or about fill the rounds.
+        const unsigned long long places = (unsigned long long)all_tiles * a.kv_heads * batch, n = all_items;
+        const uint32_t rounds = (all_items + gridDim.x - 1) / gridDim.x;
+        if (places <= 2 * n && (4ull * total <= 3 * n * all_most || (unsigned long long)rounds * total <= n * (p.per + C::SLACK / 2)))
+            p.queue = (uint32_t)places;
+    }
     auto publish = [&] {
         sh.plan = p;
         // The pages of the first tile will be wanted next.
@@ -216,6 +241,8 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
             asm volatile("prefetch.global.L1 [%0];" ::"l"(a.b.table + (long long)p.b * a.b.table_stride + at / a.page_size));
     };
     if (all_most == kDisorder) {  // (reported by load_seq) no sum above is to be relied on: nothing is computed
+        p.count = 0;
+    } else if (C::QUEUE && WARP && p.queue) {
         p.count = 0;
     } else if (all_items <= gridDim.x && all_most <= p.per + C::SLACK) {  // an item to a CTA
         p.count = c < all_items ? 1 : 0;
@@ -280,7 +307,7 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
 
 template <class C, int THREADS>
 __device__ __forceinline__ void make_plan(const AttnArgs &a, PlanShared &sh) {
-    if (a.few_tiles)
+    if (!C::QUEUE && a.few_tiles)  // (a queue is for many)
         make_plan_by<C, THREADS, false>(a, sh);
     else
         make_plan_by<C, THREADS, true>(a, sh);

@@ -7,12 +7,12 @@
 // tensor cores are the bound.
 //
 // Measured: a prompt of 8192 tokens, 16 heads of 128 on 8, causal, 275 GFLOP:
-// 230 us, 1.19 PFLOP/s, 64% of a large matrix product's rate (the tensor pipe
-// busy half the time: a unit takes 3300 cycles, the chain S, softmax, P V of
+// 220 us, 1.25 PFLOP/s, 67% of a large matrix product's rate (the tensor pipe
+// busy half the time: a unit takes 3200 cycles, the chain S, softmax, P V of
 // each tile).  A prompt of 1570 tokens, 16 heads on 2, 10 GFLOP: 32 us, of
 // which the units are less than half: most CTAs share items, whose parts (128 KB
-// each) are written and joined through L2.  64 tokens over 16001
-// positions, 66 MB of keys and values: 26 us.
+// each) are written and joined through L2.  64 tokens over 16001 positions, 66
+// MB of keys and values: 26 us.
 //
 // One CTA per SM works through its range of units (attn.cuh).
 //  * The item's 256 rows are two tiles of 128; tile t's scores S_t (fp32),
@@ -48,8 +48,10 @@ namespace w4a16 {
 namespace {
 
 constexpr int QROWS = 256, KEYS = 128;
-using Work = Cut<QROWS, KEYS, 6, 6, 128, 10, 0>;
+template <bool QUEUE>
+using Work = Cut<QROWS, KEYS, 6, 6, 128, 10, 0, QUEUE>;
 constexpr int FEW_PARTS = 4;
+constexpr int QUEUE_SLOTS = 4;  // items taken ahead
 constexpr int TC_THREADS = 384;
 constexpr int HALF = KEYS * 128;  // bytes of 64 columns of 128 rows
 constexpr float kMostSum = 32768.f;  // of 64 probabilities: 2^15, half of what binary16 holds
@@ -59,8 +61,8 @@ struct TcCfg {
     static constexpr int HALVES = DP / 64;
     static constexpr int TILE = HALVES * HALF;                    // 128 rows of Q, K or V
     static constexpr int SLOTS = DP == 64 ? 8 : 5;                // ring of K and V tiles
-    static constexpr int BARS = 2 * SLOTS + 2 * 7 + 2;
-    static constexpr size_t SMEM = 1024 + (size_t)(2 + SLOTS) * TILE + 8 * BARS + 32;
+    static constexpr int BARS = 2 * SLOTS + 2 * 7 + 2 + 2 * QUEUE_SLOTS;
+    static constexpr size_t SMEM = 1024 + (size_t)(2 + SLOTS) * TILE + 8 * BARS + 32 + 4 * QUEUE_SLOTS;
     // Tensor-memory columns.  A head of 64 leaves room for P beside S; with
     // 128, P_t lies in the columns of S_t, whose next product therefore waits
     // for O_t += P_t V to finish.
@@ -307,7 +309,79 @@ __device__ __forceinline__ void join_block(const AttnArgs &a, const Part &part, 
 // Whether both tiles take the same rows, and alternate units.
 __device__ __forceinline__ bool split_units(int rows, int n) { return rows <= 128 && n >= 2; }
 
-template <int DP>
+// A warp's way through the CTA's pieces: those of its range, or whole items
+// from a queue of all of them, the last row tiles (of causal prompts, the
+// costliest) of every head and sequence first.  The warp that TAKES, the first
+// to need an item, draws the CTA's next place and passes it on to the others.
+// Which CTA computes an item changes nothing in it: results repeat.  (QUEUE
+// false: ranges only; the code alone costs calls of few row tiles 1 us.)
+template <bool QUEUE>
+struct Walk : Pieces<Work<QUEUE>> {
+    using Base = Pieces<Work<QUEUE>>;
+    using Base::a, Base::b, Base::head, Base::left, Base::off, Base::rt, Base::s;
+    uint32_t places, taken = 0, ahead;
+    uint32_t bar0;               // QUEUE_SLOTS barriers each: place passed on, place read by all the other warps
+    volatile uint32_t *slots;
+    volatile int *abort;
+
+    __device__ __forceinline__ Walk(const AttnArgs &args, const Plan &p, uint32_t bars, volatile uint32_t *sl, volatile int *ab)
+        : Base(args, p), places(p.queue), ahead(blockIdx.x), bar0(bars), slots(sl), abort(ab) {}
+
+    __device__ __forceinline__ bool find(uint32_t place) {  // false for one that the sequence does not have
+        const uint32_t per_tile = (uint32_t)a.b.batch * a.kv_heads, back = place / per_tile, at = place - back * per_tile;
+        b = (int)(at / (uint32_t)a.kv_heads);
+        head = (int)(at - b * (uint32_t)a.kv_heads);
+        s = load_seq(a.b, b);
+        rt = row_tiles<Work<QUEUE>>(a, s) - 1 - (int)back;
+        return rt >= 0;
+    }
+    template <bool TAKES>
+    __device__ __forceinline__ bool next() {
+        if (QUEUE && places != 0) {
+            const int lane = threadIdx.x & 31;
+            const uint32_t i = taken % QUEUE_SLOTS, phase = taken / QUEUE_SLOTS & 1;
+            const uint32_t full = bar0 + 8 * i, empty = full + 8 * QUEUE_SLOTS;
+            ++taken;
+            uint32_t place;
+            if (TAKES) {
+                do {  // (the next place is on its way while this one is worked on)
+                    place = uniform(ahead);
+                    if (place >= places) break;
+                    if (lane == 0) ahead = gridDim.x + atomicAdd(a.taken, 1u);
+                } while (!find(place));
+                if (!__all_sync(~0u, wait(empty, phase ^ 1, abort))) return false;
+                if (lane == 0) {
+                    slots[i] = place;
+                    mbar_arrive(full);
+                }
+            } else {
+                if (!__all_sync(~0u, wait(full, phase, abort))) return false;
+                place = slots[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty);
+                if (place < places) find(place);
+            }
+            left = place < places ? 0x40000000u : 0;  // (more than any item costs: one whole item)
+            off = 0;
+        }
+        return Base::next();
+    }
+    // By one thread of the warp that takes, after its last: the last CTA of all leaves the queue as it was.
+    __device__ __forceinline__ void finish() {
+        if (!QUEUE || places == 0) return;
+        __threadfence();
+        const unsigned before = atomicAdd(a.finished, 1u);
+        if (before == gridDim.x - 1) {
+            if (atomicExch(a.taken, 0u) != places) atomicExch(&g_wait_expired, 1);  // (a workspace that was not zeroed)
+            *a.finished = 0;
+        } else if (before >= gridDim.x) {
+            atomicExch(&g_wait_expired, 1);
+        }
+    }
+};
+
+// QUEUE: the items may come from a queue.
+template <int DP, bool QUEUE>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ AttnArgs a) {
@@ -331,7 +405,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     auto p_full = [&](int t, int h) { return bar0 + 8u * (2 * C::SLOTS + 6 + 2 * t + h); };
     auto turn = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 10 + t); };  // tile t may issue its products
     auto o_half = [&](int t) { return bar0 + 8u * (2 * C::SLOTS + 12 + t); };  // the first half of P_t V done
-    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 14), join_bar = end_bar + 8;
+    const uint32_t end_bar = bar0 + 8u * (2 * C::SLOTS + 14), join_bar = end_bar + 8, queue_bar = join_bar + 8;
+    volatile uint32_t *queue_slots = reinterpret_cast<volatile uint32_t *>(tail + 28);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -354,6 +429,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         prefetch_maps(&map_k, &map_v);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (QUEUE && threadIdx.x < 32 + QUEUE_SLOTS && threadIdx.x >= 32) {
+        const uint32_t at = queue_bar + 8 * (threadIdx.x - 32);
+        mbar_init(at, 1);
+        mbar_init(at + 8 * QUEUE_SLOTS, TC_THREADS / 32 - 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
             (uint32_t)__cvta_generic_to_shared(tmem_slot)));
@@ -367,12 +448,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         plan_sh.begun_before = begin.before;
     }
     fence_before();
-    make_plan<Work, TC_THREADS>(a, plan_sh);  // (its barriers also publish the above)
+    make_plan<Work<QUEUE>, TC_THREADS>(a, plan_sh);  // (its barriers also publish the above)
     fence_after();
     if (threadIdx.x == BEGINNER) cta_has_begun(a, begin);
     const uint32_t tmem = *tmem_slot;
     const Plan plan = plan_sh.plan;
-    Pieces<Work> pc(a, plan);
+    Walk<QUEUE> pc(a, plan, queue_bar, queue_slots, abort);
 
     if (warp >= 8) {
         if (warp == 8 || warp == 11) {
@@ -382,7 +463,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const int boxes = KEYS / a.box_rows;  // at most 16
             int it = is_v ? 1 : 0;
             bool ok = true;
-            while (ok && uniform(pc.next())) {
+            while (ok && uniform(is_v ? pc.template next<false>() : pc.template next<true>())) {
                 const int n = uniform(pc.n), head = uniform(pc.head);
                 int p0 = uniform(pc.it.t0 + pc.tile0) * KEYS;
                 for (int i = 0; i < n; ++i, it += 2, p0 += KEYS) {
@@ -403,6 +484,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     }
                 }
             }
+            if (!is_v && lane == 0) pc.finish();
             // Every copy has landed before the CTA may exit (those whose slot was taken again, by a tile up to one after
             // this warp's last, have).
             for (int k = it - 2; k >= 0 && k > it - 1 - C::SLOTS; k -= 2)
@@ -440,7 +522,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     commit(kv_empty(at));
                 }
             };
-            while (ok && uniform(pc.next())) {
+            while (ok && uniform(pc.template next<false>())) {
                 const int n = uniform(pc.n), rows = uniform(pc.rows());
                 const bool split = split_units(rows, n), both_tiles = rows > 128;
                 auto hand_on = [&](int slots) {  // slots that this tile does not use
@@ -528,7 +610,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         bool waits = true;       // and whether it may wait for the others'
         uint32_t steps = 0;
         int it = 0;
-        while (pc.next()) {
+        while (pc.template next<false>()) {
             const int first_slot = it;
             it += 2 * pc.n;
             const int rows = pc.rows(), row0 = pc.row0();
@@ -788,7 +870,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const Part part = i == 0 ? shared0 : shared1;
             auto sync = [] { asm volatile("bar.sync 3, 256;" ::: "memory"); };
             // Few parts: ranges of columns, by copies, some 26 bytes a cycle where loads of the same parts ran at 17
-            // (prompts of 1570 and 8192 tokens: 33 and 229 us, against 43 and 250 by blocks).  Many: blocks of rows
+            // (a prompt of 1570 tokens: 33 us, against 43 by blocks).  Many: blocks of rows
             // and columns, as a joiner's range of columns would be a few bytes.
             const bool few = part.parts <= FEW_PARTS;
             const int groups = a.head_dim / 4, blocks = (part.rows + 31) / 32 * ((a.head_dim + 31) / 32);
@@ -828,11 +910,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     }
 }
 
-template <int DP>
+template <int DP, bool QUEUE>
 int launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
     static_assert(TcCfg<DP>::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
-    if (!set_smem_once(reinterpret_cast<const void *>(attn_tc_kernel<DP>), (int)TcCfg<DP>::SMEM)) return W4_ERR_LAUNCH;
-    return launch_dependent(attn_tc_kernel<DP>, grid, TC_THREADS, TcCfg<DP>::SMEM, stream, mk, mv, a);
+    if (!set_smem_once(reinterpret_cast<const void *>(attn_tc_kernel<DP, QUEUE>), (int)TcCfg<DP>::SMEM)) return W4_ERR_LAUNCH;
+    return launch_dependent(attn_tc_kernel<DP, QUEUE>, grid, TC_THREADS, TcCfg<DP>::SMEM, stream, mk, mv, a);
 }
 
 }  // namespace
@@ -840,7 +922,9 @@ int launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, i
 int attn_tc_rows() { return QROWS; }
 
 int attn_tc_launch(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
-    return a.head_dim <= 64 ? launch_tc<64>(mk, mv, a, grid, stream) : launch_tc<128>(mk, mv, a, grid, stream);
+    if (a.head_dim <= 64)
+        return a.may_queue ? launch_tc<64, true>(mk, mv, a, grid, stream) : launch_tc<64, false>(mk, mv, a, grid, stream);
+    return a.may_queue ? launch_tc<128, true>(mk, mv, a, grid, stream) : launch_tc<128, false>(mk, mv, a, grid, stream);
 }
 
 // This translation unit's records, as attn_status.

@@ -175,6 +175,25 @@ def test_items_left_whole_or_cut(w4, q, n, kv):
         run(w4, Batch(ql, kl, 16, seed=n + q), 4, 2, 256)
 
 
+@pytest.mark.parametrize("ql,kl,hq,hkv,d,causal", [
+    ([600] * 6, [600] * 6, 16, 8, 128, True), ([1300, 700, 0, 900, 1300, 40, 1000], [1300, 750, 9, 900, 2000, 40, 1000], 16, 8, 128, True),
+    ([700, 650, 0, 655], [700, 900, 0, 655], 28, 4, 64, True), ([2100], [2100], 32, 8, 128, True),
+    ([900] * 5, [900] * 5, 16, 4, 64, False), ([1, 1200, 1200, 1, 1200], [50, 1200, 1200, 2000, 1300], 16, 8, 128, True)])
+def test_items_from_a_queue(w4, ql, kl, hq, hkv, d, causal):
+    """More items than blocks, none costlier than an even share: taken whole, and the same whoever takes them."""
+    import torch
+    batch = Batch(ql, kl, 16, seed=len(ql), extra_rows=3)
+    y, lse = run(w4, batch, hq, hkv, d, causal)
+    q, kc, vc = data(batch, hq, hkv, d, 0)
+    cache, kb = w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch)
+    ws = w4.attention_workspace(cache, hq, kb.max_q_len)
+    for _ in range(5):
+        y2 = torch.full(q.shape, 7.0, dtype=torch.float16, device="cuda")
+        w4.f16_attention(to_dev(q), cache, kb, y=y2, causal=causal, workspace=ws)
+        assert bool((y == y2).all()) and not bool(ws[:2048].any()) and not bool(ws[2056:2064].any())
+    assert w4.device_status() == 0
+
+
 def test_max_q_len_is_a_hint(w4):
     """Results hold whatever max_q_len says."""
     for hint in (0, 1, 5, 10**6):
@@ -319,6 +338,23 @@ def test_workspace_that_was_not_zeroed(w4):
     cache, kb = w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch)
     ws = w4.attention_workspace(cache, 16, 1)
     ws[:1024] = 1   # counts of parts far past any item's
+    w4.f16_attention(to_dev(q), cache, kb, workspace=ws)
+    assert w4.device_status() == 8 and w4.device_status() == 0
+    ws.zero_()
+    wy, _, ty, _ = attention(q, kc, vc, batch, 128**-0.5)
+    check(w4.f16_attention(to_dev(q), cache, kb, workspace=ws), wy, ty, "y")
+    assert w4.device_status() == 0
+
+
+@pytest.mark.parametrize("word", [514, 515])
+def test_queue_that_was_not_zeroed(w4, word):
+    """A queue that does not begin with its first item is reported."""
+    import torch
+    batch = Batch([600] * 6, [600] * 6, 16, seed=5)
+    q, kc, vc = data(batch, 16, 8, 128, 5)
+    cache, kb = w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch)
+    ws = w4.attention_workspace(cache, 16, 600)
+    ws.view(torch.int32)[word] = 1000
     w4.f16_attention(to_dev(q), cache, kb, workspace=ws)
     assert w4.device_status() == 8 and w4.device_status() == 0
     ws.zero_()

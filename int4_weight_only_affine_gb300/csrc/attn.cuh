@@ -11,10 +11,10 @@
 // range per CTA, equal to within a unit, whatever the lengths; cuts near an
 // item's end are moved to it; where the items are few and alike each goes
 // whole to one CTA, and where they are many and none costs more than an even
-// share they are taken whole from a queue (Cut, make_plan_by).  An item cut by a range boundary is
-// computed in parts: each part's CTA leaves its unnormalised output, running
-// maximum and sum in the workspace and counts itself in; when a CTA is done
-// with its own range it waits for the parts of the items it shares and joins
+// share they are taken whole from a queue (Cut, make_plan_by).  An item cut by
+// a range boundary is computed in parts: each part's CTA leaves its
+// unnormalised output, running maximum and sum in the workspace and counts
+// itself in; when a CTA is done with its own range it waits for the parts of the items it shares and joins
 // its share of their rows, in the parts' order.  A CTA waits only if every CTA
 // of the launch had begun when it counted its part in (so each will finish,
 // whatever else the GPU runs); otherwise it says so as it counts, and the last
@@ -75,7 +75,7 @@ struct Part {
 //    takes 26 us with LONG = 0, 28 with 1; 600 positions of heads of 256 with
 //    4 rows 16.9 with 0, 14.2 with 1.
 // QUEUE: where there are more items than CTAs, none much above an even share,
-// no item need be cut (prompt of 8192 tokens, 16 heads of 128 on 8: 220 us,
+// no item need be cut (prompt of 8192 tokens, 16 heads of 128 on 8: 222 us,
 // against 229 in ranges; two of 1000, 32 heads on 8: 37, against 43; of 2048:
 // 53, against 57).
 template <int ROWS_, int KEYS_, int EXTRA_, int LEAST_, int FEW_ROWS_, int SLACK_, int LONG_, bool QUEUE_>

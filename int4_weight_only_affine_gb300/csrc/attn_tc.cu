@@ -7,7 +7,7 @@
 // tensor cores are the bound.
 //
 // Measured: a prompt of 8192 tokens, 16 heads of 128 on 8, causal, 275 GFLOP:
-// 220 us, 1.25 PFLOP/s, 67% of a large matrix product's rate (the tensor pipe
+// 222 us, 1.24 PFLOP/s, 66% of a large matrix product's rate (the tensor pipe
 // busy half the time: a unit takes 3200 cycles, the chain S, softmax, P V of
 // each tile).  A prompt of 1570 tokens, 16 heads on 2, 10 GFLOP: 32 us, of
 // which the units are less than half: most CTAs share items, whose parts (128 KB

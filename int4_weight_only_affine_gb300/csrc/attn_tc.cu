@@ -253,6 +253,7 @@ __device__ __forceinline__ void join_columns(const AttnArgs &a, const Part &part
         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(ring + row * pitch + 8 * g) : "memory");
         *reinterpret_cast<uint2 *>(a.y + (part.q0 + gr / a.group) * a.y_token + head * a.y_head + 4 * (g0 + g)) = v;
     }
+    fence_proxy_async_smem();  // the ring's use by threads above, before the copies of the next columns (one CTA joins all)
     sync();
 }
 

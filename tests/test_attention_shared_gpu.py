@@ -1,0 +1,51 @@
+"""f16_attention beside other work on the GPU: blocks that begin late, and items joined by one block."""
+import numpy as np
+import pytest
+
+from _attn import Batch
+from _gpu import require_gpu, to_dev
+from test_attention_gpu import data, device_batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def w4():
+    require_gpu()
+    import int4_weight_only_affine_gb300 as w4
+    return w4
+
+
+def call_of(w4, batch, hq, hkv, d, seed):
+    """(run(y, lse, stream), tokens): one call with a workspace of its own."""
+    q, kc, vc = data(batch, hq, hkv, d, seed)
+    tq, cache, kb = to_dev(q), w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch)
+    ws = w4.attention_workspace(cache, hq, kb.max_q_len)
+
+    def run(y, lse=None, stream=None):
+        w4.f16_attention(tq, cache, kb, y=y, lse=lse, workspace=ws, stream=stream)
+    run.workspace = ws
+    return run
+
+
+def sentinels(n, tokens, hq, d):
+    import torch
+    return ([torch.full((tokens, hq, d), 7.0, dtype=torch.float16, device="cuda") for _ in range(n)],
+            [torch.full((tokens, hq), 7.0, device="cuda") for _ in range(n)])
+
+
+@pytest.mark.parametrize("ql,kl,hq,hkv,d", [([700], [2500], 16, 2, 128), ([2000], [2000], 8, 8, 64), ([300, 100], [2000, 1100], 16, 8, 128),
+                                            ([1570], [1570], 16, 2, 128), ([90, 33], [700, 650], 28, 4, 64), ([250], [2100], 10, 2, 80)])
+def test_one_block_joins_all_columns(w4, ql, kl, hq, hkv, d):
+    """Items of a few parts whose columns one block joins range by range (no block may wait): the bits of the shared
+    join, every time."""
+    import torch
+    call = call_of(w4, Batch(ql, kl, 16, seed=3), hq, hkv, d, 3)
+    ys, ls = sentinels(31, sum(ql), hq, d)
+    call(ys[0], ls[0])
+    call.workspace.view(torch.int32)[513] = 2**30   # blocks begun in earlier calls, which the count of all calls lacks
+    for y, l in zip(ys[1:], ls[1:]):
+        call(y, l)
+    assert w4.device_status() == 0 and not bool(call.workspace[:2048].any())
+    for y, l in zip(ys[1:], ls[1:]):
+        assert bool((y == ys[0]).all()) and bool((l == ls[0]).all())

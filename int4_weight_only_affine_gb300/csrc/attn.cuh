@@ -16,9 +16,9 @@
 // unnormalised output, running maximum and sum in the workspace and counts
 // itself in; when a CTA is done with its own range it waits for the parts of the items it shares and joins
 // its share of their rows, in the parts' order.  A CTA waits only if every CTA
-// of the launch had begun when it counted its part in (so each will finish,
+// of the launch had begun whenever it counted a part in (so each will finish,
 // whatever else the GPU runs); otherwise it says so as it counts, and the last
-// to count a part of the item in joins all of it.  (A cooperative launch would
+// to count a part of the item in joins all of it (join_rule.h).  (A cooperative launch would
 // promise the same, but is not overlapped with the end of the kernel before:
 // 2.6 us a call.)  Every CTA works its range out from the lengths by itself:
 // the host needs no lengths, and no result depends on which CTA computes it, so
@@ -27,6 +27,7 @@
 
 #include <math.h>
 
+#include "join_rule.h"
 #include "kv.cuh"
 
 namespace w4a16 {
@@ -494,8 +495,6 @@ __device__ __forceinline__ void cta_has_begun(const AttnArgs &a, const Begin &b)
     if (b.mine + 1 == b.before + gridDim.x) *a.begun_before = b.before + gridDim.x;
 }
 
-constexpr unsigned kCountMask = 0xFFFFu, kWontWait = 0x10000u;
-
 // Counts a part in, by a thread that its writers have synchronised with;
 // returns the item's count with it, and clears `waits` where the CTA may not
 // wait for the others.  COPIED: the parts are read by copies.
@@ -505,41 +504,27 @@ __device__ __forceinline__ unsigned count_part(const AttnArgs &a, const Part &p,
     asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(begun) : "l"(a.begun) : "memory");
     __threadfence();
     if (COPIED) asm volatile("fence.proxy.async.global;" ::: "memory");
-    const bool all = begun == begun_before + gridDim.x;
-    waits = waits && all;
-    const unsigned mine = 1u + (all ? 0u : kWontWait);
+    const unsigned mine = part_mark(begun == begun_before + gridDim.x, waits);
     return atomicAdd(a.arrived + p.first, mine) + mine;
 }
 
-// What a CTA joins of an item it shares.
-enum : int { kJoinNothing = 0, kJoinShare = 1, kJoinAll = 2 };
-
-// Asked by one thread with the count as it saw it; with `waits` it waits until
-// all `parts` arrivals are in.  A wait is bounded: when it runs out, and where
-// there are more arrivals than parts (a workspace that was not zeroed),
+// What this CTA joins (join_mode), asked by one thread with the count as it
+// saw it; with `waits` it waits until all `parts` arrivals are in.  A wait is
+// bounded: when it runs out, and where there are more arrivals than parts,
 // w4a16_device_status says so.
 __device__ __forceinline__ int await_parts(const AttnArgs &a, const Part &p, unsigned seen, bool waits, unsigned parts) {
     unsigned now = seen;
-    if (waits) {
-        uint64_t t0 = 0;
-        for (uint32_t spin = 0;; ++spin) {  // (the first look does not need `seen`, which may still be on its way)
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(a.arrived + p.first) : "memory");
-            if ((now & kCountMask) >= parts) break;
-            if ((spin & 63) == 63) {
-                const uint64_t t = global_ns();
-                if (t0 == 0) t0 = t;
-                if (t - t0 > kWaitNs) break;
-            }
-        }
-        if ((now & kCountMask) == parts && now < kWontWait) return kJoinShare;
-    }
-    if ((now & kCountMask) > parts || (now >> 16) > parts || (waits && (now & kCountMask) < parts)) {
-        atomicExch(&g_wait_expired, 1);
-        return kJoinNothing;
-    }
-    if ((seen & kCountMask) != parts) return kJoinNothing;
-    __threadfence();
-    return seen < kWontWait ? kJoinShare : kJoinAll;
+    if (waits)  // (the first look does not need `seen`, which may still be on its way)
+        now = await_count(parts, kWaitNs, [&] {
+            unsigned v;
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.arrived + p.first) : "memory");
+            return v;
+        }, [] { return global_ns(); });
+    bool failed;
+    const int mode = join_mode(now, seen, waits, parts, failed);
+    if (failed) atomicExch(&g_wait_expired, 1);
+    if (!waits && mode != kJoinNothing) __threadfence();
+    return mode;
 }
 
 // A CTA is done with an item: the last of them all leaves its counts at zero.

@@ -49,3 +49,32 @@ def test_one_block_joins_all_columns(w4, ql, kl, hq, hkv, d):
     assert w4.device_status() == 0 and not bool(call.workspace[:2048].any())
     for y, l in zip(ys[1:], ls[1:]):
         assert bool((y == ys[0]).all()) and bool((l == ls[0]).all())
+
+
+@pytest.mark.parametrize("q,n,most,hq,hkv,d", [(1, 48, 8192, 16, 8, 128), (1, 48, 3000, 14, 2, 64), (24, 12, 8192, 16, 8, 128),
+                                               (200, 5, 6000, 16, 2, 128), (1, 30, 4000, 8, 4, 256)])
+def test_ragged_batch_beside_short_calls(w4, q, n, most, hq, hkv, d):
+    """Blocks that share two items each, some beginning late as short calls of another stream hold SMs: every row is
+    written, with the bits of the call alone."""
+    import torch
+    g = np.random.RandomState(n + d)
+    kl = np.maximum(np.exp(g.uniform(np.log(most / 16), np.log(most), n)).astype(int), q)
+    batch = Batch([q] * n, kl, 16, seed=n)
+    big = call_of(w4, batch, hq, hkv, d, 1)
+    small = call_of(w4, Batch([1], [16], 16, seed=2), 4, 1, d, 2)
+    times = 40
+    ys, ls = sentinels(times + 1, batch.tokens, hq, d)
+    scrap = torch.empty(1, 4, d, dtype=torch.float16, device="cuda")
+    big(ys[0], ls[0])
+    assert w4.device_status() == 0
+    s0, s1 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(1, times + 1):
+        for _ in range(4):
+            small(scrap, stream=s1)
+        big(ys[i], ls[i], stream=s0)
+    torch.cuda.synchronize()
+    assert w4.device_status() == 0
+    for i in range(1, times + 1):
+        assert bool((ys[i] == ys[0]).all()) and bool((ls[i] == ls[0]).all()), i
+    assert not bool(big.workspace[:2048].any()) and not bool(small.workspace[:2048].any())

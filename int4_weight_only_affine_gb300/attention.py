@@ -17,6 +17,7 @@ index tensors are read on the device when the kernels run.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -72,6 +73,21 @@ def _heads(t: torch.Tensor, name: str):
         raise ValueError(f"the dim elements of {name} must be contiguous")
     # The stride of a dimension of one entry is never used; any value torch keeps there will do.
     return t.data_ptr(), (st if n > 1 else 8), (sh if h > 1 else 8)
+
+
+def _on(stream):
+    """Context for making a tensor that a call on `stream` uses: the memory belongs to that stream, so that its fill
+    and its next use are ordered with the call."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _result(shape, device, stream) -> torch.Tensor:
+    """A float16 output made for a call on `stream`, kept for work that the current stream has on it when it is dropped."""
+    with _on(stream):
+        y = torch.empty(shape, dtype=torch.float16, device=device)
+    if stream is not None:
+        y.record_stream(torch.cuda.current_stream())
+    return y
 
 
 def _ints(t: torch.Tensor, name: str) -> int:
@@ -199,9 +215,9 @@ def f16_rope(x: torch.Tensor, rope: Rope, positions: torch.Tensor | None = None,
              stream=None) -> torch.Tensor:
     """y[t][h] = x[t][h] turned to positions[t] (int32; token t is at position t
     when None).  y may be x."""
-    if y is None:
-        y = torch.empty(x.shape, dtype=torch.float16, device=x.device)
     px, xt, xh = _heads(x, "x")
+    if y is None:
+        y = _result(x.shape, x.device, stream)
     py, yt, yh = _heads(y, "y")
     n, h, d = x.shape
     if y.shape != x.shape:
@@ -229,9 +245,9 @@ def f16_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBat
     pq = py = None
     qt = qh = yt = yh = hq = 0
     if q is not None:
-        if y is None:
-            y = torch.empty(q.shape, dtype=torch.float16, device=q.device)
         pq, qt, qh = _heads(q, "q")
+        if y is None:
+            y = _result(q.shape, q.device, stream)
         py, yt, yh = _heads(y, "y")
         hq = q.shape[1]
         if q.shape[0] != n or q.shape[2] != cache.head_dim or y.shape != q.shape:
@@ -252,7 +268,7 @@ def attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, max_q_
 def attention_workspace(cache: KVCache, q_heads: int, max_q_len: int) -> torch.Tensor:
     """A zero-filled workspace for f16_attention on this cache with up to
     max_q_len new tokens of a sequence (reusable by every later call that needs
-    no more)."""
+    no more).  Filled on the current stream: calls on another one have to come after it."""
     need = attention_workspace_bytes(q_heads, cache.heads, cache.head_dim, max_q_len)
     return torch.zeros(max(need, 16), dtype=torch.uint8, device=cache.k.device)
 
@@ -269,14 +285,15 @@ def f16_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, y: torch.Tens
     pq, qt, qh = _heads(q, "q")
     n, h, d = q.shape
     if y is None:
-        y = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        y = _result(q.shape, q.device, stream)
     py, yt, yh = _heads(y, "y")
     if n != batch.total_q or d != cache.head_dim or y.shape != q.shape:
         raise ValueError(f"q and y must be [{batch.total_q}][heads][{cache.head_dim}]")
     if lse is not None and lse.shape != (n, h):
         raise ValueError(f"lse must be [{n}][{h}]")
     if workspace is None:
-        workspace = attention_workspace(cache, h, batch.max_q_len)
+        with _on(stream):
+            workspace = attention_workspace(cache, h, batch.max_q_len)
     _check("f16_attention",
            lib.f16_attention(pq, qt, qh, py, yt, yh, None if lse is None else _dev(lse, "lse", (torch.float32,)), h,
                              d**-0.5 if scale is None else scale, 1 if causal else 0, window, cache.ptr, batch.ptr,

@@ -78,3 +78,34 @@ def test_ragged_batch_beside_short_calls(w4, q, n, most, hq, hkv, d):
     for i in range(1, times + 1):
         assert bool((ys[i] == ys[0]).all()) and bool((ls[i] == ls[0]).all()), i
     assert not bool(big.workspace[:2048].any()) and not bool(small.workspace[:2048].any())
+
+
+def test_call_on_another_stream_without_a_workspace(w4):
+    """The workspace and outputs that a call makes are ordered with its stream, however busy the current one is."""
+    import torch
+    batch = Batch([1, 60], [9000, 3000], 16, seed=7)
+    hq, hkv, d = 16, 2, 128
+    q, kc, vc = data(batch, hq, hkv, d, 7)
+    tq, cache, kb = to_dev(q), w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch)
+    want = w4.f16_attention(tq, cache, kb)
+    rope = w4.Rope(*w4.rope_turns(d))
+    want_r = w4.f16_rope(tq, rope)
+    side = torch.cuda.Stream()
+    # Memory that earlier work left full of ones, on both streams, for the calls to find.
+    size = w4.attention_workspace_bytes(hq, hkv, d, 60)
+    for s in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(s):
+            full = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+            del full
+    torch.cuda.synchronize()
+    ys = []
+    for i in range(5):
+        torch.cuda._sleep(4000000)   # the current stream is busy for some ms
+        y = w4.f16_attention(tq, cache, kb, stream=side)
+        ys.append((y, w4.f16_rope(tq, rope, stream=side)))
+        scrap = torch.ones(size, dtype=torch.uint8, device="cuda")   # where a dropped workspace might have been
+        del scrap
+    torch.cuda.synchronize()
+    assert w4.device_status() == 0
+    for y, r in ys:
+        assert bool((y == want).all()) and bool((r == want_r).all())

@@ -106,7 +106,9 @@ def rope_turns(rot: int, base: float = 10000.0, method: str | None = None, stret
     "ntk"     base * stretch ** (rot / (rot - 2)) in place of base;
     "yarn"    theta_i where a pair turns more than beta_fast times in
               original_len positions, theta_i / stretch where fewer than
-              beta_slow times, linear in i between; factor 0.1 ln stretch + 1;
+              beta_slow times, linear in i between the whole i at or beyond
+              these (within 0 .. rot - 1, past the last pair where it still
+              turns more often); factor 0.1 ln stretch + 1;
     "bands"   theta_i for wavelengths below original_len / high, theta_i /
               stretch above original_len / low, interpolated in
               original_len / wavelength between.
@@ -128,7 +130,8 @@ def rope_turns(rot: int, base: float = 10000.0, method: str | None = None, stret
     elif method == "yarn":
         def index(turns):  # of the pair that turns so many times over the original context
             return rot * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
-        lo, hi = max(math.floor(index(beta_fast)), 0), min(math.ceil(index(beta_slow)), rot // 2 - 1)
+        # (Past the last pair, rot // 2 - 1, where every pair turns more than beta_slow times.)
+        lo, hi = max(math.floor(index(beta_fast)), 0), min(math.ceil(index(beta_slow)), rot - 1)
         ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(rot // 2)]
         theta = [t * (1 - r) + t / stretch * r for t, r in zip(theta, ramp)]
         factor = 0.1 * math.log(stretch) + 1.0

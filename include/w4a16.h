@@ -345,7 +345,8 @@ W4A16_API int f16_gemm_ex(const uint16_t *x16, const uint16_t *w16, uint16_t *y,
  * read on the device, so that a captured graph can be replayed with others;
  * those out of range are clamped or skipped, never followed, and reported by
  * w4a16_device_status as W4_ERR_INDEX (with offsets out of order, f16_attention
- * writes nothing).
+ * writes nothing; of a sequence whose length or offsets are out of range,
+ * f16_kv_append writes no keys or values).
  */
 typedef struct {
     const int32_t *block_table; /* [batch][table_stride], the first max_pages of a row are used */

@@ -176,7 +176,7 @@ __device__ __forceinline__ void make_plan_by(const AttnArgs &a, PlanShared &sh) 
     const uint32_t batch = (uint32_t)a.b.batch, per = (batch + workers - 1) / workers;
     const uint32_t b0 = min(worker * per, batch), b1 = min(b0 + per, batch);
     uint32_t mine = 0, items = 0, most = 0, tiles = 0, cost = 0;  // cost: of a head of the worker's last sequence
-    Seq s = {0, 0, 0, true};
+    Seq s = {0, 0, 0, true, true};
     for (uint32_t b = b0; b < b1; ++b) {
         s = load_seq(a.b, (int)b);
         cost = head_cost<C, WARP>(a, s, most);

@@ -40,6 +40,7 @@ struct KvBatch {
 struct Seq {
     int q0, qn, kv;
     bool ordered;  // the offsets ascend, within the tensors
+    bool fits;     // the length is one that the table has room for
 };
 
 __device__ __forceinline__ Seq load_seq(const KvBatch &b, int i) {
@@ -49,7 +50,8 @@ __device__ __forceinline__ Seq load_seq(const KvBatch &b, int i) {
     s.qn = min(max(o1, s.q0), b.total_q) - s.q0;
     s.kv = min(max(kv, 0), b.max_kv);
     s.ordered = s.q0 == o0 && s.q0 + s.qn == o1;
-    if (!s.ordered || s.kv != kv) atomicExch(&g_bad_index, 1);
+    s.fits = s.kv == kv;
+    if (!s.ordered || !s.fits) atomicExch(&g_bad_index, 1);
     return s;
 }
 

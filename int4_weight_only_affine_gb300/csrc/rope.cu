@@ -209,7 +209,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const __gr
     if (t < s.q0 || t >= s.q0 + s.qn) return;  // offsets out of order: reported by load_seq
     const int p = s.kv - s.qn + (t - s.q0);
     int page = -1;
-    if (p >= 0) {
+    // (A position from a clamped length or offset may be another token's: nothing is written there.)
+    if (p >= 0 && s.ordered && s.fits) {
         page = __ldg(a.b.table + (long long)b * a.b.table_stride + p / a.page_size);
         if ((unsigned)page >= (unsigned)a.num_pages) {
             page = -1;

@@ -293,3 +293,32 @@ def test_wrong_arguments_are_refused(w4):
     with pytest.raises(w4.W4A16Error) as e:
         w4.f16_kv_append(k, k, cache, kb, rope=rope_of(w4, thetas(128)))
     assert e.value.status == 2
+
+
+@pytest.mark.parametrize("tokens", [1, 30])
+def test_append_skips_sequences_out_of_range(w4, tokens):
+    """A length past the table or below zero, or offsets past the tensors: reported, and the cached tokens stay."""
+    import torch
+    g = np.random.RandomState(tokens)
+    n, page, pages = 3, 16, 4
+    table = np.arange(n * pages).reshape(n, pages).astype(np.int32)
+    kc, vc = (to_dev(g.standard_normal((n * pages, page, 2, 64)).astype(np.float16)) for _ in range(2))
+    k, v = (to_dev(g.standard_normal((n * tokens, 2, 64)).astype(np.float16)) for _ in range(2))
+    good = np.array([40, 50, 60], np.int32)
+    offsets = (np.arange(n + 1) * tokens).astype(np.int32)
+    past = offsets.copy()
+    past[-1] += 5
+    for lens, offs, bad in ((np.array([40, 65, 60], np.int32), offsets, 1), (np.array([40, 2**31 - 1, 60], np.int32), offsets, 1),
+                            (np.array([-1, 50, 60], np.int32), offsets, 0), (good, past, 2)):
+        a, b = kc.clone(), vc.clone()
+        kb = w4.KVBatch(to_dev(table), to_dev(offs), to_dev(lens), n * tokens, tokens)
+        w4.f16_kv_append(k, v, w4.KVCache(a, b), kb)
+        assert w4.device_status() == 9 and w4.device_status() == 0
+        want_k, want_v = kc.clone(), vc.clone()
+        for s in range(n):
+            for i in range(tokens):
+                p = int(good[s]) - tokens + i
+                if s != bad:
+                    want_k[s * pages + p // page, p % page] = k[s * tokens + i]
+                    want_v[s * pages + p // page, p % page] = v[s * tokens + i]
+        assert bool((a == want_k).all()) and bool((b == want_v).all()), (lens.tolist(), offs.tolist())

@@ -287,6 +287,7 @@ def f16_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, y: torch.Tens
     reused); a fresh one is made when None."""
     pq, qt, qh = _heads(q, "q")
     n, h, d = q.shape
+    window = max(min(window, 2**31 - 1), -1)  # (passed as 32 bits; every position is below, a negative one is refused)
     if y is None:
         y = _result(q.shape, q.device, stream)
     py, yt, yh = _heads(y, "y")

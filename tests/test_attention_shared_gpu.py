@@ -109,3 +109,17 @@ def test_call_on_another_stream_without_a_workspace(w4):
     assert w4.device_status() == 0
     for y, r in ys:
         assert bool((y == want).all()) and bool((r == want_r).all())
+
+
+def test_windows_wider_than_32_bits(w4):
+    """A window beyond any position is no window; a negative one is refused, whatever its lower 32 bits are."""
+    batch = Batch([1, 40], [700, 90], 16, seed=1)
+    q, kc, vc = data(batch, 4, 2, 64, 1)
+    tq, cache, kb = to_dev(q), w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch)
+    want = w4.f16_attention(tq, cache, kb)
+    for window in (2**31 - 1, 2**31, 2**32 + 5, 2**63 - 1):
+        assert bool((w4.f16_attention(tq, cache, kb, window=window) == want).all()), window
+    for window in (-1, -2**31 - 1, 5 - 2**32):
+        with pytest.raises(w4.W4A16Error) as e:
+            w4.f16_attention(tq, cache, kb, window=window)
+        assert e.value.status == 2

@@ -123,3 +123,41 @@ def test_windows_wider_than_32_bits(w4):
         with pytest.raises(w4.W4A16Error) as e:
             w4.f16_attention(tq, cache, kb, window=window)
         assert e.value.status == 2
+
+
+@pytest.mark.parametrize("hq,hkv,d,tokens", [(16, 8, 128, 60), (14, 2, 64, 9), (4, 4, 80, 100)])
+def test_dominant_probability_of_few_rows(w4, hq, hkv, d, tokens):
+    """Few rows over long contexts: one position far above those before it takes nearly all of a row.  Its probability
+    must not lose bits of its own: bound without its rounding to binary16.
+
+    Scores are exact (q a multiple of 1/64, k of 1/8, all columns alike): position 200 lies 2**8.. 2**15 above 128-191,
+    which lie far above the rest.  Bound: the result's rounding, the other positions' roundings, exponentials and
+    sums as in the oracle's."""
+    g = np.random.RandomState(d)
+    n = 700
+    batch = Batch([tokens], [n], 16, seed=d)
+    _, kc, vc = data(batch, hq, hkv, d, d, garbage=False)
+    unit = 0.875 if d == 128 else 1.0 if d == 80 else 1.25
+    level = np.full(n, -2.5)
+    level[128:192], level[200] = 0.0, unit
+    page, at = batch.slot(0, np.arange(n))
+    kc[page, at] = level[:, None, None]
+    steps = g.randint(45, 65, (tokens, hq)) / 64.0
+    q = np.broadcast_to(steps[:, :, None], (tokens, hq, d)).astype(np.float16)
+    scale = d**-0.5
+    bits = steps * unit * d * scale * np.log2(np.e)
+    assert 8.2 < bits.min() and bits.max() < 14.9
+    y = w4.f16_attention(to_dev(np.ascontiguousarray(q)), w4.KVCache(to_dev(kc), to_dev(vc)), device_batch(w4, batch))
+    assert w4.device_status() == 0
+    y = y.cpu().numpy().astype(np.float64)
+    p = np.exp(steps[..., None] * d * np.float64(np.float32(scale)) * (level - unit))
+    p[np.broadcast_to(np.arange(n) > (n - tokens + np.arange(tokens))[:, None, None], p.shape)] = 0.0
+    p /= p.sum(-1, keepdims=True)
+    for h in range(hq):
+        v = vc[page, at, h * hkv // hq].astype(np.float64)
+        want, every = p[:, h] @ v, p[:, h] @ np.abs(v)
+        rest = every - p[:, h, 200:201] * np.abs(v[200])
+        tol = (2.0**-11 * (np.abs(want) + rest) + n * 2.0**-25 * np.abs(v).max()
+               + (2.0**-16 + (n / 16 + 8) * 2.0**-22) * every + 2.0**-25)
+        err = np.abs(y[:, h] - want)
+        assert np.all(err <= tol), float((err / tol).max())

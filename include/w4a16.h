@@ -443,6 +443,8 @@ W4A16_API int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head, 
  *   scale   > 0, finite;  causal 0 or 1;  window >= 0 (0: none)
  *   total_q x q_heads x max_pages x page_size up to about 2^42 (W4_ERR_SHAPE)
  *   q_heads a multiple of the cache's heads, at most 1024 for each
+ *   (head_dim above 128: every call reads K and V once per 16 rows of a
+ *   sequence and key/value head, so long prompts are several times slower)
  *   workspace  device buffer of at least f16_attention_workspace_bytes bytes,
  *              16-byte aligned, ZERO-FILLED before its first use and then
  *              passed unchanged to later calls (its counters are left ready for

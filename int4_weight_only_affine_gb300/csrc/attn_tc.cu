@@ -9,10 +9,12 @@
 // Measured: a prompt of 8192 tokens, 16 heads of 128 on 8, causal, 275 GFLOP:
 // 222 us, 1.24 PFLOP/s, 66% of a large matrix product's rate (the tensor pipe
 // busy half the time: a unit takes 3200 cycles, the chain S, softmax, P V of
-// each tile).  A prompt of 1570 tokens, 16 heads on 2, 10 GFLOP: 32 us, of
-// which the units are less than half: most CTAs share items, whose parts (128 KB
-// each) are written and joined through L2.  64 tokens over 16001 positions, 66
-// MB of keys and values: 26 us.
+// each tile).  A prompt of 1570 tokens, 16 heads on 2, 10 GFLOP: 32 us, 60000
+// cycles, of which the units (four a CTA on average) take 16000 in the mean and
+// 36000 where ten are left whole, plan and start 9000, parts written and joined
+// through L2 (128 KB each) 8000; the rest is waiting for the slower CTAs.
+// 64 tokens over 16001 positions, 66 MB of keys and values: 26 us, 22 with
+// them in L2.
 //
 // One CTA per SM works through its range of units (attn.cuh).
 //  * The item's 256 rows are two tiles of 128; tile t's scores S_t (fp32),
@@ -41,8 +43,9 @@
 //    not what they wait for, raise it at 2^8: 64 tokens over 16001 positions
 //    are 1.2 times as far from 64 bits as a plain fp32 computation (1.5 at
 //    most before, now 1.3), in the same 26.5 us (at 2^6 1.1 times, 27.7 us).
-//    More rows stay at 1.4 times or less: 2^8 takes 237 us, not 221, on a
-//    prompt of 8192 tokens for 1.3 times.
+//    With more rows it is 1.3 to 1.4 times (worst of 25 inputs 1.56, 24 tokens
+//    over 16000); 2^8 would take 237 us, not 221, on a prompt of 8192 tokens,
+//    for 1.3 times.
 //  * An item of at most 128 rows has both tiles work on the same rows, one on
 //    the even units, one on the odd ones; their sums are merged at its end.
 //  * Positions outside a row's range get probability 0; rows of V that no row

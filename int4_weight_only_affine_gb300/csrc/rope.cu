@@ -3,8 +3,10 @@
 //
 // The angle of pair i at position p is p * theta_i.  Held as a fraction of a
 // turn in 64 bits, F_i = round(2^64 theta_i / 2 pi), its reduction to one
-// turn is the wrap of an integer product: p * F_i mod 2^64, off by at most
-// |p| / 2 units of 2^-64 turns, whatever p.  The product's upper half, as a
+// turn is the wrap of an integer product, p * F_i mod 2^64, which adds no error
+// at any p: the angle is off by |p| times the error of F_i, half a unit of
+// 2^-64 turns in a correctly rounded table, up to some 2^9 units in one made
+// in binary64 (2^-24 turns at the largest p).  The product's upper half, as a
 // signed fraction of half a turn, goes to sincospif.
 //
 // Both calls move every element once in and once out and are bound by that.

@@ -414,6 +414,23 @@ W4A16_API int f16_rope(const uint16_t *x, int64_t x_token, int64_t x_head, uint1
                        int head_dim, void *stream);
 
 /*
+ * A norm of heads, applied before their rotation:
+ *     z_i = x_i * weight[i] / sqrt(mean_j x_j^2 + eps),  over the head_dim
+ * elements of a head.  Squares, sum, root and products are fp32, and the result
+ * is rounded to binary16 once, after the rotation.
+ */
+typedef struct {
+    const float *weight; /* [head_dim], device memory, 16-byte aligned */
+    float eps;           /* >= 0, finite (with 0, a head of zeros gives NaN) */
+} f16_head_norm;
+
+/* f16_rope_ex - f16_rope with a norm of each head before its rotation (NULL:
+ * none); with a norm, rotation may be NULL (nothing is turned). */
+W4A16_API int f16_rope_ex(const uint16_t *x, int64_t x_token, int64_t x_head, uint16_t *y, int64_t y_token,
+                          int64_t y_head, const int32_t *positions, const f16_rotation *rotation,
+                          const f16_head_norm *norm, int tokens, int heads, int head_dim, void *stream);
+
+/*
  * f16_kv_append - write the new tokens' keys and values into the cache, the
  * keys rotated on the way, and rotate the queries in the same launch.
  *   k, v       [total_q][cache heads][head_dim], strided
@@ -431,6 +448,15 @@ W4A16_API int f16_kv_append(const uint16_t *k, int64_t k_token, int64_t k_head, 
                             const f16_rotation *rotation, const int32_t *positions, const uint16_t *q,
                             int64_t q_token, int64_t q_head, uint16_t *y, int64_t y_token, int64_t y_head,
                             int q_heads, void *stream);
+
+/* f16_kv_append_ex - f16_kv_append with a norm of each query head and of each
+ * key head before its rotation (NULL: none for these heads).  Values are
+ * written as they are. */
+W4A16_API int f16_kv_append_ex(const uint16_t *k, int64_t k_token, int64_t k_head, const uint16_t *v, int64_t v_token,
+                               int64_t v_head, const f16_kv_cache *cache, const f16_kv_batch *batch,
+                               const f16_rotation *rotation, const int32_t *positions, const f16_head_norm *q_norm,
+                               const f16_head_norm *k_norm, const uint16_t *q, int64_t q_token, int64_t q_head,
+                               uint16_t *y, int64_t y_token, int64_t y_head, int q_heads, void *stream);
 
 /*
  * f16_attention - attention of the new tokens over the cache:

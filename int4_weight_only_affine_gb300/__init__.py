@@ -24,7 +24,7 @@ import torch
 __all__ = ["OVERLAP_PREVIOUS", "w4_gemv", "w4_gemv_seq", "GemvList", "seq_workspace", "seq_workspace_bytes", "GemvOp",
            "lm_head_argmax_topk", "lm_head_workspace_bytes", "w4_dequant_f16", "f16_gemm", "w4_gemm",
            "w4_gemm_workspace", "w4_gemm_workspace_bytes", "device_status", "W4A16Error", "LIB_PATH", "lib",
-           "KVBatch", "KVCache", "Rope", "attention_workspace", "attention_workspace_bytes", "f16_attention",
+           "HeadNorm", "KVBatch", "KVCache", "Rope", "attention_workspace", "attention_workspace_bytes", "f16_attention",
            "f16_kv_append", "f16_rope", "rope_turns"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -321,5 +321,5 @@ def device_status() -> int:
     return int(lib.w4a16_device_status())
 
 
-from .attention import (KVBatch, KVCache, Rope, attention_workspace, attention_workspace_bytes,  # noqa: E402
+from .attention import (HeadNorm, KVBatch, KVCache, Rope, attention_workspace, attention_workspace_bytes,  # noqa: E402
                         f16_attention, f16_kv_append, f16_rope, rope_turns)

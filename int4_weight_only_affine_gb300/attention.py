@@ -1,5 +1,5 @@
 """Attention with a paged key/value cache: binding of f16_rope, f16_kv_append
-and f16_attention (``include/w4a16.h``).
+(both with norms of the heads) and f16_attention (``include/w4a16.h``).
 
 A decode or prefill step of a layer, between its q/k/v projections and its o
 projection::
@@ -25,7 +25,7 @@ import torch
 
 from . import _check, _dev, _stream, lib
 
-__all__ = ["KVBatch", "KVCache", "Rope", "attention_workspace", "attention_workspace_bytes", "f16_attention",
+__all__ = ["HeadNorm", "KVBatch", "KVCache", "Rope", "attention_workspace", "attention_workspace_bytes", "f16_attention",
            "f16_kv_append", "f16_rope", "rope_turns"]
 
 _P, _I, _L, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -49,9 +49,15 @@ class _Rotation(ctypes.Structure):
     _fields_ = [("turns", _P), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("factor", _F)]
 
 
+class _Norm(ctypes.Structure):
+    _fields_ = [("weight", _P), ("eps", _F)]
+
+
 lib.f16_kv_cache_init.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I]
 lib.f16_rope.argtypes = [_P, _L, _L, _P, _L, _L, _P, _P, _I, _I, _I, _P]
 lib.f16_kv_append.argtypes = [_P, _L, _L, _P, _L, _L, _P, _P, _P, _P, _P, _L, _L, _P, _L, _L, _I, _P]
+lib.f16_rope_ex.argtypes = [_P, _L, _L, _P, _L, _L, _P, _P, _P, _I, _I, _I, _P]
+lib.f16_kv_append_ex.argtypes = [_P, _L, _L, _P, _L, _L, _P, _P, _P, _P, _P, _P, _P, _L, _L, _P, _L, _L, _I, _P]
 lib.f16_attention.argtypes = [_P, _L, _L, _P, _L, _L, _P, _I, _F, _I, _I, _P, _P, _P, _Z, _P]
 lib.f16_attention_workspace_bytes.argtypes = [_I, _I, _I, _I]
 lib.f16_attention_workspace_bytes.restype = _Z
@@ -158,6 +164,28 @@ class Rope:
         self.ptr = ctypes.addressof(self.struct)
 
 
+class HeadNorm:
+    """A norm of heads, before their rotation: x * weight / sqrt(mean x**2 + eps)
+    over a head's elements.  weight: float32 [dim] on the GPU (a float16 or
+    bfloat16 one is widened once, here, on the current stream)."""
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-6):
+        if isinstance(weight, torch.Tensor) and weight.dtype in (torch.float16, torch.bfloat16):
+            weight = weight.float()
+        pointer = _dev(weight, "weight", (torch.float32,))
+        if weight.dim() != 1:
+            raise ValueError("weight must be [dim]")
+        self.weight, self.eps, self.dim = weight, eps, weight.numel()
+        self.struct = _Norm(pointer, eps)
+        self.ptr = ctypes.addressof(self.struct)
+
+    def _of(self, dim: int) -> int:
+        """The descriptor's address, for heads of dim elements."""
+        if dim != self.dim:
+            raise ValueError(f"a norm of {self.dim} elements for heads of {dim}")
+        return self.ptr
+
+
 class KVCache:
     """A paged cache over k and v, float16 [pages][page_size][heads][dim] with any
     order of strides (a permuted view of [pages][heads][page_size][dim] is
@@ -214,10 +242,10 @@ class KVBatch:
         self.ptr = ctypes.addressof(self.struct)
 
 
-def f16_rope(x: torch.Tensor, rope: Rope, positions: torch.Tensor | None = None, y: torch.Tensor | None = None,
-             stream=None) -> torch.Tensor:
+def f16_rope(x: torch.Tensor, rope: Rope | None, positions: torch.Tensor | None = None, y: torch.Tensor | None = None,
+             stream=None, norm: HeadNorm | None = None) -> torch.Tensor:
     """y[t][h] = x[t][h] turned to positions[t] (int32; token t is at position t
-    when None).  y may be x."""
+    when None), normed before with norm (rope may be None then).  y may be x."""
     px, xt, xh = _heads(x, "x")
     if y is None:
         y = _result(x.shape, x.device, stream)
@@ -227,22 +255,29 @@ def f16_rope(x: torch.Tensor, rope: Rope, positions: torch.Tensor | None = None,
         raise ValueError("y must have the shape of x")
     if positions is not None and positions.numel() != n:
         raise ValueError("positions must be [tokens]")
-    _check("f16_rope", lib.f16_rope(px, xt, xh, py, yt, yh, None if positions is None else _ints(positions, "positions"),
-                                    rope.ptr, n, h, d, _stream(stream)))
+    pp = None if positions is None else _ints(positions, "positions")
+    if norm is None and rope is not None:
+        status = lib.f16_rope(px, xt, xh, py, yt, yh, pp, rope.ptr, n, h, d, _stream(stream))
+    else:
+        status = lib.f16_rope_ex(px, xt, xh, py, yt, yh, pp, None if rope is None else rope.ptr,
+                                 None if norm is None else norm._of(d), n, h, d, _stream(stream))
+    _check("f16_rope", status)
     return y
 
 
 def f16_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBatch, rope: Rope | None = None,
                   q: torch.Tensor | None = None, y: torch.Tensor | None = None,
-                  positions: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+                  positions: torch.Tensor | None = None, stream=None, q_norm: HeadNorm | None = None,
+                  k_norm: HeadNorm | None = None) -> torch.Tensor | None:
     """Write the new tokens' k (rotated) and v [total_q][heads][dim] into the cache;
     returns the rotated q in y (None without q).  positions: int32 [total_q]
-    for the rotation, where they are not those in the cache.  y may be q."""
+    for the rotation, where they are not those in the cache.  q_norm, k_norm:
+    norms of the query and the key heads, before they are rotated.  y may be q."""
     pk, kt, kh = _heads(k, "k")
     pv, vt, vh = _heads(v, "v")
-    n = batch.total_q
-    if k.shape != (n, cache.heads, cache.head_dim) or v.shape != k.shape:
-        raise ValueError(f"k and v must be [{n}][{cache.heads}][{cache.head_dim}]")
+    n, d = batch.total_q, cache.head_dim
+    if k.shape != (n, cache.heads, d) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{n}][{cache.heads}][{d}]")
     if positions is not None and positions.numel() != n:
         raise ValueError("positions must be [total_q]")
     pq = py = None
@@ -253,14 +288,20 @@ def f16_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBat
             y = _result(q.shape, q.device, stream)
         py, yt, yh = _heads(y, "y")
         hq = q.shape[1]
-        if q.shape[0] != n or q.shape[2] != cache.head_dim or y.shape != q.shape:
-            raise ValueError(f"q and y must be [{n}][heads][{cache.head_dim}]")
+        if q.shape[0] != n or q.shape[2] != d or y.shape != q.shape:
+            raise ValueError(f"q and y must be [{n}][heads][{d}]")
     elif y is not None:
         raise ValueError("y is the rotated q: it needs q")
-    _check("f16_kv_append",
-           lib.f16_kv_append(pk, kt, kh, pv, vt, vh, cache.ptr, batch.ptr, None if rope is None else rope.ptr,
-                             None if positions is None else _ints(positions, "positions"), pq, qt, qh, py, yt, yh, hq,
-                             _stream(stream)))
+    pr = None if rope is None else rope.ptr
+    pp = None if positions is None else _ints(positions, "positions")
+    if q_norm is None and k_norm is None:
+        status = lib.f16_kv_append(pk, kt, kh, pv, vt, vh, cache.ptr, batch.ptr, pr, pp, pq, qt, qh, py, yt, yh, hq,
+                                   _stream(stream))
+    else:
+        status = lib.f16_kv_append_ex(pk, kt, kh, pv, vt, vh, cache.ptr, batch.ptr, pr, pp,
+                                      None if q_norm is None else q_norm._of(d), None if k_norm is None else k_norm._of(d),
+                                      pq, qt, qh, py, yt, yh, hq, _stream(stream))
+    _check("f16_kv_append", status)
     return y
 
 

@@ -68,7 +68,7 @@ extern "C" {
 #define W4_ERR_WORKSPACE  6  /* workspace missing or smaller than required */
 #define W4_ERR_DEVICE     7  /* current device is not sm_103 or lacks a needed driver entry point */
 #define W4_ERR_TIMEOUT    8  /* a device-side bounded wait expired (reported by w4a16_device_status) */
-#define W4_ERR_INDEX      9  /* a kernel met a page, length or offset out of range (reported by w4a16_device_status) */
+#define W4_ERR_INDEX      9  /* a kernel met a page, length, offset or other index out of range (reported by w4a16_device_status) */
 
 /*
  * Launch flag of the *_ex calls.  W4A16_OVERLAP_PREVIOUS lets the call's
@@ -218,6 +218,79 @@ W4A16_API int lm_head_argmax_topk_noalloc(const uint16_t *x, const uint32_t *qwe
                         const uint16_t *scales, const uint16_t *biases,
                         int M, int N, int K, int group, int k,
                         int32_t *idx, float *val, void *stream);
+
+/*
+ * Rules of a selection: penalties of tokens that a request has seen, biases of
+ * listed tokens and a mask, applied to the fp32 logit z of token n in row m,
+ * in this order, each step one fp32 operation:
+ *   counts   c = counts[slot[m]][n]: bit 15 "in the prompt", the low 15 bits the
+ *            times t in the output (w4_token_counts keeps them):
+ *              c != 0:  z = z > 0 ? z / repetition[m] : z * repetition[m]
+ *              t != 0:  z = (z - frequency[m] * t) - presence[m]
+ *            a negative slot: no penalties for the row
+ *   biases   row m has the entries bias_offsets[m] <= i < bias_offsets[m + 1]:
+ *              z = z + bias_values[i]  where bias_tokens[i] == n
+ *            (entries of one token add up; negative tokens are skipped)
+ *   allowed  bit n % 32 of word n / 32 of row m: 0 = n cannot be selected
+ * Parts whose first pointer is NULL are left out.  The arrays are read on the
+ * device, so that a captured graph can be replayed with other contents; a slot,
+ * an offset or a token out of range is skipped (a list of biases as a whole) and
+ * reported by w4a16_device_status as W4_ERR_INDEX.
+ */
+typedef struct {
+    const uint16_t *counts;     /* [slots][counts_stride], or NULL */
+    int64_t counts_stride;      /* >= N */
+    const int32_t *slot;        /* [M] */
+    const float *repetition;    /* [M], NULL: 1 */
+    const float *presence;      /* [M], NULL: 0 */
+    const float *frequency;     /* [M], NULL: 0 */
+    const int32_t *bias_offsets; /* [M + 1], or NULL */
+    const int32_t *bias_tokens; /* [bias_entries] */
+    const float *bias_values;   /* [bias_entries] */
+    const uint32_t *allowed;    /* [M][allowed_stride], or NULL */
+    int64_t allowed_stride;     /* words, >= ceil(N / 32) */
+    int32_t slots;              /* >= 1 */
+    int32_t bias_entries;       /* 0 .. 2^30 */
+} w4_logit_rules;
+
+/*
+ * lm_head_argmax_topk_rules - lm_head_argmax_topk_ex with rules (NULL: none).
+ *   Of a row with fewer than k tokens that its mask allows, idx is -1 and val
+ *   -infinity past these (greedy selection of a row with none: -1).  val is the
+ *   logit after the rules.  The rules are applied to each block's logits in shared
+ *   memory before it selects, so a call reads 2 bytes of counts and one bit of
+ *   mask a logit more than without; index arrays need their natural alignment
+ *   only (rows of counts that start on 16 bytes are read fastest).
+ * Errors: as lm_head_argmax_topk.
+ */
+W4A16_API int lm_head_argmax_topk_rules(const uint16_t *x, const uint32_t *qweight,
+                        const uint16_t *scales, const uint16_t *biases,
+                        int M, int N, int K, int group, int k,
+                        int32_t *idx, float *val, const w4_logit_rules *rules,
+                        void *workspace, size_t workspace_bytes, unsigned flags, void *stream);
+
+/*
+ * w4_token_counts - count tokens in their requests' rows of `counts`.
+ *   counts   uint16 [slots][counts_stride], N tokens used: see w4_logit_rules
+ *   slot     int32 [batch]: the slot of each sequence (negative: none)
+ *   tokens   int32 [total]; negative ones are skipped
+ *   offsets  int32 [batch + 1], ascending: sequence b has the tokens
+ *            offsets[b] .. offsets[b + 1] - 1; NULL: token b alone (total = batch)
+ *   flags    W4_COUNTS_PROMPT: tokens of a prompt (bit 15 is set); without it
+ *            tokens of the output (the count goes up, and stays at 32767)
+ *            W4_COUNTS_RESET: the sequences' rows are cleared first (a request
+ *            takes its slot); their slots must differ
+ *   batch 0..65535;  total >= 0;  a token past N, a slot past the last or offsets
+ *   out of order are skipped and reported by w4a16_device_status as W4_ERR_INDEX.
+ * Pointers need their natural alignment only.  Results do not depend on the
+ * order in which tokens are counted.
+ * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_DEVICE, W4_ERR_LAUNCH.
+ */
+#define W4_COUNTS_PROMPT 1u
+#define W4_COUNTS_RESET  2u
+W4A16_API int w4_token_counts(uint16_t *counts, int64_t counts_stride, int slots, int N, const int32_t *slot,
+                              const int32_t *tokens, const int32_t *offsets, int batch, int total, unsigned flags,
+                              void *stream);
 
 /* Bytes of workspace lm_head_argmax_topk needs for these sizes (0 if the
  * sizes are invalid).  Depends only on its arguments. */

@@ -11,6 +11,9 @@ lowest nibble = lowest k), ``scales`` and ``biases`` float16 [N][K/group]
 (group 64 unless given); w[n][k] = scale * q + bias, or, with
 ``biases=None``, symmetric codes w[n][k] = scale * (q - 8).
 
+Token selection in the LM head takes rules of the requests (``rules.py``):
+penalties of the tokens that they have seen, biases and masks.
+
 Between a layer's projections: rotary positions, a paged key/value cache and
 attention over it (``attention.py``).
 """
@@ -22,7 +25,7 @@ import os
 import torch
 
 __all__ = ["OVERLAP_PREVIOUS", "w4_gemv", "w4_gemv_seq", "GemvList", "seq_workspace", "seq_workspace_bytes", "GemvOp",
-           "lm_head_argmax_topk", "lm_head_workspace_bytes", "w4_dequant_f16", "f16_gemm", "w4_gemm",
+           "lm_head_argmax_topk", "lm_head_workspace_bytes", "LogitRules", "TokenCounts", "token_counts_add", "w4_dequant_f16", "f16_gemm", "w4_gemm",
            "w4_gemm_workspace", "w4_gemm_workspace_bytes", "device_status", "W4A16Error", "LIB_PATH", "lib",
            "HeadNorm", "KVBatch", "KVCache", "Rope", "attention_workspace", "attention_workspace_bytes", "f16_attention",
            "f16_kv_append", "f16_rope", "rope_turns"]
@@ -67,6 +70,8 @@ def _load() -> ctypes.CDLL:
     L.w4_gemm_workspace_bytes.argtypes = [I, I, I]
     L.w4_gemm_workspace_bytes.restype = Z
     L.f16_gemm_ex.argtypes = [P, P, P, I, I, I, ctypes.c_uint, P]
+    L.lm_head_argmax_topk_rules.argtypes = [P, P, P, P, I, I, I, I, I, P, P, P, P, Z, ctypes.c_uint, P]
+    L.w4_token_counts.argtypes = [P, ctypes.c_int64, I, I, P, P, P, I, I, ctypes.c_uint, P]
     L.w4a16_status_string.argtypes = [I]
     L.w4a16_status_string.restype = ctypes.c_char_p
     L.w4a16_device_status.argtypes = []
@@ -230,8 +235,9 @@ def lm_head_workspace_bytes(M: int, N: int, k: int) -> int:
 def lm_head_argmax_topk(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
                         biases: torch.Tensor, k: int = 1, idx: torch.Tensor | None = None,
                         val: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                        group: int = 64, stream=None, flags: int = 0):
-    """(idx int32 [M][k], val float32 [M][k]): the k largest logits of x @ W^T per row."""
+                        group: int = 64, stream=None, flags: int = 0, rules: "LogitRules | None" = None):
+    """(idx int32 [M][k], val float32 [M][k]): the k largest logits of x @ W^T per row,
+    after `rules` where given (-1 and -infinity past the tokens that a mask leaves)."""
     N, K = _weight_dims(qweight, scales, biases, group)
     x2 = x.reshape(-1, K) if x.dim() != 2 else x
     M = x2.shape[0]
@@ -242,6 +248,14 @@ def lm_head_argmax_topk(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     need = lm_head_workspace_bytes(M, N, k)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+    if rules is not None:
+        _check("lm_head_argmax_topk",
+               lib.lm_head_argmax_topk_rules(_dev(x2, "x", _H), _dev(qweight, "qweight", _QW), _dev(scales, "scales", _H),
+                                             _biases(biases), M, N, K, group, k, _dev(idx, "idx", (torch.int32,)),
+                                             _dev(val, "val", (torch.float32,)), rules._of(M, N),
+                                             _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(), flags,
+                                             _stream(stream)))
+        return idx, val
     _check("lm_head_argmax_topk",
            lib.lm_head_argmax_topk_ex(_dev(x2, "x", _H), _dev(qweight, "qweight", _QW),
                                       _dev(scales, "scales", _H), _biases(biases),
@@ -317,9 +331,10 @@ def f16_gemm(x16: torch.Tensor, w16: torch.Tensor, y: torch.Tensor | None = None
 
 def device_status() -> int:
     """Synchronise and return the library's device-side status (0 = ok, 8 = a bounded wait expired,
-    9 = a page, length or offset was out of range)."""
+    9 = a page, length, offset or other index was out of range)."""
     return int(lib.w4a16_device_status())
 
 
 from .attention import (HeadNorm, KVBatch, KVCache, Rope, attention_workspace, attention_workspace_bytes,  # noqa: E402
                         f16_attention, f16_kv_append, f16_rope, rope_turns)
+from .rules import LogitRules, TokenCounts, token_counts_add  # noqa: E402

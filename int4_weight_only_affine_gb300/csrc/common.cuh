@@ -131,6 +131,10 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 // (one copy per translation unit; read by w4a16_device_status).
 static __device__ int g_wait_expired = 0;
 
+// Set by a kernel of this translation unit that met a page, a length, an offset
+// or another index out of range (one copy per translation unit, as above).
+static __device__ int g_bad_index = 0;
+
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s per wait
 constexpr uint32_t kMaxSpins = 1u << 26;
 

@@ -1455,7 +1455,9 @@ extern "C" int w4_gemm_ex(const uint16_t *x, const uint32_t *qweight, const uint
 namespace w4a16 {
 int gemv_wait_flag();     // gemv.cu
 int dequant_wait_flag();  // dequant.cu
+int gemv_bad_index();     // gemv.cu
 int rope_bad_index();     // rope.cu
+int counts_bad_index();   // counts.cu
 int attn_status();        // attn.cu: bit 0 an expired wait, bit 1 a bad index
 
 // Reads and clears this translation unit's expired-wait record.
@@ -1473,10 +1475,10 @@ static int gemm_wait_flag() {
 extern "C" int w4a16_device_status(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return W4_ERR_LAUNCH;
     const int a = gemm_wait_flag(), b = gemv_wait_flag(), c = dequant_wait_flag();
-    const int r = rope_bad_index(), at = attn_status();
-    if (a < 0 || b < 0 || c < 0 || r < 0 || at < 0) return W4_ERR_LAUNCH;
+    const int i = gemv_bad_index(), r = rope_bad_index(), t = counts_bad_index(), at = attn_status();
+    if (a < 0 || b < 0 || c < 0 || i < 0 || r < 0 || t < 0 || at < 0) return W4_ERR_LAUNCH;
     if (a || b || c || (at & 1)) return W4_ERR_TIMEOUT;
-    return (r || (at & 2)) ? W4_ERR_INDEX : W4A16_OK;
+    return (i || r || t || (at & 2)) ? W4_ERR_INDEX : W4A16_OK;
 }
 
 extern "C" const char *w4a16_status_string(int status) {
@@ -1490,7 +1492,7 @@ extern "C" const char *w4a16_status_string(int status) {
         case W4_ERR_WORKSPACE: return "workspace missing or too small";
         case W4_ERR_DEVICE: return "unsupported device (needs sm_103) or missing driver entry point";
         case W4_ERR_TIMEOUT: return "a device-side bounded wait expired";
-        case W4_ERR_INDEX: return "a page, length or offset out of range";
+        case W4_ERR_INDEX: return "a page, length, offset or other index out of range";
         default: return "unknown status";
     }
 }

@@ -40,6 +40,7 @@
 #include <mutex>
 
 #include "gemv_tile.cuh"
+#include "rules.cuh"
 #include "../../include/w4a16_testing.h"
 
 namespace cg = cooperative_groups;
@@ -82,6 +83,17 @@ int gemv_wait_flag() {
     return v;
 }
 
+// Reads and clears this translation unit's record of bad indexes.
+int gemv_bad_index() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_bad_index, sizeof(int)) != cudaSuccess) return -1;
+    if (v) {
+        const int zero = 0;
+        cudaMemcpyToSymbol(g_bad_index, &zero, sizeof(int));
+    }
+    return v;
+}
+
 namespace {
 
 // ---------------------------------------------------------------------------
@@ -94,7 +106,19 @@ __device__ __forceinline__ uint64_t make_key(float v, int idx) {
     return ((uint64_t)hi << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)idx);
 }
 
+// The key of a logit in shared memory; 0, below every key, for one that a mask
+// excludes.
+__device__ __forceinline__ uint64_t row_key(float v, int idx, bool ruled) {
+    return ruled && __float_as_uint(v) == kExcluded ? 0ull : make_key(v, idx);
+}
+
+// Key 0 stands for no token: index -1, value -infinity.
 __device__ __forceinline__ void decode_key(uint64_t key, float &v, int &idx) {
+    if (key == 0ull) {
+        v = -__int_as_float(0x7F800000);
+        idx = -1;
+        return;
+    }
     const uint32_t hi = (uint32_t)(key >> 32);
     const uint32_t u = (hi & 0x80000000u) ? (hi & 0x7FFFFFFFu) : ~hi;
     v = __uint_as_float(u);
@@ -222,6 +246,7 @@ struct StreamArgs {
     int defer;   // 1: per-warp partials of all tiles kept, combined once at the end
     uint32_t stage_bytes, w_bytes;
     uint32_t off_xf, off_xsum, off_red, off_res, off_bar;
+    Rules rules;  // lm_head: applied to the logits before the selection
 };
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
@@ -231,7 +256,7 @@ __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;"
 template <int NT, bool LMHEAD, bool M1, int FMT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     stream_kernel(const __grid_constant__ CUtensorMap tm3, const __grid_constant__ CUtensorMap tm2,
-                  const StreamArgs a) {
+                  const __grid_constant__ StreamArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -337,6 +362,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         const bool sym = FMT == kFmtS128 || (FMT != kFmtG64 && f.sym);
         const bool vec = FMT == kFmtG64 ? (ng & 3) == 0 : FMT == kFmtS128 ? (ng & 3) == 0 : box_vec_ok(f);
         pdl_wait();
+        if (LMHEAD && a.rules.on)
+            rules_prefetch(a.rules, M, t0 * kTileRows, min(N, t1 * kTileRows) - t0 * kTileRows, tid, kConsumers);
         stage_activations<M1 ? 2 : 4, FMT == kFmtG32>(a.x, M, a.K, gs0, ngl, xf, xsum, tid, kConsumers);
         consumer_sync();
         int s = 0;
@@ -464,11 +491,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     const int rows = min(N, t1 * kTileRows) - n0;
     uint64_t(*lists)[64] = reinterpret_cast<uint64_t(*)[64]>(sb);  // the ring is free now
     constexpr int kWarps = kThreads / 32;
+    const bool ruled = a.rules.on;
+    if (ruled) rules_apply(a.rules, res, M, N, n0, rows, tid, kThreads);
     if (a.k == 1) {
         // Greedy selection: warp w takes activation rows w, w + 9, ...
         for (int m = warp; m < M; m += kWarps) {
             uint64_t best = 0ull;
-            for (int i = lane; i < rows; i += 32) best = umax64(best, make_key(res[i * M + m], n0 + i));
+            for (int i = lane; i < rows; i += 32) best = umax64(best, row_key(res[i * M + m], n0 + i, ruled));
             best = shfl_max_u64(best);
             if (lane == 0) a.ws[(size_t)m * gridDim.x + blockIdx.x] = best;
         }
@@ -481,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             Key2 run{0ull, 0ull};
             for (int c0 = warp * 64; c0 < rows; c0 += kWarps * 64) {
                 const int i = c0 + lane, j = c0 + 32 + lane;
-                const Key2 c{i < rows ? make_key(res[i * M + m], n0 + i) : 0ull,
-                             j < rows ? make_key(res[j * M + m], n0 + j) : 0ull};
+                const Key2 c{i < rows ? row_key(res[i * M + m], n0 + i, ruled) : 0ull,
+                             j < rows ? row_key(res[j * M + m], n0 + j, ruled) : 0ull};
                 run = warp_insert64(run, c, lane);
             }
             lists[warp][lane] = run.a;
@@ -946,6 +975,9 @@ __global__ void __launch_bounds__(kPass2Threads)
     if (nbuf <= (unsigned)kSurvivorCap) {
         // Every survivor is in buf: rank by counting, write the best k.
         const int nb = (int)nbuf;
+        for (int i = nb + tid; i < k; i += kPass2Threads) {  // fewer than k tokens that a mask leaves
+            decode_key(0ull, val[(size_t)m * k + i], idx[(size_t)m * k + i]);
+        }
         for (int i = tid; i < nb; i += kPass2Threads) {
             const uint64_t key = buf[i];
             const int r = rank_of(key, buf, nb);
@@ -1263,6 +1295,7 @@ int gemv_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const u
     p.a.bi = bi;
     p.a.y = y;
     p.a.ws = nullptr;
+    p.a.rules = Rules{};
     const bool ov = (flags & W4A16_OVERLAP_PREVIOUS) != 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return launch_stream_any<false>(p, qw, ov, s);
@@ -1270,7 +1303,7 @@ int gemv_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const u
 
 int lmhead_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const uint16_t *bi, int M, int N, int K,
                 const WFmt &f, int k, int32_t *idx, float *val, uint64_t *ws, size_t ws_bytes, unsigned flags,
-                void *stream) {
+                void *stream, const Rules &rules = Rules{}) {
     StreamPlan p;
     if (!plan_stream(p, M, N, K, f, true, k)) return W4_ERR_SHAPE;
     const int G = p.grid;
@@ -1281,6 +1314,7 @@ int lmhead_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const
     p.a.bi = bi;
     p.a.y = nullptr;
     p.a.ws = ws;
+    p.a.rules = rules;
     const bool ov = (flags & W4A16_OVERLAP_PREVIOUS) != 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int st = launch_stream_any<true>(p, qw, ov, s);
@@ -1571,6 +1605,22 @@ extern "C" int lm_head_argmax_topk_ex(const uint16_t *x, const uint32_t *qweight
     if (!aligned16(workspace)) return W4_ERR_ALIGN;
     return lmhead_impl(x, qweight, scales, biases, M, N, K, f, k, idx, val,
                        reinterpret_cast<uint64_t *>(workspace), workspace_bytes, flags, stream);
+}
+
+extern "C" int lm_head_argmax_topk_rules(const uint16_t *x, const uint32_t *qweight, const uint16_t *scales,
+                                         const uint16_t *biases, int M, int N, int K, int group, int k, int32_t *idx,
+                                         float *val, const w4_logit_rules *rules, void *workspace,
+                                         size_t workspace_bytes, unsigned flags, void *stream) {
+    WFmt f;
+    int st = lmhead_checks(x, qweight, scales, biases, M, N, K, group, k, idx, val, f);
+    if (st != W4A16_OK) return st;
+    Rules r;
+    if ((st = check_rules(rules, N, r)) != W4A16_OK) return st;
+    if (flags & ~(unsigned)W4A16_OVERLAP_PREVIOUS) return W4_ERR_SHAPE;
+    if (!workspace) return W4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return W4_ERR_ALIGN;
+    return lmhead_impl(x, qweight, scales, biases, M, N, K, f, k, idx, val, reinterpret_cast<uint64_t *>(workspace),
+                       workspace_bytes, flags, stream, r);
 }
 
 // Scale-layout class of an operation (its arguments need not be valid yet).

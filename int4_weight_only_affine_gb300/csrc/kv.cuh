@@ -6,11 +6,6 @@
 
 namespace w4a16 {
 
-// Set by a kernel of this translation unit that met a page, a length or an
-// offset out of range (one copy per translation unit; read by
-// w4a16_device_status).
-static __device__ int g_bad_index = 0;
-
 constexpr int kMaxHeads = 1024;
 
 // Division of 0 <= n < 2^31 by a d fixed on the host: with l = ceil(log2 d)

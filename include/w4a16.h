@@ -398,6 +398,46 @@ W4A16_API int f16_gemm_ex(const uint16_t *x16, const uint16_t *w16, uint16_t *y,
                           int K, unsigned flags, void *stream);
 
 /*
+ * Low-rank adapters of a projection: N x K updates B_a A_a of a shared weight.
+ * The columns may be cut into up to four slices, each with an A of its own (the
+ * q | k | v or gate | up blocks of one projection).
+ */
+typedef struct {
+    const uint16_t *a;   /* binary16 [adapters][slices][rank][K], adapters a_adapter elements apart */
+    const uint16_t *b;   /* binary16 [adapters][N][rank], adapters b_adapter elements apart */
+    const float *scale;  /* [adapters], or NULL: 1 */
+    int64_t a_adapter, b_adapter; /* multiples of 8 */
+    int32_t adapters;    /* 1..4096 */
+    int32_t rank;        /* a multiple of 8, 8..128 */
+    int32_t K, N;        /* multiples of 8 */
+    int32_t slices;      /* 1..4 */
+    int32_t columns[4];  /* end of each slice, ascending multiples of 8; the last is N */
+} f16_adapters;
+
+/*
+ * f16_lora - adapters of many requests at once, beside a projection of theirs
+ * (w4_gemv, w4_gemm or f16_gemm, whose output is y):
+ *     out[m] = y[m] + scale[a] * (x[m] A_a^T) B_a^T,   a = ids[m],
+ *   the A being that of the column's slice; rows with a negative id get y[m].
+ *   x        binary16 [M][K], y and out binary16 [M][N]: rows x_row, y_row and
+ *            out_row elements apart (multiples of 8); out may be y, else they
+ *            must not overlap
+ *   ids      int32 [M], in any order and mix (read on the device: a captured graph
+ *            can be replayed with others); an id past the last adapter counts as
+ *            negative and is reported by w4a16_device_status as W4_ERR_INDEX.
+ *            Many rows of one adapter are fastest where they lie near each other
+ *            (rows are gathered within blocks of up to 1024)
+ *   M        >= 0
+ *   Sums are fp32 over exact products; x A^T is carried on in two binary16 numbers
+ *   a value (2^-22 of the row's largest), and out is rounded once.  Results are
+ *   deterministic; a row is not touched by what the others hold (NaN and infinities
+ *   included), but its sums may be taken in another order in another mix of rows.
+ * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_DEVICE, W4_ERR_LAUNCH.
+ */
+W4A16_API int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int64_t y_row, uint16_t *out,
+                       int64_t out_row, const f16_adapters *adapters, const int32_t *ids, int M, void *stream);
+
+/*
  * Attention with a paged key/value cache: what a decoder layer does between
  * its q/k/v projections and its o projection.  The three calls share the
  * conventions above (binary16 tensors, fp32 arithmetic, host checks, one

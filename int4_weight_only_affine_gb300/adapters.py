@@ -1,0 +1,97 @@
+"""Low-rank adapters of many requests beside a shared projection: binding of
+f16_lora (``include/w4a16.h``)::
+
+    adapters = Adapters(a, b, scale, columns=(2048, 256, 256))   # once per projection
+    y = w4_gemv(x, ...)                                          # or w4_gemm, f16_gemm
+    f16_lora(x, adapters, ids, y)                                # ids int32 [rows], negative: none
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _check, _dev, _stream, lib
+
+__all__ = ["Adapters", "f16_lora"]
+
+_P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+
+
+class _Adapters(ctypes.Structure):
+    _fields_ = [("a", _P), ("b", _P), ("scale", _P), ("a_adapter", _L), ("b_adapter", _L), ("adapters", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("slices", ctypes.c_int32),
+                ("columns", ctypes.c_int32 * 4)]
+
+
+lib.f16_lora.argtypes = [_P, _L, _P, _L, _P, _L, _P, _P, _I, _P]
+
+
+def _half(t: torch.Tensor, name: str) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float16:
+        raise TypeError(f"{name} must be a float16 tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(device pointer, row stride) of a float16 [rows][columns] tensor with contiguous rows."""
+    _half(t, name)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows][columns] with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 8  # (of one row the stride is never used)
+
+
+class Adapters:
+    """The adapters of one projection, checked and marshalled once.  Keeps its tensors;
+    their contents may change between calls (an adapter's place taken by another).
+
+    a        float16 [adapters][slices][rank][K], or [adapters][rank][K] for one slice
+    b        float16 [adapters][N][rank]
+    scale    float32 [adapters], 1 when None
+    columns  widths of the slices, which add up to N; one slice of all when None
+    """
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor | None = None, columns=None):
+        a, b = _half(a, "a"), _half(b, "b")
+        if a.dim() == 3:
+            a = a.unsqueeze(1)
+        if a.dim() != 4 or b.dim() != 3:
+            raise ValueError("a must be [adapters][slices][rank][K] and b [adapters][N][rank]")
+        n, slices, rank, k = a.shape
+        columns = (b.shape[1],) if columns is None else tuple(columns)
+        if b.shape[0] != n or b.shape[2] != rank:
+            raise ValueError(f"b must be [{n}][N][{rank}]")
+        if len(columns) != slices or not 1 <= slices <= 4 or min(columns) < 1 or sum(columns) != b.shape[1]:
+            raise ValueError(f"columns must be the widths of 1 to 4 slices, one for each of a's, that add up to {b.shape[1]}")
+        for t, name in ((a, "a"), (b, "b")):
+            if n > 0 and not t[0].is_contiguous():
+                raise ValueError(f"each adapter of {name} must be contiguous")
+        if scale is not None and scale.numel() != n:
+            raise ValueError(f"scale must be [{n}]")
+        self.a, self.b, self.scale = a, b, scale
+        self.K, self.N = k, b.shape[1]
+        ends = [sum(columns[:i + 1]) for i in range(slices)]
+        self.struct = _Adapters(a.data_ptr(), b.data_ptr(),
+                                None if scale is None else _dev(scale, "scale", (torch.float32,)),
+                                a.stride(0) if n > 1 else 8, b.stride(0) if n > 1 else 8, n, rank, k, self.N, slices,
+                                (ctypes.c_int32 * 4)(*ends))
+        self.ptr = ctypes.addressof(self.struct)
+
+
+def f16_lora(x: torch.Tensor, adapters: Adapters, ids: torch.Tensor, y: torch.Tensor, out: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """out[m] = y[m] + scale[a] * (x[m] @ A_a.T) @ B_a.T with a = ids[m] (int32; negative: y[m]).
+    x float16 [rows][K], y and out [rows][N], any row strides that are multiples of 8; out is y itself when None."""
+    px, xs = _rows(x, "x")
+    py, ys = _rows(y, "y")
+    po, os = (py, ys) if out is None else _rows(out, "out")
+    m = x.shape[0]
+    if x.shape[1] != adapters.K or y.shape != (m, adapters.N) or (out is not None and out.shape != y.shape):
+        raise ValueError(f"x must be [{m}][{adapters.K}], y and out [{m}][{adapters.N}]")
+    if ids.numel() != m:
+        raise ValueError("ids must be [rows]")
+    _check("f16_lora", lib.f16_lora(px, xs, py, ys, po, os, adapters.ptr, _dev(ids, "ids", (torch.int32,)), m,
+                                    _stream(stream)))
+    return y if out is None else out

@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libw4a16.so")
-SOURCES = ["gemv.cu", "counts.cu", "dequant.cu", "gemm.cu", "rope.cu", "attn.cu", "attn_tc.cu"]
+SOURCES = ["gemv.cu", "counts.cu", "lora.cu", "dequant.cu", "gemm.cu", "rope.cu", "attn.cu", "attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

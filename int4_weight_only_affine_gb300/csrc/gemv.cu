@@ -207,6 +207,45 @@ __device__ __forceinline__ Key2 warp_insert64(Key2 run, Key2 c, int lane) {
     return warp_merge64(run, warp_sort64(c, lane), lane);
 }
 
+// The 64 largest keys of logits z[i0 .. i1 - 1] of tokens n0 + i, sorted descending,
+// at least the k best of them exact (the rest may be left out).  The best two of each
+// lane give a lower bound of the k-th key (k of these 64 are at least as large);
+// keys below it are passed over, the others collected in `pending` (64 keys of the
+// warp in shared memory) and inserted when it is full.
+__device__ __forceinline__ Key2 warp_best64(const float *z, int n0, int i0, int i1, int k, bool ruled,
+                                            uint64_t *pending, int lane) {
+    uint64_t f0 = 0ull, f1 = 0ull;
+    for (int i = i0 + lane; i < i1; i += 32) {
+        const uint64_t key = row_key(z[i], n0 + i, ruled);
+        f1 = umax64(f1, umin64(f0, key));
+        f0 = umax64(f0, key);
+    }
+    Key2 run = warp_sort64(Key2{f0, f1}, lane);
+    if (i1 - i0 <= 64) return run;  // (all of them)
+    const uint64_t least = __shfl_sync(0xffffffffu, k <= 32 ? run.a : run.b, (k - 1) & 31);
+    run = Key2{0ull, 0ull};
+    int held = 0;
+    for (int c = i0; c < i1; c += 32) {
+        const uint64_t key = c + lane < i1 ? row_key(z[c + lane], n0 + c + lane, ruled) : 0ull;
+        const bool take = key != 0ull && key >= least;
+        const unsigned bal = __ballot_sync(0xffffffffu, take);
+        const int n = __popc(bal), at = held + __popc(bal & ((1u << lane) - 1u));
+        if (take && at < 64) pending[at] = key;
+        __syncwarp();
+        if (held + n >= 64) {
+            run = warp_insert64(run, Key2{pending[lane], pending[32 + lane]}, lane);
+            __syncwarp();
+            if (take && at >= 64) pending[at - 64] = key;
+            held -= 64;
+        }
+        held += n;
+        __syncwarp();
+    }
+    if (held > 0)
+        run = warp_insert64(run, Key2{lane < held ? pending[lane] : 0ull, 32 + lane < held ? pending[32 + lane] : 0ull}, lane);
+    return run;
+}
+
 // Combines the sorted lists of nw warps (lists[w][64] in shared memory) into
 // lists[0] with a pairwise tree; called by every thread of the block.
 __device__ void block_merge_lists(uint64_t (*lists)[64], int nw) {
@@ -246,15 +285,19 @@ struct StreamArgs {
     int defer;   // 1: per-warp partials of all tiles kept, combined once at the end
     uint32_t stage_bytes, w_bytes;
     uint32_t off_xf, off_xsum, off_red, off_res, off_bar;
+    int ldr;      // lm_head: logits [M][ldr] of the CTA's rows (odd: stored M at a time, read in rows)
     Rules rules;  // lm_head: applied to the logits before the selection
+    uint32_t off_rules;
 };
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
+constexpr int kLmThreads = kThreads + 32;  // lm_head pass 1: a warp for the rules beside the others
+
 // FMT: the scale-layout class of the weight (kFmtG64, kFmtS128, kFmtAny,
 // kFmtG32).
 template <int NT, bool LMHEAD, bool M1, int FMT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(LMHEAD ? kLmThreads : kThreads, NT == 1 ? 2 : 1)
     stream_kernel(const __grid_constant__ CUtensorMap tm3, const __grid_constant__ CUtensorMap tm2,
                   const __grid_constant__ StreamArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -279,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     uint32_t *xf = reinterpret_cast<uint32_t *>(sb + a.off_xf);
     float *xsum = reinterpret_cast<float *>(sb + a.off_xsum);
     float *red = reinterpret_cast<float *>(sb + a.off_red);  // [2][8][16*M]
-    float *res = reinterpret_cast<float *>(sb + a.off_res);  // [ntl][16*M]
+    float *res = reinterpret_cast<float *>(sb + a.off_res);  // [ntl][16*M]; lm_head: [M][ldr]
     const uint32_t bar0 = base + a.off_bar;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sb + a.off_bar + 16 * S);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -347,6 +390,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             for (int s = 0; s < S; ++s)
                 if (issued_any & (1u << s)) mbar_wait(full_bar(s), (issued_ph >> s) & 1);
         }
+    } else if (LMHEAD && warp > kConsumerWarps) {
+        // ---------------- lm_head: one more warp, for the rules of the selection ----------------
+        pdl_wait();
+        if (a.rules.on)
+            rules_begin(a.rules, RulesMemory(sb + a.off_rules, M), M, N, t0 * kTileRows,
+                        min(N, t1 * kTileRows) - t0 * kTileRows, lane);
     } else {
         // ---------------- consumers ----------------
         const int lg = lane >> 2, lt = lane & 3;
@@ -362,8 +411,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         const bool sym = FMT == kFmtS128 || (FMT != kFmtG64 && f.sym);
         const bool vec = FMT == kFmtG64 ? (ng & 3) == 0 : FMT == kFmtS128 ? (ng & 3) == 0 : box_vec_ok(f);
         pdl_wait();
-        if (LMHEAD && a.rules.on)
-            rules_prefetch(a.rules, M, t0 * kTileRows, min(N, t1 * kTileRows) - t0 * kTileRows, tid, kConsumers);
         stage_activations<M1 ? 2 : 4, FMT == kFmtG32>(a.x, M, a.K, gs0, ngl, xf, xsum, tid, kConsumers);
         consumer_sync();
         int s = 0;
@@ -441,6 +488,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                     if (!LMHEAD && C == 1) {
                         const int row = e / M, col = e % M;
                         if (row0 + row < N) a.y[(size_t)col * N + row0 + row] = __half_as_ushort(__float2half_rn(v));
+                    } else if (LMHEAD) {
+                        res[e % M * a.ldr + tl * kTileRows + e / M] = v;
                     } else {
                         res[tl * out16 + e] = v;
                     }
@@ -458,6 +507,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 if (!LMHEAD && C == 1) {
                     const int row = e / M, col = e % M, r = (t0 + tl) * kTileRows + row;
                     if (r < N) a.y[(size_t)col * N + r] = __half_as_ushort(__float2half_rn(v));
+                } else if (LMHEAD) {
+                    res[e % M * a.ldr + tl * kTileRows + e / M] = v;
                 } else {
                     res[tl * out16 + e] = v;
                 }
@@ -489,37 +540,51 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     // The keys of this CTA's rows, best first, padded with 0 (below every key).
     const int n0 = t0 * kTileRows;
     const int rows = min(N, t1 * kTileRows) - n0;
-    uint64_t(*lists)[64] = reinterpret_cast<uint64_t(*)[64]>(sb);  // the ring is free now
-    constexpr int kWarps = kThreads / 32;
+    constexpr int kWarps = kLmThreads / 32;
     const bool ruled = a.rules.on;
-    if (ruled) rules_apply(a.rules, res, M, N, n0, rows, tid, kThreads);
+    if (ruled) rules_apply(a.rules, RulesMemory(sb + a.off_rules, M), res, a.ldr, M, n0, rows, tid, kLmThreads);
     if (a.k == 1) {
-        // Greedy selection: warp w takes activation rows w, w + 9, ...
+        // Greedy selection: warp w takes activation rows w, w + 10, ...
         for (int m = warp; m < M; m += kWarps) {
             uint64_t best = 0ull;
-            for (int i = lane; i < rows; i += 32) best = umax64(best, row_key(res[i * M + m], n0 + i, ruled));
+            for (int i = lane; i < rows; i += 32) best = umax64(best, row_key(res[m * a.ldr + i], n0 + i, ruled));
             best = shfl_max_u64(best);
             if (lane == 0) a.ws[(size_t)m * gridDim.x + blockIdx.x] = best;
         }
         return;
     }
-    for (int m = 0; m < M; ++m) {
-        uint64_t *out = a.ws + ((size_t)m * gridDim.x + blockIdx.x) * a.k;
-        {
-            // Each warp keeps the best 64 of its 64-row chunks; a tree merges them.
-            Key2 run{0ull, 0ull};
-            for (int c0 = warp * 64; c0 < rows; c0 += kWarps * 64) {
-                const int i = c0 + lane, j = c0 + 32 + lane;
-                const Key2 c{i < rows ? row_key(res[i * M + m], n0 + i, ruled) : 0ull,
-                             j < rows ? row_key(res[j * M + m], n0 + j, ruled) : 0ull};
-                run = warp_insert64(run, c, lane);
-            }
+    // A row goes to `share` warps, one where there are rows for all of them or few keys.
+    uint64_t(*lists)[64] = reinterpret_cast<uint64_t(*)[64]>(sb);  // (the ring is free now)
+    uint64_t *pending = reinterpret_cast<uint64_t *>(sb) + (kWarps + warp) * 64;
+    const int share = max(1, min(kWarps / M, (rows + 127) / 128));
+    const int part = warp % share;
+    for (int m = warp / share; m < M; m += kWarps / share) {
+        const int i0 = (int)((long long)rows * part / share), i1 = (int)((long long)rows * (part + 1) / share);
+        const Key2 run = warp_best64(res + m * a.ldr, n0, i0, i1, a.k, ruled, pending, lane);
+        if (share == 1) {
+            uint64_t *out = a.ws + ((size_t)m * gridDim.x + blockIdx.x) * a.k;
+            if (lane < a.k) out[lane] = run.a;
+            if (32 + lane < a.k) out[32 + lane] = run.b;
+        } else {  // (M <= 5: every row has its warps, and each warp one row)
             lists[warp][lane] = run.a;
             lists[warp][32 + lane] = run.b;
-            block_merge_lists(lists, kWarps);
-            for (int i = tid; i < a.k; i += kThreads) out[i] = lists[0][i];
-            __syncthreads();
         }
+    }
+    if (share == 1) return;
+    const int m = warp / share;
+    for (int span = 1; span < share; span <<= 1) {
+        __syncthreads();
+        if (m < M && part % (2 * span) == 0 && part + span < share) {
+            const Key2 run = warp_merge64(Key2{lists[warp][lane], lists[warp][32 + lane]},
+                                          Key2{lists[warp + span][lane], lists[warp + span][32 + lane]}, lane);
+            lists[warp][lane] = run.a;
+            lists[warp][32 + lane] = run.b;
+        }
+    }
+    if (m < M && part == 0) {
+        __syncwarp();
+        uint64_t *out = a.ws + ((size_t)m * gridDim.x + blockIdx.x) * a.k;
+        for (int i = lane; i < a.k; i += 32) out[i] = lists[warp][i];
     }
 }
 
@@ -1040,8 +1105,8 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     a.stages = stages;
     size_t off = (size_t)stages * a.stage_bytes;
     if (lmhead) {
-        // After the main loop the ring holds the selection keys.
-        const size_t need = (size_t)(kThreads / 32) * 64 * 8;  // per-warp lists of the selection
+        // After the main loop the ring holds two lists of keys for each warp.
+        const size_t need = (size_t)(kLmThreads / 32) * 2 * 64 * 8;
         if (off < need) off = align_up(need, 1024);
     }
     a.off_xf = (uint32_t)off;
@@ -1053,7 +1118,12 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     a.defer = (force_defer || red_all <= 32 * 1024) ? 1 : 0;
     off = align_up(off + (a.defer ? red_all : (size_t)2 * kConsumerWarps * kTileRows * M * 4), 16);
     a.off_res = (uint32_t)off;
-    if (lmhead || a.C > 1) off = align_up(off + (size_t)tpc * kTileRows * M * 4, 16);
+    a.ldr = tpc * kTileRows + 1;
+    if (lmhead) off = align_up(off + (size_t)a.ldr * M * 4, 16);
+    else if (a.C > 1) off = align_up(off + (size_t)tpc * kTileRows * M * 4, 16);
+    a.off_rules = (uint32_t)off;
+    if (lmhead && a.rules.on) off += rules_bytes(M);
+    off = align_up(off, 16);
     a.off_bar = (uint32_t)off;
     off += 16 * stages + 16;
     p.smem = off + 1024;  // alignment slack
@@ -1230,7 +1300,7 @@ int launch_stream(const StreamPlan &p, const uint32_t *qw, bool overlap, cudaStr
     if (!ensure_smem(reinterpret_cast<const void *>(kern), p.smem)) return W4_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(LM ? kLmThreads : kThreads, 1, 1);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -1305,6 +1375,7 @@ int lmhead_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const
                 const WFmt &f, int k, int32_t *idx, float *val, uint64_t *ws, size_t ws_bytes, unsigned flags,
                 void *stream, const Rules &rules = Rules{}) {
     StreamPlan p;
+    p.a.rules = rules;
     if (!plan_stream(p, M, N, K, f, true, k)) return W4_ERR_SHAPE;
     const int G = p.grid;
     if ((long long)G > lm_max_blocks(N, k)) return W4_ERR_SHAPE;
@@ -1314,7 +1385,6 @@ int lmhead_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const
     p.a.bi = bi;
     p.a.y = nullptr;
     p.a.ws = ws;
-    p.a.rules = rules;
     const bool ov = (flags & W4A16_OVERLAP_PREVIOUS) != 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int st = launch_stream_any<true>(p, qw, ov, s);

@@ -428,14 +428,23 @@ typedef struct {
  *            Many rows of one adapter are fastest where they lie near each other
  *            (rows are gathered within blocks of up to 1024)
  *   M        >= 0
+ *   workspace  device buffer of at least f16_lora_workspace_bytes bytes, 16-byte
+ *              aligned; contents on entry are ignored.  Calls that may run
+ *              concurrently need separate ones.
  *   Sums are fp32 over exact products; x A^T is carried on in two binary16 numbers
  *   a value (2^-22 of the row's largest), and out is rounded once.  Results are
  *   deterministic; a row is not touched by what the others hold (NaN and infinities
  *   included), but its sums may be taken in another order in another mix of rows.
- * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_DEVICE, W4_ERR_LAUNCH.
+ * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_WORKSPACE,
+ * W4_ERR_DEVICE, W4_ERR_LAUNCH.
  */
 W4A16_API int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int64_t y_row, uint16_t *out,
-                       int64_t out_row, const f16_adapters *adapters, const int32_t *ids, int M, void *stream);
+                       int64_t out_row, const f16_adapters *adapters, const int32_t *ids, int M, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* Workspace bytes for f16_lora (0 if the sizes are invalid).  Depends only on the
+ * adapters' sizes and M (not monotonic in M: ask for the M of the call). */
+W4A16_API size_t f16_lora_workspace_bytes(const f16_adapters *adapters, int M);
 
 /*
  * Attention with a paged key/value cache: what a decoder layer does between

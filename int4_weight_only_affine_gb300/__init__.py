@@ -28,7 +28,8 @@ import os
 import torch
 
 __all__ = ["OVERLAP_PREVIOUS", "w4_gemv", "w4_gemv_seq", "GemvList", "seq_workspace", "seq_workspace_bytes", "GemvOp",
-           "lm_head_argmax_topk", "lm_head_workspace_bytes", "Adapters", "f16_lora", "LogitRules", "TokenCounts", "token_counts_add", "w4_dequant_f16", "f16_gemm", "w4_gemm",
+           "lm_head_argmax_topk", "lm_head_workspace_bytes", "Adapters", "f16_lora", "lora_workspace",
+           "lora_workspace_bytes", "LogitRules", "TokenCounts", "token_counts_add", "w4_dequant_f16", "f16_gemm", "w4_gemm",
            "w4_gemm_workspace", "w4_gemm_workspace_bytes", "device_status", "W4A16Error", "LIB_PATH", "lib",
            "HeadNorm", "KVBatch", "KVCache", "Rope", "attention_workspace", "attention_workspace_bytes", "f16_attention",
            "f16_kv_append", "f16_rope", "rope_turns"]
@@ -340,5 +341,5 @@ def device_status() -> int:
 
 from .attention import (HeadNorm, KVBatch, KVCache, Rope, attention_workspace, attention_workspace_bytes,  # noqa: E402
                         f16_attention, f16_kv_append, f16_rope, rope_turns)
-from .adapters import Adapters, f16_lora  # noqa: E402
+from .adapters import Adapters, f16_lora, lora_workspace, lora_workspace_bytes  # noqa: E402
 from .rules import LogitRules, TokenCounts, token_counts_add  # noqa: E402

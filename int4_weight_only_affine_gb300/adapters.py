@@ -7,13 +7,14 @@ f16_lora (``include/w4a16.h``)::
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
 
 from . import _check, _dev, _stream, lib
 
-__all__ = ["Adapters", "f16_lora"]
+__all__ = ["Adapters", "f16_lora", "lora_workspace", "lora_workspace_bytes"]
 
 _P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
 
@@ -24,7 +25,9 @@ class _Adapters(ctypes.Structure):
                 ("columns", ctypes.c_int32 * 4)]
 
 
-lib.f16_lora.argtypes = [_P, _L, _P, _L, _P, _L, _P, _P, _I, _P]
+lib.f16_lora.argtypes = [_P, _L, _P, _L, _P, _L, _P, _P, _I, _P, ctypes.c_size_t, _P]
+lib.f16_lora_workspace_bytes.argtypes = [_P, _I]
+lib.f16_lora_workspace_bytes.restype = ctypes.c_size_t
 
 
 def _half(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -80,10 +83,20 @@ class Adapters:
         self.ptr = ctypes.addressof(self.struct)
 
 
+def lora_workspace_bytes(adapters: Adapters, rows: int) -> int:
+    return int(lib.f16_lora_workspace_bytes(adapters.ptr, rows))
+
+
+def lora_workspace(adapters: Adapters, rows: int) -> torch.Tensor:
+    """A workspace for f16_lora with this many rows, for calls that do not overlap."""
+    return torch.empty(max(lora_workspace_bytes(adapters, rows), 16), dtype=torch.uint8, device=adapters.a.device)
+
+
 def f16_lora(x: torch.Tensor, adapters: Adapters, ids: torch.Tensor, y: torch.Tensor, out: torch.Tensor | None = None,
-             stream=None) -> torch.Tensor:
+             stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """out[m] = y[m] + scale[a] * (x[m] @ A_a.T) @ B_a.T with a = ids[m] (int32; negative: y[m]).
-    x float16 [rows][K], y and out [rows][N], any row strides that are multiples of 8; out is y itself when None."""
+    x float16 [rows][K], y and out [rows][N], any row strides that are multiples of 8; out is y itself when None.
+    workspace: from lora_workspace; a fresh one is made when None."""
     px, xs = _rows(x, "x")
     py, ys = _rows(y, "y")
     po, os = (py, ys) if out is None else _rows(out, "out")
@@ -92,6 +105,9 @@ def f16_lora(x: torch.Tensor, adapters: Adapters, ids: torch.Tensor, y: torch.Te
         raise ValueError(f"x must be [{m}][{adapters.K}], y and out [{m}][{adapters.N}]")
     if ids.numel() != m:
         raise ValueError("ids must be [rows]")
+    if workspace is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # (the memory is that stream's)
+            workspace = lora_workspace(adapters, m)
     _check("f16_lora", lib.f16_lora(px, xs, py, ys, po, os, adapters.ptr, _dev(ids, "ids", (torch.int32,)), m,
-                                    _stream(stream)))
+                                    _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(), _stream(stream)))
     return y if out is None else out

@@ -1458,7 +1458,7 @@ int dequant_wait_flag();  // dequant.cu
 int gemv_bad_index();     // gemv.cu
 int rope_bad_index();     // rope.cu
 int counts_bad_index();   // counts.cu
-int lora_bad_index();     // lora.cu
+int lora_status();        // lora.cu: as attn_status
 int attn_status();        // attn.cu: bit 0 an expired wait, bit 1 a bad index
 
 // Reads and clears this translation unit's expired-wait record.
@@ -1476,11 +1476,11 @@ static int gemm_wait_flag() {
 extern "C" int w4a16_device_status(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return W4_ERR_LAUNCH;
     const int a = gemm_wait_flag(), b = gemv_wait_flag(), c = dequant_wait_flag();
-    const int i = gemv_bad_index(), r = rope_bad_index(), t = counts_bad_index(), l = lora_bad_index();
+    const int i = gemv_bad_index(), r = rope_bad_index(), t = counts_bad_index(), l = lora_status();
     const int at = attn_status();
     if (a < 0 || b < 0 || c < 0 || i < 0 || r < 0 || t < 0 || l < 0 || at < 0) return W4_ERR_LAUNCH;
-    if (a || b || c || (at & 1)) return W4_ERR_TIMEOUT;
-    return (i || r || t || l || (at & 2)) ? W4_ERR_INDEX : W4A16_OK;
+    if (a || b || c || ((at | l) & 1)) return W4_ERR_TIMEOUT;
+    return (i || r || t || ((at | l) & 2)) ? W4_ERR_INDEX : W4A16_OK;
 }
 
 extern "C" const char *w4a16_status_string(int status) {

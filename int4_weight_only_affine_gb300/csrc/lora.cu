@@ -5,79 +5,71 @@
 //
 // What bounds it: y is read and out written once, x read once, each adapter in
 // use read once; the products (2 r flops an element of x and of y) are small
-// beside that up to ranks of about 64.  So the rows of one adapter are gathered,
-// h stays on the chip, and one launch does everything:
-//  * A cluster of up to 8 CTAs takes a unit: up to `tile` rows of one adapter, and
-//    all or one of several parts of the columns.  Its CTAs split K for h (shrink),
-//    add their partial sums through distributed shared memory (exchange), and split
-//    the columns for the second product (expand), so nothing passes through memory
-//    and no CTA waits for one outside its cluster.  Parts of one item each make h
-//    themselves: A comes from L2 then, and h is far less work than the columns.
-//  * Which rows belong to which adapter is found by every CTA itself, for a scope
-//    of up to 1024 rows: a histogram of ids in shared memory, a prefix sum
-//    over the adapters, and the rows of the unit in order by a second one (up to 32
-//    rows: matches within a warp).  Any mix of ids is served.  The CTAs of a cluster
-//    read a share of the ids each and take the rest from one another, so that they
-//    agree on their units, and meet at the same cluster barriers, even if another
-//    stream wrote ids meanwhile.
-//  * Both products are mma.sync m16n8k16.  With ranks of 16 to 64 a tcgen05 tile
-//    would be filled to an eighth, and the bytes are the bound, not the tensor rate.
-//    The order of k inside a product is free, so lane t of a quad takes 16 contiguous
-//    bytes of a row and treats them as the k indexes of two products: fragments
-//    are single 16-byte loads.
-//  * shrink: x and A pass through a ring of shared-memory stages by cp.async, rows
-//    64 bytes longer than their data, so that the fragments' loads meet no bank twice.
-//  * expand holds B's fragments of 32 columns in registers over all row tiles of the
-//    unit, with ranks up to 32 the
-//    next columns' on the way.  The order of columns inside the four
-//    products is chosen so that a lane holds 8 neighbouring ones of two rows; its
-//    16 bytes of y come ahead through a ring of its own by cp.async.
+// beside that up to ranks of about 64.  The rows of one adapter are gathered into
+// items of up to `tile` rows, and two kernels share the work:
+//  * shrink: a CTA takes an item and one of `splits` parts of K, and writes its
+//    share of h, fp32, into the workspace.  x and A pass through a ring of stages of
+//    64 k by TMA (A's rows as a box, x's as a box where they lie in a row, else
+//    gathered four to a copy) and are multiplied by tcgen05 (M = 128 rows of x, of
+//    which the item fills some, N = all ranks of all slices) into tensor memory, so
+//    that no warp touches an operand.
+//  * expand: a CTA takes an item and one of `parts` parts of the columns.  It is a
+//    programmatic dependent of shrink, which releases it once it has waited for the
+//    kernel before itself: so expand sorts the rows and asks for y and B while shrink
+//    still runs, and waits for it only before it adds up h.
+// Which rows belong to which adapter is found by every CTA itself, for a scope of up
+// to 1024 rows: a histogram of ids in shared memory, a prefix sum over the adapters,
+// and the rows of the item in order by a second one (up to 32 rows: matches within a
+// warp).  Any mix of ids is served.
+//
+// expand's products are mma.sync m16n8k16 (490 TFLOP/s measured; the second product
+// needs half of that where y streams at 6 TB/s and the rank is 64).  The order of k
+// inside a product is free, so lane t of a quad takes 16 contiguous bytes of a row
+// and treats them as the k indexes of two products: fragments are single 16-byte
+// loads.  B's fragments of 32 columns stay in registers over all rows of the item,
+// with ranks up to 32 the next columns' on the way.  The order of columns inside the
+// four products is chosen so that a lane holds 8 neighbouring ones of two rows; its 16
+// bytes of y come ahead through a ring of its own by cp.async.
+//
 // Numerics: x and A are binary16, h and the sums fp32 (K in a fixed order).  h is
 // multiplied by s_a, scaled by a power of two to the row's largest in
 // [2^12, 2^13), and split into two binary16 numbers hi + lo: the second product
 // then sees h to 2^-22 of the row's largest instead of 2^-11, for one product
 // more.  y + delta is rounded once.
-#include <cooperative_groups.h>
-
-#include <mutex>
-
 #include "common.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace w4a16 {
 namespace {
 
 constexpr int kThreads = 256, kWarps = 8;
-constexpr int kMaxCluster = 8;
 constexpr int kScope = 1024;        // rows whose ids a CTA sorts
 constexpr int kMaxAdapters = 4096;  // buckets of the histogram
 constexpr int kMaxSlices = 4;
 constexpr int kMaxRank = 128;
+constexpr int kMaxSplits = 8;
 constexpr int kColBlock = 32;  // columns of a warp's step
-constexpr int kPad = 64;       // bytes after a row of a stage
-constexpr int kSmemOfTwo = 105 * 1024, kSmemOfOne = 221 * 1024;  // dynamic shared memory of two CTAs on an SM, and of one
+constexpr int kStageK = 64;    // k of a stage of shrink's ring: rows of 128 bytes
+constexpr int kMostStages = 8;
+constexpr int kSmsOfPlan = 152;  // (the plan does not depend on the device, nor does a workspace's size)
 
 struct LoraArgs {
-    const uint16_t *x, *y, *a, *b;
+    const uint16_t *y, *b;
     uint16_t *out;
     const float *scale;
     const int32_t *ids;
-    long long x_row, y_row, out_row, a_adapter, b_adapter;
+    float *h;  // [splits][M][slices * rank]
+    long long y_row, out_row, b_adapter;
     int M, K, N, adapters, rank, slices;
     int col[kMaxSlices + 1];    // first column of each slice, N at the end
     int block[kMaxSlices + 1];  // column blocks before each slice
-    int scope, clusters;        // rows of a scope, clusters to a scope
-    int tile;                   // rows of a unit: 64 or 32
-    int parts;                  // most parts of an item's columns
+    int scope;                  // rows of a scope
+    int tile;                   // rows of an item: 64 or 32
+    int ctas;                   // of a scope, in the kernel that is launched
+    int shrinkers;              // of them in shrink
+    int splits, parts;          // most parts of K, and of an item's columns
     int copy;                   // out is not y: rows without an adapter are copied
-    int room, pool;             // bytes of shared memory for shrink's ring; behind the fragments for expand's rings
-    uint32_t off_h, off_red, off_hist;  // byte offsets in shared memory (ring and fragments at 0)
-};
-
-template <int N>
-struct Int {
-    static constexpr int value = N;
+    int boxes, box_rows;        // boxes of A's rows, of at most 256, and their rows (whole groups of 8)
+    int room, pool;             // bytes of shared memory for shrink's ring; for expand's rings
 };
 
 __device__ __forceinline__ uint32_t pack(float a, float b) {
@@ -93,19 +85,24 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint16_t *p, bool in)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(in ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Until at most `left` of this thread's newest groups are on the way.
+// Until at most `left` (0 .. 3) of this thread's newest groups are on the way.
 __device__ __forceinline__ void copies_wait(int left) {
     switch (left) {
         case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
         case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
         case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
     }
 }
-constexpr int kMostStages = 8;  // (copies_wait's most and two)
+// 64 columns of four rows of a 2-D map whose box is one row high.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int col, int r0, int r1, int r2, int r3,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(col), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+        : "memory");
+}
 
 // Exclusive prefix sum of v over the block's threads; total gets the sum.
 __device__ __forceinline__ int block_scan(int v, int *scratch, int &total) {
@@ -129,151 +126,259 @@ __device__ __forceinline__ int block_scan(int v, int *scratch, int &total) {
     return before + s - v;
 }
 
-// The products of a warp with one stage of shrink: MT tiles of 16 ranks from arow
-// on, NT tiles of 8 rows of x from xrow on, the 32-k blocks b = first, first + step, ...
-// No branch stands between loads and products, so that they overlap; what rows past
-// the last hold does not matter, as each goes into sums of its own.
-template <int MT, int NT, int MAX>
-__device__ __forceinline__ void stage_products(float (&acc)[MAX][4][4], uint32_t arow, uint32_t xrow, int pitch,
-                                               int first, int blocks, int step) {
-    for (int b = first; b < blocks; b += step) {
-        uint4 x[NT], u[MT], l[MT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) x[i] = lds128(xrow + 8 * i * pitch + 64 * b);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            u[m] = lds128(arow + 16 * m * pitch + 64 * b);
-            l[m] = lds128(arow + (16 * m + 8) * pitch + 64 * b);
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < NT; ++i) mma_16816(acc[m][i], u[m].x, l[m].x, u[m].y, l[m].y, x[i].x, x[i].y);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < NT; ++i) mma_16816(acc[m][i], u[m].z, l[m].z, u[m].w, l[m].w, x[i].z, x[i].w);
-    }
-}
+// The items of a scope: up to `tile` rows of one bucket (an adapter, or none).
+struct Sorter {
+    int *scratch;   // kWarps ints of shared memory
+    int *hist;      // [adapters + 1]: rows of each bucket
+    int id[kScope / kThreads];  // buckets of this thread's rows, in order; -1 past the scope
+    int items, first, mine;     // of all; before this thread's buckets; in them
+    unsigned leaders, same;     // of few rows: the first of each bucket; the lane's equals
+    int row0, nrow, per;
+    bool few;
 
-// How the 8 warps share a unit of n rows and `tiles` tiles of 16 ranks: groups of 32
-// rows, groups of mt rank tiles, and groups of the 32-k blocks of a stage, whose sums
-// are added at the end.  wide: the rank tiles of a group that are computed (sums of
-// rank 128 come in 2, 4 and 6); held: rows of a stage, A's and then x's from xrow on.
-// (Rows past the last of either are not filled, but what a warp reads ends inside.)
-struct Shape {
-    int rgroups, mgroups, kgroups, mt, wide, xrow, held;
-};
-__host__ __device__ inline Shape shape_of(int n, int tiles, int rk) {
-    Shape s;
-    s.rgroups = n > 32 ? 2 : 1;
-    s.mgroups = tiles > 8 && n <= 32 ? 8 : tiles > 2 ? 4 : 2;
-    s.kgroups = kWarps / (s.rgroups * s.mgroups);
-    s.mt = (tiles + s.mgroups - 1) / s.mgroups;
-    s.wide = rk < 128 ? s.mt : s.mt <= 2 ? 2 : s.mt <= 4 ? 4 : 6;
-    s.xrow = 16 * tiles;
-    const int a = 16 * ((tiles - 1) / s.mt * s.mt + s.wide), x = s.xrow + (n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64);
-    s.held = a > x ? a : x;
-    return s;
-}
+    // Parts of K: as many as give each CTA of shrink one (both kernels come to the same).
+    __device__ __forceinline__ int splits(const LoraArgs &p) const {
+        return max(1, min(p.splits, p.shrinkers / max(items, 1)));
+    }
 
-// Shrink: h[row][f], f = slice * rank + r, the sums over the CTA's share of K, for
-// the unit's n rows.  The A of all slices are one list of slices * rank rows.
-template <int RK>
-__device__ __forceinline__ void shrink(const LoraArgs &p, const uint16_t *a, const int *rows, int n, int crank,
-                                       int csize, uint8_t *smem) {
-    constexpr int MT = RK == 16 ? 1 : RK == 32 ? 2 : RK == 64 ? 4 : 6;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int F = p.slices * p.rank, tiles = (F + 15) / 16;
-    const Shape sh = shape_of(n, tiles, RK);
-    const int mt = sh.mt, kgroups = sh.kgroups, xrow = sh.xrow, held = sh.held;
-    const int rg = warp % sh.rgroups, mg = warp / sh.rgroups % sh.mgroups, kg = warp / (sh.rgroups * sh.mgroups);
-    const int kb = (p.K + 31) / 32;
-    const int k0 = 32 * (int)((long long)kb * crank / csize);
-    const int k1 = min(p.K, 32 * (int)((long long)kb * (crank + 1) / csize));
-    // Stages of 128 k, or of 64 where the room is short.
-    const int log = p.room >= 3 * held * (256 + kPad) ? 4 : 3;  // 16-byte pieces of a row
-    const int kc = 8 << log, pitch = 2 * kc + kPad, stage = held * pitch;
-    const int stages = min(kMostStages, p.room / stage);  // at least 2
-    const int chunks = (k1 - k0 + kc - 1) / kc;
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
-    const int piece = threadIdx.x & ((1 << log) - 1), first = threadIdx.x >> log, step = kThreads >> log;
-    auto copy_stage = [&](int c, uint32_t slot) {
-        const int k = k0 + c * kc + 8 * piece;
-        const bool in = k < k1;
-        uint32_t dst = slot + first * pitch + 16 * piece;
-        const uint16_t *src = a + (long long)first * p.K + (in ? k : 0);
-        for (int r = first; r < F; r += step, dst += step * pitch, src += (long long)step * p.K) copy16(dst, src, in);
-        dst = slot + (xrow + first) * pitch + 16 * piece;
-        for (int r = first; r < n; r += step, dst += step * pitch) copy16(dst, p.x + rows[r] * p.x_row + (in ? k : 0), in);
-    };
-    uint32_t fill = base, at = base;  // the slot that is filled next, and the one that is read
-    const uint32_t end = base + stages * stage;
-    for (int c = 0; c < stages - 1; ++c, fill += stage) {
-        if (c < chunks) copy_stage(c, fill);
-        copies_commit();
-    }
-    float acc[MT][4][4] = {};
-    const int blocks = mg * mt < tiles ? kc / 32 : 0;  // (a warp without a tile has none)
-    const int arow = (16 * mg * mt + g) * pitch + 16 * t, xat = (xrow + 32 * rg + g) * pitch + 16 * t;
-    auto run = [&](auto mts, auto nts) {
-        constexpr int A = decltype(mts)::value, X = decltype(nts)::value;
-        for (int c = 0; c < chunks; ++c) {
-            copies_wait(stages - 2);
-            __syncthreads();  // stage c has landed, and every warp is done with the one that is filled next
-            if (c + stages - 1 < chunks) copy_stage(c + stages - 1, fill);
-            copies_commit();
-            fill = fill + stage == end ? base : fill + stage;
-            stage_products<A, X>(acc, at + arow, at + xat, pitch, kg, blocks, kgroups);
-            at = at + stage == end ? base : at + stage;
+    __device__ __forceinline__ static bool counts(const LoraArgs &p, int b) { return b < p.adapters || (b == p.adapters && p.copy); }
+
+    // Called by every thread of the block, at its start.
+    __device__ __forceinline__ void begin(const LoraArgs &p, int scope) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        row0 = scope * p.scope;
+        nrow = min(p.scope, p.M - row0);
+        few = nrow <= 32;
+        per = (p.adapters + kThreads) / kThreads;
+        const auto bucket = [&](int r) {
+            if (r >= nrow) return -1;
+            const int v = __ldg(p.ids + row0 + r);
+            if (v >= p.adapters) atomicExch(&g_bad_index, 1);
+            return v < 0 || v >= p.adapters ? p.adapters : v;
+        };
+        if (few) {
+            // Every warp knows all rows: an item to each bucket, in the order of their first rows.
+            id[0] = bucket(lane);
+            same = __match_any_sync(~0u, id[0]);
+            leaders = __ballot_sync(~0u, id[0] >= 0 && counts(p, id[0]) && (same & ((1u << lane) - 1u)) == 0u);
+            items = __popc(leaders);
+            return;
         }
-    };
-    auto for_rows = [&](auto mts) {
-        if (n <= 8) run(mts, Int<1>());
-        else if (n <= 16) run(mts, Int<2>());
-        else run(mts, Int<4>());
-    };
-    if constexpr (MT == 1) {
-        for_rows(Int<1>());
-    } else if constexpr (MT == 2) {
-        if (mt == 1) for_rows(Int<1>());
-        else for_rows(Int<2>());
-    } else if constexpr (MT == 4) {
-        if (mt == 1) for_rows(Int<1>());
-        else if (mt == 2) for_rows(Int<2>());
-        else if (mt == 3) for_rows(Int<3>());
-        else for_rows(Int<4>());
-    } else {
-        if (sh.wide == 2) for_rows(Int<2>());
-        else if (sh.wide == 4) for_rows(Int<4>());
-        else for_rows(Int<6>());
+        constexpr int kMine = kScope / kThreads;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) id[i] = bucket(tid * kMine + i);
+        for (int i = tid; i <= p.adapters; i += kThreads) hist[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            if (id[i] >= 0) atomicAdd(hist + id[i], 1);
+        __syncthreads();
+        mine = 0;
+        for (int i = 0; i < per; ++i) {  // this thread's buckets are in a row
+            const int b = tid * per + i;
+            if (counts(p, b)) mine += (hist[b] + p.tile - 1) / p.tile;
+        }
+        first = block_scan(mine, scratch, items);
     }
-    copies_wait(0);
-    __syncthreads();  // the ring is free: h and the warps' sums take its place
-    float *h = reinterpret_cast<float *>(smem + p.off_h);
-    float *mine = kgroups == 1 ? h : reinterpret_cast<float *>(smem + p.off_red) + kg * n * F;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (m >= mt) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (32 * rg + 8 * i >= n) break;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = 32 * rg + 8 * i + 2 * t + (e & 1), f = 16 * (mg * mt + m) + g + 8 * (e >> 1);
-                if (row < n && f < F) mine[row * F + f] = acc[m][i][e];
+
+    // The rows and the bucket of an item; called by every thread, ends with a barrier.
+    // unit: 3 ints of shared memory.
+    __device__ __forceinline__ int item(const LoraArgs &p, int item, int *rows, int *unit, int &n) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        if (few) {
+            unsigned left = leaders;
+            for (int i = 0; i < item; ++i) left &= left - 1u;
+            const int lead = __ffs(left) - 1;
+            const int bucket = __shfl_sync(~0u, id[0], lead);
+            const unsigned its = __shfl_sync(~0u, same, lead);
+            n = __popc(its);
+            if (tid < 32 && its >> lane & 1u) rows[__popc(its & ((1u << lane) - 1u))] = row0 + lane;
+            __syncthreads();
+            return bucket;
+        }
+        constexpr int kMine = kScope / kThreads;
+        if (item >= first && item < first + mine) {
+            int at = first;
+            for (int i = 0; i < per; ++i) {
+                const int b = tid * per + i;
+                if (counts(p, b)) {
+                    const int c = (hist[b] + p.tile - 1) / p.tile;
+                    if (item >= at && item < at + c) {
+                        unit[0] = b;
+                        unit[1] = (item - at) * p.tile;
+                        unit[2] = min(p.tile, hist[b] - (item - at) * p.tile);
+                    }
+                    at += c;
+                }
             }
         }
+        __syncthreads();
+        const int bucket = unit[0];
+        n = unit[2];
+        int hits = 0, total;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) hits += id[i] == bucket;
+        int at = block_scan(hits, scratch, total) - unit[1];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            if (id[i] == bucket) {
+                if (at >= 0 && at < n) rows[at] = row0 + tid * kMine + i;
+                ++at;
+            }
+        __syncthreads();
+        return bucket;
     }
-    if (kgroups == 1) return;
-    __syncthreads();
-    const float *red = reinterpret_cast<const float *>(smem + p.off_red);
-    for (int e = threadIdx.x; e < n * F; e += kThreads) {
-        float v = 0.f;
-        for (int q = 0; q < kgroups; ++q) v += red[q * n * F + e];
-        h[e] = v;
-    }
+};
+
+// ---- shrink ----
+
+// Shared-memory operand of 128-byte rows, K-major, 128-byte swizzle (8 rows to 1024 bytes).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
 }
+// D[tmem] (+)= A B^T, M = 128, N = n, K = 16, binary16 operands, fp32 sums.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, int n, bool add) {
+    const uint32_t idesc = 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add));
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 8 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(addr));
+}
+
+__host__ __device__ constexpr int tmem_columns(int ranks) {
+    return ranks <= 32 ? 32 : ranks <= 64 ? 64 : ranks <= 128 ? 128 : ranks <= 256 ? 256 : 512;
+}
+
+__global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant__ CUtensorMap amap,
+                                                          const __grid_constant__ CUtensorMap xmap,
+                                                          const __grid_constant__ CUtensorMap xbox,
+                                                          const __grid_constant__ LoraArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-(uint32_t)__cvta_generic_to_shared(smem_raw) & 1023u);
+    __shared__ int scratch[kWarps], rows[64], unit[3];
+    __shared__ __align__(8) uint64_t bars[2 * kMostStages + 1];
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_flag;
+    volatile int *abort = &abort_flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t full = (uint32_t)__cvta_generic_to_shared(bars), empty = full + 8 * kMostStages,
+                   done = full + 16 * kMostStages;
+    const int F = p.slices * p.rank, F16 = (F + 15) / 16 * 16, columns = tmem_columns(F16);
+    if (tid == 0) {
+        for (int i = 0; i < 2 * kMostStages + 1; ++i) mbar_init(full + 8 * i, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&amap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&xbox) : "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(&tmem_at)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_wait();
+    pdl_launch_dependents();  // (expand may start: what it reads before its own wait is complete)
+    Sorter sorter;
+    sorter.scratch = scratch;
+    sorter.hist = reinterpret_cast<int *>(smem + p.room);
+    sorter.begin(p, blockIdx.x / p.ctas);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_at;
+    const int kb = (p.K + kStageK - 1) / kStageK, splits = sorter.splits(p);
+    uint32_t stage_no = 0, units = 0;  // stages and items so far: the barriers' phases
+    for (int u = blockIdx.x % p.ctas; u < sorter.items * splits; u += p.ctas) {
+        int n;
+        const int split = u % splits, bucket = sorter.item(p, u / splits, rows, unit, n);
+        const int c0 = (int)((long long)kb * split / splits), chunks = (int)((long long)kb * (split + 1) / splits) - c0;
+        if (bucket == p.adapters) continue;  // (alike for all threads; rows is written again after a barrier)
+        // A stage: A's rows, then x's; the products read 128 rows of x, what lies behind the
+        // item's goes into rows of the sums that nobody reads.
+        const int xrow = F16, stage = (xrow + (n + 7) / 8 * 8) * 128;
+        const int stages = min(kMostStages, (p.room - 128 * 128) / stage);
+        const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+        const bool box = n > 16 && rows[n - 1] - rows[0] == n - 1;
+        const uint32_t bytes = p.boxes * p.box_rows * 128 + (box ? (n + 7) / 8 * 8 : (n + 3) / 4 * 4) * 128;
+        if (warp == 0) {
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t i = stage_no + c, b = i % kMostStages, at = base + c % stages * stage;
+                // (A slot is free when the stage that last lay in it was read, `stages` ago.)
+                if (c >= stages) {
+                    const uint32_t last = i - stages;
+                    mbar_wait(empty + 8 * (last % kMostStages), last / kMostStages & 1, abort);
+                }
+                const int k = (c0 + c) * kStageK;
+                if (lane == 0) mbar_expect_tx(full + 8 * b, bytes);
+                __syncwarp();
+                if (lane >= 32 - p.boxes) {
+                    const int row = (lane - (32 - p.boxes)) * p.box_rows;  // (rows past F are zero, and end before x's)
+                    tma_load_3d(at + row * 128, &amap, k, row, bucket, full + 8 * b);
+                } else if (box) {  // boxes of 8 rows
+                    if (8 * lane < n) tma_load_2d(at + (xrow + 8 * lane) * 128, &xbox, k, rows[0] + 8 * lane, full + 8 * b);
+                } else if (4 * lane < n) {
+                    const int end = n - 1;
+                    tma_gather4(at + (xrow + 4 * lane) * 128, &xmap, k, rows[4 * lane], rows[min(4 * lane + 1, end)],
+                                rows[min(4 * lane + 2, end)], rows[min(4 * lane + 3, end)], full + 8 * b);
+                }
+            }
+        } else if (warp == 1 && lane == 0) {
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t i = stage_no + c, b = i % kMostStages, at = base + c % stages * stage;
+                if (!mbar_wait(full + 8 * b, i / kMostStages & 1, abort)) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+                for (int k = 0; k < kStageK / 16; ++k) {
+                    const uint64_t x = operand_desc(at + xrow * 128 + 32 * k), a = operand_desc(at + 32 * k);
+                    mma_f16(tmem, x, a, min(F16, 256), c > 0 || k > 0);
+                    if (F16 > 256) mma_f16(tmem + 256, x, operand_desc(at + 256 * 128 + 32 * k), F16 - 256, c > 0 || k > 0);
+                }
+                mma_commit(empty + 8 * b);
+            }
+            mma_commit(done);
+        }
+        __syncwarp();
+        // Every stage is read before the next item's copies come (the products are in order).
+        const bool ok = mbar_wait(done, units & 1, abort);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (warp < 2) {
+            const int r = 32 * warp + lane;
+            float *dst = p.h + ((long long)split * p.M + (r < n ? rows[r] : 0)) * F;
+            for (int f = 0; f < F; f += 8) {
+                float v[8];
+                tmem_load8(tmem + ((uint32_t)(32 * warp) << 16) + f, v);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                if (r < n && ok) {
+                    float4 *q = reinterpret_cast<float4 *>(dst + f);
+                    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+                }
+            }
+        }
+        stage_no += chunks;  // (at least one: splits are of four stages or more)
+        ++units;
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncthreads();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    __syncthreads();
+    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
+}
+
+// ---- expand ----
 
 // The fragments of the second product: for each row, block of 16 ranks and lane t
 // of a quad, the 16 bytes {hi, hi, lo, lo} of 4 ranks in a row, two to a word.  Rows
@@ -291,19 +396,15 @@ __device__ __forceinline__ int frag_at(int s, int r) {
     return ((s * (RK / 16) + k16) * 4 + t) * 16;
 }
 
-// Adds the cluster's partial sums of the rows that this CTA owns, scales and
-// splits them, and leaves the fragments with every CTA of the cluster.
+// Adds up the shares of h of the item's rows, scales and splits them into fragments.
 template <int RK>
-__device__ __forceinline__ void exchange(const LoraArgs &p, float scale, int n, uint8_t *smem, float *inv, int crank,
-                                         int csize) {
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();  // every CTA's sums are in place, and its fragments' room is free
-    float *h = reinterpret_cast<float *>(smem + p.off_h);
+__device__ __forceinline__ void gather_h(const LoraArgs &p, float scale, int splits, const int *rows, int n,
+                                         uint8_t *smem, float *inv) {
     const int R = p.slices * RK, F = p.slices * p.rank, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int pitch = frag_pitch<RK>(p.slices);
     constexpr int J = (kMaxSlices * RK + 127) / 128;  // groups of 4 ranks of a lane
     const float inf = __int_as_float(0x7F800000);
-    for (int row = crank + csize * warp; row < n; row += csize * kWarps) {
+    for (int row = warp; row < n; row += kWarps) {
         float4 v[J];
         float top = 0.f;
 #pragma unroll
@@ -311,14 +412,14 @@ __device__ __forceinline__ void exchange(const LoraArgs &p, float scale, int n, 
             const int r = 128 * j + 4 * lane;
             v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < R && r % RK < p.rank) {  // (ranks past the adapters' are zero)
-                const float *src = h + row * F + r / RK * p.rank + r % RK;
-                float4 part[kMaxCluster];
+                const float *src = p.h + (long long)rows[row] * F + r / RK * p.rank + r % RK;
+                float4 part[kMaxSplits];
 #pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c)
-                    if (c < csize) part[c] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(src, c));
+                for (int c = 0; c < kMaxSplits; ++c)  // (written by the kernel before: no read-only loads)
+                    if (c < splits) part[c] = __ldcg(reinterpret_cast<const float4 *>(src + (long long)c * p.M * F));
 #pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c)
-                    if (c < csize) {
+                for (int c = 0; c < kMaxSplits; ++c)
+                    if (c < splits) {
                         v[j].x += part[c].x;
                         v[j].y += part[c].y;
                         v[j].z += part[c].z;
@@ -339,7 +440,7 @@ __device__ __forceinline__ void exchange(const LoraArgs &p, float scale, int n, 
         const int e = (int)(__float_as_uint(top) >> 23) - 127;
         const int shift = e == 128 || top == 0.f ? 0 : 12 - max(e, -100);
         const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-        if (lane < csize) cluster.map_shared_rank(inv, lane)[row] = __uint_as_float((uint32_t)(127 - shift) << 23);
+        if (lane == 0) inv[row] = __uint_as_float((uint32_t)(127 - shift) << 23);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int r = 128 * j + 4 * lane;
@@ -348,14 +449,10 @@ __device__ __forceinline__ void exchange(const LoraArgs &p, float scale, int n, 
             const uint32_t h0 = pack(a, b), h1 = pack(c, d);
             const float2 f0 = unpack(h0), f1 = unpack(h1);
             const auto rest = [](float x, float hi) { return fabsf(x - hi) < 1e30f ? x - hi : 0.f; };  // (none of infinities)
-            const uint4 w = make_uint4(h0, h1, pack(rest(a, f0.x), rest(b, f0.y)), pack(rest(c, f1.x), rest(d, f1.y)));
-            uint8_t *dst = smem + row * pitch + frag_at<RK>(r / RK, r % RK);
-#pragma unroll
-            for (int q = 0; q < kMaxCluster; ++q)
-                if (q < csize) *reinterpret_cast<uint4 *>(cluster.map_shared_rank(dst, q)) = w;
+            *reinterpret_cast<uint4 *>(smem + row * pitch + frag_at<RK>(r / RK, r % RK)) =
+                make_uint4(h0, h1, pack(rest(a, f0.x), rest(b, f0.y)), pack(rest(c, f1.x), rest(d, f1.y)));
         }
     }
-    cluster.sync();
 }
 
 // Where a warp stands among the column blocks.
@@ -378,19 +475,20 @@ struct Columns {
     }
 };
 
-// Expand: out = y + h B^T over the CTA's column blocks [b0, b1) of the unit's rows,
-// whose addresses in y and out are yrow and orow.
-template <int RK>
+// out = y + h B^T over the CTA's column blocks [b0, b1) of the item's rows, whose
+// addresses in y and out are yrow and orow.  ready() is called by every thread once
+// the first copies are on their way; it leaves the fragments and inv in place.
+template <int RK, class Ready>
 __device__ __forceinline__ void expand(const LoraArgs &p, const uint16_t *bw, const uint16_t *const *yrow,
-                                       uint16_t *const *orow, int n, uint8_t *smem, const float *inv, int b0, int b1) {
+                                       uint16_t *const *orow, int n, uint8_t *smem, const float *inv, int b0, int b1,
+                                       Ready ready) {
     constexpr int KS = RK / 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    if (b0 + warp >= b1) return;
     const int tiles = (n + 15) / 16, pitch = frag_pitch<RK>(p.slices);
     const uint32_t frag = (uint32_t)__cvta_generic_to_shared(smem) + g * pitch + 16 * t;
     // The warp's ring of y: `depth` column blocks of up to 64 rows, 16 bytes a lane each.
     const int slot = tiles * 1024, depth = min(4, p.pool / (kWarps * slot));
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + p.off_h) + warp * depth * slot + lane * 16;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + p.tile * pitch) + warp * depth * slot + lane * 16;
     const uint32_t ring_end = ring + depth * slot;
     Columns ahead, own;
     own.start(p, b0 + warp);
@@ -430,8 +528,13 @@ __device__ __forceinline__ void expand(const LoraArgs &p, const uint16_t *bw, co
             }
         }
     };
-    load_b(own);
+    if (own.blk < b1) load_b(own);
     for (int d = 0; d < depth; ++d) copy_y(ring + d * slot);
+    ready();
+    if (own.blk >= b1) {
+        copies_wait(0);
+        return;
+    }
     uint32_t at = ring;
     while (true) {
         copies_wait(depth - 1);  // (a lane reads only what it copied itself)
@@ -500,193 +603,145 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &p, const int *rows, in
 }
 
 template <int RK>
-__global__ void __launch_bounds__(kThreads, RK == 128 ? 1 : 2) lora_kernel(const __grid_constant__ LoraArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_constant__ LoraArgs p) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int scratch[kWarps], rows[64], unit[3];
     __shared__ float inv[64];
     __shared__ const uint16_t *yrow[64];
     __shared__ uint16_t *orow[64];
-    __shared__ __align__(16) int own[kScope];  // buckets of this CTA's share of the rows, -1 past the scope
-    cg::cluster_group cluster = cg::this_cluster();
-    int *hist = reinterpret_cast<int *>(smem + p.off_hist);  // rows of each adapter; of none at the end
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int csize = (int)cluster.num_blocks(), crank = (int)cluster.block_rank(), cl = (int)blockIdx.x / csize;
-    const int scope = cl / p.clusters, q = cl % p.clusters;
-    const int row0 = scope * p.scope, nrow = min(p.scope, p.M - row0);
-    const int buckets = p.adapters + 1;
-    const bool few = nrow <= 32;
-    if (!few)
-        for (int i = tid; i < buckets; i += kThreads) hist[i] = 0;
-    pdl_wait();
-    const int share = few ? 32 : kScope / csize;  // (of few rows, the first CTA's count)
-    for (int i = tid; i < share; i += kThreads) {
-        const int r = crank * share + i;
-        int bucket = -1;
-        if (r < nrow) {
-            const int v = __ldg(p.ids + row0 + r);
-            if (v >= p.adapters) atomicExch(&g_bad_index, 1);
-            bucket = v < 0 || v >= p.adapters ? p.adapters : v;
-        }
-        own[i] = bucket;
-    }
-    cluster.sync();
-    constexpr int kMine = kScope / kThreads;
-    static_assert(kMine == 4, "a thread's rows come from one CTA in one read");
-    int id[kMine], mine = 0, first = 0, items;
-    unsigned leaders = 0, same = 0;
-    const int per = (buckets + kThreads - 1) / kThreads;
-    if (few) {
-        // Every warp knows all rows: an item to each bucket, in the order of their first rows.
-        id[0] = cluster.map_shared_rank(own, 0)[lane];
-        same = __match_any_sync(~0u, id[0]);
-        leaders = __ballot_sync(~0u, id[0] >= 0 && (id[0] < p.adapters || p.copy) && (same & ((1u << lane) - 1u)) == 0u);
-        items = __popc(leaders);
-    } else {
-        // Four rows a thread, in order.
-        const int4 four = *reinterpret_cast<const int4 *>(cluster.map_shared_rank(own, tid * kMine / share) +
-                                                          tid * kMine % share);
-        id[0] = four.x, id[1] = four.y, id[2] = four.z, id[3] = four.w;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i)
-            if (id[i] >= 0) atomicAdd(hist + id[i], 1);
-        __syncthreads();
-        // Items: up to `tile` rows of one bucket.  This thread's buckets are in a row.
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b < buckets && (b < p.adapters || p.copy)) mine += (hist[b] + p.tile - 1) / p.tile;
-        }
-        first = block_scan(mine, scratch, items);
-    }
-    const int parts = max(1, min(p.parts, p.clusters / max(items, 1)));
-    for (int u = q; u < items * parts; u += p.clusters) {
-        const int item = u % items, part = u / items;
-        int bucket, n;
-        if (few) {
-            unsigned left = leaders;
-            for (int i = 0; i < item; ++i) left &= left - 1u;
-            const int lead = __ffs(left) - 1;
-            bucket = __shfl_sync(~0u, id[0], lead);
-            const unsigned its = __shfl_sync(~0u, same, lead);
-            n = __popc(its);
-            if (tid < 32 && its >> lane & 1u) rows[__popc(its & ((1u << lane) - 1u))] = row0 + lane;
-            __syncthreads();
-        } else {
-            if (item >= first && item < first + mine) {
-                int at = first;
-                for (int i = 0; i < per; ++i) {
-                    const int b = tid * per + i;
-                    if (b < buckets && (b < p.adapters || p.copy)) {
-                        const int c = (hist[b] + p.tile - 1) / p.tile;
-                        if (item >= at && item < at + c) {
-                            unit[0] = b;
-                            unit[1] = (item - at) * p.tile;
-                            unit[2] = min(p.tile, hist[b] - (item - at) * p.tile);
-                        }
-                        at += c;
-                    }
-                }
-            }
-            __syncthreads();
-            bucket = unit[0], n = unit[2];
-            int hits = 0, total;
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) hits += id[i] == bucket;
-            int at = block_scan(hits, scratch, total) - unit[1];
-#pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                if (id[i] == bucket) {
-                    if (at >= 0 && at < n) rows[at] = row0 + tid * kMine + i;
-                    ++at;
-                }
-            __syncthreads();
-        }
-        const int cut = part * csize + crank, cuts = parts * csize;
+    const int tid = threadIdx.x;
+    Sorter sorter;
+    sorter.scratch = scratch;
+    sorter.hist = reinterpret_cast<int *>(smem + p.tile * frag_pitch<RK>(p.slices) + p.pool);
+    // (What is read before the wait was complete before shrink released this kernel.)
+    sorter.begin(p, blockIdx.x / p.ctas);
+    const int splits = sorter.splits(p), parts = max(1, min(p.parts, p.ctas / max(sorter.items, 1)));
+    bool waited = false;
+    for (int u = blockIdx.x % p.ctas; u < sorter.items * parts; u += p.ctas) {
+        int n;
+        const int part = u % parts, bucket = sorter.item(p, u / parts, rows, unit, n);
         if (bucket == p.adapters) {
+            if (!waited) pdl_wait();
+            waited = true;
             const int units = p.N / 8;
-            copy_rows(p, rows, n, 8 * (int)((long long)units * cut / cuts), 8 * (int)((long long)units * (cut + 1) / cuts));
+            copy_rows(p, rows, n, 8 * (int)((long long)units * part / parts),
+                      8 * (int)((long long)units * (part + 1) / parts));
         } else {
-            const int blocks = p.block[p.slices];
-            if (tid < n) {  // (read after the barriers of shrink)
+            if (tid < n) {
                 yrow[tid] = p.y + rows[tid] * p.y_row;
                 orow[tid] = p.out + rows[tid] * p.out_row;
             }
-            shrink<RK>(p, p.a + bucket * p.a_adapter, rows, n, crank, csize, smem);
-            exchange<RK>(p, p.scale ? __ldg(p.scale + bucket) : 1.f, n, smem, inv, crank, csize);
-            expand<RK>(p, p.b + bucket * p.b_adapter, yrow, orow, n, smem, inv, (int)((long long)blocks * cut / cuts),
-                       (int)((long long)blocks * (cut + 1) / cuts));
+            __syncthreads();
+            const int blocks = p.block[p.slices];
+            expand<RK>(p, p.b + bucket * p.b_adapter, yrow, orow, n, smem, inv,
+                       (int)((long long)blocks * part / parts), (int)((long long)blocks * (part + 1) / parts), [&] {
+                           if (!waited) pdl_wait();
+                           waited = true;
+                           gather_h<RK>(p, p.scale ? __ldg(p.scale + bucket) : 1.f, splits, rows, n, smem, inv);
+                           __syncthreads();
+                       });
         }
         __syncthreads();
     }
-    cluster.sync();  // (a CTA stays while others may read its share of the ids)
+    if (!waited) pdl_wait();  // (the kernel after this one counts on shrink's end)
 }
 
 int round_rank(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
-// Clusters of this kernel that the device holds at once (cached per kernel, size and device).
-int resident_clusters(const void *kernel, int smem, int cluster) {
-    struct Entry {
-        const void *kernel;
-        int smem, cluster, dev, n;
-    };
-    static std::mutex mu;
-    static Entry cache[64];
-    static int used = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < used; ++i)
-        if (cache[i].kernel == kernel && cache[i].smem == smem && cache[i].cluster == cluster && cache[i].dev == dev)
-            return cache[i].n;
-    if (!set_smem_once(kernel, smem)) return 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(cluster * 64, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return 0;
-    }
-    if (used < 64) cache[used++] = Entry{kernel, smem, cluster, dev, n};
-    return n;
+// How a call is cut: from its arguments alone, for the workspace's size.
+struct Cut {
+    int scopes, scope, tile, shrinkers, expanders, splits, parts;
+};
+Cut cut_of(const f16_adapters *s, int M, int blocks) {
+    Cut c;
+    c.scopes = (int)((M + (long long)kScope - 1) / kScope);
+    c.scope = (M + c.scopes - 1) / c.scopes;
+    c.tile = round_rank(s->rank) * s->slices <= 384 ? 64 : 32;
+    // Parts of K of at least four stages, parts of the columns of a block for each warp.
+    const int kb = (s->K + kStageK - 1) / kStageK;
+    c.splits = kb < 8 ? 1 : kb / 4 < kMaxSplits ? kb / 4 : kMaxSplits;
+    c.parts = (blocks + kWarps - 1) / kWarps;
+    // Two CTAs for each SM, shared by the scopes, but one for each item where the rows lie
+    // in runs, and no more than there can be work for.
+    const long long full = (c.scope + c.tile - 1) / c.tile;
+    const long long items = c.scope < full + s->adapters + 1 ? c.scope : full + s->adapters + 1;
+    const long long share = 2 * kSmsOfPlan / c.scopes, least = full + 3;
+    const long long ctas = share > least ? share : least;
+    c.shrinkers = (int)(ctas < items * c.splits ? ctas : items * c.splits);
+    c.expanders = (int)(ctas < items * c.parts ? ctas : items * c.parts);
+    return c;
 }
 
 }  // namespace
 
-// Reads and clears this translation unit's record of bad indexes.
-int lora_bad_index() {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_bad_index, sizeof(int)) != cudaSuccess) return -1;
-    if (v) {
-        const int zero = 0;
-        cudaMemcpyToSymbol(g_bad_index, &zero, sizeof(int));
-    }
-    return v;
+// Reads and clears this translation unit's records: bit 0 an expired wait, bit 1 a bad index.
+int lora_status() {
+    int w = 0, b = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&w, g_wait_expired, sizeof(int)) != cudaSuccess ||
+        cudaMemcpyFromSymbol(&b, g_bad_index, sizeof(int)) != cudaSuccess)
+        return -1;
+    if (w) cudaMemcpyToSymbol(g_wait_expired, &zero, sizeof(int));
+    if (b) cudaMemcpyToSymbol(g_bad_index, &zero, sizeof(int));
+    return (w ? 1 : 0) | (b ? 2 : 0);
 }
 }  // namespace w4a16
 
 using namespace w4a16;
 
-extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int64_t y_row, uint16_t *out,
-                        int64_t out_row, const f16_adapters *s, const int32_t *ids, int M, void *stream) {
+namespace {
+
+// Host checks of the adapters; fills the columns' part of p.
+int check_adapters(const f16_adapters *s, LoraArgs &p) {
     if (!s) return W4_ERR_NULL;
-    if (M < 0 || s->adapters < 1 || s->adapters > kMaxAdapters || s->rank < 8 || s->rank > kMaxRank ||
-        s->rank % 8 != 0 || s->K < 8 || s->K % 8 != 0 || s->N < 8 || s->N % 8 != 0 || s->slices < 1 ||
-        s->slices > kMaxSlices)
+    if (s->adapters < 1 || s->adapters > kMaxAdapters || s->rank < 8 || s->rank > kMaxRank || s->rank % 8 != 0 ||
+        s->K < 8 || s->K % 8 != 0 || s->N < 8 || s->N % 8 != 0 || s->slices < 1 || s->slices > kMaxSlices)
         return W4_ERR_SHAPE;
-    LoraArgs p = {};
     for (int i = 0; i < s->slices; ++i) {
         p.col[i + 1] = s->columns[i];
         if (s->columns[i] <= p.col[i] || s->columns[i] % 8 != 0) return W4_ERR_SHAPE;
         p.block[i + 1] = p.block[i] + (p.col[i + 1] - p.col[i] + kColBlock - 1) / kColBlock;
     }
-    if (p.col[s->slices] != s->N) return W4_ERR_SHAPE;
+    return p.col[s->slices] == s->N ? W4A16_OK : W4_ERR_SHAPE;
+}
+
+// A launch as a programmatic dependent.
+template <class K, class... A>
+int launch(K kernel, long long ctas, int smem, void *stream, const A &...args) {
+    if (ctas > 0x7FFFFFFFll) return W4_ERR_SHAPE;
+    if (!set_smem_once(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return W4_ERR_LAUNCH;
+    }
+    return W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" size_t f16_lora_workspace_bytes(const f16_adapters *s, int M) {
+    LoraArgs p = {};
+    if (M < 1 || check_adapters(s, p) != W4A16_OK) return 0;
+    return (size_t)cut_of(s, M, p.block[s->slices]).splits * M * s->slices * s->rank * sizeof(float);
+}
+
+extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int64_t y_row, uint16_t *out,
+                        int64_t out_row, const f16_adapters *s, const int32_t *ids, int M, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    LoraArgs p = {};
+    int st = check_adapters(s, p);
+    if (st != W4A16_OK) return st;
+    if (M < 0) return W4_ERR_SHAPE;
     if (M == 0) return W4A16_OK;
     if (!x || !y || !out || !ids || !s->a || !s->b) return W4_ERR_NULL;
     const auto stride_ok = [](int64_t v) { return v > 0 && v % 8 == 0; };
@@ -695,18 +750,18 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
         !stride_ok(x_row) || !stride_ok(y_row) || !stride_ok(out_row) || !stride_ok(s->a_adapter) ||
         !stride_ok(s->b_adapter))
         return W4_ERR_ALIGN;
+    if (!workspace || workspace_bytes < f16_lora_workspace_bytes(s, M)) return W4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return W4_ERR_ALIGN;
     if (device_cc() != 103) return W4_ERR_DEVICE;
-    p.x = x;
+    const Cut c = cut_of(s, M, p.block[s->slices]);
     p.y = y;
     p.out = out;
-    p.a = s->a;
     p.b = s->b;
     p.scale = s->scale;
     p.ids = ids;
-    p.x_row = x_row;
+    p.h = static_cast<float *>(workspace);
     p.y_row = y_row;
     p.out_row = out_row;
-    p.a_adapter = s->a_adapter;
     p.b_adapter = s->b_adapter;
     p.M = M;
     p.K = s->K;
@@ -714,67 +769,46 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
     p.adapters = s->adapters;
     p.rank = s->rank;
     p.slices = s->slices;
+    p.scope = c.scope;
+    p.tile = c.tile;
+    p.shrinkers = p.ctas = c.shrinkers;
+    p.splits = c.splits;
+    p.parts = c.parts;
     p.copy = out != y || out_row != y_row;
-    const int rk = round_rank(s->rank), R = rk * s->slices, F = s->rank * s->slices;
-    // 64 rows, or 32 where h and its fragments would not fit (more than 384 ranks).
-    p.tile = R <= 384 ? 64 : 32;
-    const int pitch = rk == 16   ? frag_pitch<16>(s->slices)
-                      : rk == 32 ? frag_pitch<32>(s->slices)
-                      : rk == 64 ? frag_pitch<64>(s->slices)
-                                 : frag_pitch<128>(s->slices);
-    const int frag = p.tile * pitch, h = p.tile * F * 4, hist = (s->adapters + 1) * 4;
-    p.off_h = (uint32_t)frag;
-    p.off_red = (uint32_t)(frag + h);
-    // The ring of x and A (at least two stages of 64 k), then h with the warps' sums,
-    // then expand's rings (at least a block a warp) lie in the same place behind the
-    // fragments, or over them.  Two CTAs on an SM if that is enough, else one; rank
-    // 128 has one, for its registers.
-    const int tiles = (F + 15) / 16;
-    const int held = max(shape_of(32, tiles, rk).held, shape_of(p.tile, tiles, rk).held);
-    const int red = (F <= 32 ? 128 : F <= 128 ? 64 : 0) * F * 4;  // [k groups][rows][ranks]
-    const int need = max(2 * held * (128 + kPad), max(frag + h + red, frag + kWarps * p.tile * 64));
-    p.room = (rk < 128 && need + hist <= kSmemOfTwo ? kSmemOfTwo : kSmemOfOne) - hist;
-    p.pool = p.room - frag;
-    p.off_hist = (uint32_t)p.room;
-    const int smem = p.room + hist;
-    const auto kernel = rk == 16 ? lora_kernel<16> : rk == 32 ? lora_kernel<32> : rk == 64 ? lora_kernel<64>
-                                                                                          : lora_kernel<128>;
-    const void *fn = reinterpret_cast<const void *>(kernel);
-    if (!set_smem_once(fn, smem)) return W4_ERR_LAUNCH;
-    // Clusters of 8, or of fewer CTAs where as many row tiles fill the GPU.
-    const int scopes = (int)((M + (long long)kScope - 1) / kScope);
-    p.scope = (M + scopes - 1) / scopes;
-    const int most = (p.scope + p.tile - 1) / p.tile;  // items of a scope whose rows are of one adapter
-    int cluster = kMaxCluster, resident = 0;
-    for (;; cluster /= 2) {
-        resident = resident_clusters(fn, smem, cluster);
-        if (resident < 1) return W4_ERR_LAUNCH;
-        if (cluster == 1 || (long long)scopes * most <= resident) break;
-    }
-    // Parts of an item's columns: as many as give each warp one block.
-    p.parts = (p.block[s->slices] + cluster * kWarps - 1) / (cluster * kWarps);
-    if (scopes == 1) {
-        const long long items = min((long long)M, (long long)s->adapters + 1 + M / p.tile);  // the most there can be
-        p.clusters = (int)min((long long)resident, items * p.parts);
-    } else {
-        p.clusters = most;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)scopes * p.clusters * cluster), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
-        cudaGetLastError();
-        return W4_ERR_LAUNCH;
-    }
-    return W4A16_OK;
+    const int rk = round_rank(s->rank), F = s->rank * s->slices, hist = (s->adapters + 1) * 4;
+    // A as [adapters][slices * rank][K], boxes of 64 k and all rows (two boxes of more
+    // than 256); x as [M][K], boxes of 64 k of one row, copied four at a time, and of 8.
+    CUtensorMap amap, xmap, xbox;
+    p.boxes = F > 256 ? 2 : 1;
+    p.box_rows = p.boxes == 1 ? F : (F / 2 + 7) / 8 * 8;
+    const uint64_t x_bytes = 2ull * (M > 1 ? x_row : s->K);
+    if (!make_map_3d(&amap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, s->a, (uint64_t)s->K, (uint64_t)F, (uint64_t)s->adapters,
+                     2ull * s->K, 2ull * (s->adapters > 1 ? s->a_adapter : 8), kStageK, (uint32_t)p.box_rows, 1,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kStageK, 1,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_2d(&xbox, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kStageK, 8,
+                     CU_TENSOR_MAP_SWIZZLE_128B))
+        return encode_fn() ? W4_ERR_SHAPE : W4_ERR_DEVICE;
+    // shrink: a ring of up to 8 stages, and room behind the last one for the 128 rows of
+    // x that a product reads.  Two CTAs on an SM where four stages fit that.
+    const int stage = ((F + 15) / 16 * 16 + p.tile) * 128, tail = 128 * 128;
+    const int half = 104 * 1024, whole = 216 * 1024 - hist;
+    p.room = 4 * stage + tail + hist <= half && tmem_columns((F + 15) / 16 * 16) <= 256 ? half - hist : whole;
+    if (p.room > kMostStages * stage + tail) p.room = kMostStages * stage + tail;
+    st = launch(shrink_kernel, (long long)c.scopes * c.shrinkers, p.room + hist + 1024, stream, amap, xmap, xbox, p);
+    if (st != W4A16_OK) return st;
+    // expand: the fragments, and rings of up to three column blocks for each warp.
+    const int frag = c.tile * (rk == 16   ? frag_pitch<16>(s->slices)
+                               : rk == 32 ? frag_pitch<32>(s->slices)
+                               : rk == 64 ? frag_pitch<64>(s->slices)
+                                          : frag_pitch<128>(s->slices));
+    const int block = kWarps * c.tile * 64;  // one block a warp
+    int depth = 3;
+    while (depth > 1 && frag + depth * block + hist > half) --depth;
+    p.pool = depth * block;
+    p.ctas = c.expanders;
+    const auto kernel = rk == 16 ? expand_kernel<16> : rk == 32 ? expand_kernel<32> : rk == 64 ? expand_kernel<64>
+                                                                                              : expand_kernel<128>;
+    return launch(kernel, (long long)c.scopes * c.expanders, frag + p.pool + hist, stream, p);
 }

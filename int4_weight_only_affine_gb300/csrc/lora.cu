@@ -9,7 +9,7 @@
 // items of up to `tile` rows, and two kernels share the work:
 //  * shrink: a CTA takes an item and one of `splits` parts of K, and writes its
 //    share of h, fp32, into the workspace.  x and A pass through a ring of stages of
-//    64 k by TMA (A's rows as a box, x's as a box where they lie in a row, else
+//    128 k by TMA (A's rows as a box, x's as a box where they lie in a row, else
 //    gathered four to a copy) and are multiplied by tcgen05 (M = 128 rows of x, of
 //    which the item fills some, N = all ranks of all slices) into tensor memory, so
 //    that no warp touches an operand.
@@ -48,8 +48,9 @@ constexpr int kMaxSlices = 4;
 constexpr int kMaxRank = 128;
 constexpr int kMaxSplits = 8;
 constexpr int kColBlock = 32;  // columns of a warp's step
-constexpr int kStageK = 64;    // k of a stage of shrink's ring: rows of 128 bytes
+constexpr int kHalfK = 64, kStageK = 2 * kHalfK;  // k of a stage of shrink's ring: two halves of 128-byte rows
 constexpr int kMostStages = 8;
+constexpr int kSmemOfTwo = 104 * 1024, kSmemOfOne = 216 * 1024;  // dynamic shared memory of two CTAs on an SM, and of one
 constexpr int kSmsOfPlan = 152;  // (the plan does not depend on the device, nor does a workspace's size)
 
 struct LoraArgs {
@@ -308,11 +309,11 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
         if (bucket == p.adapters) continue;  // (alike for all threads; rows is written again after a barrier)
         // A stage: A's rows, then x's; the products read 128 rows of x, what lies behind the
         // item's goes into rows of the sums that nobody reads.
-        const int xrow = F16, stage = (xrow + (n + 7) / 8 * 8) * 128;
+        const int xrow = F16, half = (xrow + (n + 7) / 8 * 8) * 128, stage = 2 * half;
         const int stages = min(kMostStages, (p.room - 128 * 128) / stage);
         const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
         const bool box = n > 16 && rows[n - 1] - rows[0] == n - 1;
-        const uint32_t bytes = p.boxes * p.box_rows * 128 + (box ? (n + 7) / 8 * 8 : (n + 3) / 4 * 4) * 128;
+        const uint32_t bytes = 2 * (p.boxes * p.box_rows * 128 + (box ? (n + 7) / 8 * 8 : (n + 3) / 4 * 4) * 128);
         if (warp == 0) {
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t i = stage_no + c, b = i % kMostStages, at = base + c % stages * stage;
@@ -324,15 +325,20 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
                 const int k = (c0 + c) * kStageK;
                 if (lane == 0) mbar_expect_tx(full + 8 * b, bytes);
                 __syncwarp();
-                if (lane >= 32 - p.boxes) {
-                    const int row = (lane - (32 - p.boxes)) * p.box_rows;  // (rows past F are zero, and end before x's)
-                    tma_load_3d(at + row * 128, &amap, k, row, bucket, full + 8 * b);
-                } else if (box) {  // boxes of 8 rows
-                    if (8 * lane < n) tma_load_2d(at + (xrow + 8 * lane) * 128, &xbox, k, rows[0] + 8 * lane, full + 8 * b);
-                } else if (4 * lane < n) {
-                    const int end = n - 1;
-                    tma_gather4(at + (xrow + 4 * lane) * 128, &xmap, k, rows[4 * lane], rows[min(4 * lane + 1, end)],
-                                rows[min(4 * lane + 2, end)], rows[min(4 * lane + 3, end)], full + 8 * b);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int kh = k + kHalfK * h;
+                    const uint32_t to = at + h * half, bar = full + 8 * b;
+                    if (lane >= 32 - p.boxes) {
+                        const int row = (lane - (32 - p.boxes)) * p.box_rows;  // (rows past F are zero, and end before x's)
+                        tma_load_3d(to + row * 128, &amap, kh, row, bucket, bar);
+                    } else if (box) {  // boxes of 8 rows
+                        if (8 * lane < n) tma_load_2d(to + (xrow + 8 * lane) * 128, &xbox, kh, rows[0] + 8 * lane, bar);
+                    } else if (4 * lane < n) {
+                        const int end = n - 1;
+                        tma_gather4(to + (xrow + 4 * lane) * 128, &xmap, kh, rows[4 * lane], rows[min(4 * lane + 1, end)],
+                                    rows[min(4 * lane + 2, end)], rows[min(4 * lane + 3, end)], bar);
+                    }
                 }
             }
         } else if (warp == 1 && lane == 0) {
@@ -342,9 +348,10 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
                 for (int k = 0; k < kStageK / 16; ++k) {
-                    const uint64_t x = operand_desc(at + xrow * 128 + 32 * k), a = operand_desc(at + 32 * k);
+                    const uint32_t from = at + k / 4 * half + k % 4 * 32;
+                    const uint64_t x = operand_desc(from + xrow * 128), a = operand_desc(from);
                     mma_f16(tmem, x, a, min(F16, 256), c > 0 || k > 0);
-                    if (F16 > 256) mma_f16(tmem + 256, x, operand_desc(at + 256 * 128 + 32 * k), F16 - 256, c > 0 || k > 0);
+                    if (F16 > 256) mma_f16(tmem + 256, x, operand_desc(from + 256 * 128), F16 - 256, c > 0 || k > 0);
                 }
                 mma_commit(empty + 8 * b);
             }
@@ -357,18 +364,25 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
         if (warp < 2) {
             const int r = 32 * warp + lane;
             float *dst = p.h + ((long long)split * p.M + (r < n ? rows[r] : 0)) * F;
-            for (int f = 0; f < F; f += 8) {
-                float v[8];
-                tmem_load8(tmem + ((uint32_t)(32 * warp) << 16) + f, v);
+            for (int f = 0; f < F; f += 32) {
+                float v[4][8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (f + 8 * q < F) tmem_load8(tmem + ((uint32_t)(32 * warp) << 16) + f + 8 * q, v[q]);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                if (r < n && ok) {
-                    float4 *q = reinterpret_cast<float4 *>(dst + f);
-                    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) asm volatile("" : "+f"(v[q][i]));  // (used after the wait)
+                    if (r < n && ok && f + 8 * q < F) {
+                        float4 *to = reinterpret_cast<float4 *>(dst + f + 8 * q);
+                        to[0] = make_float4(v[q][0], v[q][1], v[q][2], v[q][3]);
+                        to[1] = make_float4(v[q][4], v[q][5], v[q][6], v[q][7]);
+                    }
                 }
             }
         }
-        stage_no += chunks;  // (at least one: splits are of four stages or more)
+        stage_no += chunks;  // (at least one)
         ++units;
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncthreads();
@@ -379,6 +393,14 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
 }
 
 // ---- expand ----
+
+// mma_16816 from sums of zero.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 // The fragments of the second product: for each row, block of 16 ranks and lane t
 // of a quad, the 16 bytes {hi, hi, lo, lo} of 4 ranks in a row, two to a word.  Rows
@@ -541,48 +563,35 @@ __device__ __forceinline__ void expand(const LoraArgs &p, const uint16_t *bw, co
         const uint32_t f0 = frag + own.slice * (64 * KS);
         const int col = own.col + 8 * t;
         const bool cv = col < own.end;
-        // Two row tiles at a time; past the last one only the stores are left out.
-        for (int tile = 0; tile < tiles; tile += 2) {
-            float acc[2][4][4] = {};
-            uint4 old[2][2];
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) old[w][i] = lds128(at + (2 * min(tile + w, tiles - 1) + i) * 512);
+        for (int tile = 0; tile < tiles; ++tile) {
+            const uint4 old[2] = {lds128(at + 2 * tile * 512), lds128(at + (2 * tile + 1) * 512)};
+            const uint32_t row = f0 + 16 * tile * pitch;
+            float acc[4][4];
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                uint4 u[2], l[2];
+                const uint4 u = lds128(row + 64 * k), l = lds128(row + 8 * pitch + 64 * k);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const uint32_t row = f0 + 16 * min(tile + w, tiles - 1) * pitch + 64 * k;
-                    u[w] = lds128(row);
-                    l[w] = lds128(row + 8 * pitch);
+                for (int j = 0; j < 4; ++j) {
+                    if (k == 0) mma_first(acc[j], u.x, l.x, u.y, l.y, bf[j][k][0], bf[j][k][1]);
+                    else mma_16816(acc[j], u.x, l.x, u.y, l.y, bf[j][k][0], bf[j][k][1]);
                 }
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_16816(acc[w][j], u[w].x, l[w].x, u[w].y, l[w].y, bf[j][k][0], bf[j][k][1]);
-#pragma unroll
-                for (int w = 0; w < 2; ++w)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_16816(acc[w][j], u[w].z, l[w].z, u[w].w, l[w].w, bf[j][k][0], bf[j][k][1]);
+                for (int j = 0; j < 4; ++j) mma_16816(acc[j], u.z, l.z, u.w, l.w, bf[j][k][0], bf[j][k][1]);
             }
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
+            for (int i = 0; i < 2; ++i) {
+                const int r = 16 * tile + 8 * i + g;
+                const float f = inv[r];
+                const uint32_t v[4] = {old[i].x, old[i].y, old[i].z, old[i].w};
+                uint32_t o[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = 16 * (tile + w) + 8 * i + g, rs = r & 63;
-                    const float2 f = make_float2(inv[rs], inv[rs]);
-                    const uint32_t v[4] = {old[w][i].x, old[w][i].y, old[w][i].z, old[w][i].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 z = fma2(make_float2(acc[w][j][2 * i], acc[w][j][2 * i + 1]), f, unpack(v[j]));
-                        o[j] = pack(z.x, z.y);
-                    }
-                    uint16_t *dst = orow[rs] + col;
-                    if (cv && r < n) *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 y = unpack(v[j]);
+                    o[j] = pack(fmaf(acc[j][2 * i], f, y.x), fmaf(acc[j][2 * i + 1], f, y.y));
                 }
+                uint16_t *dst = orow[r] + col;
+                if (cv && r < n) *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
         own.step(p);
         if (own.blk >= b1) break;
@@ -650,7 +659,7 @@ int round_rank(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64
 
 // How a call is cut: from its arguments alone, for the workspace's size.
 struct Cut {
-    int scopes, scope, tile, shrinkers, expanders, splits, parts;
+    int scopes, scope, tile, shrinkers, expanders, splits, parts, room;
 };
 Cut cut_of(const f16_adapters *s, int M, int blocks) {
     Cut c;
@@ -660,15 +669,25 @@ Cut cut_of(const f16_adapters *s, int M, int blocks) {
     // Parts of K of at least four stages, parts of the columns of a block for each warp.
     const int kb = (s->K + kStageK - 1) / kStageK;
     c.splits = kb < 8 ? 1 : kb / 4 < kMaxSplits ? kb / 4 : kMaxSplits;
+    // shrink's ring: up to 8 stages, and room behind the last one for the 128 rows of x
+    // that a product reads.  Two CTAs on an SM where three stages fit that, else one.
+    const int F = s->rank * s->slices, hist = (s->adapters + 1) * 4;
+    const int stage = 2 * ((F + 15) / 16 * 16 + c.tile) * 128, tail = 128 * 128;
+    const bool two = 3 * stage + tail + hist <= kSmemOfTwo && tmem_columns((F + 15) / 16 * 16) <= 256;
+    c.room = (two ? kSmemOfTwo : kSmemOfOne) - hist;
+    if (c.room > kMostStages * stage + tail) c.room = kMostStages * stage + tail;
     c.parts = (blocks + kWarps - 1) / kWarps;
-    // Two CTAs for each SM, shared by the scopes, but one for each item where the rows lie
+    // As many CTAs as the SMs hold, shared by the scopes, but one for each item where the rows lie
     // in runs, and no more than there can be work for.
     const long long full = (c.scope + c.tile - 1) / c.tile;
     const long long items = c.scope < full + s->adapters + 1 ? c.scope : full + s->adapters + 1;
-    const long long share = 2 * kSmsOfPlan / c.scopes, least = full + 3;
-    const long long ctas = share > least ? share : least;
-    c.shrinkers = (int)(ctas < items * c.splits ? ctas : items * c.splits);
-    c.expanders = (int)(ctas < items * c.parts ? ctas : items * c.parts);
+    const auto ctas = [&](long long on_sm, long long parts) {
+        const long long share = on_sm * kSmsOfPlan / c.scopes, least = full + 3, most = items * parts;
+        const long long n = share > least ? share : least;
+        return (int)(n < most ? n : most);
+    };
+    c.shrinkers = ctas(two ? 2 : 1, c.splits);
+    c.expanders = ctas(2, c.parts);
     return c;
 }
 
@@ -783,19 +802,14 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
     p.box_rows = p.boxes == 1 ? F : (F / 2 + 7) / 8 * 8;
     const uint64_t x_bytes = 2ull * (M > 1 ? x_row : s->K);
     if (!make_map_3d(&amap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, s->a, (uint64_t)s->K, (uint64_t)F, (uint64_t)s->adapters,
-                     2ull * s->K, 2ull * (s->adapters > 1 ? s->a_adapter : 8), kStageK, (uint32_t)p.box_rows, 1,
+                     2ull * s->K, 2ull * (s->adapters > 1 ? s->a_adapter : 8), kHalfK, (uint32_t)p.box_rows, 1,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kStageK, 1,
+        !make_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kHalfK, 1,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_2d(&xbox, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kStageK, 8,
+        !make_map_2d(&xbox, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kHalfK, 8,
                      CU_TENSOR_MAP_SWIZZLE_128B))
         return encode_fn() ? W4_ERR_SHAPE : W4_ERR_DEVICE;
-    // shrink: a ring of up to 8 stages, and room behind the last one for the 128 rows of
-    // x that a product reads.  Two CTAs on an SM where four stages fit that.
-    const int stage = ((F + 15) / 16 * 16 + p.tile) * 128, tail = 128 * 128;
-    const int half = 104 * 1024, whole = 216 * 1024 - hist;
-    p.room = 4 * stage + tail + hist <= half && tmem_columns((F + 15) / 16 * 16) <= 256 ? half - hist : whole;
-    if (p.room > kMostStages * stage + tail) p.room = kMostStages * stage + tail;
+    p.room = c.room;
     st = launch(shrink_kernel, (long long)c.scopes * c.shrinkers, p.room + hist + 1024, stream, amap, xmap, xbox, p);
     if (st != W4A16_OK) return st;
     // expand: the fragments, and rings of up to three column blocks for each warp.
@@ -805,7 +819,7 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
                                           : frag_pitch<128>(s->slices));
     const int block = kWarps * c.tile * 64;  // one block a warp
     int depth = 3;
-    while (depth > 1 && frag + depth * block + hist > half) --depth;
+    while (depth > 1 && frag + depth * block + hist > kSmemOfTwo) --depth;
     p.pool = depth * block;
     p.ctas = c.expanders;
     const auto kernel = rk == 16 ? expand_kernel<16> : rk == 32 ? expand_kernel<32> : rk == 64 ? expand_kernel<64>

@@ -54,12 +54,12 @@ constexpr int kSmemOfTwo = 104 * 1024, kSmemOfOne = 216 * 1024;  // dynamic shar
 constexpr int kSmsOfPlan = 152;  // (the plan does not depend on the device, nor does a workspace's size)
 
 struct LoraArgs {
-    const uint16_t *y, *b;
+    const uint16_t *x, *y, *a, *b;
     uint16_t *out;
     const float *scale;
     const int32_t *ids;
     float *h;  // [splits][M][slices * rank]
-    long long y_row, out_row, b_adapter;
+    long long x_row, y_row, out_row, a_adapter, b_adapter;
     int M, K, N, adapters, rank, slices;
     int col[kMaxSlices + 1];    // first column of each slice, N at the end
     int block[kMaxSlices + 1];  // column blocks before each slice
@@ -137,9 +137,13 @@ struct Sorter {
     int row0, nrow, per;
     bool few;
 
-    // Parts of K: as many as give each CTA of shrink one (both kernels come to the same).
+    // Parts of K, and of the columns: as many as give each CTA of shrink, or of expand,
+    // one (both kernels come to the same splits).
     __device__ __forceinline__ int splits(const LoraArgs &p) const {
         return max(1, min(p.splits, p.shrinkers / max(items, 1)));
+    }
+    __device__ __forceinline__ int parts(const LoraArgs &p) const {
+        return max(1, min(p.parts, p.ctas / max(items, 1)));
     }
 
     __device__ __forceinline__ static bool counts(const LoraArgs &p, int b) { return b < p.adapters || (b == p.adapters && p.copy); }
@@ -151,28 +155,30 @@ struct Sorter {
         nrow = min(p.scope, p.M - row0);
         few = nrow <= 32;
         per = (p.adapters + kThreads) / kThreads;
-        const auto bucket = [&](int r) {
+        const auto bucket = [&](int v, int r) {
             if (r >= nrow) return -1;
-            const int v = __ldg(p.ids + row0 + r);
             if (v >= p.adapters) atomicExch(&g_bad_index, 1);
             return v < 0 || v >= p.adapters ? p.adapters : v;
         };
         if (few) {
             // Every warp knows all rows: an item to each bucket, in the order of their first rows.
-            id[0] = bucket(lane);
+            id[0] = bucket(lane < nrow ? __ldg(p.ids + row0 + lane) : -1, lane);
             same = __match_any_sync(~0u, id[0]);
             leaders = __ballot_sync(~0u, id[0] >= 0 && counts(p, id[0]) && (same & ((1u << lane) - 1u)) == 0u);
             items = __popc(leaders);
             return;
         }
         constexpr int kMine = kScope / kThreads;
+        int raw[kMine];
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) id[i] = bucket(tid * kMine + i);
-        for (int i = tid; i <= p.adapters; i += kThreads) hist[i] = 0;
+        for (int i = 0; i < kMine; ++i) raw[i] = tid * kMine + i < nrow ? __ldg(p.ids + row0 + tid * kMine + i) : -1;
+        for (int i = tid; i <= p.adapters; i += kThreads) hist[i] = 0;  // (while the ids come)
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
+        for (int i = 0; i < kMine; ++i) {
+            id[i] = bucket(raw[i], tid * kMine + i);
             if (id[i] >= 0) atomicAdd(hist + id[i], 1);
+        }
         __syncthreads();
         mine = 0;
         for (int i = 0; i < per; ++i) {  // this thread's buckets are in a row
@@ -260,7 +266,75 @@ __host__ __device__ constexpr int tmem_columns(int ranks) {
     return ranks <= 32 ? 32 : ranks <= 64 ? 64 : ranks <= 128 ? 128 : ranks <= 256 ? 256 : 512;
 }
 
-__global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant__ CUtensorMap amap,
+// Items of up to 16 rows: the products of tcgen05 cost 150 cycles each whatever the
+// rows, so a few rows are multiplied by mma.sync (ranks as M, rows as N), with
+// operands loaded straight from global memory in fragment order: lane t of a quad
+// takes 16 contiguous bytes of a row as the k indexes of two products.  The warps
+// share the CTA's part of K, blocks kb0 .. kb1 - 1 of 32 k, and add their sums through
+// shared memory, 16 * MT ranks at a time.  (64 rows of 25 adapters, 11008 k, rank 32:
+// 17 us with tcgen05, see below for this.)
+template <int MT, int NT, int AHEAD>
+__device__ __forceinline__ void shrink_few(const LoraArgs &p, const uint16_t *a, const int *rows, int n, int split,
+                                           int kb0, int kb1, float *red) {
+    constexpr int G = 16 * MT;
+    const int F = p.slices * p.rank;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int k0 = kb0 + (kb1 - kb0) * warp / kWarps, k1 = kb0 + (kb1 - kb0) * (warp + 1) / kWarps;
+    const uint16_t *xr[NT];
+    bool xv[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        xv[i] = 8 * i + g < n;
+        xr[i] = p.x + rows[xv[i] ? 8 * i + g : 0] * p.x_row + 8 * t;
+    }
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    for (int f0 = 0; f0 < F; f0 += G) {
+        float acc[MT][NT][4] = {};
+        const uint16_t *ar = a + (long long)(f0 + g) * p.K + 8 * t;
+        for (int b = k0; b < k1; b += AHEAD) {
+            uint4 av[AHEAD][2 * MT], xf[AHEAD][NT];
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q) {
+                const bool in = b + q < k1 && 32 * (b + q) + 8 * t < p.K;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) xf[q][i] = in && xv[i] ? load16(xr[i] + 32 * (b + q)) : zero;
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i)
+                    av[q][i] = in && f0 + 8 * i + g < F ? load16(ar + (long long)(8 * i) * p.K + 32 * (b + q)) : zero;
+            }
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const uint4 u = av[q][2 * m], l = av[q][2 * m + 1];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) mma_16816(acc[m][i], u.x, l.x, u.y, l.y, xf[q][i].x, xf[q][i].y);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) mma_16816(acc[m][i], u.z, l.z, u.w, l.w, xf[q][i].z, xf[q][i].w);
+                }
+        }
+        // red [warp][8 * NT rows][G]
+        float *mine = red + warp * 8 * NT * G;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mine[(8 * i + 2 * t + (e & 1)) * G + 16 * m + g + 8 * (e >> 1)] = acc[m][i][e];
+        __syncthreads();
+        for (int e = threadIdx.x; e < n * G; e += kThreads) {
+            const int r = e / G, f = f0 + e % G;
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += red[w * 8 * NT * G + e];
+            if (f < F) p.h[((long long)split * p.M + rows[r]) * F + f] = v;
+        }
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_constant__ CUtensorMap amap,
                                                           const __grid_constant__ CUtensorMap xmap,
                                                           const __grid_constant__ CUtensorMap xbox,
                                                           const __grid_constant__ LoraArgs p) {
@@ -307,6 +381,18 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
         const int split = u % splits, bucket = sorter.item(p, u / splits, rows, unit, n);
         const int c0 = (int)((long long)kb * split / splits), chunks = (int)((long long)kb * (split + 1) / splits) - c0;
         if (bucket == p.adapters) continue;  // (alike for all threads; rows is written again after a barrier)
+        if (n <= 16) {
+            const uint16_t *a = p.a + bucket * p.a_adapter;
+            const int b0 = c0 * (kStageK / 32), b1 = min((p.K + 31) / 32, (c0 + chunks) * (kStageK / 32));
+            float *red = reinterpret_cast<float *>(smem);
+            if (F <= 16) shrink_few<1, 2, 4>(p, a, rows, n, split, b0, b1, red);
+            else if (F <= 32) shrink_few<2, 2, 2>(p, a, rows, n, split, b0, b1, red);
+            else if (n <= 8) shrink_few<4, 1, 2>(p, a, rows, n, split, b0, b1, red);
+            else shrink_few<4, 2, 1>(p, a, rows, n, split, b0, b1, red);
+            fence_proxy_async_smem();  // (the next item's copies may come here)
+            __syncthreads();
+            continue;
+        }
         // A stage: A's rows, then x's; the products read 128 rows of x, what lies behind the
         // item's goes into rows of the sums that nobody reads.
         const int xrow = F16, half = (xrow + (n + 7) / 8 * 8) * 128, stage = 2 * half;
@@ -419,62 +505,77 @@ __device__ __forceinline__ int frag_at(int s, int r) {
 }
 
 // Adds up the shares of h of the item's rows, scales and splits them into fragments.
+// The sums, 4 ranks of a row to a thread, first lie where their fragments will; tops
+// holds the bits of each row's largest value, which order as the values do (infinity
+// for a row that is not finite), and is zero on entry.  Ends with a barrier.
 template <int RK>
 __device__ __forceinline__ void gather_h(const LoraArgs &p, float scale, int splits, const int *rows, int n,
-                                         uint8_t *smem, float *inv) {
-    const int R = p.slices * RK, F = p.slices * p.rank, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pitch = frag_pitch<RK>(p.slices);
-    constexpr int J = (kMaxSlices * RK + 127) / 128;  // groups of 4 ranks of a lane
-    const float inf = __int_as_float(0x7F800000);
-    for (int row = warp; row < n; row += kWarps) {
-        float4 v[J];
-        float top = 0.f;
+                                         uint8_t *smem, int *tops, float *inv) {
+    const int G = p.slices * RK / 4, F = p.slices * p.rank, pitch = frag_pitch<RK>(p.slices);
+    const uint32_t by = ((1u << 22) + G - 1) / G;  // e / G = e * by >> 22 for e < 2^13
+    const long long share = (long long)p.M * F;
+    constexpr int kAhead = 2, W = RK / 4;  // W lanes in a row hold a row's ranks of a slice
+    for (int e0 = threadIdx.x; e0 < (n * G + 31) / 32 * 32; e0 += kAhead * kThreads) {
+        float4 v[kAhead];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int r = 128 * j + 4 * lane;
-            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < R && r % RK < p.rank) {  // (ranks past the adapters' are zero)
-                const float *src = p.h + (long long)rows[row] * F + r / RK * p.rank + r % RK;
-                float4 part[kMaxSplits];
+        for (int q = 0; q < kAhead; ++q) v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < splits; c += 4) {
+            float4 part[kAhead][4];
 #pragma unroll
-                for (int c = 0; c < kMaxSplits; ++c)  // (written by the kernel before: no read-only loads)
-                    if (c < splits) part[c] = __ldcg(reinterpret_cast<const float4 *>(src + (long long)c * p.M * F));
+            for (int q = 0; q < kAhead; ++q) {
+                const int e = e0 + q * kThreads, row = (int)(e * by >> 22), r = 4 * (e - row * G);
+                const bool in = e < n * G && r % RK < p.rank;  // (ranks past the adapters' are zero)
+                const float *src = p.h + (long long)rows[in ? row : 0] * F + (in ? r / RK * p.rank + r % RK : 0) + c * share;
 #pragma unroll
-                for (int c = 0; c < kMaxSplits; ++c)
-                    if (c < splits) {
-                        v[j].x += part[c].x;
-                        v[j].y += part[c].y;
-                        v[j].z += part[c].z;
-                        v[j].w += part[c].w;
-                    }
-                v[j].x *= scale;
-                v[j].y *= scale;
-                v[j].z *= scale;
-                v[j].w *= scale;
+                for (int i = 0; i < 4; ++i)  // (written by the kernel before: no read-only loads)
+                    part[q][i] = in && c + i < splits ? __ldcg(reinterpret_cast<const float4 *>(src + i * share))
+                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            const float m = fmaxf(fmaxf(fabsf(v[j].x), fabsf(v[j].y)), fmaxf(fabsf(v[j].z), fabsf(v[j].w)));
-            const bool nan = v[j].x != v[j].x || v[j].y != v[j].y || v[j].z != v[j].z || v[j].w != v[j].w;
-            top = fmaxf(top, nan ? inf : m);
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[q].x += part[q][i].x;
+                    v[q].y += part[q][i].y;
+                    v[q].z += part[q][i].z;
+                    v[q].w += part[q][i].w;
+                }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        // 2^(12 - e) for a largest value in [2^e, 2^(e + 1)); 1 for rows of zeros and those that are not finite.
-        const int e = (int)(__float_as_uint(top) >> 23) - 127;
-        const int shift = e == 128 || top == 0.f ? 0 : 12 - max(e, -100);
-        const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-        if (lane == 0) inv[row] = __uint_as_float((uint32_t)(127 - shift) << 23);
+        for (int q = 0; q < kAhead; ++q) {
+            const int e = e0 + q * kThreads, row = (int)(e * by >> 22), r = 4 * (e - row * G);
+            v[q].x *= scale;
+            v[q].y *= scale;
+            v[q].z *= scale;
+            v[q].w *= scale;
+            const float m = fmaxf(fmaxf(fabsf(v[q].x), fabsf(v[q].y)), fmaxf(fabsf(v[q].z), fabsf(v[q].w)));
+            const bool nan = v[q].x != v[q].x || v[q].y != v[q].y || v[q].z != v[q].z || v[q].w != v[q].w;
+            int top = nan ? 0x7F800000 : __float_as_int(m);
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int r = 128 * j + 4 * lane;
-            if (r >= R) continue;
-            const float a = v[j].x * up, b = v[j].y * up, c = v[j].z * up, d = v[j].w * up;
-            const uint32_t h0 = pack(a, b), h1 = pack(c, d);
-            const float2 f0 = unpack(h0), f1 = unpack(h1);
-            const auto rest = [](float x, float hi) { return fabsf(x - hi) < 1e30f ? x - hi : 0.f; };  // (none of infinities)
-            *reinterpret_cast<uint4 *>(smem + row * pitch + frag_at<RK>(r / RK, r % RK)) =
-                make_uint4(h0, h1, pack(rest(a, f0.x), rest(b, f0.y)), pack(rest(c, f1.x), rest(d, f1.y)));
+            for (int o = W / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+            if (e < n * G) {
+                *reinterpret_cast<float4 *>(smem + row * pitch + frag_at<RK>(r / RK, r % RK)) = v[q];
+                if (r % RK == 0) atomicMax(tops + row, top);
+            }
         }
     }
+    __syncthreads();
+    for (int e = threadIdx.x; e < n * G; e += kThreads) {
+        const int row = (int)(e * by >> 22), r = 4 * (e - row * G);
+        // 2^(12 - x) for a largest value in [2^x, 2^(x + 1)); 1 for rows of zeros and those that are not finite.
+        const int top = tops[row], x = (top >> 23) - 127;
+        const int shift = x == 128 || top == 0 ? 0 : 12 - max(x, -100);
+        const float up = __int_as_float((127 + shift) << 23);
+        if (r == 0) inv[row] = __int_as_float((127 - shift) << 23);
+        uint4 *at = reinterpret_cast<uint4 *>(smem + row * pitch + frag_at<RK>(r / RK, r % RK));
+        const float4 v = *reinterpret_cast<const float4 *>(at);
+        const float a = v.x * up, b = v.y * up, c = v.z * up, d = v.w * up;
+        const uint32_t h0 = pack(a, b), h1 = pack(c, d);
+        const float2 f0 = unpack(h0), f1 = unpack(h1);
+        const auto rest = [](float x, float hi) { return fabsf(x - hi) < 1e30f ? x - hi : 0.f; };  // (none of infinities)
+        *at = make_uint4(h0, h1, pack(rest(a, f0.x), rest(b, f0.y)), pack(rest(c, f1.x), rest(d, f1.y)));
+    }
+    __syncthreads();
 }
 
 // Where a warp stands among the column blocks.
@@ -616,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int scratch[kWarps], rows[64], unit[3];
     __shared__ float inv[64];
+    __shared__ int tops[64];
     __shared__ const uint16_t *yrow[64];
     __shared__ uint16_t *orow[64];
     const int tid = threadIdx.x;
@@ -624,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
     sorter.hist = reinterpret_cast<int *>(smem + p.tile * frag_pitch<RK>(p.slices) + p.pool);
     // (What is read before the wait was complete before shrink released this kernel.)
     sorter.begin(p, blockIdx.x / p.ctas);
-    const int splits = sorter.splits(p), parts = max(1, min(p.parts, p.ctas / max(sorter.items, 1)));
+    const int splits = sorter.splits(p), parts = sorter.parts(p);
     bool waited = false;
     for (int u = blockIdx.x % p.ctas; u < sorter.items * parts; u += p.ctas) {
         int n;
@@ -636,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
             copy_rows(p, rows, n, 8 * (int)((long long)units * part / parts),
                       8 * (int)((long long)units * (part + 1) / parts));
         } else {
+            if (tid < 64) tops[tid] = 0;
             if (tid < n) {
                 yrow[tid] = p.y + rows[tid] * p.y_row;
                 orow[tid] = p.out + rows[tid] * p.out_row;
@@ -646,8 +749,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
                        (int)((long long)blocks * part / parts), (int)((long long)blocks * (part + 1) / parts), [&] {
                            if (!waited) pdl_wait();
                            waited = true;
-                           gather_h<RK>(p, p.scale ? __ldg(p.scale + bucket) : 1.f, splits, rows, n, smem, inv);
-                           __syncthreads();
+                           gather_h<RK>(p, p.scale ? __ldg(p.scale + bucket) : 1.f, splits, rows, n, smem, tops, inv);
                        });
         }
         __syncthreads();
@@ -666,16 +768,16 @@ Cut cut_of(const f16_adapters *s, int M, int blocks) {
     c.scopes = (int)((M + (long long)kScope - 1) / kScope);
     c.scope = (M + c.scopes - 1) / c.scopes;
     c.tile = round_rank(s->rank) * s->slices <= 384 ? 64 : 32;
-    // Parts of K of at least four stages, parts of the columns of a block for each warp.
+    // Parts of K of a stage or more, parts of the columns of a block for each warp.
     const int kb = (s->K + kStageK - 1) / kStageK;
-    c.splits = kb < 8 ? 1 : kb / 4 < kMaxSplits ? kb / 4 : kMaxSplits;
+    c.splits = kb < kMaxSplits ? kb : kMaxSplits;
     // shrink's ring: up to 8 stages, and room behind the last one for the 128 rows of x
     // that a product reads.  Two CTAs on an SM where three stages fit that, else one.
     const int F = s->rank * s->slices, hist = (s->adapters + 1) * 4;
     const int stage = 2 * ((F + 15) / 16 * 16 + c.tile) * 128, tail = 128 * 128;
     const bool two = 3 * stage + tail + hist <= kSmemOfTwo && tmem_columns((F + 15) / 16 * 16) <= 256;
     c.room = (two ? kSmemOfTwo : kSmemOfOne) - hist;
-    if (c.room > kMostStages * stage + tail) c.room = kMostStages * stage + tail;
+    if (c.room > kMostStages * stage + tail) c.room = kMostStages * stage + tail;  // (at least 32 KB, for shrink_few)
     c.parts = (blocks + kWarps - 1) / kWarps;
     // As many CTAs as the SMs hold, shared by the scopes, but one for each item where the rows lie
     // in runs, and no more than there can be work for.
@@ -773,7 +875,11 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
     if (!aligned16(workspace)) return W4_ERR_ALIGN;
     if (device_cc() != 103) return W4_ERR_DEVICE;
     const Cut c = cut_of(s, M, p.block[s->slices]);
+    p.x = x;
     p.y = y;
+    p.a = s->a;
+    p.x_row = x_row;
+    p.a_adapter = s->a_adapter;
     p.out = out;
     p.b = s->b;
     p.scale = s->scale;

@@ -72,7 +72,7 @@ struct LoraArgs {
     int col[kMaxSlices + 1];    // first column of each slice, N at the end
     int block[kMaxSlices + 1];  // column blocks before each slice
     int scope;                  // rows of a scope
-    int tile;                   // rows of an item: 64 or 32
+    int tile, stile;            // rows of an item: 64 or 32; of shrink's items: 128 or 64
     int ctas;                   // of a scope, in the kernel that is launched
     int shrinkers;              // of them in shrink
     int splits, parts;          // most parts of K, and of an item's columns
@@ -140,7 +140,9 @@ struct Sorter {
     int *scratch;   // kWarps ints of shared memory
     int *hist;      // [adapters + 1]: rows of each bucket
     int id[kScope / kThreads];  // buckets of this thread's rows, in order; -1 past the scope
-    int items, first, mine;     // of all; before this thread's buckets; in them
+    int items, shrunk;          // of all, of p.tile rows and of p.stile
+    int first, mine;            // of `tile` rows: before this thread's buckets; in them
+    int tile;
     unsigned leaders, same;     // of few rows: the first of each bucket; the lane's equals
     int row0, nrow, per;
     bool few;
@@ -148,7 +150,7 @@ struct Sorter {
     // Parts of K, and of the columns: as many as give each CTA of shrink, or of expand,
     // one (both kernels come to the same splits).
     __device__ __forceinline__ int splits(const LoraArgs &p) const {
-        return max(1, min(p.splits, p.shrinkers / max(items, 1)));
+        return max(1, min(p.splits, p.shrinkers / max(shrunk, 1)));
     }
     __device__ __forceinline__ int parts(const LoraArgs &p) const {
         return max(1, min(p.parts, p.ctas / max(items, 1)));
@@ -156,9 +158,10 @@ struct Sorter {
 
     __device__ __forceinline__ static bool counts(const LoraArgs &p, int b) { return b < p.adapters || (b == p.adapters && p.copy); }
 
-    // Called by every thread of the block, at its start.
-    __device__ __forceinline__ void begin(const LoraArgs &p, int scope) {
+    // Called by every thread of the block, at its start, for items of rows_ rows (p.tile or p.stile).
+    __device__ __forceinline__ void begin(const LoraArgs &p, int scope, int rows_) {
         const int tid = threadIdx.x, lane = tid & 31;
+        tile = rows_;
         row0 = scope * p.scope;
         nrow = min(p.scope, p.M - row0);
         few = nrow <= kFewRows;
@@ -173,7 +176,7 @@ struct Sorter {
             id[0] = bucket(lane < nrow ? __ldg(p.ids + row0 + lane) : -1, lane);
             same = __match_any_sync(~0u, id[0]);
             leaders = __ballot_sync(~0u, id[0] >= 0 && counts(p, id[0]) && (same & ((1u << lane) - 1u)) == 0u);
-            items = __popc(leaders);
+            items = shrunk = __popc(leaders);
             return;
         }
         constexpr int kMine = kScope / kThreads;
@@ -188,12 +191,16 @@ struct Sorter {
             if (id[i] >= 0) atomicAdd(hist + id[i], 1);
         }
         __syncthreads();
-        mine = 0;
+        int both = 0, all;  // items of p.tile rows, and of p.stile << 16 (at most 1025 each)
         for (int i = 0; i < per; ++i) {  // this thread's buckets are in a row
             const int b = tid * per + i;
-            if (counts(p, b)) mine += (hist[b] + p.tile - 1) / p.tile;
+            if (counts(p, b)) both += (hist[b] + p.tile - 1) / p.tile + ((hist[b] + p.stile - 1) / p.stile << 16);
         }
-        first = block_scan(mine, scratch, items);
+        const int before = block_scan(both, scratch, all), shift = tile == p.stile ? 16 : 0;
+        items = all & 0xFFFF;
+        shrunk = all >> 16;
+        first = before >> shift & 0xFFFF;
+        mine = both >> shift & 0xFFFF;
     }
 
     // The rows and the bucket of an item; called by every thread, ends with a barrier.
@@ -217,11 +224,11 @@ struct Sorter {
             for (int i = 0; i < per; ++i) {
                 const int b = tid * per + i;
                 if (counts(p, b)) {
-                    const int c = (hist[b] + p.tile - 1) / p.tile;
+                    const int c = (hist[b] + tile - 1) / tile;
                     if (item >= at && item < at + c) {
                         unit[0] = b;
-                        unit[1] = (item - at) * p.tile;
-                        unit[2] = min(p.tile, hist[b] - (item - at) * p.tile);
+                        unit[1] = (item - at) * tile;
+                        unit[2] = min(tile, hist[b] - (item - at) * tile);
                     }
                     at += c;
                 }
@@ -348,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
                                                           const __grid_constant__ LoraArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-(uint32_t)__cvta_generic_to_shared(smem_raw) & 1023u);
-    __shared__ int scratch[kWarps], rows[64], unit[3];
+    __shared__ int scratch[kWarps], rows[128], unit[3];
     __shared__ __align__(8) uint64_t bars[2 * kMostStages + 1];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     Sorter sorter;
     sorter.scratch = scratch;
     sorter.hist = reinterpret_cast<int *>(smem + p.room);
-    sorter.begin(p, blockIdx.x / p.ctas);
+    sorter.begin(p, blockIdx.x / p.ctas, p.stile);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -385,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     const int kb = (p.K + kStageK - 1) / kStageK, splits = sorter.splits(p);
     if (p.frags && tid == 0 && blockIdx.x % p.ctas == 0) p.splits_of[blockIdx.x / p.ctas] = splits;
     uint32_t stage_no = 0, units = 0;  // stages and items so far: the barriers' phases
-    for (int u = blockIdx.x % p.ctas; u < sorter.items * splits; u += p.ctas) {
+    for (int u = blockIdx.x % p.ctas; u < sorter.shrunk * splits; u += p.ctas) {
         int n;
         const int split = u % splits, bucket = sorter.item(p, u / splits, rows, unit, n);
         const int c0 = (int)((long long)kb * split / splits), chunks = (int)((long long)kb * (split + 1) / splits) - c0;
@@ -427,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
                     if (lane >= 32 - p.boxes) {
                         const int row = (lane - (32 - p.boxes)) * p.box_rows;  // (rows past F are zero, and end before x's)
                         tma_load_3d(to + row * 128, &amap, kh, row, bucket, bar);
-                    } else if (box) {  // boxes of 8 rows
+                    }
+                    if (box) {  // boxes of 8 rows
                         if (8 * lane < n) tma_load_2d(to + (xrow + 8 * lane) * 128, &xbox, kh, rows[0] + 8 * lane, bar);
                     } else if (4 * lane < n) {
                         const int end = n - 1;
@@ -456,9 +464,9 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
         // Every stage is read before the next item's copies come (the products are in order).
         const bool ok = mbar_wait(done, units & 1, abort);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (warp < 2) {
-            const int r = 32 * warp + lane;
-            float *dst = p.h + ((long long)split * p.M + (r < n ? rows[r] : 0)) * F;
+        // The sums go out row by row through the ring's place (rows 16 bytes longer than their data).
+        const int r = 32 * warp + lane, pitch = 4 * F + 16;
+        if (32 * warp < n) {
             for (int f = 0; f < F; f += 32) {
                 float v[4][8];
 #pragma unroll
@@ -469,12 +477,21 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
                 for (int q = 0; q < 4; ++q) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) asm volatile("" : "+f"(v[q][i]));  // (used after the wait)
-                    if (r < n && ok && f + 8 * q < F) {
-                        float4 *to = reinterpret_cast<float4 *>(dst + f + 8 * q);
+                    if (f + 8 * q < F) {
+                        float4 *to = reinterpret_cast<float4 *>(smem + r * pitch + 4 * (f + 8 * q));
                         to[0] = make_float4(v[q][0], v[q][1], v[q][2], v[q][3]);
                         to[1] = make_float4(v[q][4], v[q][5], v[q][6], v[q][7]);
                     }
                 }
+            }
+            fence_proxy_async_smem();
+            if (r < n && ok) {
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                 p.h + ((long long)split * p.M + rows[r]) * F),
+                             "r"(base + r * pitch), "r"(4 * F)
+                             : "memory");
+                bulk_commit_group();
+                bulk_wait_group<0>();
             }
         }
         stage_no += chunks;  // (at least one)
@@ -787,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
     sorter.scratch = scratch;
     sorter.hist = reinterpret_cast<int *>(smem + p.tile * frag_pitch<RK>(p.slices) + p.pool);
     // (What is read before the wait was complete before shrink released its dependent.)
-    sorter.begin(p, blockIdx.x / p.ctas);
+    sorter.begin(p, blockIdx.x / p.ctas, p.tile);
     const int splits = sorter.splits(p), parts = sorter.parts(p);
     bool waited = false;
     for (int u = blockIdx.x % p.ctas; u < sorter.items * parts; u += p.ctas) {
@@ -833,7 +850,7 @@ int round_rank(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64
 
 // How a call is cut: from its arguments alone, for the workspace's size.
 struct Cut {
-    int scopes, scope, tile, shrinkers, expanders, splits, parts, room;
+    int scopes, scope, tile, stile, shrinkers, expanders, splits, parts, room;
 };
 Cut cut_of(const f16_adapters *s, int M, int blocks) {
     Cut c;
@@ -844,10 +861,11 @@ Cut cut_of(const f16_adapters *s, int M, int blocks) {
     const int kb = (s->K + kStageK - 1) / kStageK;
     c.splits = kb < kMaxSplits ? kb : kMaxSplits;
     // shrink's ring: up to 8 stages, and room behind the last one for the 128 rows of x
-    // that a product reads.  Two CTAs on an SM where three stages fit that, else one.
+    // that a product reads.  Two CTAs on an SM where two stages fit that, and the sums, else one.
     const int F = s->rank * s->slices, hist = (s->adapters + 1) * 4;
-    const int stage = 2 * ((F + 15) / 16 * 16 + c.tile) * 128, tail = 128 * 128;
-    const bool two = 3 * stage + tail + hist <= kSmemOfTwo && tmem_columns((F + 15) / 16 * 16) <= 256;
+    c.stile = F <= 192 ? 128 : 64;
+    const int stage = 2 * ((F + 15) / 16 * 16 + c.stile) * 128, tail = 128 * 128;
+    const bool two = (2 * stage + tail > 4 * c.stile * (F + 4) ? 2 * stage + tail : 4 * c.stile * (F + 4)) + hist <= kSmemOfTwo && tmem_columns((F + 15) / 16 * 16) <= 256;
     c.room = (two ? kSmemOfTwo : kSmemOfOne) - hist;
     if (c.room > kMostStages * stage + tail) c.room = kMostStages * stage + tail;  // (at least 32 KB, for shrink_few)
     c.parts = (blocks + kWarps - 1) / kWarps;
@@ -855,13 +873,14 @@ Cut cut_of(const f16_adapters *s, int M, int blocks) {
     // in runs, and no more than there can be work for.
     const long long full = (c.scope + c.tile - 1) / c.tile;
     const long long items = c.scope < full + s->adapters + 1 ? c.scope : full + s->adapters + 1;
-    const auto ctas = [&](long long on_sm, long long parts) {
-        const long long share = on_sm * kSmsOfPlan / c.scopes, least = full + 3, most = items * parts;
+    const auto ctas = [&](long long on_sm, long long rows, long long parts) {
+        const long long share = on_sm * kSmsOfPlan / c.scopes, least = (c.scope + rows - 1) / rows + 3,
+                        most = items * parts;
         const long long n = share > least ? share : least;
         return (int)(n < most ? n : most);
     };
-    c.shrinkers = ctas(two ? 2 : 1, c.splits);
-    c.expanders = ctas(2, c.parts);
+    c.shrinkers = ctas(two ? 2 : 1, c.stile, c.splits);
+    c.expanders = ctas(2, c.tile, c.parts);
     return c;
 }
 
@@ -995,6 +1014,7 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
     p.slices = s->slices;
     p.scope = c.scope;
     p.tile = c.tile;
+    p.stile = c.stile;
     p.shrinkers = p.ctas = c.shrinkers;
     p.splits = c.splits;
     p.parts = c.parts;

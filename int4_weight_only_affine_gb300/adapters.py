@@ -7,7 +7,6 @@ f16_lora (``include/w4a16.h``)::
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -38,12 +37,15 @@ def _half(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-def _rows(t: torch.Tensor, name: str):
-    """(device pointer, row stride) of a float16 [rows][columns] tensor with contiguous rows."""
+def _rows(t: torch.Tensor, name: str, shape):
+    """(device pointer, row stride) of a float16 tensor of this shape with contiguous rows."""
     _half(t, name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows][columns] with contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 8  # (of one row the stride is never used)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [{shape[0]}][{shape[1]}]")
+    strides = t.stride()
+    if strides[1] != 1 and shape[1] > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), strides[0] if shape[0] > 1 else 8  # (of one row the stride is never used)
 
 
 class Adapters:
@@ -81,15 +83,19 @@ class Adapters:
                                 a.stride(0) if n > 1 else 8, b.stride(0) if n > 1 else 8, n, rank, k, self.N, slices,
                                 (ctypes.c_int32 * 4)(*ends))
         self.ptr = ctypes.addressof(self.struct)
+        self.device = a.device
+        self.sized = None  # (rows, workspace bytes) asked last
 
 
 def lora_workspace_bytes(adapters: Adapters, rows: int) -> int:
-    return int(lib.f16_lora_workspace_bytes(adapters.ptr, rows))
+    if adapters.sized is None or adapters.sized[0] != rows:
+        adapters.sized = rows, int(lib.f16_lora_workspace_bytes(adapters.ptr, rows))
+    return adapters.sized[1]
 
 
 def lora_workspace(adapters: Adapters, rows: int) -> torch.Tensor:
     """A workspace for f16_lora with this many rows, for calls that do not overlap."""
-    return torch.empty(max(lora_workspace_bytes(adapters, rows), 16), dtype=torch.uint8, device=adapters.a.device)
+    return torch.empty(max(lora_workspace_bytes(adapters, rows), 16), dtype=torch.uint8, device=adapters.device)
 
 
 def f16_lora(x: torch.Tensor, adapters: Adapters, ids: torch.Tensor, y: torch.Tensor, out: torch.Tensor | None = None,
@@ -97,16 +103,16 @@ def f16_lora(x: torch.Tensor, adapters: Adapters, ids: torch.Tensor, y: torch.Te
     """out[m] = y[m] + scale[a] * (x[m] @ A_a.T) @ B_a.T with a = ids[m] (int32; negative: y[m]).
     x float16 [rows][K], y and out [rows][N], any row strides that are multiples of 8; out is y itself when None.
     workspace: from lora_workspace; a fresh one is made when None."""
-    px, xs = _rows(x, "x")
-    py, ys = _rows(y, "y")
-    po, os = (py, ys) if out is None else _rows(out, "out")
-    m = x.shape[0]
-    if x.shape[1] != adapters.K or y.shape != (m, adapters.N) or (out is not None and out.shape != y.shape):
-        raise ValueError(f"x must be [{m}][{adapters.K}], y and out [{m}][{adapters.N}]")
-    if ids.numel() != m:
-        raise ValueError("ids must be [rows]")
-    if workspace is None:
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # (the memory is that stream's)
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    m = ids.numel()
+    px, xs = _rows(x, "x", (m, adapters.K))
+    py, ys = _rows(y, "y", (m, adapters.N))
+    po, os = (py, ys) if out is None else _rows(out, "out", (m, adapters.N))
+    if workspace is None and stream is None:
+        workspace = lora_workspace(adapters, m)
+    elif workspace is None:
+        with torch.cuda.stream(stream):  # (the memory is that stream's)
             workspace = lora_workspace(adapters, m)
     _check("f16_lora", lib.f16_lora(px, xs, py, ys, po, os, adapters.ptr, _dev(ids, "ids", (torch.int32,)), m,
                                     _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(), _stream(stream)))

@@ -48,6 +48,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kScope = 1024;        // rows whose ids a CTA sorts
 constexpr int kFewRows = 32;        // rows that a warp sorts
+constexpr int kFewOfItem = 16;      // rows that shrink multiplies by mma.sync
 constexpr int kMaxAdapters = 4096;  // buckets of the histogram
 constexpr int kMaxSlices = 4;
 constexpr int kMaxRank = 128;
@@ -364,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
     const uint32_t full = (uint32_t)__cvta_generic_to_shared(bars), empty = full + 8 * kMostStages,
                    done = full + 16 * kMostStages;
     const int F = p.slices * p.rank, F16 = (F + 15) / 16 * 16, columns = tmem_columns(F16);
-    if (tid == 0) {
+    const bool tensor = p.M > kFewOfItem;  // some item may be of many rows
+    if (tid == 0 && tensor) {
         for (int i = 0; i < 2 * kMostStages + 1; ++i) mbar_init(full + 8 * i, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
         asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&xbox) : "memory");
     }
-    if (warp == 2) {
+    if (warp == 2 && tensor) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          (uint32_t)__cvta_generic_to_shared(&tmem_at)),
                      "r"(columns)
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
         const int split = u % splits, bucket = sorter.item(p, u / splits, rows, unit, n);
         const int c0 = (int)((long long)kb * split / splits), chunks = (int)((long long)kb * (split + 1) / splits) - c0;
         if (bucket == p.adapters) continue;  // (alike for all threads; rows is written again after a barrier)
-        if (n <= 16) {
+        if (n <= kFewOfItem) {
             const uint16_t *a = p.a + bucket * p.a_adapter;
             const int b0 = c0 * (kStageK / 32), b1 = min((p.K + 31) / 32, (c0 + chunks) * (kStageK / 32));
             float *red = reinterpret_cast<float *>(smem);
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     }
     __syncthreads();
-    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
+    if (warp == 2 && tensor) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
 }
 
 // ---- expand ----
@@ -1022,17 +1024,19 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
     const int rk = round_rank(s->rank), F = s->rank * s->slices, hist = (s->adapters + 1) * 4;
     // A as [adapters][slices * rank][K], boxes of 64 k and all rows (two boxes of more
     // than 256); x as [M][K], boxes of 64 k of one row, copied four at a time, and of 8.
-    CUtensorMap amap, xmap, xbox;
+    // (None is used where every item has few rows.)
+    CUtensorMap amap = {}, xmap = {}, xbox = {};
     p.boxes = F > 256 ? 2 : 1;
     p.box_rows = p.boxes == 1 ? F : (F / 2 + 7) / 8 * 8;
     const uint64_t x_bytes = 2ull * (M > 1 ? x_row : s->K);
-    if (!make_map_3d(&amap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, s->a, (uint64_t)s->K, (uint64_t)F, (uint64_t)s->adapters,
+    if (M > kFewOfItem &&
+        (!make_map_3d(&amap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, s->a, (uint64_t)s->K, (uint64_t)F, (uint64_t)s->adapters,
                      2ull * s->K, 2ull * (s->adapters > 1 ? s->a_adapter : 8), kHalfK, (uint32_t)p.box_rows, 1,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kHalfK, 1,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_2d(&xbox, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kHalfK, 8,
-                     CU_TENSOR_MAP_SWIZZLE_128B))
+                     CU_TENSOR_MAP_SWIZZLE_128B)))
         return encode_fn() ? W4_ERR_SHAPE : W4_ERR_DEVICE;
     p.room = c.room;
     st = launch(shrink_kernel, (long long)c.scopes * c.shrinkers, p.room + hist + 1024, stream, amap, xmap, xbox, p);

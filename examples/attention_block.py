@@ -1,5 +1,6 @@
 """A decoder layer's attention block on int4 weights: q/k/v projections, rotary
-positions, a paged cache, attention over it, o projection.
+positions, a paged cache, attention over it, o projection; norms of the query
+and key heads and low-rank adapters of each request where the block has them.
 
 Four prompts of different lengths go in as one batch (their projections
 dequantised once, or through the int4 GEMM up to 128 tokens), then single
@@ -23,10 +24,12 @@ import synth  # noqa: E402
 
 
 class AttentionBlock:
-    """The block and its cache.  The projections of q, k and v are one weight."""
+    """The block and its cache.  The projections of q, k and v are one weight.
+    norms: normalise the query and key heads; adapters: how many requests can
+    choose from, of this rank."""
 
     def __init__(self, hidden=2048, q_heads=16, kv_heads=2, dim=128, pages=256, page_size=16, max_tokens=512,
-                 base=1e6, seed=0, device="cuda"):
+                 base=1e6, seed=0, device="cuda", norms=False, adapters=0, rank=16):
         self.hidden, self.q_heads, self.kv_heads, self.dim, self.page_size = hidden, q_heads, kv_heads, dim, page_size
         self.qkv = self._weight(seed, (q_heads + 2 * kv_heads) * dim, hidden, device)
         self.o = self._weight(seed + 1, hidden, q_heads * dim, device)
@@ -34,6 +37,19 @@ class AttentionBlock:
         self.cache = w4.KVCache(*(torch.zeros(shape, dtype=torch.float16, device=device) for _ in range(2)))
         self.rope = w4.Rope(*w4.rope_turns(dim, base=base, device=device))
         self.workspace = w4.attention_workspace(self.cache, q_heads, max_tokens)
+        gen = torch.Generator(device=device).manual_seed(seed)
+        self.q_norm = self.k_norm = self.qkv_adapters = self.o_adapters = None
+        if norms:
+            self.q_norm, self.k_norm = (w4.HeadNorm(1 + 0.2 * torch.randn(dim, generator=gen, device=device)) for _ in range(2))
+        if adapters:
+            self.qkv_adapters = self._adapters(gen, adapters, rank, hidden, [q_heads * dim, kv_heads * dim, kv_heads * dim])
+            self.o_adapters = self._adapters(gen, adapters, rank, q_heads * dim, [hidden])
+
+    @staticmethod
+    def _adapters(gen, n, rank, k, columns):
+        a, b = (torch.randn(*shape, generator=gen, device=gen.device) for shape in
+                ((n, len(columns), rank, k), (n, sum(columns), rank)))
+        return w4.Adapters((a * k**-0.5).half(), (b * 0.1).half(), columns=columns)
 
     @staticmethod
     def _weight(seed, n, k, device):
@@ -50,14 +66,19 @@ class AttentionBlock:
             return w4.w4_gemm(x, *weight)
         return w4.f16_gemm(x, w4.w4_dequant_f16(*weight))
 
-    def __call__(self, x, batch):
-        """x [tokens][hidden]: the new tokens of the batch's sequences, one after the other."""
+    def __call__(self, x, batch, ids=None):
+        """x [tokens][hidden]: the new tokens of the batch's sequences, one after the other;
+        ids int32 [tokens]: the adapter of each (negative: none)."""
         n, hq, hk, d = x.shape[0], self.q_heads, self.kv_heads, self.dim
-        qkv = self._project(x, self.qkv).view(n, hq + 2 * hk, d)
+        qkv = self._project(x, self.qkv)
+        if ids is not None:
+            w4.f16_lora(x, self.qkv_adapters, ids, qkv)
+        qkv = qkv.view(n, hq + 2 * hk, d)
         q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
-        w4.f16_kv_append(k, v, self.cache, batch, rope=self.rope, q=q, y=q)
-        y = w4.f16_attention(q, self.cache, batch, workspace=self.workspace)
-        return self._project(y.view(n, hq * d), self.o)
+        w4.f16_kv_append(k, v, self.cache, batch, rope=self.rope, q=q, y=q, q_norm=self.q_norm, k_norm=self.k_norm)
+        y = w4.f16_attention(q, self.cache, batch, workspace=self.workspace).view(n, hq * d)
+        out = self._project(y, self.o)
+        return out if ids is None else w4.f16_lora(y, self.o_adapters, ids, out)
 
 
 def page_table(lengths, page_size, pages, seed=0):

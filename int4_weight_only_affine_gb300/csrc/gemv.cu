@@ -214,6 +214,15 @@ __device__ __forceinline__ Key2 warp_insert64(Key2 run, Key2 c, int lane) {
 // warp in shared memory) and inserted when it is full.
 __device__ __forceinline__ Key2 warp_best64(const float *z, int n0, int i0, int i1, int k, bool ruled,
                                             uint64_t *pending, int lane) {
+    if (i1 - i0 <= 192) {  // (up to three chunks cost no more than the bound)
+        Key2 run{0ull, 0ull};
+        for (int c = i0; c < i1; c += 64) {
+            const int i = c + lane, j = c + 32 + lane;
+            const Key2 next{i < i1 ? row_key(z[i], n0 + i, ruled) : 0ull, j < i1 ? row_key(z[j], n0 + j, ruled) : 0ull};
+            run = c == i0 ? warp_sort64(next, lane) : warp_insert64(run, next, lane);
+        }
+        return run;
+    }
     uint64_t f0 = 0ull, f1 = 0ull;
     for (int i = i0 + lane; i < i1; i += 32) {
         const uint64_t key = row_key(z[i], n0 + i, ruled);
@@ -221,7 +230,6 @@ __device__ __forceinline__ Key2 warp_best64(const float *z, int n0, int i0, int 
         f0 = umax64(f0, key);
     }
     Key2 run = warp_sort64(Key2{f0, f1}, lane);
-    if (i1 - i0 <= 64) return run;  // (all of them)
     const uint64_t least = __shfl_sync(0xffffffffu, k <= 32 ? run.a : run.b, (k - 1) & 31);
     run = Key2{0ull, 0ull};
     int held = 0;
@@ -292,14 +300,20 @@ struct StreamArgs {
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
-constexpr int kLmThreads = kThreads + 32;  // lm_head pass 1: a warp for the rules beside the others
+constexpr int kLmThreads = kThreads + 32;  // lm_head pass 1 with rules: a warp for them beside the others
 
 // FMT: the scale-layout class of the weight (kFmtG64, kFmtS128, kFmtAny,
 // kFmtG32).
-template <int NT, bool LMHEAD, bool M1, int FMT>
-__global__ void __launch_bounds__(LMHEAD ? kLmThreads : kThreads, NT == 1 ? 2 : 1)
+// HEAD: kLinear, or lm_head's pass 1 without or with rules (kernels of their own: with
+// the rules' code in one kernel a call without rules took 36.4 us for 35.2 at one row of
+// 2048 by 151936).
+constexpr int kLinear = 0, kLmHead = 1, kLmHeadRules = 2;
+template <int NT, int HEAD, bool M1, int FMT>
+__global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, NT == 1 ? 2 : 1)
     stream_kernel(const __grid_constant__ CUtensorMap tm3, const __grid_constant__ CUtensorMap tm2,
                   const __grid_constant__ StreamArgs a) {
+    constexpr bool LMHEAD = HEAD != kLinear, kRuled = HEAD == kLmHeadRules;
+    constexpr int kWarps = (kRuled ? kLmThreads : kThreads) / 32;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -318,6 +332,7 @@ __global__ void __launch_bounds__(LMHEAD ? kLmThreads : kThreads, NT == 1 ? 2 : 
     const int ngl = max(0, gs1 - gs0);
     const int nch = (ngl + kChunkGroups - 1) / kChunkGroups;
     const int out16 = kTileRows * M;
+    const int by_m = LMHEAD && !M1 ? (65536 + M - 1) / M : 0;  // e / M = e * by_m >> 16 for e < out16 <= 256
 
     uint32_t *xf = reinterpret_cast<uint32_t *>(sb + a.off_xf);
     float *xsum = reinterpret_cast<float *>(sb + a.off_xsum);
@@ -390,12 +405,11 @@ __global__ void __launch_bounds__(LMHEAD ? kLmThreads : kThreads, NT == 1 ? 2 : 
             for (int s = 0; s < S; ++s)
                 if (issued_any & (1u << s)) mbar_wait(full_bar(s), (issued_ph >> s) & 1);
         }
-    } else if (LMHEAD && warp > kConsumerWarps) {
-        // ---------------- lm_head: one more warp, for the rules of the selection ----------------
+    } else if (kRuled && warp > kConsumerWarps) {
+        // ---------------- lm_head with rules: one more warp, for them ----------------
         pdl_wait();
-        if (a.rules.on)
-            rules_begin(a.rules, RulesMemory(sb + a.off_rules, M), M, N, t0 * kTileRows,
-                        min(N, t1 * kTileRows) - t0 * kTileRows, lane);
+        rules_begin(a.rules, RulesMemory(sb + a.off_rules, M), M, N, t0 * kTileRows,
+                    min(N, t1 * kTileRows) - t0 * kTileRows, lane);
     } else {
         // ---------------- consumers ----------------
         const int lg = lane >> 2, lt = lane & 3;
@@ -489,7 +503,8 @@ __global__ void __launch_bounds__(LMHEAD ? kLmThreads : kThreads, NT == 1 ? 2 : 
                         const int row = e / M, col = e % M;
                         if (row0 + row < N) a.y[(size_t)col * N + row0 + row] = __half_as_ushort(__float2half_rn(v));
                     } else if (LMHEAD) {
-                        res[e % M * a.ldr + tl * kTileRows + e / M] = v;
+                        const int row = M1 ? e : e * by_m >> 16;
+                        res[(e - row * M) * a.ldr + tl * kTileRows + row] = v;
                     } else {
                         res[tl * out16 + e] = v;
                     }
@@ -508,7 +523,8 @@ __global__ void __launch_bounds__(LMHEAD ? kLmThreads : kThreads, NT == 1 ? 2 : 
                     const int row = e / M, col = e % M, r = (t0 + tl) * kTileRows + row;
                     if (r < N) a.y[(size_t)col * N + r] = __half_as_ushort(__float2half_rn(v));
                 } else if (LMHEAD) {
-                    res[e % M * a.ldr + tl * kTileRows + e / M] = v;
+                    const int row = M1 ? e : e * by_m >> 16;
+                    res[(e - row * M) * a.ldr + tl * kTileRows + row] = v;
                 } else {
                     res[tl * out16 + e] = v;
                 }
@@ -540,14 +556,12 @@ __global__ void __launch_bounds__(LMHEAD ? kLmThreads : kThreads, NT == 1 ? 2 : 
     // The keys of this CTA's rows, best first, padded with 0 (below every key).
     const int n0 = t0 * kTileRows;
     const int rows = min(N, t1 * kTileRows) - n0;
-    constexpr int kWarps = kLmThreads / 32;
-    const bool ruled = a.rules.on;
-    if (ruled) rules_apply(a.rules, RulesMemory(sb + a.off_rules, M), res, a.ldr, M, n0, rows, tid, kLmThreads);
+    if (kRuled) rules_apply(a.rules, RulesMemory(sb + a.off_rules, M), res, a.ldr, M, n0, rows, tid, kLmThreads);
     if (a.k == 1) {
-        // Greedy selection: warp w takes activation rows w, w + 10, ...
+        // Greedy selection: warp w takes every kWarps-th activation row from w on.
         for (int m = warp; m < M; m += kWarps) {
             uint64_t best = 0ull;
-            for (int i = lane; i < rows; i += 32) best = umax64(best, row_key(res[m * a.ldr + i], n0 + i, ruled));
+            for (int i = lane; i < rows; i += 32) best = umax64(best, row_key(res[m * a.ldr + i], n0 + i, kRuled));
             best = shfl_max_u64(best);
             if (lane == 0) a.ws[(size_t)m * gridDim.x + blockIdx.x] = best;
         }
@@ -556,11 +570,11 @@ __global__ void __launch_bounds__(LMHEAD ? kLmThreads : kThreads, NT == 1 ? 2 : 
     // A row goes to `share` warps, one where there are rows for all of them or few keys.
     uint64_t(*lists)[64] = reinterpret_cast<uint64_t(*)[64]>(sb);  // (the ring is free now)
     uint64_t *pending = reinterpret_cast<uint64_t *>(sb) + (kWarps + warp) * 64;
-    const int share = max(1, min(kWarps / M, (rows + 127) / 128));
+    const int share = max(1, min(kWarps / M, (rows + 63) / 64));
     const int part = warp % share;
     for (int m = warp / share; m < M; m += kWarps / share) {
         const int i0 = (int)((long long)rows * part / share), i1 = (int)((long long)rows * (part + 1) / share);
-        const Key2 run = warp_best64(res + m * a.ldr, n0, i0, i1, a.k, ruled, pending, lane);
+        const Key2 run = warp_best64(res + m * a.ldr, n0, i0, i1, a.k, kRuled, pending, lane);
         if (share == 1) {
             uint64_t *out = a.ws + ((size_t)m * gridDim.x + blockIdx.x) * a.k;
             if (lane < a.k) out[lane] = run.a;
@@ -891,12 +905,12 @@ __global__ void __launch_bounds__(kSeqThreads, 1) seq_kernel(const __grid_consta
 template <int FMT>
 const void *stream_kernel_ptr_f(int M, bool lmhead) {
     if (lmhead)
-        return M == 1 ? (const void *)stream_kernel<1, true, true, FMT>
-               : M <= 8 ? (const void *)stream_kernel<1, true, false, FMT>
-                        : (const void *)stream_kernel<2, true, false, FMT>;
-    return M == 1 ? (const void *)stream_kernel<1, false, true, FMT>
-           : M <= 8 ? (const void *)stream_kernel<1, false, false, FMT>
-                    : (const void *)stream_kernel<2, false, false, FMT>;
+        return M == 1 ? (const void *)stream_kernel<1, kLmHead, true, FMT>
+               : M <= 8 ? (const void *)stream_kernel<1, kLmHead, false, FMT>
+                        : (const void *)stream_kernel<2, kLmHead, false, FMT>;
+    return M == 1 ? (const void *)stream_kernel<1, kLinear, true, FMT>
+           : M <= 8 ? (const void *)stream_kernel<1, kLinear, false, FMT>
+                    : (const void *)stream_kernel<2, kLinear, false, FMT>;
 }
 
 const void *stream_kernel_ptr(int M, bool lmhead, int fmt) {
@@ -1282,7 +1296,7 @@ bool ensure_smem(const void *kern, size_t bytes) {
     return true;
 }
 
-template <int NT, bool LM, bool M1, int FMT>
+template <int NT, int HEAD, bool M1, int FMT>
 int launch_stream(const StreamPlan &p, const uint32_t *qw, bool overlap, cudaStream_t st) {
     CUtensorMap tm3, tm2;
     const uint64_t KW = (uint64_t)p.a.K / 8;
@@ -1296,11 +1310,11 @@ int launch_stream(const StreamPlan &p, const uint32_t *qw, bool overlap, cudaStr
     } else {
         tm3 = tm2;  // never used: every chunk takes the 2-D path
     }
-    auto kern = stream_kernel<NT, LM, M1, FMT>;
+    auto kern = stream_kernel<NT, HEAD, M1, FMT>;
     if (!ensure_smem(reinterpret_cast<const void *>(kern), p.smem)) return W4_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid, 1, 1);
-    cfg.blockDim = dim3(LM ? kLmThreads : kThreads, 1, 1);
+    cfg.blockDim = dim3(HEAD == kLmHeadRules ? kLmThreads : kThreads, 1, 1);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -1333,21 +1347,21 @@ int check_common(const void *x, const uint32_t *qw, const uint16_t *sc, const ui
     return W4A16_OK;
 }
 
-template <bool LM, int FMT>
+template <int HEAD, int FMT>
 int launch_stream_f(const StreamPlan &p, const uint32_t *qw, bool ov, cudaStream_t s) {
     const int M = p.a.M;
-    return M == 1 ? launch_stream<1, LM, true, FMT>(p, qw, ov, s)
-           : M <= 8 ? launch_stream<1, LM, false, FMT>(p, qw, ov, s)
-                    : launch_stream<2, LM, false, FMT>(p, qw, ov, s);
+    return M == 1 ? launch_stream<1, HEAD, true, FMT>(p, qw, ov, s)
+           : M <= 8 ? launch_stream<1, HEAD, false, FMT>(p, qw, ov, s)
+                    : launch_stream<2, HEAD, false, FMT>(p, qw, ov, s);
 }
 
-template <bool LM>
+template <int HEAD>
 int launch_stream_any(const StreamPlan &p, const uint32_t *qw, bool ov, cudaStream_t s) {
     const int fmt = fmt_class(p.a.f);
-    return fmt == kFmtG64    ? launch_stream_f<LM, kFmtG64>(p, qw, ov, s)
-           : fmt == kFmtS128 ? launch_stream_f<LM, kFmtS128>(p, qw, ov, s)
-           : fmt == kFmtG32  ? launch_stream_f<LM, kFmtG32>(p, qw, ov, s)
-                             : launch_stream_f<LM, kFmtAny>(p, qw, ov, s);
+    return fmt == kFmtG64    ? launch_stream_f<HEAD, kFmtG64>(p, qw, ov, s)
+           : fmt == kFmtS128 ? launch_stream_f<HEAD, kFmtS128>(p, qw, ov, s)
+           : fmt == kFmtG32  ? launch_stream_f<HEAD, kFmtG32>(p, qw, ov, s)
+                             : launch_stream_f<HEAD, kFmtAny>(p, qw, ov, s);
 }
 
 int gemv_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const uint16_t *bi, uint16_t *y, int M,
@@ -1368,7 +1382,7 @@ int gemv_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const u
     p.a.rules = Rules{};
     const bool ov = (flags & W4A16_OVERLAP_PREVIOUS) != 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return launch_stream_any<false>(p, qw, ov, s);
+    return launch_stream_any<kLinear>(p, qw, ov, s);
 }
 
 int lmhead_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const uint16_t *bi, int M, int N, int K,
@@ -1387,7 +1401,7 @@ int lmhead_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const
     p.a.ws = ws;
     const bool ov = (flags & W4A16_OVERLAP_PREVIOUS) != 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int st = launch_stream_any<true>(p, qw, ov, s);
+    const int st = rules.on ? launch_stream_any<kLmHeadRules>(p, qw, ov, s) : launch_stream_any<kLmHead>(p, qw, ov, s);
     if (st != W4A16_OK) return st;
     // Pass 2 is launched as a programmatic dependent: its launch overlaps pass 1
     // and it waits (griddepcontrol.wait) for pass 1's results.

@@ -288,7 +288,7 @@ __host__ __device__ constexpr int tmem_columns(int ranks) {
 // takes 16 contiguous bytes of a row as the k indexes of two products.  The warps
 // share the CTA's part of K, blocks kb0 .. kb1 - 1 of 32 k, and add their sums through
 // shared memory, 16 * MT ranks at a time.  (64 rows of 25 adapters, 11008 k, rank 32:
-// 17 us with tcgen05, see below for this.)
+// 14.1 us, 17 with tcgen05.)
 template <int MT, int NT, int AHEAD>
 __device__ __forceinline__ void shrink_few(const LoraArgs &p, const uint16_t *a, const int *rows, int n, int split,
                                            int kb0, int kb1, float *red) {
@@ -946,7 +946,7 @@ int launch(K kernel, long long ctas, int smem, void *stream, const A &...args) {
 namespace {
 
 // Whether join runs: where there are more ranks than 64 for many rows.  (1570 rows on
-// q|k|v, rank 64: 24.9 us with it, 33.5 without; on gate|up, rank 16: 47.4 and 43.0.)
+// q|k|v, rank 64: 24.2 us with it, 33.5 without; on gate|up, rank 16: 47.4 and 43.0.)
 bool joined(const f16_adapters *s, int M) { return M > kFewRows && s->slices * s->rank > 64; }
 
 // The workspace: the shares of h, then what join leaves.

@@ -26,7 +26,7 @@
 //
 // Measured: rope of 16384 tokens x 16 heads of 128, 134 MB, 21.5 us, 6.2 TB/s;
 // append of 16384 tokens, 16 + 2 x 8 heads, 268 MB, 43.7 us, 6.1 TB/s, against
-// 6.69 TB/s of a plain copy.  Steps of a few tokens: 1.5 and 2.5 us in a graph,
+// 6.69 TB/s of a plain copy.  Steps of a few tokens: 1.7 and 2.4 us in a graph,
 // the launch and one chain of dependent reads.  With norms: the same rope 25.2 us;
 // an append of 18 heads of 64, 6500 tokens, 36.9 us (25.2 without): instructions.
 #include <math.h>
@@ -114,7 +114,7 @@ __device__ __forceinline__ float2 turn_of(const Rot &r, int i, int p) {
 // Those of the lane's unit, pairs 4u .. 4u + 3.  The lanes that hold the same
 // unit of different heads (sub = 0 .. side - 1) turn alike, and four or two of
 // them share the sines out among themselves (SHARE: not where a lane has one head
-// and the path from its load to its store counts: 2.60 us against 2.76 for a
+// and the path from its load to its store counts: 2.41 us against 2.76 for a
 // step of 16 tokens).  Every lane of the warp takes part.
 template <bool SHARE>
 __device__ __forceinline__ Turn turns_of(const Rot &r, int u, int units, int side, int sub, bool rotated, int p) {
@@ -136,10 +136,10 @@ __device__ __forceinline__ Turn turns_of(const Rot &r, int u, int units, int sid
             t.c[2 + k] = __shfl_sync(~0u, v.x, units + u);
             t.s[2 + k] = __shfl_sync(~0u, v.y, units + u);
         }
-    } else {
+    } else if (rotated) {  // (one branch, so that the four loads go out together)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (rotated) v = turn_of(r, 4 * u + i, p);
+            v = turn_of(r, 4 * u + i, p);
             t.c[i] = v.x;
             t.s[i] = v.y;
         }

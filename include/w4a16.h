@@ -279,9 +279,10 @@ W4A16_API int lm_head_argmax_topk_rules(const uint16_t *x, const uint32_t *qweig
  *   flags    W4_COUNTS_PROMPT: tokens of a prompt (bit 15 is set); without it
  *            tokens of the output (the count goes up, and stays at 32767)
  *            W4_COUNTS_RESET: the sequences' rows are cleared first (a request
- *            takes its slot); their slots must differ
- *   batch 0..65535;  total >= 0;  a token past N, a slot past the last or offsets
- *   out of order are skipped and reported by w4a16_device_status as W4_ERR_INDEX.
+ *            takes its slot); of sequences with one slot the last takes it
+ *   batch 0..65535;  total >= 0;  a token past N, a slot past the last, offsets
+ *   out of order and slots taken again are skipped and reported by
+ *   w4a16_device_status as W4_ERR_INDEX.
  * Pointers need their natural alignment only.  Results do not depend on the
  * order in which tokens are counted.
  * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_DEVICE, W4_ERR_LAUNCH.
@@ -420,8 +421,8 @@ typedef struct {
  *     out[m] = y[m] + scale[a] * (x[m] A_a^T) B_a^T,   a = ids[m],
  *   the A being that of the column's slice; rows with a negative id get y[m].
  *   x        binary16 [M][K], y and out binary16 [M][N]: rows x_row, y_row and
- *            out_row elements apart (multiples of 8); out may be y, else they
- *            must not overlap
+ *            out_row elements apart (multiples of 8; out_row >= N); out may be y,
+ *            else they must not overlap
  *   ids      int32 [M], in any order and mix (read on the device: a captured graph
  *            can be replayed with others); an id past the last adapter counts as
  *            negative and is reported by w4a16_device_status as W4_ERR_INDEX.
@@ -443,7 +444,8 @@ W4A16_API int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int6
                        size_t workspace_bytes, void *stream);
 
 /* Workspace bytes for f16_lora (0 if the sizes are invalid).  Depends only on the
- * adapters' sizes and M (not monotonic in M: ask for the M of the call). */
+ * adapters' sizes and M, and grows with M: a workspace for the most rows serves
+ * all calls with fewer. */
 W4A16_API size_t f16_lora_workspace_bytes(const f16_adapters *adapters, int M);
 
 /*

@@ -88,20 +88,21 @@ class Adapters:
 
 
 def lora_workspace_bytes(adapters: Adapters, rows: int) -> int:
-    if adapters.sized is None or adapters.sized[0] != rows:
-        adapters.sized = rows, int(lib.f16_lora_workspace_bytes(adapters.ptr, rows))
-    return adapters.sized[1]
+    sized = adapters.sized
+    if sized is None or sized[0] != rows:
+        adapters.sized = sized = rows, int(lib.f16_lora_workspace_bytes(adapters.ptr, rows))
+    return sized[1]
 
 
 def lora_workspace(adapters: Adapters, rows: int) -> torch.Tensor:
-    """A workspace for f16_lora with this many rows, for calls that do not overlap."""
+    """A workspace for f16_lora with up to this many rows, for calls that do not overlap."""
     return torch.empty(max(lora_workspace_bytes(adapters, rows), 16), dtype=torch.uint8, device=adapters.device)
 
 
 def f16_lora(x: torch.Tensor, adapters: Adapters, ids: torch.Tensor, y: torch.Tensor, out: torch.Tensor | None = None,
              stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """out[m] = y[m] + scale[a] * (x[m] @ A_a.T) @ B_a.T with a = ids[m] (int32; negative: y[m]).
-    x float16 [rows][K], y and out [rows][N], any row strides that are multiples of 8; out is y itself when None.
+    x float16 [rows][K], y and out [rows][N], any row strides that are multiples of 8 (out's rows apart); out is y itself when None.
     workspace: from lora_workspace; a fresh one is made when None."""
     if not isinstance(ids, torch.Tensor):
         raise TypeError("ids must be a torch.Tensor")

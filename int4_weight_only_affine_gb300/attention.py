@@ -290,8 +290,8 @@ def f16_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBat
         hq = q.shape[1]
         if q.shape[0] != n or q.shape[2] != d or y.shape != q.shape:
             raise ValueError(f"q and y must be [{n}][heads][{d}]")
-    elif y is not None:
-        raise ValueError("y is the rotated q: it needs q")
+    elif y is not None or q_norm is not None:
+        raise ValueError("y is the rotated q, and q_norm norms it: they need q")
     pr = None if rope is None else rope.ptr
     pp = None if positions is None else _ints(positions, "positions")
     if q_norm is None and k_norm is None:

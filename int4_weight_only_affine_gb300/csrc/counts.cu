@@ -14,8 +14,8 @@
 // its share of the sequence's tokens in shared memory and writes the row once,
 // so that clearing costs no pass of its own.  Every block of a row reads the
 // sequence's tokens (from L2); the row's write bounds the call.  Blocks of half
-// and twice the tokens were measured 10 % and 25 % slower (16 rows of 151936,
-// 4096 tokens each).
+// and twice the tokens were measured 10 % and 25 % slower (16 rows of 151936
+// and 20900 tokens: 3.8 us).
 #include "common.cuh"
 
 namespace w4a16 {
@@ -94,8 +94,13 @@ __global__ void __launch_bounds__(kThreads) reset_kernel(const CountArgs a) {
     const int b = blockIdx.y, lo = blockIdx.x * kSpan, span = min(kSpan, a.N - lo);
     uint16_t *row = row_of(a, b);
     if (!row) return;
+    bool taken = false;  // by a later sequence: the row is that one's
+    for (int i = b + 1 + threadIdx.x; i < a.batch; i += kThreads) taken |= __ldg(a.slot + i) == __ldg(a.slot + b);
     for (int i = threadIdx.x; i < kSpan / 4; i += kThreads) reinterpret_cast<uint4 *>(seen)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+    if (__syncthreads_or(taken)) {
+        if (threadIdx.x == 0) atomicExch(&g_bad_index, 1);
+        return;
+    }
     int first, end;
     if (sequence(a, b, first, end)) {
         constexpr int kAhead = 8;

@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
         asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&xbox) : "memory");
     }
+    // (Kept through the wait: the kernel before has its tensor memory already, or, being
+    // one that takes it after it released this one, more shared memory than is left beside.)
     if (warp == 2 && tensor) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          (uint32_t)__cvta_generic_to_shared(&tmem_at)),
@@ -986,6 +988,7 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
         !stride_ok(x_row) || !stride_ok(y_row) || !stride_ok(out_row) || !stride_ok(s->a_adapter) ||
         !stride_ok(s->b_adapter))
         return W4_ERR_ALIGN;
+    if (M > 1 && out_row < s->N) return W4_ERR_SHAPE;
     const Cut c = cut_of(s, M, p.block[s->slices]);
     const Workspace ws = workspace_of(s, M, c);
     if (!workspace || workspace_bytes < ws.bytes) return W4_ERR_WORKSPACE;

@@ -28,7 +28,7 @@
 // append of 16384 tokens, 16 + 2 x 8 heads, 268 MB, 43.7 us, 6.1 TB/s, against
 // 6.69 TB/s of a plain copy.  Steps of a few tokens: 1.7 and 2.4 us in a graph,
 // the launch and one chain of dependent reads.  With norms: the same rope 25.2 us;
-// an append of 18 heads of 64, 6500 tokens, 36.9 us (25.2 without): instructions.
+// an append of 14 + 2 x 2 heads of 64, 25000 tokens, 37.0 us (25.3 without): instructions.
 #include <math.h>
 #include <string.h>
 
@@ -47,7 +47,7 @@ namespace {
 constexpr int kManyHeads = 8, kSomeHeads = 4;
 constexpr int kWarps = 4;
 constexpr int kBlocks = 8;  // resident on an SM
-constexpr int kAppendBlocks = 7;  // (append of 6500 tokens, 14 + 2 x 2 heads of 64: 25.2 us; 8: 26.9, spilling; 6: 26.7)
+constexpr int kAppendBlocks = 7;  // (append of 25000 tokens, 14 + 2 x 2 heads of 64: 25.2 us; 8: 26.9, spilling; 6: 26.7)
 constexpr int kNormBlocks = 6;  // with norms, whose sums and weights take registers (the same append: 36.9; 8: 39.6; 5: 38.1)
 
 struct Rot {

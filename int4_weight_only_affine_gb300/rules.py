@@ -7,7 +7,7 @@ A decoding loop over requests in slots::
     token_counts_add(counts, slots, prompts, offsets, prompt=True, reset=True)   # requests take their slots
     rules = LogitRules(counts, slots, repetition, presence, frequency, biases, allowed)   # once per batch
     idx, val = lm_head_argmax_topk(x, ..., rules=rules)      # each step
-    token_counts_add(counts, slots, idx[:, 0])
+    token_counts_add(counts, slots, chosen)                  # int32 [rows], idx[:, 0] where greedy
 
 Everything but the shapes is read on the device when the kernels run: a
 captured graph can be replayed with other slots, penalties, masks and biases.
@@ -63,7 +63,7 @@ def token_counts_add(counts: TokenCounts, slots: torch.Tensor, tokens: torch.Ten
     sequences' rows: sequence b, in slot slots[b] (int32; negative: none), has the
     tokens offsets[b] .. offsets[b + 1] - 1 (int32 [batch + 1]), or token b where
     offsets is None.  prompt: they are a prompt's, else the output's.  reset: the
-    rows are cleared before (requests take their slots, which must differ)."""
+    rows are cleared before (requests take their slots; of equal ones the last takes it, and device_status reports it)."""
     batch = slots.numel()
     if offsets is not None and offsets.numel() != batch + 1:
         raise ValueError("offsets must be [batch + 1]")

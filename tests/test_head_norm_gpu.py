@@ -196,6 +196,11 @@ def test_wrong_norms_are_refused(w4):
         w4.HeadNorm(w.double())
     with pytest.raises(ValueError):
         w4.HeadNorm(w.view(8, 8))
+    page = torch.zeros(2, 16, 4, 64, dtype=torch.float16, device="cuda")
+    ints = torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):  # a norm of queries that are not there
+        w4.f16_kv_append(x, x, w4.KVCache(page, page.clone()), w4.KVBatch(ints[:1].view(1, 1), ints, ints[:1], 3, 3),
+                         q_norm=w4.HeadNorm(w))
     for eps in (-1e-6, float("nan"), float("inf")):
         with pytest.raises(w4.W4A16Error) as e:
             w4.f16_rope(x, None, norm=w4.HeadNorm(w, eps))

@@ -240,6 +240,17 @@ def test_captured_streams_and_two_at_once(w4):
     assert empty.shape == (0, 192)
 
 
+def test_one_workspace_for_fewer_rows(w4):
+    """A workspace for many rows, with garbage in it, serves calls with fewer, one after the other."""
+    ws = w4.lora_workspace(Case(1, 64, (256, 256), 48, 3, [0]).adapters(w4), 1500)
+    ws.fill_(0xFF)
+    for m in (1500, 1, 17, 33, 200, 1025):
+        c = Case(m, 64, (256, 256), 48, 3, some_ids(m, 3, m), seed=m)
+        y = to_dev(c.y)
+        w4.f16_lora(to_dev(c.x), c.adapters(w4), to_dev(c.ids), y, workspace=ws)
+        c.check(w4, y)
+
+
 def test_wrong_arguments_are_refused(w4):
     import torch
     c = Case(4, 64, (40, 24), 16, 3, [0, 1, 2, -1], seed=12)

@@ -133,6 +133,20 @@ def test_lora_workspace_holds_what_is_written(calls, m):
     assert workspace_bytes(calls, adapters(), 0) == workspace_bytes(calls, None, 5) == 0
 
 
+def test_lora_rows_of_out_do_not_overlap(calls):
+    s = adapters()
+    for os, m, code in ((56, 2, "W4_ERR_SHAPE"), (8, 5, "W4_ERR_SHAPE"), (56, 1, "W4_ERR_WORKSPACE"), (64, 2, "W4_ERR_WORKSPACE")):
+        assert calls.f16_lora(FAKE, 64, FAKE, 64, FAKE, os, ref(s), FAKE, m, None, 0, None) == C[code], (os, m)
+
+
+def test_lora_workspace_grows_with_the_rows(calls):
+    for rank, slices, k in ((8, 1, 64), (16, 3, 2048), (32, 2, 896), (64, 3, 2048), (128, 4, 11008)):
+        ends = (ctypes.c_int32 * 4)(*(64 * (i + 1) for i in range(slices)))
+        s = adapters(rank=rank, slices=slices, K=k, N=64 * slices, columns=ends)
+        sizes = [workspace_bytes(calls, s, m) for m in (*range(1, 2200), 4096, 4097, 65536, 70001, 1 << 20)]
+        assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
 def test_rules(calls):
     def pick(r, ws=FAKE, n=1 << 30, flags=0, N=1000, idx=FAKE):
         return calls.lm_head_argmax_topk_rules(FAKE, FAKE, FAKE, FAKE, 2, N, 64, 64, 5, idx, FAKE, ref(r), ws, n, flags, None)

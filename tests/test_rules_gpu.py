@@ -356,6 +356,25 @@ def test_token_counts_bad_indexes(w4):
             assert w4.device_status() == 9 and w4.device_status() == 0
 
 
+def test_reset_of_one_slot_twice(w4):
+    """The last of the sequences with one slot takes it, whole, whatever the others count; it is reported."""
+    g = np.random.RandomState(5)
+    n, batch = 20011, 301
+    where = g.randint(0, 40, batch).astype(np.int32)
+    where[-1] = where[0]
+    lens = g.randint(0, 60, batch)
+    offsets = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    tokens = g.randint(0, n, offsets[-1]).astype(np.int32)
+    want = np.full((40, n), 3, np.int64)
+    for b in range(batch):
+        want[where[b]] = np.bincount(tokens[offsets[b]:offsets[b + 1]], minlength=n)
+    for _ in range(3):
+        table = to_dev(np.full((40, n), 3, np.int16))
+        w4.token_counts_add(w4.TokenCounts(table), to_dev(where), to_dev(tokens), to_dev(offsets), reset=True)
+        assert np.array_equal(table.cpu().numpy().astype(np.int64), want)
+        assert w4.device_status() == 9 and w4.device_status() == 0
+
+
 def test_wrong_rules_are_refused(w4):
     import torch
     head = Head(2, 100, 64, seed=9)

@@ -1136,7 +1136,7 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     if (lmhead) off = align_up(off + (size_t)a.ldr * M * 4, 16);
     else if (a.C > 1) off = align_up(off + (size_t)tpc * kTileRows * M * 4, 16);
     a.off_rules = (uint32_t)off;
-    if (lmhead && a.rules.on) off += rules_bytes(M);
+    if (lmhead && a.rules.on) off += rules_bytes(a.rules, M);
     off = align_up(off, 16);
     a.off_bar = (uint32_t)off;
     off += 16 * stages + 16;
@@ -1390,7 +1390,13 @@ int lmhead_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const
                 void *stream, const Rules &rules = Rules{}) {
     StreamPlan p;
     p.a.rules = rules;
-    if (!plan_stream(p, M, N, K, f, true, k)) return W4_ERR_SHAPE;
+    if (!plan_stream(p, M, N, K, f, true, k)) {
+        // (Where shared memory is nearly full the biases are searched for once more at the end.)
+        p = StreamPlan();
+        p.a.rules = rules;
+        p.a.rules.most = 0;
+        if (rules.most == 0 || !plan_stream(p, M, N, K, f, true, k)) return W4_ERR_SHAPE;
+    }
     const int G = p.grid;
     if ((long long)G > lm_max_blocks(N, k)) return W4_ERR_SHAPE;
     if (ws_bytes < (size_t)M * G * k * sizeof(uint64_t)) return W4_ERR_WORKSPACE;

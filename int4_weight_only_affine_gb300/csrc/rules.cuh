@@ -32,6 +32,7 @@ struct Rules {
     int slots, entries;
     int vec;  // rows of counts start on 16 bytes
     int on;
+    int most;  // biases in the block's tokens that there is room for
 };
 
 // What stands in place of a masked logit: a NaN that no operation makes.
@@ -49,17 +50,17 @@ struct BiasHit {
     int m, at, token;
     float value;
 };
-constexpr int kMaxHits = 256;  // more of them are left to the warps, one list after the other
+constexpr int kMaxHits = 256;  // (or none, where shared memory is short); more of them are left to the warps, one list after the other
 
 // The block's memory of the rules: rows, hits and their number.
-__host__ __device__ constexpr size_t rules_bytes(int M) { return M * sizeof(RowRule) + kMaxHits * sizeof(BiasHit) + 16; }
+inline size_t rules_bytes(const Rules &r, int M) { return 16 + M * sizeof(RowRule) + r.most * sizeof(BiasHit); }
 struct RulesMemory {
     RowRule *rule;
     BiasHit *hits;
     int *nhits;
     __device__ __forceinline__ RulesMemory(uint8_t *p, int M)
-        : rule(reinterpret_cast<RowRule *>(p + 16 + kMaxHits * sizeof(BiasHit))),
-          hits(reinterpret_cast<BiasHit *>(p + 16)), nhits(reinterpret_cast<int *>(p)) {}
+        : rule(reinterpret_cast<RowRule *>(p + 16)), hits(reinterpret_cast<BiasHit *>(p + 16 + M * sizeof(RowRule))),
+          nhits(reinterpret_cast<int *>(p)) {}
 };
 
 // Done by one warp of its own while the others stream weights: reads the rows'
@@ -105,7 +106,7 @@ __device__ __forceinline__ void rules_begin(const Rules &r, const RulesMemory &k
                 const bool mine = tok[q] >= n0 && tok[q] < n0 + rows;
                 const unsigned bal = __ballot_sync(~0u, mine);
                 const int h = found + __popc(bal & ((1u << lane) - 1u)), i = at + 32 * q + lane;
-                if (mine && h < kMaxHits) k.hits[h] = BiasHit{m, i, tok[q], __ldg(r.bval + i)};
+                if (mine && h < r.most) k.hits[h] = BiasHit{m, i, tok[q], __ldg(r.bval + i)};
                 found += __popc(bal);  // (hits lie in the order of their lists)
             }
         }
@@ -199,7 +200,7 @@ __device__ __forceinline__ void rules_apply(const Rules &r, const RulesMemory &k
     __syncthreads();
     if (!r.boff) return;
     const int n = *k.nhits;
-    if (n <= kMaxHits) {
+    if (n <= r.most) {
         // The first hit of a token adds all of that token, in their order.
         for (int h = tid; h < n; h += threads) {
             const BiasHit b = k.hits[h];
@@ -256,6 +257,7 @@ inline int check_rules(const w4_logit_rules *u, int N, Rules &r) {
         r.astride = 4 * u->allowed_stride;
     }
     r.on = r.counts || r.boff || r.allowed;
+    r.most = r.boff ? kMaxHits : 0;
     return W4A16_OK;
 }
 

@@ -160,6 +160,32 @@ def test_rules_formats_and_full_vocabulary(w4, group, symmetric):
         check(w4, head, top, rule, rules_of(w4, rule))
 
 
+@pytest.mark.parametrize("m", [7, 16])
+def test_rules_at_the_widest_rows(w4, m):
+    """Up to the largest K that a selection takes, where little shared memory is left for the rules."""
+    import torch
+    n = 1000
+
+    def taken(k):
+        x = torch.zeros(m, k, dtype=torch.float16, device="cuda")
+        scales = torch.zeros(n, k // 64, dtype=torch.float16, device="cuda")
+        try:
+            w4.lm_head_argmax_topk(x, torch.zeros(n, k // 8, dtype=torch.int32, device="cuda"), scales, scales, k=5)
+        except w4.W4A16Error as e:
+            assert e.status == 2
+            return False
+        return True
+    lo, hi = 64, 32768 + 64
+    while hi - lo > 64:
+        k = (lo + hi) // 128 * 64
+        lo, hi = (k, hi) if taken(k) else (lo, k)
+    assert 1024 <= lo <= 32768
+    for k in (lo, lo - 64, lo - 192):
+        head = Head(m, n, k, seed=k)
+        rule = random_rule(np.random.RandomState(k), m, n, m + 1, 0.3)
+        check(w4, head, 9, rule, rules_of(w4, rule))
+
+
 def test_rules_parts_alone(w4):
     head = Head(5, 3001, 128, seed=3)
     full = random_rule(np.random.RandomState(8), 5, 3001, 9, 0.4)

@@ -298,9 +298,24 @@ struct StreamArgs {
     uint32_t off_rules;
 };
 
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
-
-constexpr int kLmThreads = kThreads + 32;  // lm_head pass 1 with rules: a warp for them beside the others
+// The consumers of a CTA are teams of 8 warps that take its tiles in turn, each with its
+// own half of the ring.  Two teams for lm_head's 9 to 16 rows, whose activations leave an
+// SM one CTA: 76.3 us for 89.0 with one team at 16 rows of 2048 by 151936, greedy, and
+// 93.4 for 112.5 with the 50 best.  One team else: with 8 rows two CTAs share an SM, and
+// other weights give a CTA a tile or two (16 rows of 11008 by 2048: 13.4 us, 16.2 with two
+// teams; 2048 by 22016: 15.5 and 14.4).
+__host__ __device__ constexpr int teams_of(int M, bool lmhead) { return lmhead && M > 8 ? 2 : 1; }
+template <int TEAMS>
+__device__ __forceinline__ void consumer_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(TEAMS * kConsumers) : "memory");
+}
+template <int TEAMS>
+__device__ __forceinline__ void stream_team_sync(int team) {
+    if (TEAMS == 1) consumer_sync<1>();
+    else asm volatile("bar.sync %0, %1;" ::"r"(2 + team), "n"(kConsumers) : "memory");
+}
+// Threads of a CTA: the consumers, the producer's warp, and in lm_head's pass 1 with rules a warp for them.
+__host__ __device__ constexpr int stream_threads(int teams, bool ruled) { return teams * kConsumers + (ruled ? 64 : 32); }
 
 // FMT: the scale-layout class of the weight (kFmtG64, kFmtS128, kFmtAny,
 // kFmtG32).
@@ -309,11 +324,12 @@ constexpr int kLmThreads = kThreads + 32;  // lm_head pass 1 with rules: a warp 
 // 2048 by 151936).
 constexpr int kLinear = 0, kLmHead = 1, kLmHeadRules = 2;
 template <int NT, int HEAD, bool M1, int FMT>
-__global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD == kLmHeadRules), NT == 1 ? 2 : 1)
     stream_kernel(const __grid_constant__ CUtensorMap tm3, const __grid_constant__ CUtensorMap tm2,
                   const __grid_constant__ StreamArgs a) {
     constexpr bool LMHEAD = HEAD != kLinear, kRuled = HEAD == kLmHeadRules;
-    constexpr int kWarps = (kRuled ? kLmThreads : kThreads) / 32;
+    constexpr int TEAMS = LMHEAD ? NT : 1, kAll = stream_threads(TEAMS, kRuled), kWarps = kAll / 32;
+    constexpr int kProducer = TEAMS * kConsumerWarps;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -336,7 +352,7 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
 
     uint32_t *xf = reinterpret_cast<uint32_t *>(sb + a.off_xf);
     float *xsum = reinterpret_cast<float *>(sb + a.off_xsum);
-    float *red = reinterpret_cast<float *>(sb + a.off_red);  // [2][8][16*M]
+    float *red = reinterpret_cast<float *>(sb + a.off_red);  // [2][8][16*M]: two tiles in turn, or one of each team
     float *res = reinterpret_cast<float *>(sb + a.off_res);  // [ntl][16*M]; lm_head: [M][ldr]
     const uint32_t bar0 = base + a.off_bar;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sb + a.off_bar + 16 * S);
@@ -354,18 +370,19 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
     }
     __syncthreads();
 
-    if (warp == kConsumerWarps) {
+    if (warp == kProducer) {
         // ---------------- producer: weights need no dependency wait ----------------
         if (lane == 0) {
             uint32_t issued_ph = 0, issued_any = 0;
-            int it = 0;
+            const int ring = S / TEAMS;  // stages of a team: every TEAMS-th
             bool ok = true;
             for (int tl = 0; tl < ntl && ok; ++tl) {
                 const int t = t0 + tl;
                 const bool tail = (t + 1) * kTileRows > N;
+                int it = tl / TEAMS * nch;
                 for (int ch = 0; ch < nch; ++ch, ++it) {
-                    const int s = it % S;
-                    const uint32_t ph = (it / S) & 1;
+                    const int s = it % ring * TEAMS + tl % TEAMS;
+                    const uint32_t ph = (it / ring) & 1;
                     if (!mbar_wait(empty_bar(s), ph ^ 1, abort_flag)) {
                         ok = false;
                         break;
@@ -405,7 +422,7 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
             for (int s = 0; s < S; ++s)
                 if (issued_any & (1u << s)) mbar_wait(full_bar(s), (issued_ph >> s) & 1);
         }
-    } else if (kRuled && warp > kConsumerWarps) {
+    } else if (kRuled && warp > kProducer) {
         // ---------------- lm_head with rules: one more warp, for them ----------------
         pdl_wait();
         rules_begin(a.rules, RulesMemory(sb + a.off_rules, M), M, N, t0 * kTileRows,
@@ -413,11 +430,12 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
     } else {
         // ---------------- consumers ----------------
         const int lg = lane >> 2, lt = lane & 3;
-        // Warp w takes box w of every stage: groups 4w .. 4w+3 of the chunk.
+        const int team = TEAMS == 1 ? 0 : warp / kConsumerWarps, tw = warp - team * kConsumerWarps;
+        // Warp w of a team takes box w of its stages: groups 4w .. 4w+3 of the chunk.
         int off[4];
-        box_offsets(off, warp, lg, lt);
+        box_offsets(off, tw, lg, lt);
         const int xoff = lane_xoff(M, lg, lt), xd1 = lane_xd1(M, lg);
-        const int goff = FMT == kFmtG32 ? g32_offset(warp, lg, lt) : 0;
+        const int goff = FMT == kFmtG32 ? g32_offset(tw, lg, lt) : 0;
         WFmt f = a.f;
         // The fixed classes' layouts follow from ng (fewer live registers).
         if (FMT == kFmtG64) f.ngs = ng;
@@ -425,11 +443,11 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
         const bool sym = FMT == kFmtS128 || (FMT != kFmtG64 && f.sym);
         const bool vec = FMT == kFmtG64 ? (ng & 3) == 0 : FMT == kFmtS128 ? (ng & 3) == 0 : box_vec_ok(f);
         pdl_wait();
-        stage_activations<M1 ? 2 : 4, FMT == kFmtG32>(a.x, M, a.K, gs0, ngl, xf, xsum, tid, kConsumers);
-        consumer_sync();
-        int s = 0;
+        stage_activations<M1 ? 2 : 4, FMT == kFmtG32>(a.x, M, a.K, gs0, ngl, xf, xsum, tid, TEAMS * kConsumers);
+        consumer_sync<TEAMS>();
+        int s = team;
         uint32_t ph = 0;
-        for (int tl = 0; tl < ntl; ++tl) {
+        for (int tl = team; tl < ntl; tl += TEAMS) {
             const int t = t0 + tl;
             const int row0 = t * kTileRows;
             const bool tail = row0 + kTileRows > N;
@@ -443,16 +461,16 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
                     // The producer copies no scales for the ragged last tile (its rows
                     // end inside the arrays); fill them here, rows past N repeated.
                     const int ngs = f.ngs;
-                    for (int i = tid; i < (sym ? 1 : 2) * kTileRows * ngs; i += kConsumers) {
+                    for (int i = tw * 32 + lane; i < (sym ? 1 : 2) * kTileRows * ngs; i += kConsumers) {
                         const int arr = i / (kTileRows * ngs), r = (i / ngs) % kTileRows, gi = i % ngs;
                         const uint16_t *src = arr ? a.bi : a.sc;
                         sp[i] = src[(size_t)min(row0 + r, N - 1) * ngs + gi];
                     }
                     fence_proxy_async_smem();  // a later bulk copy reuses these bytes
-                    consumer_sync();
+                    stream_team_sync<TEAMS>(team);
                 }
                 if (ok) {
-                    const int g = gs0 + ch * kChunkGroups + kBoxGroups * warp;
+                    const int g = gs0 + ch * kChunkGroups + kBoxGroups * tw;
                     const int n = min(kBoxGroups, gs1 - g);
                     const int gl = g - gs0;
                     const uint4 *xl = reinterpret_cast<const uint4 *>(xf) + (size_t)gl * 2 * M * 4 + xoff;
@@ -464,14 +482,14 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_bar(s));
-                if (++s == S) {
-                    s = 0;
+                if ((s += TEAMS) == S + team) {
+                    s = team;
                     ph ^= 1;
                 }
             }
             if (a.defer) {
                 // Keep this warp's partial; all tiles are combined once at the end.
-                float *mine = red + ((size_t)tl * kConsumerWarps + warp) * out16;
+                float *mine = red + ((size_t)tl * kConsumerWarps + tw) * out16;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -482,8 +500,10 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
                     }
                 continue;
             }
-            // Per-tile reduction over the 8 consumer warps, fixed order.
-            float *mine = red + ((tl & 1) * kConsumerWarps + warp) * out16;
+            // Per-tile reduction over the team's 8 warps, fixed order.  (The parity of tl is the
+            // team's where there are two: its last tile's sums have been read before these come.)
+            float *mine = red + ((tl & 1) * kConsumerWarps + tw) * out16;
+            if (TEAMS > 1) stream_team_sync<TEAMS>(team);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -492,8 +512,8 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
                     const int col = nt * 8 + 2 * lt + (i & 1);
                     if (col < M) mine[row * M + col] = acc.template value<FMT == kFmtS128 ? -8 : 1>(nt, i);
                 }
-            consumer_sync();
-            if (warp == (tl & (kConsumerWarps - 1))) {
+            stream_team_sync<TEAMS>(team);
+            if (tw == (tl / TEAMS & (kConsumerWarps - 1))) {
                 const float *grp = red + (tl & 1) * kConsumerWarps * out16;
                 for (int e = lane; e < out16; e += 32) {
                     float v = 0.f;
@@ -512,8 +532,8 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
             }
         }
         if (a.defer) {
-            consumer_sync();
-            for (int i = tid; i < ntl * out16; i += kConsumers) {
+            consumer_sync<TEAMS>();
+            for (int i = tid; i < ntl * out16; i += TEAMS * kConsumers) {
                 const int tl = i / out16, e = i % out16;
                 const float *grp = red + (size_t)tl * kConsumerWarps * out16;
                 float v = 0.f;
@@ -540,7 +560,7 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
             cluster.sync();
             for (int tl = rank; tl < ntl; tl += C) {
                 const int row0 = (t0 + tl) * kTileRows;
-                for (int e = tid; e < out16; e += kThreads) {
+                for (int e = tid; e < out16; e += kAll) {
                     float v = 0.f;
                     for (int q = 0; q < C; ++q) v += cluster.map_shared_rank(res, q)[tl * out16 + e];
                     const int row = e / M, col = e % M;
@@ -556,7 +576,7 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
     // The keys of this CTA's rows, best first, padded with 0 (below every key).
     const int n0 = t0 * kTileRows;
     const int rows = min(N, t1 * kTileRows) - n0;
-    if (kRuled) rules_apply(a.rules, RulesMemory(sb + a.off_rules, M), res, a.ldr, M, n0, rows, tid, kLmThreads);
+    if (kRuled) rules_apply(a.rules, RulesMemory(sb + a.off_rules, M), res, a.ldr, M, n0, rows, tid, kAll);
     if (a.k == 1) {
         // Greedy selection: warp w takes every kWarps-th activation row from w on.
         for (int m = warp; m < M; m += kWarps) {
@@ -579,7 +599,7 @@ __global__ void __launch_bounds__(HEAD == kLmHeadRules ? kLmThreads : kThreads, 
             uint64_t *out = a.ws + ((size_t)m * gridDim.x + blockIdx.x) * a.k;
             if (lane < a.k) out[lane] = run.a;
             if (32 + lane < a.k) out[32 + lane] = run.b;
-        } else {  // (M <= 5: every row has its warps, and each warp one row)
+        } else {  // (every row has its warps, and each warp one row)
             lists[warp][lane] = run.a;
             lists[warp][32 + lane] = run.b;
         }
@@ -1115,12 +1135,13 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     // Codes, then the tile's scale rows [16][ngs] (and bias rows).
     a.stage_bytes = (uint32_t)align_up((size_t)a.w_bytes + (a.f.sym ? 32u : 64u) * a.f.ngs, 1024);
     // As many stages as the byte budget allows: the ring is what keeps HBM busy.
-    const int stages = (int)max((size_t)2, min((size_t)kMaxStages, ring_budget / a.stage_bytes));
+    const int stages = (int)max((size_t)2, min((size_t)kMaxStages, ring_budget / a.stage_bytes)) / teams_of(M, lmhead) *
+                       teams_of(M, lmhead);
     a.stages = stages;
     size_t off = (size_t)stages * a.stage_bytes;
     if (lmhead) {
         // After the main loop the ring holds two lists of keys for each warp.
-        const size_t need = (size_t)(kLmThreads / 32) * 2 * 64 * 8;
+        const size_t need = (size_t)(stream_threads(teams_of(M, true), true) / 32) * 2 * 64 * 8;
         if (off < need) off = align_up(need, 1024);
     }
     a.off_xf = (uint32_t)off;
@@ -1153,7 +1174,7 @@ bool ensure_smem(const void *kern, size_t bytes);
 
 // Clusters of C CTAs (this kernel, this shared memory) that can be resident
 // at once; cached per (kernel, C, bytes, device).
-int max_active_clusters(const void *kern, int C, size_t smem, int fallback) {
+int max_active_clusters(const void *kern, int threads, int C, size_t smem, int fallback) {
     struct Entry {
         const void *kern;
         int C, dev;
@@ -1174,7 +1195,7 @@ int max_active_clusters(const void *kern, int C, size_t smem, int fallback) {
     if (!ensure_smem(kern, smem)) return fallback;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C * 64, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1223,7 +1244,8 @@ bool plan_with_cluster(StreamPlan &p, int C, int slots, int per_sm, bool lmhead)
         // of the layout actually launched (fewer clusters mean more tiles per
         // cluster and possibly a larger layout, so check again).
         for (int iter = 0; iter < 3; ++iter) {
-            const int act = max_active_clusters(stream_kernel_ptr(a.M, lmhead, fmt_class(a.f)), C, p.smem, ncl);
+            const int act = max_active_clusters(stream_kernel_ptr(a.M, lmhead, fmt_class(a.f)),
+                                                stream_threads(teams_of(a.M, lmhead), false), C, p.smem, ncl);
             if (act >= ncl) break;
             ncl = max(1, act);
             if (!fit_layout(p, lmhead, per_sm, (a.tiles + ncl - 1) / ncl, slice)) return false;
@@ -1314,7 +1336,7 @@ int launch_stream(const StreamPlan &p, const uint32_t *qw, bool overlap, cudaStr
     if (!ensure_smem(reinterpret_cast<const void *>(kern), p.smem)) return W4_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid, 1, 1);
-    cfg.blockDim = dim3(HEAD == kLmHeadRules ? kLmThreads : kThreads, 1, 1);
+    cfg.blockDim = dim3(stream_threads(teams_of(p.a.M, HEAD != kLinear), HEAD == kLmHeadRules), 1, 1);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];

@@ -15,7 +15,6 @@ namespace w4a16 {
 constexpr int kTileRows = 16;                    // output rows per MMA tile
 constexpr int kConsumerWarps = 8;
 constexpr int kConsumers = kConsumerWarps * 32;  // 256
-constexpr int kThreads = kConsumers + 32;        // + one producer warp
 constexpr int kChunkGroups = 32;                 // groups per stage (8 boxes)
 constexpr int kBoxGroups = 4;                    // 128 bytes of codes per row
 constexpr int kBoxBytes = kTileRows * 128;       // 2 KB per TMA box

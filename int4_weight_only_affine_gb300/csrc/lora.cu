@@ -48,7 +48,9 @@ namespace {
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kScope = 1024;        // rows whose ids a CTA sorts
 constexpr int kFewRows = 32;        // rows that a warp sorts
-constexpr int kFewOfItem = 16;      // rows that shrink multiplies by mma.sync
+constexpr int kFewOfItem = 16;      // rows that shrink multiplies by mma.sync,
+constexpr int kFewRanks = 96;       // with up to so many ranks in all, or where no item of a call has more rows (64 rows of
+                                    // 32 adapters on q|k|v, us by mma.sync and by tcgen05: 96 ranks 14.4, 14.9; 192 24.1, 18.8)
 constexpr int kMaxAdapters = 4096;  // buckets of the histogram
 constexpr int kMaxSlices = 4;
 constexpr int kMaxRank = 128;
@@ -56,6 +58,8 @@ constexpr int kMaxSplits = 8;
 constexpr int kColBlock = 32;  // columns of a warp's step
 constexpr int kHalfK = 64, kStageK = 2 * kHalfK;  // k of a stage of shrink's ring: two halves of 128-byte rows
 constexpr int kMostStages = 8;
+constexpr int kBoxRows = 64;  // rows of x in one copy, where they lie in a row (a copy takes some 70 ns to issue, whatever its
+                              // size; with 8 rows to a copy 1500 rows of K 11008, rank 128, took 37.6 us for 31.7)
 constexpr int kSmemOfTwo = 104 * 1024, kSmemOfOne = 216 * 1024;  // dynamic shared memory of two CTAs on an SM, and of one
 constexpr int kSmsOfPlan = 152;  // (the plan does not depend on the device, nor does a workspace's size)
 
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
         const int split = u % splits, bucket = sorter.item(p, u / splits, rows, unit, n);
         const int c0 = (int)((long long)kb * split / splits), chunks = (int)((long long)kb * (split + 1) / splits) - c0;
         if (bucket == p.adapters) continue;  // (alike for all threads; rows is written again after a barrier)
-        if (n <= kFewOfItem) {
+        if (n <= kFewOfItem && (F <= kFewRanks || !tensor)) {
             const uint16_t *a = p.a + bucket * p.a_adapter;
             const int b0 = c0 * (kStageK / 32), b1 = min((p.K + 31) / 32, (c0 + chunks) * (kStageK / 32));
             float *red = reinterpret_cast<float *>(smem);
@@ -415,11 +419,12 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
         }
         // A stage: A's rows, then x's; the products read 128 rows of x, what lies behind the
         // item's goes into rows of the sums that nobody reads.
-        const int xrow = F16, half = (xrow + (n + 7) / 8 * 8) * 128, stage = 2 * half;
+        const bool box = n > 16 && rows[n - 1] - rows[0] == n - 1;
+        const int xrow = F16, xrows = box ? (n + kBoxRows - 1) / kBoxRows * kBoxRows : (n + 7) / 8 * 8;
+        const int half = (xrow + xrows) * 128, stage = 2 * half;
         const int stages = min(kMostStages, (p.room - 128 * 128) / stage);
         const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
-        const bool box = n > 16 && rows[n - 1] - rows[0] == n - 1;
-        const uint32_t bytes = 2 * (p.boxes * p.box_rows * 128 + (box ? (n + 7) / 8 * 8 : (n + 3) / 4 * 4) * 128);
+        const uint32_t bytes = 2 * (p.boxes * p.box_rows * 128 + (box ? xrows : (n + 3) / 4 * 4) * 128);
         if (warp == 0) {
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t i = stage_no + c, b = i % kMostStages, at = base + c % stages * stage;
@@ -439,8 +444,9 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
                         const int row = (lane - (32 - p.boxes)) * p.box_rows;  // (rows past F are zero, and end before x's)
                         tma_load_3d(to + row * 128, &amap, kh, row, bucket, bar);
                     }
-                    if (box) {  // boxes of 8 rows
-                        if (8 * lane < n) tma_load_2d(to + (xrow + 8 * lane) * 128, &xbox, kh, rows[0] + 8 * lane, bar);
+                    if (box) {  // (what lies behind the item's rows is read too, and zero behind the last of all)
+                        if (kBoxRows * lane < n)
+                            tma_load_2d(to + (xrow + kBoxRows * lane) * 128, &xbox, kh, rows[0] + kBoxRows * lane, bar);
                     } else if (4 * lane < n) {
                         const int end = n - 1;
                         tma_gather4(to + (xrow + 4 * lane) * 128, &xmap, kh, rows[4 * lane], rows[min(4 * lane + 1, end)],
@@ -948,7 +954,7 @@ int launch(K kernel, long long ctas, int smem, void *stream, const A &...args) {
 namespace {
 
 // Whether join runs: where there are more ranks than 64 for many rows.  (1570 rows on
-// q|k|v, rank 64: 24.2 us with it, 33.5 without; on gate|up, rank 16: 47.4 and 43.0.)
+// q|k|v, rank 64: 23.5 us with it, 33.5 without; on gate|up, rank 16: 47.4 and 43.0.)
 bool joined(const f16_adapters *s, int M) { return M > kFewRows && s->slices * s->rank > 64; }
 
 // The workspace: the shares of h, then what join leaves.
@@ -1026,7 +1032,7 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
     p.copy = out != y || out_row != y_row;
     const int rk = round_rank(s->rank), F = s->rank * s->slices, hist = (s->adapters + 1) * 4;
     // A as [adapters][slices * rank][K], boxes of 64 k and all rows (two boxes of more
-    // than 256); x as [M][K], boxes of 64 k of one row, copied four at a time, and of 8.
+    // than 256); x as [M][K], boxes of 64 k of one row, copied four at a time, and of kBoxRows.
     // (None is used where every item has few rows.)
     CUtensorMap amap = {}, xmap = {}, xbox = {};
     p.boxes = F > 256 ? 2 : 1;
@@ -1038,7 +1044,7 @@ extern "C" int f16_lora(const uint16_t *x, int64_t x_row, const uint16_t *y, int
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kHalfK, 1,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_2d(&xbox, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kHalfK, 8,
+        !make_map_2d(&xbox, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)s->K, (uint64_t)M, x_bytes, kHalfK, kBoxRows,
                      CU_TENSOR_MAP_SWIZZLE_128B)))
         return encode_fn() ? W4_ERR_SHAPE : W4_ERR_DEVICE;
     p.room = c.room;

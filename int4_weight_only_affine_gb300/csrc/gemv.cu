@@ -285,6 +285,7 @@ struct StreamArgs {
     int C;       // CTAs per cluster splitting K
     int tiles;   // ceil(N / 16)
     int stages;  // ring depth
+    int width;   // warps of a team
     int ng;      // groups (64-k blocks) along K
     WFmt f;      // scale layout (quantisation group, symmetric codes)
     int units;   // 8-group units along K
@@ -298,24 +299,30 @@ struct StreamArgs {
     uint32_t off_rules;
 };
 
-// The consumers of a CTA are teams of 8 warps that take its tiles in turn, each with its
-// own half of the ring.  Two teams for lm_head's 9 to 16 rows, whose activations leave an
-// SM one CTA: 76.3 us for 89.0 with one team at 16 rows of 2048 by 151936, greedy, and
-// 93.4 for 112.5 with the 50 best.  One team else: with 8 rows two CTAs share an SM, and
-// other weights give a CTA a tile or two (16 rows of 11008 by 2048: 13.4 us, 16.2 with two
-// teams; 2048 by 22016: 15.5 and 14.4).
-__host__ __device__ constexpr int teams_of(int M, bool lmhead) { return lmhead && M > 8 ? 2 : 1; }
-template <int TEAMS>
+// The consumers of a CTA are teams of `width` warps that take its tiles in turn, each team
+// with its own share of the ring; a warp takes a box (4 groups) of a tile's chunk of K.
+//  * Width 8, one team: w4_gemv, and lm_head of up to 8 rows (two CTAs share an SM).
+//  * 16 warps for lm_head's 9 to 16 rows, whose activations leave an SM one CTA: 73.4 us
+//    for 89.0 with 8 warps at 16 rows of 2048 by 151936, greedy, 90.8 for 112.5 with the 50
+//    best.  Not for w4_gemv, where a CTA has a tile or two (16 rows of 11008 by 2048: 13.4
+//    us, 16.2 with two teams; 2048 by 22016: 15.5 and 14.4).
+//  * Width 4 for lm_head with K up to 1024, whose tiles have 4 boxes, where a CTA has more
+//    than one: 1024 by 151936, greedy, 25.0, 26.8, 27.8 and 44.0 us at 1, 2, 8 and 16 rows for
+//    26.0, 42.3, 32.9 and 55.4 with width 8 (1000 rows of weights, one tile a CTA: 6.6 for 6.3).
+constexpr int kNarrowGroups = 16;
+constexpr int width_of(int ng, bool lmhead, int tpc) { return lmhead && ng <= kNarrowGroups && tpc > 1 ? 4 : 8; }
+__host__ __device__ constexpr int consumer_warps(int M, bool lmhead) { return lmhead && M > 8 ? 16 : 8; }
+template <int WARPS>
 __device__ __forceinline__ void consumer_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(TEAMS * kConsumers) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
 }
-template <int TEAMS>
+template <int WARPS, int WIDTH>
 __device__ __forceinline__ void stream_team_sync(int team) {
-    if (TEAMS == 1) consumer_sync<1>();
-    else asm volatile("bar.sync %0, %1;" ::"r"(2 + team), "n"(kConsumers) : "memory");
+    if (WARPS == WIDTH) consumer_sync<WARPS>();
+    else asm volatile("bar.sync %0, %1;" ::"r"(2 + team), "n"(WIDTH * 32) : "memory");
 }
 // Threads of a CTA: the consumers, the producer's warp, and in lm_head's pass 1 with rules a warp for them.
-__host__ __device__ constexpr int stream_threads(int teams, bool ruled) { return teams * kConsumers + (ruled ? 64 : 32); }
+__host__ __device__ constexpr int stream_threads(int warps, bool ruled) { return 32 * warps + (ruled ? 64 : 32); }
 
 // FMT: the scale-layout class of the weight (kFmtG64, kFmtS128, kFmtAny,
 // kFmtG32).
@@ -323,13 +330,15 @@ __host__ __device__ constexpr int stream_threads(int teams, bool ruled) { return
 // the rules' code in one kernel a call without rules took 36.4 us for 35.2 at one row of
 // 2048 by 151936).
 constexpr int kLinear = 0, kLmHead = 1, kLmHeadRules = 2;
-template <int NT, int HEAD, bool M1, int FMT>
-__global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD == kLmHeadRules), NT == 1 ? 2 : 1)
+template <int NT, int HEAD, bool M1, int FMT, int WIDTH>
+__global__ void __launch_bounds__(stream_threads(consumer_warps(8 * NT, HEAD != kLinear), HEAD == kLmHeadRules), NT == 1 ? 2 : 1)
     stream_kernel(const __grid_constant__ CUtensorMap tm3, const __grid_constant__ CUtensorMap tm2,
                   const __grid_constant__ StreamArgs a) {
     constexpr bool LMHEAD = HEAD != kLinear, kRuled = HEAD == kLmHeadRules;
-    constexpr int TEAMS = LMHEAD ? NT : 1, kAll = stream_threads(TEAMS, kRuled), kWarps = kAll / 32;
-    constexpr int kProducer = TEAMS * kConsumerWarps;
+    constexpr int kProducer = consumer_warps(8 * NT, LMHEAD);  // (the warp after the consumers)
+    constexpr int TEAMS = kProducer / WIDTH, kAll = stream_threads(kProducer, kRuled), kWarps = kAll / 32;
+    // Sums of tiles by warps: two tiles of each team in turn, or one where those of 16 rows fill more.
+    constexpr int kTurns = kProducer == 8 ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -352,7 +361,7 @@ __global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD 
 
     uint32_t *xf = reinterpret_cast<uint32_t *>(sb + a.off_xf);
     float *xsum = reinterpret_cast<float *>(sb + a.off_xsum);
-    float *red = reinterpret_cast<float *>(sb + a.off_red);  // [2][8][16*M]: two tiles in turn, or one of each team
+    float *red = reinterpret_cast<float *>(sb + a.off_red);  // [16][16*M]: a warp's kTurns
     float *res = reinterpret_cast<float *>(sb + a.off_res);  // [ntl][16*M]; lm_head: [M][ldr]
     const uint32_t bar0 = base + a.off_bar;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sb + a.off_bar + 16 * S);
@@ -362,7 +371,7 @@ __global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), kConsumerWarps);
+            mbar_init(empty_bar(s), WIDTH);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -430,7 +439,7 @@ __global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD 
     } else {
         // ---------------- consumers ----------------
         const int lg = lane >> 2, lt = lane & 3;
-        const int team = TEAMS == 1 ? 0 : warp / kConsumerWarps, tw = warp - team * kConsumerWarps;
+        const int team = TEAMS == 1 ? 0 : warp / WIDTH, tw = warp - team * WIDTH;
         // Warp w of a team takes box w of its stages: groups 4w .. 4w+3 of the chunk.
         int off[4];
         box_offsets(off, tw, lg, lt);
@@ -443,8 +452,8 @@ __global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD 
         const bool sym = FMT == kFmtS128 || (FMT != kFmtG64 && f.sym);
         const bool vec = FMT == kFmtG64 ? (ng & 3) == 0 : FMT == kFmtS128 ? (ng & 3) == 0 : box_vec_ok(f);
         pdl_wait();
-        stage_activations<M1 ? 2 : 4, FMT == kFmtG32>(a.x, M, a.K, gs0, ngl, xf, xsum, tid, TEAMS * kConsumers);
-        consumer_sync<TEAMS>();
+        stage_activations<M1 ? 2 : 4, FMT == kFmtG32>(a.x, M, a.K, gs0, ngl, xf, xsum, tid, 32 * kProducer);
+        consumer_sync<kProducer>();
         int s = team;
         uint32_t ph = 0;
         for (int tl = team; tl < ntl; tl += TEAMS) {
@@ -461,13 +470,13 @@ __global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD 
                     // The producer copies no scales for the ragged last tile (its rows
                     // end inside the arrays); fill them here, rows past N repeated.
                     const int ngs = f.ngs;
-                    for (int i = tw * 32 + lane; i < (sym ? 1 : 2) * kTileRows * ngs; i += kConsumers) {
+                    for (int i = tw * 32 + lane; i < (sym ? 1 : 2) * kTileRows * ngs; i += 32 * WIDTH) {
                         const int arr = i / (kTileRows * ngs), r = (i / ngs) % kTileRows, gi = i % ngs;
                         const uint16_t *src = arr ? a.bi : a.sc;
                         sp[i] = src[(size_t)min(row0 + r, N - 1) * ngs + gi];
                     }
                     fence_proxy_async_smem();  // a later bulk copy reuses these bytes
-                    stream_team_sync<TEAMS>(team);
+                    stream_team_sync<kProducer, WIDTH>(team);
                 }
                 if (ok) {
                     const int g = gs0 + ch * kChunkGroups + kBoxGroups * tw;
@@ -489,7 +498,7 @@ __global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD 
             }
             if (a.defer) {
                 // Keep this warp's partial; all tiles are combined once at the end.
-                float *mine = red + ((size_t)tl * kConsumerWarps + tw) * out16;
+                float *mine = red + ((size_t)tl * WIDTH + tw) * out16;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -500,10 +509,10 @@ __global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD 
                     }
                 continue;
             }
-            // Per-tile reduction over the team's 8 warps, fixed order.  (The parity of tl is the
-            // team's where there are two: its last tile's sums have been read before these come.)
-            float *mine = red + ((tl & 1) * kConsumerWarps + tw) * out16;
-            if (TEAMS > 1) stream_team_sync<TEAMS>(team);
+            // Per-tile reduction over the team's warps, fixed order.
+            const int place = (kTurns == 2 ? (tl / TEAMS & 1) * kProducer : 0) + team * WIDTH;
+            float *mine = red + (place + tw) * out16;
+            if (kTurns == 1) stream_team_sync<kProducer, WIDTH>(team);  // (the tile before has been read)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -512,13 +521,13 @@ __global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD 
                     const int col = nt * 8 + 2 * lt + (i & 1);
                     if (col < M) mine[row * M + col] = acc.template value<FMT == kFmtS128 ? -8 : 1>(nt, i);
                 }
-            stream_team_sync<TEAMS>(team);
-            if (tw == (tl / TEAMS & (kConsumerWarps - 1))) {
-                const float *grp = red + (tl & 1) * kConsumerWarps * out16;
+            stream_team_sync<kProducer, WIDTH>(team);
+            if (tw == (tl / TEAMS & (WIDTH - 1))) {
+                const float *grp = red + place * out16;
                 for (int e = lane; e < out16; e += 32) {
                     float v = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kConsumerWarps; ++w) v += grp[w * out16 + e];
+                    for (int w = 0; w < WIDTH; ++w) v += grp[w * out16 + e];
                     if (!LMHEAD && C == 1) {
                         const int row = e / M, col = e % M;
                         if (row0 + row < N) a.y[(size_t)col * N + row0 + row] = __half_as_ushort(__float2half_rn(v));
@@ -532,13 +541,13 @@ __global__ void __launch_bounds__(stream_threads(HEAD == kLinear ? 1 : NT, HEAD 
             }
         }
         if (a.defer) {
-            consumer_sync<TEAMS>();
-            for (int i = tid; i < ntl * out16; i += TEAMS * kConsumers) {
+            consumer_sync<kProducer>();
+            for (int i = tid; i < ntl * out16; i += 32 * kProducer) {
                 const int tl = i / out16, e = i % out16;
-                const float *grp = red + (size_t)tl * kConsumerWarps * out16;
+                const float *grp = red + (size_t)tl * WIDTH * out16;
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < kConsumerWarps; ++w) v += grp[w * out16 + e];
+                for (int w = 0; w < WIDTH; ++w) v += grp[w * out16 + e];
                 if (!LMHEAD && C == 1) {
                     const int row = e / M, col = e % M, r = (t0 + tl) * kTileRows + row;
                     if (r < N) a.y[(size_t)col * N + r] = __half_as_ushort(__float2half_rn(v));
@@ -925,12 +934,12 @@ __global__ void __launch_bounds__(kSeqThreads, 1) seq_kernel(const __grid_consta
 template <int FMT>
 const void *stream_kernel_ptr_f(int M, bool lmhead) {
     if (lmhead)
-        return M == 1 ? (const void *)stream_kernel<1, kLmHead, true, FMT>
-               : M <= 8 ? (const void *)stream_kernel<1, kLmHead, false, FMT>
-                        : (const void *)stream_kernel<2, kLmHead, false, FMT>;
-    return M == 1 ? (const void *)stream_kernel<1, kLinear, true, FMT>
-           : M <= 8 ? (const void *)stream_kernel<1, kLinear, false, FMT>
-                    : (const void *)stream_kernel<2, kLinear, false, FMT>;
+        return M == 1 ? (const void *)stream_kernel<1, kLmHead, true, FMT, 8>
+               : M <= 8 ? (const void *)stream_kernel<1, kLmHead, false, FMT, 8>
+                        : (const void *)stream_kernel<2, kLmHead, false, FMT, 8>;
+    return M == 1 ? (const void *)stream_kernel<1, kLinear, true, FMT, 8>
+           : M <= 8 ? (const void *)stream_kernel<1, kLinear, false, FMT, 8>
+                    : (const void *)stream_kernel<2, kLinear, false, FMT, 8>;
 }
 
 const void *stream_kernel_ptr(int M, bool lmhead, int fmt) {
@@ -1135,13 +1144,13 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     // Codes, then the tile's scale rows [16][ngs] (and bias rows).
     a.stage_bytes = (uint32_t)align_up((size_t)a.w_bytes + (a.f.sym ? 32u : 64u) * a.f.ngs, 1024);
     // As many stages as the byte budget allows: the ring is what keeps HBM busy.
-    const int stages = (int)max((size_t)2, min((size_t)kMaxStages, ring_budget / a.stage_bytes)) / teams_of(M, lmhead) *
-                       teams_of(M, lmhead);
+    const int width = a.width = width_of(a.ng, lmhead, tpc), warps = consumer_warps(M, lmhead), teams = warps / width;
+    const int stages = (int)max((size_t)max(2, teams), min((size_t)kMaxStages, ring_budget / a.stage_bytes)) / teams * teams;
     a.stages = stages;
     size_t off = (size_t)stages * a.stage_bytes;
     if (lmhead) {
         // After the main loop the ring holds two lists of keys for each warp.
-        const size_t need = (size_t)(stream_threads(teams_of(M, true), true) / 32) * 2 * 64 * 8;
+        const size_t need = (size_t)(stream_threads(warps, true) / 32) * 2 * 64 * 8;
         if (off < need) off = align_up(need, 1024);
     }
     a.off_xf = (uint32_t)off;
@@ -1149,9 +1158,9 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     a.off_xsum = (uint32_t)off;
     off = align_up(off + (size_t)slice_groups * M * 4 * xsums, 16);
     a.off_red = (uint32_t)off;
-    const size_t red_all = (size_t)tpc * kConsumerWarps * kTileRows * M * 4;
+    const size_t red_all = (size_t)tpc * width * kTileRows * M * 4;
     a.defer = (force_defer || red_all <= 32 * 1024) ? 1 : 0;
-    off = align_up(off + (a.defer ? red_all : (size_t)2 * kConsumerWarps * kTileRows * M * 4), 16);
+    off = align_up(off + (a.defer ? red_all : (size_t)16 * kTileRows * M * 4), 16);
     a.off_res = (uint32_t)off;
     a.ldr = tpc * kTileRows + 1;
     if (lmhead) off = align_up(off + (size_t)a.ldr * M * 4, 16);
@@ -1245,7 +1254,7 @@ bool plan_with_cluster(StreamPlan &p, int C, int slots, int per_sm, bool lmhead)
         // cluster and possibly a larger layout, so check again).
         for (int iter = 0; iter < 3; ++iter) {
             const int act = max_active_clusters(stream_kernel_ptr(a.M, lmhead, fmt_class(a.f)),
-                                                stream_threads(teams_of(a.M, lmhead), false), C, p.smem, ncl);
+                                                stream_threads(consumer_warps(a.M, lmhead), false), C, p.smem, ncl);
             if (act >= ncl) break;
             ncl = max(1, act);
             if (!fit_layout(p, lmhead, per_sm, (a.tiles + ncl - 1) / ncl, slice)) return false;
@@ -1318,7 +1327,7 @@ bool ensure_smem(const void *kern, size_t bytes) {
     return true;
 }
 
-template <int NT, int HEAD, bool M1, int FMT>
+template <int NT, int HEAD, bool M1, int FMT, int WIDTH>
 int launch_stream(const StreamPlan &p, const uint32_t *qw, bool overlap, cudaStream_t st) {
     CUtensorMap tm3, tm2;
     const uint64_t KW = (uint64_t)p.a.K / 8;
@@ -1332,11 +1341,11 @@ int launch_stream(const StreamPlan &p, const uint32_t *qw, bool overlap, cudaStr
     } else {
         tm3 = tm2;  // never used: every chunk takes the 2-D path
     }
-    auto kern = stream_kernel<NT, HEAD, M1, FMT>;
+    auto kern = stream_kernel<NT, HEAD, M1, FMT, WIDTH>;
     if (!ensure_smem(reinterpret_cast<const void *>(kern), p.smem)) return W4_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid, 1, 1);
-    cfg.blockDim = dim3(stream_threads(teams_of(p.a.M, HEAD != kLinear), HEAD == kLmHeadRules), 1, 1);
+    cfg.blockDim = dim3(stream_threads(consumer_warps(p.a.M, HEAD != kLinear), HEAD == kLmHeadRules), 1, 1);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -1369,12 +1378,19 @@ int check_common(const void *x, const uint32_t *qw, const uint16_t *sc, const ui
     return W4A16_OK;
 }
 
+template <int HEAD, int FMT, int WIDTH>
+int launch_stream_w(const StreamPlan &p, const uint32_t *qw, bool ov, cudaStream_t s) {
+    const int M = p.a.M;
+    return M == 1 ? launch_stream<1, HEAD, true, FMT, WIDTH>(p, qw, ov, s)
+           : M <= 8 ? launch_stream<1, HEAD, false, FMT, WIDTH>(p, qw, ov, s)
+                    : launch_stream<2, HEAD, false, FMT, WIDTH>(p, qw, ov, s);
+}
+
 template <int HEAD, int FMT>
 int launch_stream_f(const StreamPlan &p, const uint32_t *qw, bool ov, cudaStream_t s) {
-    const int M = p.a.M;
-    return M == 1 ? launch_stream<1, HEAD, true, FMT>(p, qw, ov, s)
-           : M <= 8 ? launch_stream<1, HEAD, false, FMT>(p, qw, ov, s)
-                    : launch_stream<2, HEAD, false, FMT>(p, qw, ov, s);
+    if constexpr (HEAD != kLinear)
+        if (p.a.width == 4) return launch_stream_w<HEAD, FMT, 4>(p, qw, ov, s);
+    return launch_stream_w<HEAD, FMT, 8>(p, qw, ov, s);
 }
 
 template <int HEAD>

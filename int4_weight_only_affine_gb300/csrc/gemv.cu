@@ -326,6 +326,7 @@ __host__ __device__ constexpr int stream_threads(int warps, bool ruled) { return
 
 // FMT: the scale-layout class of the weight (kFmtG64, kFmtS128, kFmtAny,
 // kFmtG32).
+// WIDTH: warps of a team (see above).
 // HEAD: kLinear, or lm_head's pass 1 without or with rules (kernels of their own: with
 // the rules' code in one kernel a call without rules took 36.4 us for 35.2 at one row of
 // 2048 by 151936).

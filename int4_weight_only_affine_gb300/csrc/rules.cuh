@@ -12,8 +12,8 @@
 // counts and a bit of mask per logit, against the 0.5625 K bytes of weight that
 // made it: they are bound by the latency of these reads, which a block therefore
 // asks into L2 while it still streams weights, and issues several at a time.
-// 151936 tokens: one row, K 1024, penalties, 28.3 us for 25.9 without; 16 rows, K 2048,
-// penalties, 300 biases a row and a mask, top 50, 105 us for 93.
+// 151936 tokens: one row, K 1024, penalties, 26.6 us for 24.8 without; 16 rows, K 2048,
+// penalties, 300 biases a row and a mask, top 50, 104 us for 91.5.
 #pragma once
 
 #include "common.cuh"

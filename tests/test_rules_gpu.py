@@ -160,6 +160,18 @@ def test_rules_formats_and_full_vocabulary(w4, group, symmetric):
         check(w4, head, top, rule, rules_of(w4, rule))
 
 
+@pytest.mark.parametrize("k", [64, 448, 960, 1024, 1088])
+@pytest.mark.parametrize("m", [1, 2, 8, 9, 16])
+def test_rules_of_many_narrow_tiles(w4, m, k):
+    """Several tiles of four boxes and fewer a block, and of five, the last one ragged; with and without rules."""
+    n = 16 * 304 * 2 + 1003
+    head = Head(m, n, k, seed=k)
+    rule = random_rule(np.random.RandomState(k), m, n, m + 1, 0.1)
+    for top in (1, 30):
+        check(w4, head, top, {}, None)
+        check(w4, head, top, rule, rules_of(w4, rule))
+
+
 @pytest.mark.parametrize("m", [7, 16])
 def test_rules_at_the_widest_rows(w4, m):
     """Up to the largest K that a selection takes, where little shared memory is left for the rules."""

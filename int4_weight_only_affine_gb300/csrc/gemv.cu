@@ -309,8 +309,13 @@ struct StreamArgs {
 //  * Width 4 for lm_head with K up to 1024, whose tiles have 4 boxes, where a CTA has more
 //    than one: 1024 by 151936, greedy, 25.0, 26.8, 27.8 and 44.0 us at 1, 2, 8 and 16 rows for
 //    26.0, 42.3, 32.9 and 55.4 with width 8 (1000 rows of weights, one tile a CTA: 6.6 for 6.3).
+//    (Affine groups of 64 and symmetric ones of 128 only: kernels of the other formats would
+//    add a half to the time that this file takes to compile.)
 constexpr int kNarrowGroups = 16;
-constexpr int width_of(int ng, bool lmhead, int tpc) { return lmhead && ng <= kNarrowGroups && tpc > 1 ? 4 : 8; }
+constexpr bool narrow_fmt(int fmt) { return fmt == kFmtG64 || fmt == kFmtS128; }
+constexpr int width_of(int ng, int fmt, bool lmhead, int tpc) {
+    return lmhead && narrow_fmt(fmt) && ng <= kNarrowGroups && tpc > 1 ? 4 : 8;
+}
 __host__ __device__ constexpr int consumer_warps(int M, bool lmhead) { return lmhead && M > 8 ? 16 : 8; }
 template <int WARPS>
 __device__ __forceinline__ void consumer_sync() {
@@ -1145,7 +1150,7 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     // Codes, then the tile's scale rows [16][ngs] (and bias rows).
     a.stage_bytes = (uint32_t)align_up((size_t)a.w_bytes + (a.f.sym ? 32u : 64u) * a.f.ngs, 1024);
     // As many stages as the byte budget allows: the ring is what keeps HBM busy.
-    const int width = a.width = width_of(a.ng, lmhead, tpc), warps = consumer_warps(M, lmhead), teams = warps / width;
+    const int width = a.width = width_of(a.ng, fmt_class(a.f), lmhead, tpc), warps = consumer_warps(M, lmhead), teams = warps / width;
     const int stages = (int)max((size_t)max(2, teams), min((size_t)kMaxStages, ring_budget / a.stage_bytes)) / teams * teams;
     a.stages = stages;
     size_t off = (size_t)stages * a.stage_bytes;
@@ -1389,7 +1394,7 @@ int launch_stream_w(const StreamPlan &p, const uint32_t *qw, bool ov, cudaStream
 
 template <int HEAD, int FMT>
 int launch_stream_f(const StreamPlan &p, const uint32_t *qw, bool ov, cudaStream_t s) {
-    if constexpr (HEAD != kLinear)
+    if constexpr (HEAD != kLinear && narrow_fmt(FMT))
         if (p.a.width == 4) return launch_stream_w<HEAD, FMT, 4>(p, qw, ov, s);
     return launch_stream_w<HEAD, FMT, 8>(p, qw, ov, s);
 }

@@ -230,7 +230,8 @@ W4A16_API int lm_head_argmax_topk_noalloc(const uint16_t *x, const uint32_t *qwe
  *            a negative slot: no penalties for the row
  *   biases   row m has the entries bias_offsets[m] <= i < bias_offsets[m + 1]:
  *              z = z + bias_values[i]  where bias_tokens[i] == n
- *            (entries of one token add up; negative tokens are skipped)
+ *            (entries of one token one after the other, in the list's order; negative
+ *            tokens are skipped)
  *   allowed  bit n % 32 of word n / 32 of row m: 0 = n cannot be selected
  * Parts whose first pointer is NULL are left out.  The arrays are read on the
  * device, so that a captured graph can be replayed with other contents; a slot,

@@ -6,7 +6,7 @@
 // For logit l of token n in row m, with c = counts[slot[m]][n]:
 //     c != 0:            z = l > 0 ? l / repetition : l * repetition
 //     t = c & 0x7FFF:    z = z - frequency * t;   t != 0: z = z - presence
-//     biases:            z = z + (sum of the row's values for n)
+//     biases:            z = z + value, for each of the row's entries for n in the list's order
 //     mask bit 0:        n cannot be selected
 // each step one fp32 operation, rounded to nearest.  The rules read 2 bytes of
 // counts and a bit of mask per logit, against the 0.5625 K bytes of weight that
@@ -114,8 +114,8 @@ __device__ __forceinline__ void rules_begin(const Rules &r, const RulesMemory &k
     if (lane == 0) *k.nhits = found;
 }
 
-// Biases of row m, by one warp: 32 entries at a time in order; entries of one token
-// inside a chunk are added up by the first of their lanes, in order.
+// Biases of row m, by one warp: 32 entries at a time; the first lane of a token
+// adds all of that token in the chunk to its logit, in order.
 __device__ __noinline__ void rules_biases_in_order(const Rules &r, float *z, int n0, int rows, int o0, int o1, int lane) {
     for (int at = o0; at < o1; at += 32) {
         const int tok = at + lane < o1 ? __ldg(r.btok + at + lane) : -1;
@@ -123,15 +123,14 @@ __device__ __noinline__ void rules_biases_in_order(const Rules &r, float *z, int
         if (!__any_sync(~0u, mine)) continue;
         const float v = mine ? __ldg(r.bval + at + lane) : 0.f;
         const unsigned same = __match_any_sync(~0u, mine ? tok : -1 - lane);
-        float sum = v;
+        const float old = mine ? z[tok - n0] : 0.f;
+        float sum = old;
         for (int l = 0; l < 32; ++l) {
             const float w = __shfl_sync(~0u, v, l);
-            if (same >> l & 1u) sum = same & ((1u << l) - 1u) ? __fadd_rn(sum, w) : w;
+            if (same >> l & 1u) sum = __fadd_rn(sum, w);
         }
-        if (mine && (same & ((1u << lane) - 1u)) == 0u) {
-            float *p = z + (tok - n0);
-            if (__float_as_uint(*p) != kExcluded) *p = __fadd_rn(*p, sum);
-        }
+        __syncwarp();  // (every lane has read its logit)
+        if (mine && (same & ((1u << lane) - 1u)) == 0u && __float_as_uint(old) != kExcluded) z[tok - n0] = sum;
         __syncwarp();
     }
 }
@@ -201,17 +200,20 @@ __device__ __forceinline__ void rules_apply(const Rules &r, const RulesMemory &k
     if (!r.boff) return;
     const int n = *k.nhits;
     if (n <= r.most) {
-        // The first hit of a token adds all of that token, in their order.
+        // The first hit of a token adds all of that token to its logit, in their order (as the
+        // other branch does: the result must not depend on how many hits a block has).
         for (int h = tid; h < n; h += threads) {
             const BiasHit b = k.hits[h];
             bool first = true;
             for (int i = 0; i < h; ++i) first = first && (k.hits[i].m != b.m || k.hits[i].token != b.token);
             if (!first) continue;
-            float sum = b.value;
-            for (int i = h + 1; i < n; ++i)
-                if (k.hits[i].m == b.m && k.hits[i].token == b.token) sum = __fadd_rn(sum, k.hits[i].value);
             float *p = res + b.m * ld + (b.token - n0);
-            if (__float_as_uint(*p) != kExcluded) *p = __fadd_rn(*p, sum);
+            float z = *p;
+            if (__float_as_uint(z) == kExcluded) continue;
+            z = __fadd_rn(z, b.value);
+            for (int i = h + 1; i < n; ++i)
+                if (k.hits[i].m == b.m && k.hits[i].token == b.token) z = __fadd_rn(z, k.hits[i].value);
+            *p = z;
         }
     } else {
         for (int m = tid >> 5; m < M; m += threads >> 5)

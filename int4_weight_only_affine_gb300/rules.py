@@ -85,7 +85,7 @@ class LogitRules:
     repetition             float32 [rows]: seen tokens' logits are divided (positive) or multiplied by it
     presence, frequency    float32 [rows]: taken off the logits of output tokens, once, and per occurrence
     biases                 (offsets int32 [rows + 1], tokens int32, values float32): added to row r's tokens
-                           offsets[r] .. offsets[r + 1] - 1
+                           offsets[r] .. offsets[r + 1] - 1, one entry after the other
     allowed                int32 [rows][words], bit n % 32 of word n // 32: token n can be selected
     """
 

@@ -258,6 +258,37 @@ def test_biases_of_one_token_add_up(w4):
     assert w4.device_status() == 0
 
 
+def added_in_order(logits, biases):
+    """Every entry of a list added to its token's logit, one fp32 addition after the other."""
+    z = logits.copy()
+    offsets, tokens, values = biases
+    for r in range(len(z)):
+        for i in range(offsets[r], offsets[r + 1]):
+            if tokens[i] >= 0:
+                z[r, tokens[i]] = np.float32(z[r, tokens[i]] + values[i])
+    return z
+
+
+@pytest.mark.parametrize("lens", [(200, 0, 0), (33, 64, 7), (200, 300, 0), (1, 200, 1000)])
+def test_biases_of_one_token_round_in_order(w4, lens):
+    """Entries of one token whose sums are not exact and that cancel, in one chunk of 32 and across chunks, in lists of
+    few entries a block and of many: bit for bit as in the definition, whatever the other rows' lists hold."""
+    g = np.random.RandomState(sum(lens))
+    m, n = 3, 48
+    head = Head(m, n, 64, seed=11)
+    offsets = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    tokens = g.randint(-2, 12, offsets[-1]).astype(np.int32)
+    tokens[::9] += 30
+    values = (g.standard_normal(offsets[-1]) * 10.0 ** g.randint(-3, 8, offsets[-1])).astype(np.float32)
+    values[2::6] = 1e8
+    values[5::6] = -1e8
+    biases = (offsets, tokens, values)
+    want = best(added_in_order(head.logits, biases), np.ones((m, n), bool), n)
+    idx, val = head.pick(w4, n, rules_of(w4, dict(biases=biases)))
+    assert np.array_equal(val.view(np.uint32), (want[1] + np.float32(0)).view(np.uint32))
+    assert np.array_equal(idx, want[0])
+
+
 def test_bad_indexes_are_skipped_and_reported(w4):
     m, n = 4, 500
     head = Head(m, n, 64, seed=6)

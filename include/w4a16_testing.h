@@ -4,7 +4,8 @@
  * They exist so that a test can drive the failure path of the device-side
  * bounded waits (a wait that expires reports W4_ERR_TIMEOUT through
  * w4a16_device_status and the kernel returns) without faulting or hanging a
- * GPU.  Status codes are those of w4a16.h.
+ * GPU, and can see on a host without a GPU what a call would launch.  Status
+ * codes are those of w4a16.h.
  */
 #ifndef W4A16_TESTING_H
 #define W4A16_TESTING_H
@@ -30,6 +31,19 @@ extern "C" {
  * with w4_gemv_seq calls on other host threads.
  */
 W4A16_API int w4a16_testing_set_seq_wait(unsigned long long wait_ns, unsigned target_bump);
+
+/*
+ * w4a16_testing_lm_head_plan - what lm_head_argmax_topk(_rules) launches for
+ * these sizes on a GPU of `sms` SMs.  Makes no CUDA call; of the rules only which
+ * parts are there counts.  Returns W4A16_OK, or the code with which the call
+ * would refuse the sizes.
+ */
+typedef struct {
+    int32_t blocks, stages, stage_bytes; /* grid, and the ring of weights of a block */
+    int32_t smem;                        /* bytes of shared memory of a block */
+} w4a16_testing_lm_head;
+W4A16_API int w4a16_testing_lm_head_plan(int M, int N, int K, int group, int symmetric, int k,
+                                         const w4_logit_rules *rules, int sms, w4a16_testing_lm_head *out);
 
 #ifdef __cplusplus
 }

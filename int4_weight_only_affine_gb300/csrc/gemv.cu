@@ -286,6 +286,7 @@ struct StreamArgs {
     int tiles;   // ceil(N / 16)
     int stages;  // ring depth
     int width;   // warps of a team
+    int warps;   // of consumers
     int ng;      // groups (64-k blocks) along K
     WFmt f;      // scale layout (quantisation group, symmetric codes)
     int units;   // 8-group units along K
@@ -299,16 +300,21 @@ struct StreamArgs {
     uint32_t off_rules;
 };
 
-// The consumers of a CTA are teams of `width` warps that take its tiles in turn, each team
-// with its own share of the ring; a warp takes a box (4 groups) of a tile's chunk of K.
+// The consumers of a CTA are teams of `width` warps that take its tiles in turn; a warp takes
+// a box (4 groups) of a tile's chunk of K.  One ring feeds them, the chunks of the teams'
+// tiles in turn (with a share of the stages for each team, chunk after chunk of one tile, one
+// of three stages was not used and the other team's often empty: 9 rows of 6144 by 151936,
+// greedy, 274 us for 158; 16 rows of 2560, 154 for 101).
 //  * Width 8, one team: w4_gemv, and lm_head of up to 8 rows (two CTAs share an SM).
 //  * 16 warps for lm_head's 9 to 16 rows, whose activations leave an SM one CTA: 73.4 us
 //    for 89.0 with 8 warps at 16 rows of 2048 by 151936, greedy, 90.8 for 112.5 with the 50
-//    best.  Not for w4_gemv, where a CTA has a tile or two (16 rows of 11008 by 2048: 13.4
-//    us, 16.2 with two teams; 2048 by 22016: 15.5 and 14.4).
+//    best.  Not where the ring has two stages only, which one team keeps as busy (11 rows of
+//    5120 by 151936, greedy, 175 us, 197 with two teams; the 50 best 197 and 213), and not for
+//    w4_gemv, where a CTA has a tile or two (16 rows of 11008 by 2048: 13.4 us, 16.2 with two
+//    teams; 2048 by 22016: 15.5 and 14.4).
 //  * Width 4 for lm_head with K up to 1024, whose tiles have 4 boxes, where a CTA has more
-//    than one: 1024 by 151936, greedy, 25.0, 26.8, 27.8 and 44.0 us at 1, 2, 8 and 16 rows for
-//    26.0, 42.3, 32.9 and 55.4 with width 8 (1000 rows of weights, one tile a CTA: 6.6 for 6.3).
+//    than one: 1024 by 151936, greedy, 22.2, 24.6, 25.8 and 43.0 us at 1, 4, 8 and 16 rows for
+//    25.8, 28.9, 32.0 and 55.4 with width 8 (1000 rows of weights, one tile a CTA: 6.6 for 6.3).
 //    (Affine groups of 64 and symmetric ones of 128 only: kernels of the other formats would
 //    add a half to the time that this file takes to compile.)
 constexpr int kNarrowGroups = 16;
@@ -316,7 +322,7 @@ constexpr bool narrow_fmt(int fmt) { return fmt == kFmtG64 || fmt == kFmtS128; }
 constexpr int width_of(int ng, int fmt, bool lmhead, int tpc) {
     return lmhead && narrow_fmt(fmt) && ng <= kNarrowGroups && tpc > 1 ? 4 : 8;
 }
-__host__ __device__ constexpr int consumer_warps(int M, bool lmhead) { return lmhead && M > 8 ? 16 : 8; }
+constexpr int warps_of(int M, bool lmhead, int stages) { return lmhead && M > 8 && stages > 2 ? 16 : 8; }
 template <int WARPS>
 __device__ __forceinline__ void consumer_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
@@ -331,20 +337,20 @@ __host__ __device__ constexpr int stream_threads(int warps, bool ruled) { return
 
 // FMT: the scale-layout class of the weight (kFmtG64, kFmtS128, kFmtAny,
 // kFmtG32).
-// WIDTH: warps of a team (see above).
+// WIDTH: warps of a team; WARPS: of all consumers (see above).
 // HEAD: kLinear, or lm_head's pass 1 without or with rules (kernels of their own: with
 // the rules' code in one kernel a call without rules took 36.4 us for 35.2 at one row of
 // 2048 by 151936).
 constexpr int kLinear = 0, kLmHead = 1, kLmHeadRules = 2;
-template <int NT, int HEAD, bool M1, int FMT, int WIDTH>
-__global__ void __launch_bounds__(stream_threads(consumer_warps(8 * NT, HEAD != kLinear), HEAD == kLmHeadRules), NT == 1 ? 2 : 1)
+template <int NT, int HEAD, bool M1, int FMT, int WIDTH, int WARPS>
+__global__ void __launch_bounds__(stream_threads(WARPS, HEAD == kLmHeadRules), NT == 1 ? 2 : 1)
     stream_kernel(const __grid_constant__ CUtensorMap tm3, const __grid_constant__ CUtensorMap tm2,
                   const __grid_constant__ StreamArgs a) {
     constexpr bool LMHEAD = HEAD != kLinear, kRuled = HEAD == kLmHeadRules;
-    constexpr int kProducer = consumer_warps(8 * NT, LMHEAD);  // (the warp after the consumers)
-    constexpr int TEAMS = kProducer / WIDTH, kAll = stream_threads(kProducer, kRuled), kWarps = kAll / 32;
+    constexpr int kProducer = WARPS;  // (the warp after the consumers)
+    constexpr int TEAMS = WARPS / WIDTH, kAll = stream_threads(WARPS, kRuled), kWarps = kAll / 32;
     // Sums of tiles by warps: two tiles of each team in turn, or one where those of 16 rows fill more.
-    constexpr int kTurns = kProducer == 8 ? 2 : 1;
+    constexpr int kTurns = WARPS == 8 ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -389,50 +395,53 @@ __global__ void __launch_bounds__(stream_threads(consumer_warps(8 * NT, HEAD != 
         // ---------------- producer: weights need no dependency wait ----------------
         if (lane == 0) {
             uint32_t issued_ph = 0, issued_any = 0;
-            const int ring = S / TEAMS;  // stages of a team: every TEAMS-th
+            // One ring for all teams: chunk after chunk of the teams' tiles in turn.
+            int s = 0;
+            uint32_t ph = 0;
             bool ok = true;
-            for (int tl = 0; tl < ntl && ok; ++tl) {
-                const int t = t0 + tl;
-                const bool tail = (t + 1) * kTileRows > N;
-                int it = tl / TEAMS * nch;
-                for (int ch = 0; ch < nch; ++ch, ++it) {
-                    const int s = it % ring * TEAMS + tl % TEAMS;
-                    const uint32_t ph = (it / ring) & 1;
-                    if (!mbar_wait(empty_bar(s), ph ^ 1, abort_flag)) {
-                        ok = false;
-                        break;
+            for (int first = 0; first < ntl && ok; first += TEAMS)
+                for (int ch = 0; ch < nch && ok; ++ch)
+                    for (int tl = first; tl < (TEAMS == 1 ? first + 1 : min(first + TEAMS, ntl)); ++tl) {
+                        const int t = t0 + tl;
+                        const bool tail = (t + 1) * kTileRows > N;
+                        if (!mbar_wait(empty_bar(s), ph ^ 1, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        const int cg0 = gs0 + ch * kChunkGroups;
+                        const int len = min(kChunkGroups, gs1 - cg0);
+                        const int q0 = cg0 / kBoxGroups;
+                        const int nbox = (len + kBoxGroups - 1) / kBoxGroups;
+                        // The tile's scale rows (and bias rows) are contiguous: [16][ngs].
+                        const bool sym = FMT == kFmtS128 || (FMT != kFmtG64 && a.f.sym);
+                        const int ngs = FMT == kFmtG64 ? ng : FMT == kFmtS128 ? ng >> 1 : a.f.ngs;
+                        const uint32_t sbytes = tail ? 0u : 32u * ngs;
+                        const uint32_t sball = sym ? sbytes : 2 * sbytes;
+                        const uint32_t st = base + s * a.stage_bytes;
+                        if (q0 + nbox <= a.nq_full) {
+                            // One 3-D copy: cq quads x 16 rows x 128 B, the same swizzled
+                            // image as cq separate 16 x 128 B boxes.
+                            mbar_expect_tx(full_bar(s), a.cq * kBoxBytes + sball);
+                            tma_load_3d(st, &tm3, 0, t * kTileRows, q0, full_bar(s));
+                        } else {
+                            // The chunk holding the ragged end of a row: one box per quad.
+                            mbar_expect_tx(full_bar(s), nbox * kBoxBytes + sball);
+                            for (int b = 0; b < nbox; ++b)
+                                tma_load_2d(st + b * kBoxBytes, &tm2, (q0 + b) * 32, t * kTileRows, full_bar(s));
+                        }
+                        if (!tail) {
+                            bulk_load(st + a.w_bytes, a.sc + (size_t)t * kTileRows * ngs, sbytes, full_bar(s));
+                            if (!sym)
+                                bulk_load(st + a.w_bytes + sbytes, a.bi + (size_t)t * kTileRows * ngs, sbytes,
+                                          full_bar(s));
+                        }
+                        issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+                        issued_any |= 1u << s;
+                        if (++s == S) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
-                    const int cg0 = gs0 + ch * kChunkGroups;
-                    const int len = min(kChunkGroups, gs1 - cg0);
-                    const int q0 = cg0 / kBoxGroups;
-                    const int nbox = (len + kBoxGroups - 1) / kBoxGroups;
-                    // The tile's scale rows (and bias rows) are contiguous: [16][ngs].
-                    const bool sym = FMT == kFmtS128 || (FMT != kFmtG64 && a.f.sym);
-                    const int ngs = FMT == kFmtG64 ? ng : FMT == kFmtS128 ? ng >> 1 : a.f.ngs;
-                    const uint32_t sbytes = tail ? 0u : 32u * ngs;
-                    const uint32_t sball = sym ? sbytes : 2 * sbytes;
-                    const uint32_t st = base + s * a.stage_bytes;
-                    if (q0 + nbox <= a.nq_full) {
-                        // One 3-D copy: cq quads x 16 rows x 128 B, the same swizzled
-                        // image as cq separate 16 x 128 B boxes.
-                        mbar_expect_tx(full_bar(s), a.cq * kBoxBytes + sball);
-                        tma_load_3d(st, &tm3, 0, t * kTileRows, q0, full_bar(s));
-                    } else {
-                        // The chunk holding the ragged end of a row: one box per quad.
-                        mbar_expect_tx(full_bar(s), nbox * kBoxBytes + sball);
-                        for (int b = 0; b < nbox; ++b)
-                            tma_load_2d(st + b * kBoxBytes, &tm2, (q0 + b) * 32, t * kTileRows, full_bar(s));
-                    }
-                    if (!tail) {
-                        bulk_load(st + a.w_bytes, a.sc + (size_t)t * kTileRows * ngs, sbytes, full_bar(s));
-                        if (!sym)
-                            bulk_load(st + a.w_bytes + sbytes, a.bi + (size_t)t * kTileRows * ngs, sbytes,
-                                      full_bar(s));
-                    }
-                    issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
-                    issued_any |= 1u << s;
-                }
-            }
             // Every copy issued here has landed before the CTA moves on.
             for (int s = 0; s < S; ++s)
                 if (issued_any & (1u << s)) mbar_wait(full_bar(s), (issued_ph >> s) & 1);
@@ -460,8 +469,18 @@ __global__ void __launch_bounds__(stream_threads(consumer_warps(8 * NT, HEAD != 
         pdl_wait();
         stage_activations<M1 ? 2 : 4, FMT == kFmtG32>(a.x, M, a.K, gs0, ngl, xf, xsum, tid, 32 * kProducer);
         consumer_sync<kProducer>();
-        int s = team;
+        int s = 0;
         uint32_t ph = 0;
+        const auto advance = [&](int by) {  // by at most TEAMS stages of at least two
+            s += by;
+#pragma unroll
+            for (int i = 0; i < (TEAMS + 1) / 2; ++i)
+                if (s >= S) {
+                    s -= S;
+                    ph ^= 1;
+                }
+        };
+        if (TEAMS > 1) advance(team);
         for (int tl = team; tl < ntl; tl += TEAMS) {
             const int t = t0 + tl;
             const int row0 = t * kTileRows;
@@ -497,10 +516,7 @@ __global__ void __launch_bounds__(stream_threads(consumer_warps(8 * NT, HEAD != 
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_bar(s));
-                if ((s += TEAMS) == S + team) {
-                    s = team;
-                    ph ^= 1;
-                }
+                advance(TEAMS == 1 ? 1 : min(TEAMS, ntl - (tl - team)));  // (the last tiles may be fewer than teams)
             }
             if (a.defer) {
                 // Keep this warp's partial; all tiles are combined once at the end.
@@ -516,7 +532,7 @@ __global__ void __launch_bounds__(stream_threads(consumer_warps(8 * NT, HEAD != 
                 continue;
             }
             // Per-tile reduction over the team's warps, fixed order.
-            const int place = (kTurns == 2 ? (tl / TEAMS & 1) * kProducer : 0) + team * WIDTH;
+            const int place = (kTurns == 2 ? (tl / TEAMS & 1) * WARPS : 0) + team * WIDTH;
             float *mine = red + (place + tw) * out16;
             if (kTurns == 1) stream_team_sync<kProducer, WIDTH>(team);  // (the tile before has been read)
 #pragma unroll
@@ -938,21 +954,17 @@ __global__ void __launch_bounds__(kSeqThreads, 1) seq_kernel(const __grid_consta
 }
 
 template <int FMT>
-const void *stream_kernel_ptr_f(int M, bool lmhead) {
-    if (lmhead)
-        return M == 1 ? (const void *)stream_kernel<1, kLmHead, true, FMT, 8>
-               : M <= 8 ? (const void *)stream_kernel<1, kLmHead, false, FMT, 8>
-                        : (const void *)stream_kernel<2, kLmHead, false, FMT, 8>;
-    return M == 1 ? (const void *)stream_kernel<1, kLinear, true, FMT, 8>
-           : M <= 8 ? (const void *)stream_kernel<1, kLinear, false, FMT, 8>
-                    : (const void *)stream_kernel<2, kLinear, false, FMT, 8>;
+const void *linear_kernel_ptr_f(int M) {
+    return M == 1 ? (const void *)stream_kernel<1, kLinear, true, FMT, 8, 8>
+           : M <= 8 ? (const void *)stream_kernel<1, kLinear, false, FMT, 8, 8>
+                    : (const void *)stream_kernel<2, kLinear, false, FMT, 8, 8>;
 }
 
-const void *stream_kernel_ptr(int M, bool lmhead, int fmt) {
-    return fmt == kFmtG64    ? stream_kernel_ptr_f<kFmtG64>(M, lmhead)
-           : fmt == kFmtS128 ? stream_kernel_ptr_f<kFmtS128>(M, lmhead)
-           : fmt == kFmtG32  ? stream_kernel_ptr_f<kFmtG32>(M, lmhead)
-                             : stream_kernel_ptr_f<kFmtAny>(M, lmhead);
+const void *linear_kernel_ptr(int M, int fmt) {
+    return fmt == kFmtG64    ? linear_kernel_ptr_f<kFmtG64>(M)
+           : fmt == kFmtS128 ? linear_kernel_ptr_f<kFmtS128>(M)
+           : fmt == kFmtG32  ? linear_kernel_ptr_f<kFmtG32>(M)
+                             : linear_kernel_ptr_f<kFmtAny>(M);
 }
 
 // lm_head pass 2: one CTA per activation row merges the G*k candidates
@@ -1150,9 +1162,10 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     // Codes, then the tile's scale rows [16][ngs] (and bias rows).
     a.stage_bytes = (uint32_t)align_up((size_t)a.w_bytes + (a.f.sym ? 32u : 64u) * a.f.ngs, 1024);
     // As many stages as the byte budget allows: the ring is what keeps HBM busy.
-    const int width = a.width = width_of(a.ng, fmt_class(a.f), lmhead, tpc), warps = consumer_warps(M, lmhead), teams = warps / width;
-    const int stages = (int)max((size_t)max(2, teams), min((size_t)kMaxStages, ring_budget / a.stage_bytes)) / teams * teams;
+    const int stages = (int)max((size_t)2, min((size_t)kMaxStages, ring_budget / a.stage_bytes));
     a.stages = stages;
+    const int warps = a.warps = warps_of(M, lmhead, stages);
+    const int width = a.width = warps == 8 && M > 8 ? 8 : width_of(a.ng, fmt_class(a.f), lmhead, tpc);
     size_t off = (size_t)stages * a.stage_bytes;
     if (lmhead) {
         // After the main loop the ring holds two lists of keys for each warp.
@@ -1184,7 +1197,7 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
 // two rings in flight), one otherwise.
 int ctas_per_sm(int M) { return M <= 8 ? 2 : 1; }
 
-const void *stream_kernel_ptr(int M, bool lmhead, int fmt);
+const void *linear_kernel_ptr(int M, int fmt);
 bool ensure_smem(const void *kern, size_t bytes);
 
 // Clusters of C CTAs (this kernel, this shared memory) that can be resident
@@ -1259,8 +1272,7 @@ bool plan_with_cluster(StreamPlan &p, int C, int slots, int per_sm, bool lmhead)
         // of the layout actually launched (fewer clusters mean more tiles per
         // cluster and possibly a larger layout, so check again).
         for (int iter = 0; iter < 3; ++iter) {
-            const int act = max_active_clusters(stream_kernel_ptr(a.M, lmhead, fmt_class(a.f)),
-                                                stream_threads(consumer_warps(a.M, lmhead), false), C, p.smem, ncl);
+            const int act = max_active_clusters(linear_kernel_ptr(a.M, fmt_class(a.f)), stream_threads(8, false), C, p.smem, ncl);
             if (act >= ncl) break;
             ncl = max(1, act);
             if (!fit_layout(p, lmhead, per_sm, (a.tiles + ncl - 1) / ncl, slice)) return false;
@@ -1270,7 +1282,7 @@ bool plan_with_cluster(StreamPlan &p, int C, int slots, int per_sm, bool lmhead)
     return true;
 }
 
-bool plan_stream(StreamPlan &p, int M, int N, int K, const WFmt &f, bool lmhead, int k) {
+bool plan_stream(StreamPlan &p, int M, int N, int K, const WFmt &f, bool lmhead, int k, int sms) {
     StreamArgs &a = p.a;
     a.M = M;
     a.N = N;
@@ -1281,7 +1293,7 @@ bool plan_stream(StreamPlan &p, int M, int N, int K, const WFmt &f, bool lmhead,
     a.units = (a.ng + 7) / 8;
     a.tiles = (N + kTileRows - 1) / kTileRows;
     const int per_sm = ctas_per_sm(M);
-    int slots = sm_count() * per_sm;
+    int slots = sms * per_sm;
     if (lmhead) slots = min(slots, kMaxCandidates / k);
     // Split K over a cluster only when the tiles alone cannot spread evenly
     // over the SMs or the activations of a whole row do not fit (cost = work
@@ -1333,7 +1345,7 @@ bool ensure_smem(const void *kern, size_t bytes) {
     return true;
 }
 
-template <int NT, int HEAD, bool M1, int FMT, int WIDTH>
+template <int NT, int HEAD, bool M1, int FMT, int WIDTH, int WARPS>
 int launch_stream(const StreamPlan &p, const uint32_t *qw, bool overlap, cudaStream_t st) {
     CUtensorMap tm3, tm2;
     const uint64_t KW = (uint64_t)p.a.K / 8;
@@ -1347,11 +1359,11 @@ int launch_stream(const StreamPlan &p, const uint32_t *qw, bool overlap, cudaStr
     } else {
         tm3 = tm2;  // never used: every chunk takes the 2-D path
     }
-    auto kern = stream_kernel<NT, HEAD, M1, FMT, WIDTH>;
+    auto kern = stream_kernel<NT, HEAD, M1, FMT, WIDTH, WARPS>;
     if (!ensure_smem(reinterpret_cast<const void *>(kern), p.smem)) return W4_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid, 1, 1);
-    cfg.blockDim = dim3(stream_threads(consumer_warps(p.a.M, HEAD != kLinear), HEAD == kLmHeadRules), 1, 1);
+    cfg.blockDim = dim3(stream_threads(WARPS, HEAD == kLmHeadRules), 1, 1);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -1387,9 +1399,11 @@ int check_common(const void *x, const uint32_t *qw, const uint16_t *sc, const ui
 template <int HEAD, int FMT, int WIDTH>
 int launch_stream_w(const StreamPlan &p, const uint32_t *qw, bool ov, cudaStream_t s) {
     const int M = p.a.M;
-    return M == 1 ? launch_stream<1, HEAD, true, FMT, WIDTH>(p, qw, ov, s)
-           : M <= 8 ? launch_stream<1, HEAD, false, FMT, WIDTH>(p, qw, ov, s)
-                    : launch_stream<2, HEAD, false, FMT, WIDTH>(p, qw, ov, s);
+    if (M == 1) return launch_stream<1, HEAD, true, FMT, WIDTH, 8>(p, qw, ov, s);
+    if (M <= 8) return launch_stream<1, HEAD, false, FMT, WIDTH, 8>(p, qw, ov, s);
+    if constexpr (HEAD != kLinear)
+        if (p.a.warps == 16) return launch_stream<2, HEAD, false, FMT, WIDTH, 16>(p, qw, ov, s);
+    return launch_stream<2, HEAD, false, FMT, 8, 8>(p, qw, ov, s);
 }
 
 template <int HEAD, int FMT>
@@ -1417,7 +1431,7 @@ int gemv_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const u
     if (!aligned16(y)) return W4_ERR_ALIGN;
     if (flags & ~(unsigned)W4A16_OVERLAP_PREVIOUS) return W4_ERR_SHAPE;
     StreamPlan p;
-    if (!plan_stream(p, M, N, K, f, false, 1)) return W4_ERR_SHAPE;
+    if (!plan_stream(p, M, N, K, f, false, 1, sm_count())) return W4_ERR_SHAPE;
     p.a.x = x;
     p.a.sc = sc;
     p.a.bi = bi;
@@ -1429,18 +1443,21 @@ int gemv_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const u
     return launch_stream_any<kLinear>(p, qw, ov, s);
 }
 
+bool plan_lm_head(StreamPlan &p, int M, int N, int K, const WFmt &f, int k, const Rules &rules, int sms) {
+    p.a.rules = rules;
+    if (plan_stream(p, M, N, K, f, true, k, sms)) return true;
+    // (Where shared memory is nearly full the biases are searched for once more at the end.)
+    p = StreamPlan();
+    p.a.rules = rules;
+    p.a.rules.most = 0;
+    return rules.most != 0 && plan_stream(p, M, N, K, f, true, k, sms);
+}
+
 int lmhead_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const uint16_t *bi, int M, int N, int K,
                 const WFmt &f, int k, int32_t *idx, float *val, uint64_t *ws, size_t ws_bytes, unsigned flags,
                 void *stream, const Rules &rules = Rules{}) {
     StreamPlan p;
-    p.a.rules = rules;
-    if (!plan_stream(p, M, N, K, f, true, k)) {
-        // (Where shared memory is nearly full the biases are searched for once more at the end.)
-        p = StreamPlan();
-        p.a.rules = rules;
-        p.a.rules.most = 0;
-        if (rules.most == 0 || !plan_stream(p, M, N, K, f, true, k)) return W4_ERR_SHAPE;
-    }
+    if (!plan_lm_head(p, M, N, K, f, k, rules, sm_count())) return W4_ERR_SHAPE;
     const int G = p.grid;
     if ((long long)G > lm_max_blocks(N, k)) return W4_ERR_SHAPE;
     if (ws_bytes < (size_t)M * G * k * sizeof(uint64_t)) return W4_ERR_WORKSPACE;
@@ -1755,6 +1772,21 @@ extern "C" int lm_head_argmax_topk_rules(const uint16_t *x, const uint32_t *qwei
     if (!aligned16(workspace)) return W4_ERR_ALIGN;
     return lmhead_impl(x, qweight, scales, biases, M, N, K, f, k, idx, val, reinterpret_cast<uint64_t *>(workspace),
                        workspace_bytes, flags, stream, r);
+}
+
+extern "C" int w4a16_testing_lm_head_plan(int M, int N, int K, int group, int symmetric, int k,
+                                          const w4_logit_rules *rules, int sms, w4a16_testing_lm_head *out) {
+    if (!out) return W4_ERR_NULL;
+    WFmt f;
+    Rules r;
+    const int st = check_rules(rules, N, r);
+    if (st != W4A16_OK) return st;
+    if (M < 1 || M > 16 || N < 1 || K < 64 || K % 64 != 0 || k < 1 || k > 64 || k > N || sms < 1) return W4_ERR_SHAPE;
+    if (!make_fmt(f, K, group, symmetric != 0)) return W4_ERR_GROUP;
+    StreamPlan p;
+    if (!plan_lm_head(p, M, N, K, f, k, r, sms)) return W4_ERR_SHAPE;
+    *out = w4a16_testing_lm_head{p.grid, p.a.stages, (int)p.a.stage_bytes, (int)p.smem};
+    return W4A16_OK;
 }
 
 // Scale-layout class of an operation (its arguments need not be valid yet).

@@ -1,0 +1,61 @@
+"""lm_head_argmax_topk where its ring of weights is short: long rows, many tiles a block, the last shapes that are taken.
+
+Weights and activations on coarse grids, made and multiplied on the device: every sum of products is exact in fp32 in
+any order, so the selection is known exactly."""
+import pytest
+
+from _gpu import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def w4():
+    require_gpu()
+    import int4_weight_only_affine_gb300 as w4
+    yield w4
+    assert w4.device_status() == 0
+
+
+class Head:
+    def __init__(self, m, n, k, group=64, symmetric=False, seed=0):
+        import torch
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.m, self.n, self.k, self.group = m, n, k, group
+        x = (torch.randn(m, k, generator=g, device="cuda") * 8).round_().clamp_(-32, 32).div_(8)
+        qw = torch.randint(-2**31, 2**31, (n, k // 8), generator=g, device="cuda", dtype=torch.int32)
+        steps = torch.randint(4, 41, (n, k // group), generator=g, device="cuda").float()
+        bias = -8 * steps
+        if not symmetric:
+            bias += torch.randint(-2, 3, steps.shape, generator=g, device="cuda")
+        self.logits = torch.empty(m, n, device="cuda")
+        shifts = torch.arange(0, 32, 4, device="cuda", dtype=torch.int32)
+        for at in range(0, n, 8192):
+            rows = slice(at, min(at + 8192, n))
+            q = ((qw[rows, :, None] >> shifts) & 15).reshape(-1, k // group, group).float()
+            w = (q * steps[rows, :, None] + bias[rows, :, None]).reshape(-1, k) * 2.0**-11
+            self.logits[:, rows] = x @ w.T
+        self.dev = (x.half(), qw, (steps * 2.0**-11).half(), None if symmetric else (bias * 2.0**-11).half())
+
+    def check(self, w4, top, logits=None, **kw):
+        import torch
+        idx, val = w4.lm_head_argmax_topk(*self.dev, k=top, group=self.group, **kw)
+        want, at = torch.sort(self.logits if logits is None else logits, dim=1, descending=True, stable=True)
+        assert torch.equal(val, want[:, :top]) and torch.equal(idx, at[:, :top].int())
+
+
+@pytest.mark.parametrize("m", [9, 16])
+@pytest.mark.parametrize("k", [2112, 4096, 4160])
+@pytest.mark.parametrize("n", [16 * 152 + 5, 16 * 152 * 2, 16 * 152 * 3 + 11])
+def test_two_teams_over_several_chunks(w4, m, k, n):
+    """One, two and three or four tiles a block, for two teams, of two or three chunks of K each."""
+    head = Head(m, n, k, seed=n + k)
+    for top in (1, 20):
+        head.check(w4, top)
+
+
+@pytest.mark.parametrize("m,n,k", [(16, 151936, 2560), (9, 151936, 6144), (12, 32000, 5120), (9, 32000, 8192)])
+def test_two_teams_with_two_or_three_stages(w4, m, n, k):
+    head = Head(m, n, k, seed=m)
+    for top in (1, 50):
+        head.check(w4, top)

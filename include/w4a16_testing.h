@@ -39,8 +39,11 @@ W4A16_API int w4a16_testing_set_seq_wait(unsigned long long wait_ns, unsigned ta
  * would refuse the sizes.
  */
 typedef struct {
-    int32_t blocks, stages, stage_bytes; /* grid, and the ring of weights of a block */
-    int32_t smem;                        /* bytes of shared memory of a block */
+    int32_t blocks;      /* grid */
+    int32_t stages;      /* of the ring of weights of a block, */
+    int32_t teams;       /* whose stages are this many teams' in turn */
+    int32_t stage_bytes;
+    int32_t smem;        /* bytes of shared memory of a block */
 } w4a16_testing_lm_head;
 W4A16_API int w4a16_testing_lm_head_plan(int M, int N, int K, int group, int symmetric, int k,
                                          const w4_logit_rules *rules, int sms, w4a16_testing_lm_head *out);

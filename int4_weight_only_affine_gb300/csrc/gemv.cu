@@ -300,20 +300,19 @@ struct StreamArgs {
     uint32_t off_rules;
 };
 
-// The consumers of a CTA are teams of `width` warps that take its tiles in turn; a warp takes
-// a box (4 groups) of a tile's chunk of K.  One ring feeds them, the chunks of the teams'
-// tiles in turn (with a share of the stages for each team, chunk after chunk of one tile, one
-// of three stages was not used and the other team's often empty: 9 rows of 6144 by 151936,
-// greedy, 274 us for 158; 16 rows of 2560, 154 for 101).
+// The consumers of a CTA are teams of `width` warps that take its tiles in turn, each team with
+// its own stages of the ring; a warp takes a box (4 groups) of a tile's chunk of K.  Chunks of
+// the teams' tiles are copied in turn (with all chunks of one team's tile before the other's,
+// and one stage a team, 9 rows of 6144 by 151936, greedy, took 274 us for 167).
 //  * Width 8, one team: w4_gemv, and lm_head of up to 8 rows (two CTAs share an SM).
 //  * 16 warps for lm_head's 9 to 16 rows, whose activations leave an SM one CTA: 73.4 us
 //    for 89.0 with 8 warps at 16 rows of 2048 by 151936, greedy, 90.8 for 112.5 with the 50
-//    best.  Not where the ring has two stages only, which one team keeps as busy (11 rows of
+//    best.  Not where the ring has two or three stages, which one team keeps as busy (11 rows of
 //    5120 by 151936, greedy, 175 us, 197 with two teams; the 50 best 197 and 213), and not for
 //    w4_gemv, where a CTA has a tile or two (16 rows of 11008 by 2048: 13.4 us, 16.2 with two
 //    teams; 2048 by 22016: 15.5 and 14.4).
 //  * Width 4 for lm_head with K up to 1024, whose tiles have 4 boxes, where a CTA has more
-//    than one: 1024 by 151936, greedy, 22.2, 24.6, 25.8 and 43.0 us at 1, 4, 8 and 16 rows for
+//    than one: 1024 by 151936, greedy, 21.5, 23.9, 25.6 and 41.0 us at 1, 4, 8 and 16 rows for
 //    25.8, 28.9, 32.0 and 55.4 with width 8 (1000 rows of weights, one tile a CTA: 6.6 for 6.3).
 //    (Affine groups of 64 and symmetric ones of 128 only: kernels of the other formats would
 //    add a half to the time that this file takes to compile.)
@@ -322,7 +321,17 @@ constexpr bool narrow_fmt(int fmt) { return fmt == kFmtG64 || fmt == kFmtS128; }
 constexpr int width_of(int ng, int fmt, bool lmhead, int tpc) {
     return lmhead && narrow_fmt(fmt) && ng <= kNarrowGroups && tpc > 1 ? 4 : 8;
 }
-constexpr int warps_of(int M, bool lmhead, int stages) { return lmhead && M > 8 && stages > 2 ? 16 : 8; }
+// Warps of consumers and of a team for a ring with room for so many stages; the stages that are
+// used are a multiple of the teams (below).
+struct Teams {
+    int warps, width;
+};
+inline Teams teams_of(int M, int ng, int fmt, bool lmhead, int tpc, int stages) {
+    Teams t{lmhead && M > 8 ? 16 : 8, width_of(ng, fmt, lmhead, tpc)};
+    if (t.width == 4 && stages < t.warps / 4) t.width = 8;
+    if (t.width == 8 && stages < 2 * (t.warps / 8)) t.warps = 8;
+    return t;
+}
 template <int WARPS>
 __device__ __forceinline__ void consumer_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
@@ -395,13 +404,20 @@ __global__ void __launch_bounds__(stream_threads(WARPS, HEAD == kLmHeadRules), N
         // ---------------- producer: weights need no dependency wait ----------------
         if (lane == 0) {
             uint32_t issued_ph = 0, issued_any = 0;
-            // One ring for all teams: chunk after chunk of the teams' tiles in turn.
+            // Chunks of the teams' tiles in turn.  S is a multiple of TEAMS, so that a slot of the
+            // ring is always the same team's: a team waits for a phase of its slot having seen
+            // the one before, as a wait by parity must.
             int s = 0;
             uint32_t ph = 0;
             bool ok = true;
             for (int first = 0; first < ntl && ok; first += TEAMS)
                 for (int ch = 0; ch < nch && ok; ++ch)
-                    for (int tl = first; tl < (TEAMS == 1 ? first + 1 : min(first + TEAMS, ntl)); ++tl) {
+                    for (int tl = first; tl < first + TEAMS; ++tl) {
+                        if (TEAMS > 1 && tl >= ntl) {  // (the last tiles may be fewer than teams)
+                            s = s + 1 == S ? 0 : s + 1;
+                            ph ^= s == 0;
+                            continue;
+                        }
                         const int t = t0 + tl;
                         const bool tail = (t + 1) * kTileRows > N;
                         if (!mbar_wait(empty_bar(s), ph ^ 1, abort_flag)) {
@@ -469,18 +485,8 @@ __global__ void __launch_bounds__(stream_threads(WARPS, HEAD == kLmHeadRules), N
         pdl_wait();
         stage_activations<M1 ? 2 : 4, FMT == kFmtG32>(a.x, M, a.K, gs0, ngl, xf, xsum, tid, 32 * kProducer);
         consumer_sync<kProducer>();
-        int s = 0;
+        int s = team;
         uint32_t ph = 0;
-        const auto advance = [&](int by) {  // by at most TEAMS stages of at least two
-            s += by;
-#pragma unroll
-            for (int i = 0; i < (TEAMS + 1) / 2; ++i)
-                if (s >= S) {
-                    s -= S;
-                    ph ^= 1;
-                }
-        };
-        if (TEAMS > 1) advance(team);
         for (int tl = team; tl < ntl; tl += TEAMS) {
             const int t = t0 + tl;
             const int row0 = t * kTileRows;
@@ -516,7 +522,10 @@ __global__ void __launch_bounds__(stream_threads(WARPS, HEAD == kLmHeadRules), N
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_bar(s));
-                advance(TEAMS == 1 ? 1 : min(TEAMS, ntl - (tl - team)));  // (the last tiles may be fewer than teams)
+                if ((s += TEAMS) == S + team) {
+                    s = team;
+                    ph ^= 1;
+                }
             }
             if (a.defer) {
                 // Keep this warp's partial; all tiles are combined once at the end.
@@ -1162,10 +1171,10 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     // Codes, then the tile's scale rows [16][ngs] (and bias rows).
     a.stage_bytes = (uint32_t)align_up((size_t)a.w_bytes + (a.f.sym ? 32u : 64u) * a.f.ngs, 1024);
     // As many stages as the byte budget allows: the ring is what keeps HBM busy.
-    const int stages = (int)max((size_t)2, min((size_t)kMaxStages, ring_budget / a.stage_bytes));
-    a.stages = stages;
-    const int warps = a.warps = warps_of(M, lmhead, stages);
-    const int width = a.width = warps == 8 && M > 8 ? 8 : width_of(a.ng, fmt_class(a.f), lmhead, tpc);
+    const int room = (int)max((size_t)2, min((size_t)kMaxStages, ring_budget / a.stage_bytes));
+    const Teams team = teams_of(M, a.ng, fmt_class(a.f), lmhead, tpc, room);
+    const int warps = a.warps = team.warps, width = a.width = team.width;
+    const int stages = a.stages = room / (warps / width) * (warps / width);
     size_t off = (size_t)stages * a.stage_bytes;
     if (lmhead) {
         // After the main loop the ring holds two lists of keys for each warp.
@@ -1785,7 +1794,7 @@ extern "C" int w4a16_testing_lm_head_plan(int M, int N, int K, int group, int sy
     if (!make_fmt(f, K, group, symmetric != 0)) return W4_ERR_GROUP;
     StreamPlan p;
     if (!plan_lm_head(p, M, N, K, f, k, r, sms)) return W4_ERR_SHAPE;
-    *out = w4a16_testing_lm_head{p.grid, p.a.stages, (int)p.a.stage_bytes, (int)p.smem};
+    *out = w4a16_testing_lm_head{p.grid, p.a.stages, p.a.warps / p.a.width, (int)p.a.stage_bytes, (int)p.smem};
     return W4A16_OK;
 }
 

@@ -295,7 +295,8 @@ struct StreamArgs {
     int defer;   // 1: per-warp partials of all tiles kept, combined once at the end
     uint32_t stage_bytes, w_bytes;
     uint32_t off_xf, off_xsum, off_red, off_res, off_bar;
-    int ldr;      // lm_head: logits [M][ldr] of the CTA's rows (odd: stored M at a time, read in rows)
+    int ldr;      // lm_head: logits [M][ldr] of the CTA's rows (odd where there is room: stored M at a time, read in rows)
+    int lists;    // lm_head: warps that there is room for in the selection (two lists of keys each)
     Rules rules;  // lm_head: applied to the logits before the selection
     uint32_t off_rules;
 };
@@ -628,11 +629,11 @@ __global__ void __launch_bounds__(stream_threads(WARPS, HEAD == kLmHeadRules), N
         return;
     }
     // A row goes to `share` warps, one where there are rows for all of them or few keys.
-    uint64_t(*lists)[64] = reinterpret_cast<uint64_t(*)[64]>(sb);  // (the ring is free now)
-    uint64_t *pending = reinterpret_cast<uint64_t *>(sb) + (kWarps + warp) * 64;
-    const int share = max(1, min(kWarps / M, (rows + 63) / 64));
+    uint64_t(*lists)[64] = reinterpret_cast<uint64_t(*)[64]>(sb);  // (the ring is free now, and what lies before the logits)
+    uint64_t *pending = reinterpret_cast<uint64_t *>(sb) + (a.lists + warp) * 64;
+    const int share = max(1, min(a.lists / M, (rows + 63) / 64));
     const int part = warp % share;
-    for (int m = warp / share; m < M; m += kWarps / share) {
+    for (int m = warp < a.lists ? warp / share : M; m < M; m += a.lists / share) {
         const int i0 = (int)((long long)rows * part / share), i1 = (int)((long long)rows * (part + 1) / share);
         const Key2 run = warp_best64(res + m * a.ldr, n0, i0, i1, a.k, kRuled, pending, lane);
         if (share == 1) {
@@ -1156,6 +1157,7 @@ struct StreamPlan {
     StreamArgs a;
     int grid;
     size_t smem;
+    bool tight = false;  // lm_head: no byte more than a selection needs at all, where the usual layout does not fit
 };
 
 // force_defer: keep every warp's partial of every tile (no per-tile barrier)
@@ -1176,9 +1178,9 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     const int warps = a.warps = team.warps, width = a.width = team.width;
     const int stages = a.stages = room / (warps / width) * (warps / width);
     size_t off = (size_t)stages * a.stage_bytes;
-    if (lmhead) {
-        // After the main loop the ring holds two lists of keys for each warp.
-        const size_t need = (size_t)(stream_threads(warps, true) / 32) * 2 * 64 * 8;
+    constexpr size_t kLists = 2 * 64 * 8;  // of a warp, in place of the ring after the main loop
+    if (lmhead && !p.tight) {
+        const size_t need = (size_t)(stream_threads(warps, true) / 32) * kLists;
         if (off < need) off = align_up(need, 1024);
     }
     a.off_xf = (uint32_t)off;
@@ -1187,10 +1189,12 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     off = align_up(off + (size_t)slice_groups * M * 4 * xsums, 16);
     a.off_red = (uint32_t)off;
     const size_t red_all = (size_t)tpc * width * kTileRows * M * 4;
-    a.defer = (force_defer || red_all <= 32 * 1024) ? 1 : 0;
-    off = align_up(off + (a.defer ? red_all : (size_t)16 * kTileRows * M * 4), 16);
+    const size_t red_turns = (size_t)16 * kTileRows * M * 4;
+    a.defer = (force_defer || red_all <= (p.tight && red_turns < 32 * 1024 ? red_turns : 32 * 1024)) ? 1 : 0;
+    off = align_up(off + (a.defer ? red_all : red_turns), 16);
     a.off_res = (uint32_t)off;
-    a.ldr = tpc * kTileRows + 1;
+    a.lists = (int)min((size_t)(stream_threads(warps, lmhead && a.rules.on) / 32), off / kLists);
+    a.ldr = tpc * kTileRows + (p.tight ? 0 : 1);
     if (lmhead) off = align_up(off + (size_t)a.ldr * M * 4, 16);
     else if (a.C > 1) off = align_up(off + (size_t)tpc * kTileRows * M * 4, 16);
     a.off_rules = (uint32_t)off;
@@ -1267,7 +1271,9 @@ bool fit_layout(StreamPlan &p, bool lmhead, int per_sm, int tpc, int slice) {
         layout_stream(p, p.a.M, lmhead, budget - (per_sm == 2 ? 24 * 1024 : 0), tpc, slice);
         if (p.smem <= per_cta) return true;
     }
-    return false;
+    if (!p.tight) return false;
+    layout_stream(p, p.a.M, lmhead, 0, tpc, slice);  // two stages
+    return p.smem <= per_cta;
 }
 
 bool plan_with_cluster(StreamPlan &p, int C, int slots, int per_sm, bool lmhead) {
@@ -1452,14 +1458,18 @@ int gemv_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const u
     return launch_stream_any<kLinear>(p, qw, ov, s);
 }
 
+// What a selection launches: the usual layout, else one with less room for the biases, which
+// are then searched for once more at the end, else the tightest.
 bool plan_lm_head(StreamPlan &p, int M, int N, int K, const WFmt &f, int k, const Rules &rules, int sms) {
-    p.a.rules = rules;
-    if (plan_stream(p, M, N, K, f, true, k, sms)) return true;
-    // (Where shared memory is nearly full the biases are searched for once more at the end.)
-    p = StreamPlan();
-    p.a.rules = rules;
-    p.a.rules.most = 0;
-    return rules.most != 0 && plan_stream(p, M, N, K, f, true, k, sms);
+    for (int spare = 0; spare < 3; ++spare) {
+        if (spare == 1 && rules.most == 0) continue;
+        p = StreamPlan();
+        p.a.rules = rules;
+        if (spare > 0) p.a.rules.most = 0;
+        p.tight = spare == 2;
+        if (plan_stream(p, M, N, K, f, true, k, sms)) return true;
+    }
+    return false;
 }
 
 int lmhead_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const uint16_t *bi, int M, int N, int K,

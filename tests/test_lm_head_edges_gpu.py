@@ -2,6 +2,8 @@
 
 Weights and activations on coarse grids, made and multiplied on the device: every sum of products is exact in fp32 in
 any order, so the selection is known exactly."""
+import ctypes
+
 import pytest
 
 from _gpu import require_gpu
@@ -58,4 +60,36 @@ def test_two_teams_over_several_chunks(w4, m, k, n):
 def test_two_teams_with_two_or_three_stages(w4, m, n, k):
     head = Head(m, n, k, seed=m)
     for top in (1, 50):
+        head.check(w4, top)
+
+
+def last_taken(w4, m, k, group, symmetric, top, most):
+    """The largest vocabulary that is taken, from the plan on the host (w4a16_testing_lm_head: five numbers)."""
+    import torch
+    f = w4.lib.w4a16_testing_lm_head_plan
+    f.argtypes = [ctypes.c_int] * 6 + [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]
+    out, sms = (ctypes.c_int32 * 5)(), torch.cuda.get_device_properties(0).multi_processor_count
+    lo, hi = top, most
+    while hi - lo > 1:
+        n = (lo + hi) // 2
+        lo, hi = (n, hi) if f(m, n, k, group, int(symmetric), top, None, sms, out) == 0 else (lo, n)
+    return lo
+
+
+@pytest.mark.parametrize("m,k,group,symmetric,top", [(1, 64, 64, False, 2), (3, 64, 64, False, 1), (8, 128, 64, False, 5),
+                                                     (9, 256, 32, False, 3), (16, 1024, 64, False, 20), (16, 1024, 64, False, 1),
+                                                     (12, 896, 128, True, 50), (7, 3648, 64, False, 9), (16, 2816, 64, False, 1)])
+def test_the_widest_vocabulary(w4, m, k, group, symmetric, top):
+    n = last_taken(w4, m, k, group, symmetric, top, (1 << 24) // top)
+    assert n > 100000
+    head = Head(m, n, k, group, symmetric, seed=m)
+    head.check(w4, top)
+
+
+@pytest.mark.parametrize("m,n,k,group,symmetric", [(7, 151936, 3648, 64, False), (11, 151936, 5760, 64, False),
+                                                   (14, 262144, 2816, 64, False), (6, 128256, 4992, 128, True),
+                                                   (16, 350000, 1024, 64, False)])
+def test_wide_vocabularies(w4, m, n, k, group, symmetric):
+    head = Head(m, n, k, group, symmetric, seed=m)
+    for top in (1, 30):
         head.check(w4, top)

@@ -45,3 +45,45 @@ def test_a_stage_belongs_to_one_team(plan):
                     assert p.stages % p.teams == 0 and p.stages >= (2 * p.teams if k > 2048 else p.teams), (m, n, k)
                     most.add((p.teams, min(p.stages, 5)))
     assert {(1, 2), (1, 3), (2, 4), (4, 5)} <= most
+
+
+def aligned(n, to=16):
+    return (n + to - 1) // to * to
+
+
+def least_smem(m, n, k, group, symmetric, top):
+    """What a block cannot do without: two stages of weights, its rows' activations and their sums, a tile's sums by
+    warps (two tiles in turn, or all of them where these are few), and the logits."""
+    blocks = min(-(-n // 16), min(SMS * (2 if m <= 8 else 1), 16384 // top))
+    tiles, groups = -(-(-(-n // 16)) // blocks), k // 64
+    stage = aligned(min(32, groups + 3) // 4 * 2048 + (32 if symmetric else 64) * (k // group), 1024)
+    size = 2 * stage + aligned(groups * m * 128)
+    size = aligned(size + groups * m * 4 * (2 if group == 32 else 1))
+    size = aligned(size + min(2 * 8 * 16 * m * 4, tiles * 8 * 16 * m * 4))
+    size = aligned(size + tiles * 16 * m * 4)
+    return size + 16 * 2 + 16 + 1024
+
+
+WIDE = [(7, 3648, 151936, 64, False), (11, 5760, 151936, 64, False), (14, 2816, 262144, 64, False),
+        (6, 4992, 128256, 128, True), (16, 1024, 350000, 64, False), (16, 896, 396416, 64, False), (9, 1024, 778240, 64, False)]
+
+
+@pytest.mark.parametrize("m,k,n,group,symmetric", WIDE)
+def test_wide_selections_are_taken(plan, m, k, n, group, symmetric):
+    p = plan(m, n, k, group, symmetric)
+    assert p and p.smem <= SMEM // (2 if m <= 8 else 1)
+
+
+@pytest.mark.parametrize("group,symmetric", [(64, False), (128, True), (32, False), (128, False), (32, True)])
+def test_every_selection_that_fits_is_taken(plan, group, symmetric):
+    taken = 0
+    for n in (1000, 32000, 50257, 128256, 151936, 200064, 262144, 384256, 500009, 900000, 2000000):
+        for m in range(1, 17):
+            for top in (1, 5, 50, 64):
+                if n * top > 1 << 24:
+                    continue
+                for k in (*range(128, 2049, 128), *range(2176, 17000, 256 if group > 64 else 192)):
+                    fits = least_smem(m, n, k, group, symmetric, top) <= SMEM // (2 if m <= 8 else 1)
+                    assert (plan(m, n, k, group, symmetric, top) is not None) == fits, (m, n, k, top)
+                    taken += fits
+    assert taken > 10000

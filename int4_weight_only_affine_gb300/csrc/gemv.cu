@@ -299,6 +299,7 @@ struct StreamArgs {
     int lists;    // lm_head: warps that there is room for in the selection (two lists of keys each)
     Rules rules;  // lm_head: applied to the logits before the selection
     uint32_t off_rules;
+    int late;     // the rules have no memory of their own: they are read into the ring after the main loop
 };
 
 // The consumers of a CTA are teams of `width` warps that take its tiles in turn, each team with
@@ -466,6 +467,7 @@ __global__ void __launch_bounds__(stream_threads(WARPS, HEAD == kLmHeadRules), N
     } else if (kRuled && warp > kProducer) {
         // ---------------- lm_head with rules: one more warp, for them ----------------
         pdl_wait();
+        if (a.late) __syncthreads();  // (the barrier behind the main loop; the others wait at one more)
         rules_begin(a.rules, RulesMemory(sb + a.off_rules, M), M, N, t0 * kTileRows,
                     min(N, t1 * kTileRows) - t0 * kTileRows, lane);
     } else {
@@ -593,6 +595,7 @@ __global__ void __launch_bounds__(stream_threads(WARPS, HEAD == kLmHeadRules), N
         }
     }
     __syncthreads();
+    if (kRuled && a.late && warp <= kProducer) __syncthreads();
 
     if (!LMHEAD) {
         if (C > 1) {
@@ -1197,9 +1200,9 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
     a.ldr = tpc * kTileRows + (p.tight ? 0 : 1);
     if (lmhead) off = align_up(off + (size_t)a.ldr * M * 4, 16);
     else if (a.C > 1) off = align_up(off + (size_t)tpc * kTileRows * M * 4, 16);
-    a.off_rules = (uint32_t)off;
-    if (lmhead && a.rules.on) off += rules_bytes(a.rules, M);
-    off = align_up(off, 16);
+    // (Late, the rules lie at the start of the ring, whose two stages of 3 KB or more hold them.)
+    a.off_rules = a.late ? 0u : (uint32_t)off;
+    if (lmhead && a.rules.on && !a.late) off = align_up(off + rules_bytes(a.rules, M), 16);
     a.off_bar = (uint32_t)off;
     off += 16 * stages + 16;
     p.smem = off + 1024;  // alignment slack
@@ -1458,14 +1461,15 @@ int gemv_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const u
     return launch_stream_any<kLinear>(p, qw, ov, s);
 }
 
-// What a selection launches: the usual layout, else one with less room for the biases, which
-// are then searched for once more at the end, else the tightest.
+// What a selection launches: the usual layout; where that does not fit, one without memory for
+// the rules beside it; else the tightest.  With rules, then, every shape is taken that is
+// taken without.
 bool plan_lm_head(StreamPlan &p, int M, int N, int K, const WFmt &f, int k, const Rules &rules, int sms) {
     for (int spare = 0; spare < 3; ++spare) {
-        if (spare == 1 && rules.most == 0) continue;
+        if (spare == 1 && !rules.on) continue;
         p = StreamPlan();
         p.a.rules = rules;
-        if (spare > 0) p.a.rules.most = 0;
+        p.a.late = rules.on && spare > 0;
         p.tight = spare == 2;
         if (plan_stream(p, M, N, K, f, true, k, sms)) return true;
     }

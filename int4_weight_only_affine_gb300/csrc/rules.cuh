@@ -32,7 +32,7 @@ struct Rules {
     int slots, entries;
     int vec;  // rows of counts start on 16 bytes
     int on;
-    int most;  // biases in the block's tokens that there is room for
+    int most;  // biases in the block's tokens that there is room for: kMaxHits, or none without biases
 };
 
 // What stands in place of a masked logit: a NaN that no operation makes.
@@ -50,7 +50,7 @@ struct BiasHit {
     int m, at, token;
     float value;
 };
-constexpr int kMaxHits = 256;  // (or none, where shared memory is short); more of them are left to the warps, one list after the other
+constexpr int kMaxHits = 256;  // more of them are left to the warps, one list after the other
 
 // The block's memory of the rules: rows, hits and their number.
 inline size_t rules_bytes(const Rules &r, int M) { return 16 + M * sizeof(RowRule) + r.most * sizeof(BiasHit); }
@@ -63,8 +63,8 @@ struct RulesMemory {
           nhits(reinterpret_cast<int *>(p)) {}
 };
 
-// Done by one warp of its own while the others stream weights: reads the rows'
-// rules, asks the counts and masks of tokens n0 .. n0 + rows - 1 into L2, and
+// Done by one warp of its own while the others stream weights (after that, where shared
+// memory is short): reads the rows' rules, asks the counts and masks of tokens n0 .. n0 + rows - 1 into L2, and
 // searches the lists of biases for these tokens.  M <= 16.
 __device__ __forceinline__ void rules_begin(const Rules &r, const RulesMemory &k, int M, int N, int n0, int rows,
                                             int lane) {

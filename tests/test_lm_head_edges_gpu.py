@@ -93,3 +93,44 @@ def test_wide_vocabularies(w4, m, n, k, group, symmetric):
     head = Head(m, n, k, group, symmetric, seed=m)
     for top in (1, 30):
         head.check(w4, top)
+
+
+def ruled(head, seed, mask_only):
+    """Rules for a head's rows, and its logits after them (fp32 steps; masked ones are -infinity)."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    m, n, z = head.m, head.n, head.logits.clone()
+    kw = {}
+    if not mask_only:
+        counts = torch.randint(-2**15, 2**15, (m + 2, n), generator=g, device="cuda", dtype=torch.int16)
+        counts[torch.rand(m + 2, n, generator=g, device="cuda") < 0.8] = 0
+        kw["counts"], kw["slots"] = counts, torch.randperm(m + 2, generator=g, device="cuda")[:m].int()
+        kw["repetition"] = 1 + 0.05 * torch.randint(0, 8, (m,), generator=g, device="cuda")
+        kw["presence"] = 0.125 * torch.randint(0, 5, (m,), generator=g, device="cuda")
+        kw["frequency"] = 0.001 * torch.randint(0, 5, (m,), generator=g, device="cuda")
+        c = counts[kw["slots"].long()]
+        t, rep = (c & 0x7FFF).float(), kw["repetition"][:, None]
+        z = torch.where(c != 0, torch.where(z > 0, z / rep, z * rep), z)
+        z = torch.where(t > 0, (z - kw["frequency"][:, None] * t) - kw["presence"][:, None], z)
+        tokens = torch.stack([torch.randperm(n, generator=g, device="cuda")[:300] for _ in range(m)])
+        values = 0.25 * torch.randint(-40, 41, tokens.shape, generator=g, device="cuda")
+        z.scatter_add_(1, tokens, values)
+        offsets = (300 * torch.arange(m + 1, device="cuda")).int()
+        kw["biases"] = (offsets, tokens.int().reshape(-1), values.reshape(-1))
+    allowed = torch.rand(m, (n + 31) // 32 * 32, generator=g, device="cuda") < 0.5
+    bits = (allowed.view(m, -1, 32).long() << torch.arange(32, device="cuda")).sum(-1)
+    kw["allowed"] = bits.to(torch.int32)
+    return kw, z.masked_fill(~allowed[:, :n], float("-inf"))
+
+
+@pytest.mark.parametrize("m,n,k,group", [(16, 131072, 3584, 64), (6, 32000, 4032, 64), (4, 128256, 6912, 64), (3, 151936, 6976, 32),
+                                         (2, 200064, 8960, 32), (16, 384256, 1024, 64), (9, 890112, 256, 32)])
+def test_rules_on_the_widest_selections(w4, m, n, k, group):
+    """Where the rules have no shared memory of their own."""
+    head = Head(m, n, k, group, seed=k)
+    for mask_only in (True, False):
+        kw, z = ruled(head, m, mask_only)
+        if not mask_only:
+            kw["counts"] = w4.TokenCounts(kw["counts"])
+        for top in (1, 17):
+            head.check(w4, top, z, rules=w4.LogitRules(**kw))

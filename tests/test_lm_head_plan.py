@@ -87,3 +87,33 @@ def test_every_selection_that_fits_is_taken(plan, group, symmetric):
                     assert (plan(m, n, k, group, symmetric, top) is not None) == fits, (m, n, k, top)
                     taken += fits
     assert taken > 10000
+
+
+class Rules(ctypes.Structure):
+    _fields_ = [("counts", ctypes.c_void_p), ("counts_stride", ctypes.c_int64), ("slot", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("bias_offsets", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("allowed", ctypes.c_void_p), ("allowed_stride", ctypes.c_int64), ("slots", ctypes.c_int32),
+                ("bias_entries", ctypes.c_int32)]
+
+
+RULED = [(16, 131072, 3584, 64, False), (6, 32000, 4032, 64, False), (4, 128256, 6912, 64, False), (3, 151936, 6976, 32, False),
+         (2, 200064, 8960, 32, False), (16, 384256, 1024, 64, False)]
+
+
+@pytest.mark.parametrize("group,symmetric", [(64, False), (128, True), (32, False)])
+def test_rules_take_what_is_taken_without(plan, group, symmetric):
+    there = ctypes.c_void_p(16)       # (only looked at as a pointer)
+    mask = Rules(allowed=there, allowed_stride=1 << 20)
+    every = Rules(there, 1 << 24, there, there, there, there, there, there, there, there, 1 << 20, 8, 999)
+    shapes = [(m, n, k) for n in (1000, 32000, 128256, 151936, 200064, 262144) for m in range(1, 17)
+              for k in range(128, 17000, 128)]
+    shapes += [(m, n, k) for m, n, k, g, s in RULED if (g, s) == (group, symmetric)]
+    taken = 0
+    for m, n, k in shapes:
+        plain = plan(m, n, k, group, symmetric, 5)
+        for rules in (mask, every):
+            p = plan(m, n, k, group, symmetric, 5, ctypes.byref(rules))
+            assert (p is None) == (plain is None), (m, n, k)
+        taken += plain is not None
+    assert taken > 2000

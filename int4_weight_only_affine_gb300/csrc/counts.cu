@@ -157,7 +157,7 @@ using namespace w4a16;
 extern "C" int w4_token_counts(uint16_t *counts, int64_t counts_stride, int slots, int N, const int32_t *slot,
                                const int32_t *tokens, const int32_t *offsets, int batch, int total, unsigned flags,
                                void *stream) {
-    if (!counts || !slot) return W4_ERR_NULL;
+    if (!counts || (!slot && batch != 0)) return W4_ERR_NULL;  // (an empty array may have no address)
     if (slots < 1 || N < 1 || counts_stride < N || batch < 0 || total < 0 || (!offsets && total != batch) ||
         batch > 65535 || (flags & ~(unsigned)(W4_COUNTS_PROMPT | W4_COUNTS_RESET)) != 0)
         return W4_ERR_SHAPE;

@@ -182,3 +182,10 @@ def test_token_counts(calls):
         assert count(**kw) == C[code], kw
     assert count(total=0, tokens=None) == C["W4A16_OK"]
     assert count(batch=0, total=0, tokens=None, flags=2) == C["W4A16_OK"]
+
+
+def test_no_sequences_to_count(calls):
+    """Empty arrays have no address."""
+    for flags in (0, 1, 2, 3):
+        for offsets in (FAKE, None):
+            assert calls.w4_token_counts(FAKE, 1000, 4, 1000, None, None, offsets, 0, 0, flags, None) == C["W4A16_OK"]

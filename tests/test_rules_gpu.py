@@ -409,6 +409,22 @@ def test_token_counts_of_a_step(w4):
     assert w4.device_status() == 0
 
 
+def test_token_counts_of_nothing(w4):
+    """A step in which no request begins, and one whose requests bring no tokens."""
+    import torch
+    t = counts_on(w4, np.full((3, 50), 7, np.uint16), "new")
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for prompt in (False, True):
+        for reset in (False, True):
+            w4.token_counts_add(t, none, none, prompt=prompt, reset=reset)
+            w4.token_counts_add(t, none, none, offsets=zero, prompt=prompt, reset=reset)
+            w4.token_counts_add(t, zero, none, offsets=torch.zeros(2, dtype=torch.int32, device="cuda"), prompt=prompt)
+    assert bool((t.counts == 7).all())
+    w4.token_counts_add(t, zero + 2, none, offsets=torch.zeros(2, dtype=torch.int32, device="cuda"), reset=True)
+    assert bool((t.counts[:2] == 7).all()) and bool((t.counts[2] == 0).all())
+
+
 def test_token_counts_bad_indexes(w4):
     n = 64
     start = np.zeros((3, n), np.uint16)

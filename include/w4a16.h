@@ -281,9 +281,11 @@ W4A16_API int lm_head_argmax_topk_rules(const uint16_t *x, const uint32_t *qweig
  *            tokens of the output (the count goes up, and stays at 32767)
  *            W4_COUNTS_RESET: the sequences' rows are cleared first (a request
  *            takes its slot); of sequences with one slot the last takes it
- *   batch 0..65535;  total >= 0;  a token past N, a slot past the last, offsets
- *   out of order and slots taken again are skipped and reported by
- *   w4a16_device_status as W4_ERR_INDEX.
+ *   batch 0..65535;  total >= 0;  a token past N, a slot past the last, the tokens
+ *   of a sequence whose offsets are out of order or past total, and slots taken
+ *   again are skipped (a row is cleared all the same) and reported by
+ *   w4a16_device_status as W4_ERR_INDEX.  Tokens that such offsets give to several
+ *   sequences may count for any of them; rows that no sequence names stay as they are.
  * Pointers need their natural alignment only.  Results do not depend on the
  * order in which tokens are counted.
  * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_DEVICE, W4_ERR_LAUNCH.

@@ -7,7 +7,8 @@
 // sequence by a binary search of the offsets and changes its entry with a 16-bit
 // compare-and-swap, which is exact at any number of equal tokens; lanes that
 // hold the same entry let the first of them do it for all.  Entries are whole
-// numbers, so the order of the updates does not show.  A call is one chain of
+// numbers, so the order of the updates does not show.  Further blocks look the
+// sequences over, for those that no token leads to.  A call is one chain of
 // three or four dependent reads: 2 to 3 us, whatever it counts.
 //
 // New requests (reset_kernel): a block owns 8192 tokens of one slot's row, counts
@@ -30,6 +31,7 @@ struct CountArgs {
     long long stride;
     const int32_t *slot, *tokens, *offsets;
     int slots, N, batch, total, prompt;
+    unsigned token_blocks;  // of add_kernel
 };
 
 // The tokens [first, end) of sequence b; false (reported) if its offsets are out of order.
@@ -50,7 +52,16 @@ __device__ __forceinline__ uint16_t *row_of(const CountArgs &a, int b) {
 
 __global__ void __launch_bounds__(kThreads) add_kernel(const CountArgs a) {
     pdl_wait();
-    const long long t = (long long)blockIdx.x * kThreads + threadIdx.x;
+    long long t = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (blockIdx.x >= a.token_blocks) {  // the blocks behind the tokens look the sequences over, a thread to each
+        t -= (long long)a.token_blocks * kThreads;
+        int first, end;
+        if (t < a.batch) {
+            sequence(a, (int)t, first, end);
+            row_of(a, (int)t);
+        }
+        return;
+    }
     const int lane = threadIdx.x & 31;
     uint16_t *p = nullptr;
     if (t < a.total) {
@@ -92,6 +103,8 @@ __global__ void __launch_bounds__(kThreads) reset_kernel(const CountArgs a) {
     __shared__ __align__(16) uint32_t seen[kSpan];  // bit 31: in the prompt; the rest: times in the output
     pdl_wait();
     const int b = blockIdx.y, lo = blockIdx.x * kSpan, span = min(kSpan, a.N - lo);
+    int first, end;
+    const bool ordered = sequence(a, b, first, end);
     uint16_t *row = row_of(a, b);
     if (!row) return;
     bool taken = false;  // by a later sequence: the row is that one's
@@ -101,8 +114,7 @@ __global__ void __launch_bounds__(kThreads) reset_kernel(const CountArgs a) {
         if (threadIdx.x == 0) atomicExch(&g_bad_index, 1);
         return;
     }
-    int first, end;
-    if (sequence(a, b, first, end)) {
+    if (ordered) {
         constexpr int kAhead = 8;
         for (int at = first; at < end; at += kAhead * kThreads) {
             int n[kAhead];
@@ -169,10 +181,10 @@ extern "C" int w4_token_counts(uint16_t *counts, int64_t counts_stride, int slot
     if (batch == 0 || (total == 0 && !reset)) return W4A16_OK;
     if (device_cc() != 103) return W4_ERR_DEVICE;
     const CountArgs a{counts, counts_stride, slot, tokens, offsets, slots, N, batch, total,
-                      (flags & W4_COUNTS_PROMPT) != 0};
+                      (flags & W4_COUNTS_PROMPT) != 0, (unsigned)((total + (long long)kThreads - 1) / kThreads)};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = reset ? dim3((unsigned)((N + (long long)kSpan - 1) / kSpan), (unsigned)batch, 1)
-                        : dim3((unsigned)((total + (long long)kThreads - 1) / kThreads), 1, 1);
+                        : dim3(a.token_blocks + (offsets ? (unsigned)((batch + kThreads - 1) / kThreads) : 0u), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr;

@@ -441,6 +441,20 @@ def test_token_counts_bad_indexes(w4):
             assert w4.device_status() == 9 and w4.device_status() == 0
 
 
+@pytest.mark.parametrize("slots,offsets", [([0, 1, 2], [0, 5, 3, 8]), ([0, 1, 2], [0, 8, 2, 8]), ([0, 9, 2], [0, 4, 4, 8]),
+                                           ([0, 1, 9], [0, 4, 8, 8]), ([-1, 0, -1], [0, 3, 8, 6]), ([0, 2, -1], [0, 4, 8, 9])])
+@pytest.mark.parametrize("reset", [False, True])
+def test_token_counts_bad_sequences_without_tokens_of_their_own(w4, slots, offsets, reset):
+    """Offsets out of order and slots past the last are reported, whether or not a token falls into their sequence; rows
+    that no sequence names stay."""
+    t = counts_on(w4, np.full((4, 40), 5, np.uint16), "new")
+    w4.token_counts_add(t, to_dev(np.array(slots, np.int32)), to_dev(np.arange(8, dtype=np.int32)),
+                        to_dev(np.array(offsets, np.int32)), reset=reset)
+    assert w4.device_status() == 9 and w4.device_status() == 0
+    got = t.counts.cpu().numpy()
+    assert all((got[r] == 5).all() for r in range(4) if r not in slots)
+
+
 def test_reset_of_one_slot_twice(w4):
     """The last of the sequences with one slot takes it, whole, whatever the others count; it is reported."""
     g = np.random.RandomState(5)

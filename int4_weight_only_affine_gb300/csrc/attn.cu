@@ -528,7 +528,7 @@ template <int DP, bool WIDE>
 int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
     using C = RowCfg<DP>;
     static_assert(C::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
-    if (!set_smem_once(reinterpret_cast<const void *>(attn_rows_kernel<DP, WIDE>), (int)C::SMEM)) return W4_ERR_LAUNCH;
+    if (!ensure_smem(reinterpret_cast<const void *>(attn_rows_kernel<DP, WIDE>), C::SMEM)) return W4_ERR_LAUNCH;
     return launch_dependent(attn_rows_kernel<DP, WIDE>, grid, C::THREADS, C::SMEM, stream, mk, mv, a);
 }
 

@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 template <int DP, bool QUEUE>
 int launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid, cudaStream_t stream) {
     static_assert(TcCfg<DP>::SMEM + sizeof(PlanShared) <= 227 * 1024, "shared memory");
-    if (!set_smem_once(reinterpret_cast<const void *>(attn_tc_kernel<DP, QUEUE>), (int)TcCfg<DP>::SMEM)) return W4_ERR_LAUNCH;
+    if (!ensure_smem(reinterpret_cast<const void *>(attn_tc_kernel<DP, QUEUE>), TcCfg<DP>::SMEM)) return W4_ERR_LAUNCH;
     return launch_dependent(attn_tc_kernel<DP, QUEUE>, grid, TC_THREADS, TcCfg<DP>::SMEM, stream, mk, mv, a);
 }
 

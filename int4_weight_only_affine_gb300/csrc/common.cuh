@@ -6,9 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
-
 #include "../../include/w4a16.h"
+#include "smem_limits.h"
 
 namespace w4a16 {
 
@@ -55,29 +54,22 @@ inline int launch_status() {
     return e == cudaSuccess ? W4A16_OK : W4_ERR_LAUNCH;
 }
 
-// Raise a kernel's dynamic shared-memory limit to `bytes` on the current
-// device, once per (kernel, device, size) and thread-safe, so that launches
-// captured into CUDA graphs make no attribute calls.  False if the runtime
+// Makes a kernel's dynamic shared-memory limit on the current device at least
+// `bytes` (see SmemLimits; one table for the whole library).  False if the runtime
 // refuses (its error is cleared).
-inline bool set_smem_once(const void *kern, int bytes) {
-    struct Entry {
-        const void *kern;
-        int dev, bytes;
-    };
-    static std::mutex mu;
-    static Entry done[64];
-    static int n = 0;
+inline bool ensure_smem(const void *kern, size_t bytes) {
+    static SmemLimits<> limits;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < n; ++i)
-        if (done[i].kern == kern && done[i].dev == dev && done[i].bytes >= bytes) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    if (n < 64) done[n++] = Entry{kern, dev, bytes};
-    return true;
+    const bool ok = limits.raise(
+        kern, dev, (int)bytes,
+        [&](int b) { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, b) == cudaSuccess; },
+        [&] {
+            cudaFuncAttributes attr;
+            return cudaFuncGetAttributes(&attr, kern) == cudaSuccess ? attr.maxDynamicSharedSizeBytes : -1;
+        });
+    if (!ok) cudaGetLastError();  // leave no stale error for a later launch check
+    return ok;
 }
 
 // Number of SMs of the current device (cached per device).

@@ -1246,11 +1246,11 @@ static int gemm_impl(const uint16_t *x16, const uint16_t *w16, uint16_t *y, int 
                          (uint64_t)N * 2, 128, 64, BK, 2, CU_TENSOR_MAP_SWIZZLE_128B))
             return W4_ERR_DEVICE;
     }
-    if (!set_smem_once(reinterpret_cast<const void *>(gemm_kernel), (int)SMEM_BYTES)) return W4_ERR_LAUNCH;
+    if (!ensure_smem(reinterpret_cast<const void *>(gemm_kernel), SMEM_BYTES)) return W4_ERR_LAUNCH;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (M > BM) {
         // CTA pairs: 256 x 256 tiles, half the operand traffic per SM.
-        if (!set_smem_once(reinterpret_cast<const void *>(gemm2_kernel), (int)SMEM2_BYTES)) return W4_ERR_LAUNCH;
+        if (!ensure_smem(reinterpret_cast<const void *>(gemm2_kernel), SMEM2_BYTES)) return W4_ERR_LAUNCH;
         const int tiles = ((M + 255) / 256) * ((N + BN - 1) / BN);
         int pairs = sm_count() / 2;
         if (pairs > tiles) pairs = tiles;
@@ -1378,7 +1378,7 @@ int w4gemm_impl(const uint16_t *x, const uint32_t *qweight, const uint16_t *scal
     if (!make_map_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)K / 8, (uint64_t)N, (uint64_t)K / 2,
                      32, FBN, CU_TENSOR_MAP_SWIZZLE_128B))
         return W4_ERR_DEVICE;
-    if (!set_smem_once(reinterpret_cast<const void *>(w4gemm_kernel), (int)F_SMEM)) return W4_ERR_LAUNCH;
+    if (!ensure_smem(reinterpret_cast<const void *>(w4gemm_kernel), F_SMEM)) return W4_ERR_LAUNCH;
     const int sms = sm_count();
     W4GemmArgs a;
     a.sc = scales;

@@ -1214,7 +1214,6 @@ bool layout_stream(StreamPlan &p, int M, bool lmhead, size_t ring_budget, int tp
 int ctas_per_sm(int M) { return M <= 8 ? 2 : 1; }
 
 const void *linear_kernel_ptr(int M, int fmt);
-bool ensure_smem(const void *kern, size_t bytes);
 
 // Clusters of C CTAs (this kernel, this shared memory) that can be resident
 // at once; cached per (kernel, C, bytes, device).
@@ -1332,35 +1331,6 @@ bool plan_stream(StreamPlan &p, int M, int N, int K, const WFmt &f, bool lmhead,
     }
     if (bestC == 0) return false;
     return plan_with_cluster(p, bestC, slots, per_sm, lmhead);
-}
-
-// Raise a kernel's dynamic shared-memory limit once per (kernel, device), and
-// only upwards, so that launches captured into CUDA graphs issue no attribute
-// calls.
-bool ensure_smem(const void *kern, size_t bytes) {
-    struct Grant {
-        const void *kern;
-        int dev;
-        size_t bytes;
-    };
-    static std::mutex mu;
-    static Grant grants[64];
-    static int ngrants = 0;
-    if (bytes <= 48 * 1024) return true;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    std::lock_guard<std::mutex> lock(mu);
-    int slot = -1;
-    for (int i = 0; i < ngrants; ++i)
-        if (grants[i].kern == kern && grants[i].dev == dev) slot = i;
-    if (slot >= 0 && grants[slot].bytes >= bytes) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
-        cudaGetLastError();  // leave no stale error for a later launch check
-        return false;
-    }
-    if (slot < 0 && ngrants < 64) slot = ngrants++;
-    if (slot >= 0) grants[slot] = Grant{kern, dev, bytes};
-    return true;
 }
 
 template <int NT, int HEAD, bool M1, int FMT, int WIDTH, int WARPS>

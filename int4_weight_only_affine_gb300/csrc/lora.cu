@@ -931,7 +931,7 @@ int check_adapters(const f16_adapters *s, LoraArgs &p) {
 template <class K, class... A>
 int launch(K kernel, long long ctas, int smem, void *stream, const A &...args) {
     if (ctas > 0x7FFFFFFFll) return W4_ERR_SHAPE;
-    if (!set_smem_once(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_LAUNCH;
+    if (!ensure_smem(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);

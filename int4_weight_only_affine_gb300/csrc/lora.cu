@@ -870,14 +870,14 @@ Cut cut_of(const f16_adapters *s, int M, int blocks) {
     // Parts of K of a stage or more, parts of the columns of a block for each warp.
     const int kb = (s->K + kStageK - 1) / kStageK;
     c.splits = kb < kMaxSplits ? kb : kMaxSplits;
-    // shrink's ring: up to 8 stages, and room behind the last one for the 128 rows of x
-    // that a product reads.  Two CTAs on an SM where two stages fit that, and the sums, else one.
+    // shrink's ring: as many stages as fit an item's rows, up to 8, and room behind the last one
+    // for the 128 rows of x that a product reads.  Two CTAs on an SM where two stages of the
+    // largest item fit that, and the sums, else one.  (shrink_few needs 32 KB of it.)
     const int F = s->rank * s->slices, hist = (s->adapters + 1) * 4;
     c.stile = F <= 192 ? 128 : 64;
     const int stage = 2 * ((F + 15) / 16 * 16 + c.stile) * 128, tail = 128 * 128;
     const bool two = (2 * stage + tail > 4 * c.stile * (F + 4) ? 2 * stage + tail : 4 * c.stile * (F + 4)) + hist <= kSmemOfTwo && tmem_columns((F + 15) / 16 * 16) <= 256;
     c.room = (two ? kSmemOfTwo : kSmemOfOne) - hist;
-    if (c.room > kMostStages * stage + tail) c.room = kMostStages * stage + tail;  // (at least 32 KB, for shrink_few)
     c.parts = (blocks + kWarps - 1) / kWarps;
     // As many CTAs as the SMs hold, shared by the scopes, but one for each item where the rows lie
     // in runs, and no more than there can be work for.

@@ -119,6 +119,20 @@ def test_projection_sizes(w4, k, columns, rank, m):
     c.check(w4, run(w4, c))
 
 
+@pytest.mark.parametrize("rank,slices", [(32, 3), (128, 3), (128, 4), (24, 4), (64, 3), (72, 4)])
+@pytest.mark.parametrize("k,m", [(2048, 300), (2056, 1100), (5000, 150)])
+@pytest.mark.parametrize("order", ["runs", "mixed"])
+def test_rings_of_long_rows(w4, rank, slices, k, m, order):
+    """Items of more than 16 rows whose K passes the ring several times: rows that lie in a row and gathered ones, all
+    ranks from 96 to 512 (items of 64 rows above 192, two boxes of A above 256), a K that ends inside a stage."""
+    columns = (72, 40, 8, 16)[:slices]
+    ids = np.repeat([2, -1, 0, 1], [m // 2, m // 10, m // 4, m - m // 2 - m // 10 - m // 4])
+    if order == "mixed":
+        ids = np.random.RandomState(m).permutation(ids)
+    c = Case(m, k, columns, rank, 3, ids, seed=rank + m)
+    c.check(w4, run(w4, c, in_place=order == "mixed"))
+
+
 def test_many_adapters(w4):
     """Histograms of more buckets than threads, and the most there can be."""
     for adapters, m in ((300, 257), (4096, 600)):

@@ -22,6 +22,7 @@ attention over it (``attention.py``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -117,6 +118,30 @@ def _stream(stream) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _on(stream):
+    """Context for making a tensor that a call on `stream` uses: the memory belongs to that stream, so that its fill
+    and its next use are ordered with the call."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _result(shape, device, stream, dtype=torch.float16) -> torch.Tensor:
+    """An output made for a call on `stream`, kept for work that the current stream has on it when it is dropped."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        y = torch.empty(shape, dtype=dtype, device=device)
+    y.record_stream(torch.cuda.current_stream())
+    return y
+
+
+def _rows_of(x: torch.Tensor, k: int, stream) -> torch.Tensor:
+    """x as [rows][k]; a copy, where it takes one, is the call's stream's."""
+    if x.dim() == 2:
+        return x
+    with _on(stream):
+        return x.reshape(-1, k)
+
+
 _QW = (torch.int32, getattr(torch, "uint32", torch.int32))
 OVERLAP_PREVIOUS = 1  # W4A16_OVERLAP_PREVIOUS: stream weights before the previous kernel finishes
 _H = (torch.float16,)
@@ -142,10 +167,10 @@ def w4_gemv(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, biases
     """y[M][N] = x[M][K] @ W^T for the int4 weight (M <= 16).  flags: 0 or
     OVERLAP_PREVIOUS (the weights must not be written by the previous kernel)."""
     N, K = _weight_dims(qweight, scales, biases, group)
-    x2 = x.reshape(-1, K) if x.dim() != 2 else x
+    x2 = _rows_of(x, K, stream)
     M = x2.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _result((M, N), x.device, stream)
     _check("w4_gemv", lib.w4_gemv_ex(_dev(x2, "x", _H), _dev(qweight, "qweight", _QW),
                                      _dev(scales, "scales", _H), _biases(biases),
                                      _dev(y, "y", _H), M, N, K, group, flags, _stream(stream)))
@@ -228,7 +253,8 @@ def w4_gemv_seq(ops, workspace: torch.Tensor | None = None, group: int = 64, str
     Returns the list of y."""
     gl = ops if isinstance(ops, GemvList) else GemvList(ops, group)
     if workspace is None:
-        workspace = gl.workspace()
+        with _on(stream):
+            workspace = gl.workspace()
     return gl.run(workspace, stream)
 
 
@@ -243,15 +269,15 @@ def lm_head_argmax_topk(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     """(idx int32 [M][k], val float32 [M][k]): the k largest logits of x @ W^T per row,
     after `rules` where given (-1 and -infinity past the tokens that a mask leaves)."""
     N, K = _weight_dims(qweight, scales, biases, group)
-    x2 = x.reshape(-1, K) if x.dim() != 2 else x
+    x2 = _rows_of(x, K, stream)
     M = x2.shape[0]
     if idx is None:
-        idx = torch.empty((M, k), dtype=torch.int32, device=x.device)
+        idx = _result((M, k), x.device, stream, torch.int32)
     if val is None:
-        val = torch.empty((M, k), dtype=torch.float32, device=x.device)
-    need = lm_head_workspace_bytes(M, N, k)
+        val = _result((M, k), x.device, stream, torch.float32)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        with _on(stream):
+            workspace = torch.empty(max(lm_head_workspace_bytes(M, N, k), 16), dtype=torch.uint8, device=x.device)
     if rules is not None:
         _check("lm_head_argmax_topk",
                lib.lm_head_argmax_topk_rules(_dev(x2, "x", _H), _dev(qweight, "qweight", _QW), _dev(scales, "scales", _H),
@@ -278,7 +304,7 @@ def w4_dequant_f16(qweight: torch.Tensor, scales: torch.Tensor, biases: torch.Te
     (it may then run concurrently with it)."""
     N, K = _weight_dims(qweight, scales, biases, group)
     if w16 is None:
-        w16 = torch.empty((K, N), dtype=torch.float16, device=qweight.device)
+        w16 = _result((K, N), qweight.device, stream)
     _check("w4_dequant_f16",
            lib.w4_dequant_f16_ex(_dev(qweight, "qweight", _QW), _dev(scales, "scales", _H),
                                  _biases(biases), _dev(w16, "w16", _H), N, K, group, flags,
@@ -303,12 +329,13 @@ def w4_gemm(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, biases
     tensor-core GEMM (M <= 128).  workspace: from w4_gemm_workspace (zero-filled
     once, then reused); a fresh one is made when None."""
     N, K = _weight_dims(qweight, scales, biases, group)
-    x2 = x.reshape(-1, K) if x.dim() != 2 else x
+    x2 = _rows_of(x, K, stream)
     M = x2.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _result((M, N), x.device, stream)
     if workspace is None:
-        workspace = w4_gemm_workspace(M, N, K, x.device)
+        with _on(stream):
+            workspace = w4_gemm_workspace(M, N, K, x.device)
     _check("w4_gemm", lib.w4_gemm_ex(_dev(x2, "x", _H), _dev(qweight, "qweight", _QW), _dev(scales, "scales", _H),
                                      _biases(biases), _dev(y, "y", _H), M, N, K, group,
                                      _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(), flags,
@@ -327,7 +354,7 @@ def f16_gemm(x16: torch.Tensor, w16: torch.Tensor, y: torch.Tensor | None = None
     if K2 != K:
         raise ValueError("inner dimensions differ")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x16.device)
+        y = _result((M, N), x16.device, stream)
     _check("f16_gemm", lib.f16_gemm_ex(_dev(x16, "x16", _H), _dev(w16, "w16", _H), _dev(y, "y", _H),
                                        M, N, K, flags, _stream(stream)))
     return y

@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from . import _check, _dev, _stream, lib
+from . import _check, _dev, _on, _stream, lib
 
 __all__ = ["Adapters", "f16_lora", "lora_workspace", "lora_workspace_bytes"]
 
@@ -110,10 +110,8 @@ def f16_lora(x: torch.Tensor, adapters: Adapters, ids: torch.Tensor, y: torch.Te
     px, xs = _rows(x, "x", (m, adapters.K))
     py, ys = _rows(y, "y", (m, adapters.N))
     po, os = (py, ys) if out is None else _rows(out, "out", (m, adapters.N))
-    if workspace is None and stream is None:
-        workspace = lora_workspace(adapters, m)
-    elif workspace is None:
-        with torch.cuda.stream(stream):  # (the memory is that stream's)
+    if workspace is None:
+        with _on(stream):
             workspace = lora_workspace(adapters, m)
     _check("f16_lora", lib.f16_lora(px, xs, py, ys, po, os, adapters.ptr, _dev(ids, "ids", (torch.int32,)), m,
                                     _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(), _stream(stream)))

@@ -17,13 +17,12 @@ index tensors are read on the device when the kernels run.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
 import torch
 
-from . import _check, _dev, _stream, lib
+from . import _check, _dev, _on, _result, _stream, lib
 
 __all__ = ["HeadNorm", "KVBatch", "KVCache", "Rope", "attention_workspace", "attention_workspace_bytes", "f16_attention",
            "f16_kv_append", "f16_rope", "rope_turns"]
@@ -79,21 +78,6 @@ def _heads(t: torch.Tensor, name: str):
         raise ValueError(f"the dim elements of {name} must be contiguous")
     # The stride of a dimension of one entry is never used; any value torch keeps there will do.
     return t.data_ptr(), (st if n > 1 else 8), (sh if h > 1 else 8)
-
-
-def _on(stream):
-    """Context for making a tensor that a call on `stream` uses: the memory belongs to that stream, so that its fill
-    and its next use are ordered with the call."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _result(shape, device, stream) -> torch.Tensor:
-    """A float16 output made for a call on `stream`, kept for work that the current stream has on it when it is dropped."""
-    with _on(stream):
-        y = torch.empty(shape, dtype=torch.float16, device=device)
-    if stream is not None:
-        y.record_stream(torch.cuda.current_stream())
-    return y
 
 
 def _ints(t: torch.Tensor, name: str) -> int:

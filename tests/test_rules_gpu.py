@@ -340,6 +340,29 @@ def test_captured_and_replayed_with_other_contents(w4):
     assert np.array_equal(got.cpu().numpy(), want_idx)
 
 
+def test_outputs_of_a_call_on_another_stream(w4):
+    """Memory that the current stream has freed but not finished with does not become another stream's output."""
+    import torch
+    head = Head(2, 700, 64, seed=3)
+    rule = random_rule(np.random.RandomState(3), 2, 700, 3, 0.3)
+    rules = rules_of(w4, rule)
+    want = best(*ruled(head.logits, **rule), 4)
+    x, qw, s, b = head.dev
+    side = torch.cuda.Stream()
+    for which in (rules, None):       # (loads the kernels, which waits for the GPU)
+        head.pick(w4, 4, which)
+    torch.cuda.synchronize()
+    for which in (rules, None):
+        torch.cuda._sleep(20000000)   # the current stream is busy for some ms
+        late = [torch.full((2, 4), -9, dtype=dtype, device="cuda") for dtype in (torch.int32, torch.float32)]
+        late.append(torch.full((w4.lm_head_workspace_bytes(2, 700, 4),), 255, dtype=torch.uint8, device="cuda"))
+        del late                      # (its fills are still to come)
+        idx, val = w4.lm_head_argmax_topk(x, qw, s, b, k=4, stream=side, rules=which)
+        torch.cuda.synchronize()
+        expect = want if which is not None else best(head.logits, np.ones((2, 700), bool), 4)
+        assert np.array_equal(idx.cpu().numpy(), expect[0]) and np.array_equal(val.cpu().numpy(), expect[1])
+
+
 # ------------------------------------------------------------ token counts
 
 def counted(counts, n, slots, tokens, offsets, prompt, reset):

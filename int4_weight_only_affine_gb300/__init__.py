@@ -191,7 +191,9 @@ def _seq_array(ops, group):
         x, qw, s, b, y, wait = op[:6]
         g = op[6] if len(op) > 6 else group
         N, K = _weight_dims(qw, s, b, g)
-        x2 = x.reshape(-1, K) if x.dim() != 2 else x
+        if not x.is_contiguous():  # (a copy would be gone, and stale, when the list runs)
+            raise ValueError("x must be contiguous")
+        x2 = x.reshape(-1, K)
         if M is None:
             M = x2.shape[0]
         elif x2.shape[0] != M:

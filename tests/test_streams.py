@@ -81,3 +81,13 @@ def test_memory_belongs_to_the_stream_of_the_call(w4, stream):
     outputs(lambda: w4.w4_gemm(x, qw, s, s, stream=stream), 1, 1)
     outputs(lambda: w4.f16_gemm(x, torch.ones(64, 8).half(), stream=stream), 1)
     outputs(lambda: w4.w4_gemv_seq([(x, qw, s, s, x, False)], stream=stream), 0, 1)
+
+
+def test_a_list_takes_no_copy_of_its_activations(w4):
+    """A list keeps addresses: an x that only a copy could bring into rows is refused."""
+    w4, state = w4
+    qw, s = torch.ones(8, 8, dtype=torch.int32), torch.ones(8, 1).half()
+    apart = torch.ones(3, 64, 1).half().expand(3, 64, 2).transpose(1, 2)
+    with pytest.raises(ValueError):
+        w4.GemvList([(apart, qw, s, s, torch.ones(6, 8).half(), False)])
+    assert w4.GemvList([(torch.ones(3, 2, 64).half(), qw, s, s, torch.ones(6, 8).half(), False)]).M == 6

@@ -111,11 +111,19 @@ def _stream(stream) -> int:
         return stream.cuda_stream
     # The current stream's handle without a Stream object around it (2.6 us a call).
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# (torch.cuda's own looks first whether CUDA is there at all; a call that has tensors knows.)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _here(t: torch.Tensor):
+    """Refuses a call whose tensors are not on the current device, on which its kernels would run."""
+    if t.is_cuda and t.get_device() != _current_device():
+        raise ValueError(f"the tensors of the call are on {t.device}, which is not the current device")
 
 
 def _on(stream):
@@ -136,8 +144,6 @@ def _result(shape, device, stream, dtype=torch.float16) -> torch.Tensor:
 
 def _rows_of(x: torch.Tensor, k: int, stream) -> torch.Tensor:
     """x as [rows][k]; a copy, where it takes one, is the call's stream's."""
-    if x.dim() == 2:
-        return x
     with _on(stream):
         return x.reshape(-1, k)
 
@@ -167,7 +173,8 @@ def w4_gemv(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, biases
     """y[M][N] = x[M][K] @ W^T for the int4 weight (M <= 16).  flags: 0 or
     OVERLAP_PREVIOUS (the weights must not be written by the previous kernel)."""
     N, K = _weight_dims(qweight, scales, biases, group)
-    x2 = _rows_of(x, K, stream)
+    _here(x)
+    x2 = x if x.dim() == 2 else _rows_of(x, K, stream)
     M = x2.shape[0]
     if y is None:
         y = _result((M, N), x.device, stream)
@@ -237,6 +244,7 @@ class GemvList:
         return torch.zeros(self.workspace_bytes(), dtype=torch.uint8, device=self.ops[0][0].device)
 
     def run(self, workspace: torch.Tensor, stream=None):
+        _here(workspace)
         _check("w4_gemv_seq", lib.w4_gemv_seq(self.ptr, self.nops, self.M,
                                               _dev(workspace, "workspace", (torch.uint8,)), workspace.numel(),
                                               0, _stream(stream)))
@@ -271,7 +279,8 @@ def lm_head_argmax_topk(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     """(idx int32 [M][k], val float32 [M][k]): the k largest logits of x @ W^T per row,
     after `rules` where given (-1 and -infinity past the tokens that a mask leaves)."""
     N, K = _weight_dims(qweight, scales, biases, group)
-    x2 = _rows_of(x, K, stream)
+    _here(x)
+    x2 = x if x.dim() == 2 else _rows_of(x, K, stream)
     M = x2.shape[0]
     if idx is None:
         idx = _result((M, k), x.device, stream, torch.int32)
@@ -305,6 +314,7 @@ def w4_dequant_f16(qweight: torch.Tensor, scales: torch.Tensor, biases: torch.Te
     OVERLAP_PREVIOUS when this call shares no memory with the previous kernel
     (it may then run concurrently with it)."""
     N, K = _weight_dims(qweight, scales, biases, group)
+    _here(qweight)
     if w16 is None:
         w16 = _result((K, N), qweight.device, stream)
     _check("w4_dequant_f16",
@@ -331,7 +341,8 @@ def w4_gemm(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, biases
     tensor-core GEMM (M <= 128).  workspace: from w4_gemm_workspace (zero-filled
     once, then reused); a fresh one is made when None."""
     N, K = _weight_dims(qweight, scales, biases, group)
-    x2 = _rows_of(x, K, stream)
+    _here(x)
+    x2 = x if x.dim() == 2 else _rows_of(x, K, stream)
     M = x2.shape[0]
     if y is None:
         y = _result((M, N), x.device, stream)
@@ -355,6 +366,7 @@ def f16_gemm(x16: torch.Tensor, w16: torch.Tensor, y: torch.Tensor | None = None
     K2, N = w16.shape
     if K2 != K:
         raise ValueError("inner dimensions differ")
+    _here(x16)
     if y is None:
         y = _result((M, N), x16.device, stream)
     _check("f16_gemm", lib.f16_gemm_ex(_dev(x16, "x16", _H), _dev(w16, "w16", _H), _dev(y, "y", _H),

@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from . import _check, _dev, _on, _stream, lib
+from . import _check, _dev, _here, _on, _stream, lib
 
 __all__ = ["Adapters", "f16_lora", "lora_workspace", "lora_workspace_bytes"]
 
@@ -108,6 +108,9 @@ def f16_lora(x: torch.Tensor, adapters: Adapters, ids: torch.Tensor, y: torch.Te
         raise TypeError("ids must be a torch.Tensor")
     m = ids.numel()
     px, xs = _rows(x, "x", (m, adapters.K))
+    _here(x)
+    if x.device != adapters.device:
+        raise ValueError(f"x is on {x.device}, the adapters on {adapters.device}")
     py, ys = _rows(y, "y", (m, adapters.N))
     po, os = (py, ys) if out is None else _rows(out, "out", (m, adapters.N))
     if workspace is None:

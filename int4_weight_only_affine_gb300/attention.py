@@ -22,7 +22,7 @@ import math
 
 import torch
 
-from . import _check, _dev, _on, _result, _stream, lib
+from . import _check, _dev, _here, _on, _result, _stream, lib
 
 __all__ = ["HeadNorm", "KVBatch", "KVCache", "Rope", "attention_workspace", "attention_workspace_bytes", "f16_attention",
            "f16_kv_append", "f16_rope", "rope_turns"]
@@ -231,6 +231,7 @@ def f16_rope(x: torch.Tensor, rope: Rope | None, positions: torch.Tensor | None 
     """y[t][h] = x[t][h] turned to positions[t] (int32; token t is at position t
     when None), normed before with norm (rope may be None then).  y may be x."""
     px, xt, xh = _heads(x, "x")
+    _here(x)
     if y is None:
         y = _result(x.shape, x.device, stream)
     py, yt, yh = _heads(y, "y")
@@ -258,6 +259,7 @@ def f16_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: KVBat
     for the rotation, where they are not those in the cache.  q_norm, k_norm:
     norms of the query and the key heads, before they are rotated.  y may be q."""
     pk, kt, kh = _heads(k, "k")
+    _here(k)
     pv, vt, vh = _heads(v, "v")
     n, d = batch.total_q, cache.head_dim
     if k.shape != (n, cache.heads, d) or v.shape != k.shape:
@@ -311,6 +313,7 @@ def f16_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, y: torch.Tens
     scores.  workspace: from attention_workspace (zero-filled once, then
     reused); a fresh one is made when None."""
     pq, qt, qh = _heads(q, "q")
+    _here(q)
     n, h, d = q.shape
     window = max(min(window, 2**31 - 1), -1)  # (passed as 32 bits; every position is below, a negative one is refused)
     if y is None:

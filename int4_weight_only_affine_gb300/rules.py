@@ -18,7 +18,7 @@ import ctypes
 
 import torch
 
-from . import _check, _dev, _stream, lib
+from . import _check, _dev, _here, _stream, lib
 
 __all__ = ["LogitRules", "TokenCounts", "token_counts_add"]
 
@@ -64,6 +64,7 @@ def token_counts_add(counts: TokenCounts, slots: torch.Tensor, tokens: torch.Ten
     tokens offsets[b] .. offsets[b + 1] - 1 (int32 [batch + 1]), or token b where
     offsets is None.  prompt: they are a prompt's, else the output's.  reset: the
     rows are cleared before (requests take their slots; of equal ones the last takes it, and device_status reports it)."""
+    _here(counts.counts)
     batch = slots.numel()
     if offsets is not None and offsets.numel() != batch + 1:
         raise ValueError("offsets must be [batch + 1]")

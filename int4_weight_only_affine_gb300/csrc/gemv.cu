@@ -413,13 +413,9 @@ __global__ void __launch_bounds__(stream_threads(WARPS, HEAD == kLmHeadRules), N
             uint32_t ph = 0;
             bool ok = true;
             for (int first = 0; first < ntl && ok; first += TEAMS)
-                for (int ch = 0; ch < nch && ok; ++ch)
+                for (int ch = 0; ch < nch && ok; ++ch) {
                     for (int tl = first; tl < first + TEAMS; ++tl) {
-                        if (TEAMS > 1 && tl >= ntl) {  // (the last tiles may be fewer than teams)
-                            s = s + 1 == S ? 0 : s + 1;
-                            ph ^= s == 0;
-                            continue;
-                        }
+                        if (TEAMS > 1 && tl >= ntl) break;
                         const int t = t0 + tl;
                         const bool tail = (t + 1) * kTileRows > N;
                         if (!mbar_wait(empty_bar(s), ph ^ 1, abort_flag)) {
@@ -460,6 +456,14 @@ __global__ void __launch_bounds__(stream_threads(WARPS, HEAD == kLmHeadRules), N
                             ph ^= 1;
                         }
                     }
+                    if (TEAMS > 1 && first + TEAMS > ntl) {  // the last tiles may be fewer than teams
+                        s += first + TEAMS - ntl;
+                        if (s >= S) {
+                            s -= S;
+                            ph ^= 1;
+                        }
+                    }
+                }
             // Every copy issued here has landed before the CTA moves on.
             for (int s = 0; s < S; ++s)
                 if (issued_any & (1u << s)) mbar_wait(full_bar(s), (issued_ph >> s) & 1);

@@ -314,7 +314,7 @@ struct StreamArgs {
 //    w4_gemv, where a CTA has a tile or two (16 rows of 11008 by 2048: 13.4 us, 16.2 with two
 //    teams; 2048 by 22016: 15.5 and 14.4).
 //  * Width 4 for lm_head with K up to 1024, whose tiles have 4 boxes, where a CTA has more
-//    than one: 1024 by 151936, greedy, 21.5, 23.9, 25.6 and 41.0 us at 1, 4, 8 and 16 rows for
+//    than one: 1024 by 151936, greedy, 22.3, 24.8, 25.8 and 39.8 us at 1, 4, 8 and 16 rows for
 //    25.8, 28.9, 32.0 and 55.4 with width 8 (1000 rows of weights, one tile a CTA: 6.6 for 6.3).
 //    (Affine groups of 64 and symmetric ones of 128 only: kernels of the other formats would
 //    add a half to the time that this file takes to compile.)

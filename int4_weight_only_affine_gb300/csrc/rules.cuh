@@ -12,8 +12,10 @@
 // counts and a bit of mask per logit, against the 0.5625 K bytes of weight that
 // made it: they are bound by the latency of these reads, which a block therefore
 // asks into L2 while it still streams weights, and issues several at a time.
-// 151936 tokens: one row, K 1024, penalties, 26.6 us for 24.8 without; 16 rows, K 2048,
-// penalties, 300 biases a row and a mask, top 50, 104 us for 91.5.
+// 151936 tokens: one row, K 1024, penalties, 24.4 us for 22.5 without; 16 rows, K 2048,
+// penalties, 300 biases a row and a mask, top 50, 105 us for 91.1.  Every block reads
+// all lists of biases, by one warp: with 1000, 3000 and 10000 entries a row these no
+// longer hide behind the stream (124, 261 and 707 us).
 #pragma once
 
 #include "common.cuh"

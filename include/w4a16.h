@@ -436,7 +436,7 @@ typedef struct {
  *              aligned; contents on entry are ignored.  Calls that may run
  *              concurrently need separate ones.
  *   Sums are fp32 over exact products; x A^T is carried on in two binary16 numbers
- *   a value (2^-22 of the row's largest), and out is rounded once.  Results are
+ *   a value (2^-22 of the row's largest finite one), and out is rounded once.  Results are
  *   deterministic; a row is not touched by what the others hold (NaN and infinities
  *   included), but its sums may be taken in another order in another mix of rows.
  * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN, W4_ERR_WORKSPACE,

@@ -559,17 +559,21 @@ __device__ __forceinline__ float4 add_shares(const float *src, long long share, 
     }
     return v;
 }
-// Bits of the largest of four values, which order as they do; infinity's if one is not a number.
+// Bits of the largest finite one of four values, which order as they do.  (What is not
+// finite stays so under any power of two, and sets none: a row's other ranks and slices are
+// scaled as without it.)
 __device__ __forceinline__ int top_of(const float4 &v) {
-    const float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-    const bool nan = v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w;
-    return nan ? 0x7F800000 : __float_as_int(m);
+    const auto bits = [](float x) {
+        const int b = __float_as_int(fabsf(x));
+        return b < 0x7F800000 ? b : 0;
+    };
+    return max(max(bits(v.x), bits(v.y)), max(bits(v.z), bits(v.w)));
 }
 // Power of two of a row: 12 - x for a largest value (its bits) in [2^x, 2^(x + 1)); 0 for
-// rows of zeros and those that are not finite.
+// rows of zeros.
 __device__ __forceinline__ int shift_of(int top) {
     const int x = (top >> 23) - 127;
-    return x == 128 || top == 0 ? 0 : 12 - max(x, -100);
+    return top == 0 ? 0 : 12 - max(x, -100);
 }
 __device__ __forceinline__ uint4 fragment(const float4 &v, float up) {
     const float a = v.x * up, b = v.y * up, c = v.z * up, d = v.w * up;
@@ -632,8 +636,8 @@ __device__ __forceinline__ void load_fragments(const LoraArgs &p, const int *row
 
 // Adds up the shares of h of the item's rows, scales and splits them into fragments.
 // The sums, 4 ranks of a row to a thread, first lie where their fragments will; tops
-// holds the bits of each row's largest value, which order as the values do (infinity
-// for a row that is not finite), and is zero on entry.  Ends with a barrier.
+// holds the bits of each row's largest finite value, which order as the values do,
+// and is zero on entry.  Ends with a barrier.
 template <int RK>
 __device__ __forceinline__ void gather_h(const LoraArgs &p, float scale, int splits, const int *rows, int n,
                                          uint8_t *smem, int *tops, float *inv) {

@@ -174,6 +174,24 @@ def test_rows_that_are_not_finite_stay_apart(w4):
     assert not np.isfinite(got[6]).any() and np.isnan(got[9]).all() and np.isnan(got[3, :64]).all()
 
 
+@pytest.mark.parametrize("m,rank", [(9, 16), (40, 16), (40, 40), (300, 72)])
+def test_a_slice_that_is_not_finite_leaves_the_others(w4, m, rank):
+    """An adapter with an infinity or a NaN in one slice's A: the columns of its other slices are as without it, with
+    x A^T beyond binary16's range as well as below it."""
+    for size in (30.0, 2.0**-12):
+        c = Case(m, 128, (64, 40, 8), rank, 3, np.arange(m) % 3, seed=13, big=size)
+        c.x = (c.x * np.float16(300 if size > 1 else 1)).astype(np.float16)
+        c.b = (c.b.astype(np.float64) * (1e-6 if size > 1 else 1.0)).astype(np.float16)
+        c.scale = np.array([1000.0, 1.0, 1e-3] if size > 1 else [1.0, 1e-3, 0.1], np.float32)
+        for value in (np.inf, np.nan):
+            c.a[:, 0, 3, 5] = 0
+            out, tol = c.want()
+            c.a[:, 0, 3, 5] = value
+            got = run(w4, c, in_place=value == np.inf).cpu().numpy()
+            assert np.all(np.abs(got[:, 64:].astype(np.float64) - out[:, 64:]) <= tol[:, 64:])
+            assert not np.isfinite(got[:, :64][np.abs(c.x[:, 5]) > 0]).all(axis=1).any()
+
+
 def test_strides(w4):
     """Rows of x, y and out inside wider tensors, adapters apart from each other; nothing else is written."""
     import torch

@@ -142,8 +142,16 @@ def _result(shape, device, stream, dtype=torch.float16) -> torch.Tensor:
     return y
 
 
+def _room(t: torch.Tensor, n: int, name: str):
+    """Refuses an output or an input that is smaller than what the call writes or reads."""
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, the call needs {n}")
+
+
 def _rows_of(x: torch.Tensor, k: int, stream) -> torch.Tensor:
     """x as [rows][k]; a copy, where it takes one, is the call's stream's."""
+    if x.dim() == 2:
+        raise ValueError(f"x must be [rows][{k}]")
     with _on(stream):
         return x.reshape(-1, k)
 
@@ -174,10 +182,11 @@ def w4_gemv(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, biases
     OVERLAP_PREVIOUS (the weights must not be written by the previous kernel)."""
     N, K = _weight_dims(qweight, scales, biases, group)
     _here(x)
-    x2 = x if x.dim() == 2 else _rows_of(x, K, stream)
+    x2 = x if x.dim() == 2 and x.shape[1] == K else _rows_of(x, K, stream)
     M = x2.shape[0]
     if y is None:
         y = _result((M, N), x.device, stream)
+    _room(y, M * N, "y")
     _check("w4_gemv", lib.w4_gemv_ex(_dev(x2, "x", _H), _dev(qweight, "qweight", _QW),
                                      _dev(scales, "scales", _H), _biases(biases),
                                      _dev(y, "y", _H), M, N, K, group, flags, _stream(stream)))
@@ -200,7 +209,8 @@ def _seq_array(ops, group):
         N, K = _weight_dims(qw, s, b, g)
         if not x.is_contiguous():  # (a copy would be gone, and stale, when the list runs)
             raise ValueError("x must be contiguous")
-        x2 = x.reshape(-1, K)
+        x2 = x if x.dim() == 2 and x.shape[1] == K else _rows_of(x, K, None)
+        _room(y, x2.shape[0] * N, "y")
         if M is None:
             M = x2.shape[0]
         elif x2.shape[0] != M:
@@ -280,12 +290,14 @@ def lm_head_argmax_topk(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     after `rules` where given (-1 and -infinity past the tokens that a mask leaves)."""
     N, K = _weight_dims(qweight, scales, biases, group)
     _here(x)
-    x2 = x if x.dim() == 2 else _rows_of(x, K, stream)
+    x2 = x if x.dim() == 2 and x.shape[1] == K else _rows_of(x, K, stream)
     M = x2.shape[0]
     if idx is None:
         idx = _result((M, k), x.device, stream, torch.int32)
     if val is None:
         val = _result((M, k), x.device, stream, torch.float32)
+    _room(idx, M * k, "idx")
+    _room(val, M * k, "val")
     if workspace is None:
         with _on(stream):
             workspace = torch.empty(max(lm_head_workspace_bytes(M, N, k), 16), dtype=torch.uint8, device=x.device)
@@ -317,6 +329,7 @@ def w4_dequant_f16(qweight: torch.Tensor, scales: torch.Tensor, biases: torch.Te
     _here(qweight)
     if w16 is None:
         w16 = _result((K, N), qweight.device, stream)
+    _room(w16, K * N, "w16")
     _check("w4_dequant_f16",
            lib.w4_dequant_f16_ex(_dev(qweight, "qweight", _QW), _dev(scales, "scales", _H),
                                  _biases(biases), _dev(w16, "w16", _H), N, K, group, flags,
@@ -342,10 +355,11 @@ def w4_gemm(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, biases
     once, then reused); a fresh one is made when None."""
     N, K = _weight_dims(qweight, scales, biases, group)
     _here(x)
-    x2 = x if x.dim() == 2 else _rows_of(x, K, stream)
+    x2 = x if x.dim() == 2 and x.shape[1] == K else _rows_of(x, K, stream)
     M = x2.shape[0]
     if y is None:
         y = _result((M, N), x.device, stream)
+    _room(y, M * N, "y")
     if workspace is None:
         with _on(stream):
             workspace = w4_gemm_workspace(M, N, K, x.device)
@@ -369,6 +383,7 @@ def f16_gemm(x16: torch.Tensor, w16: torch.Tensor, y: torch.Tensor | None = None
     _here(x16)
     if y is None:
         y = _result((M, N), x16.device, stream)
+    _room(y, M * N, "y")
     _check("f16_gemm", lib.f16_gemm_ex(_dev(x16, "x16", _H), _dev(w16, "w16", _H), _dev(y, "y", _H),
                                        M, N, K, flags, _stream(stream)))
     return y

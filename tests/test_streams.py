@@ -91,3 +91,29 @@ def test_a_list_takes_no_copy_of_its_activations(w4):
     with pytest.raises(ValueError):
         w4.GemvList([(apart, qw, s, s, torch.ones(6, 8).half(), False)])
     assert w4.GemvList([(torch.ones(3, 2, 64).half(), qw, s, s, torch.ones(6, 8).half(), False)]).M == 6
+
+
+def test_activations_and_outputs_too_small_are_refused(w4):
+    w4, state = w4
+    x, qw, s = torch.ones(3, 64).half(), torch.ones(8, 8, dtype=torch.int32), torch.ones(8, 1).half()
+    few, ints, floats = torch.ones(23).half(), torch.ones(5, dtype=torch.int32), torch.ones(5)
+    w16 = torch.ones(64, 8).half()
+    narrow, y = torch.ones(3, 56).half(), torch.ones(3, 8).half()
+    gemv = lambda x=x, y=y: w4.w4_gemv(x, qw, s, s, y=y)  # noqa: E731
+    gemm = lambda x=x, y=y: w4.w4_gemm(x, qw, s, s, y=y)  # noqa: E731
+    dense = lambda x=x, y=y: w4.f16_gemm(x, w16, y=y)  # noqa: E731
+    listed = lambda x=x, y=y: w4.GemvList([(x, qw, s, s, y, False)])  # noqa: E731
+    pick = lambda x=x, **kw: w4.lm_head_argmax_topk(x, qw, s, s, k=2, **kw)  # noqa: E731
+    for call in (gemv, gemm, dense, listed, pick):
+        call()
+        with pytest.raises(ValueError):
+            call(x=narrow)
+    for call in (gemv, gemm, dense, listed):
+        with pytest.raises(ValueError):
+            call(y=few)
+    for kw in (dict(idx=ints), dict(val=floats)):
+        with pytest.raises(ValueError):
+            pick(**kw)
+    with pytest.raises(ValueError):
+        w4.w4_dequant_f16(qw, s, s, w16=torch.ones(511).half())
+    assert w4.w4_gemv(x, qw, s, s, y=torch.ones(40).half()).shape == (40,)    # room enough

@@ -1422,14 +1422,12 @@ int gemv_impl(const uint16_t *x, const uint32_t *qw, const uint16_t *sc, const u
     if (!y) return W4_ERR_NULL;
     if (!aligned16(y)) return W4_ERR_ALIGN;
     if (flags & ~(unsigned)W4A16_OVERLAP_PREVIOUS) return W4_ERR_SHAPE;
-    StreamPlan p;
+    StreamPlan p{};  // (no rules)
     if (!plan_stream(p, M, N, K, f, false, 1, sm_count())) return W4_ERR_SHAPE;
     p.a.x = x;
     p.a.sc = sc;
     p.a.bi = bi;
     p.a.y = y;
-    p.a.ws = nullptr;
-    p.a.rules = Rules{};
     const bool ov = (flags & W4A16_OVERLAP_PREVIOUS) != 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return launch_stream_any<kLinear>(p, qw, ov, s);
